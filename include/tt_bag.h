@@ -400,6 +400,74 @@ int tt_factorize(int64_t n, int exact, int32_t out[3]);
 int tt_full_weight(const tt_desc *desc, const float *const cores[3], int table, int64_t first,
                    int64_t count, float *out, void *stream);
 
+/* ---------------------------------------------------------------- vocabulary-head losses
+ * Losses of hidden [n, d] against an embedding table used as an output head, weight [v, d]
+ * (a dense table, or rows decompressed by tt_full_weight), without the [n, v] logits: the
+ * forward keeps a running maximum and sum per position, the backward forms the gradient of
+ * the logits for a piece of the vocabulary at a time.  With z_iv = <hidden_i, weight_v>,
+ *   cross entropy (k == 0):  loss_i = lse_i - (1 - e) z_i,t(i) - (e / v) sum_v z_iv,
+ *     lse_i = log sum_v exp z_iv, e = label_smoothing; positions whose target is ignore_index
+ *     do not count;
+ *   distillation (k >= 1), from the k top logits of a teacher, T = temperature:
+ *     q_i = softmax(teacher_i / T) over the entries (index >= 0, logit above -inf),
+ *     lse_i = log sum_v exp(z_iv / T),
+ *     loss_i = T^2 sum_j q_ij (log q_ij - z_i,idx(ij) / T + lse_i);
+ *     entries may repeat a row; positions without entries do not count.
+ * A position that does not count has loss 0 and a zero gradient, adds nothing to dweight or
+ * to a mean's divisor, and its hidden row is not used.  A mean over none is 0.  A target or
+ * teacher index >= v (a target < 0 other than ignore_index) sets TT_DEV_BAD_INDEX in
+ * *dev_status (may be NULL) and is treated as ignored / as no entry.
+ *
+ * hidden, weight and the gradients are of desc->dtype; rows of hidden and weight have unit
+ * stride inside and hidden_stride / weight_stride elements between them, of any alignment of
+ * their elements; the gradients are contiguous.  Losses and grad_loss are fp32.  Products of
+ * 16-bit inputs are exact and summed in fp32; fp32 inputs enter the matrix cores as two fp16
+ * parts each (22 bits, scaled by a power of two of the tensor's largest value).  The logits'
+ * gradient is rounded once to the inputs' 16-bit type (fp32: two fp16 parts).  dweight and
+ * dhidden do not depend on the order of any atomics.
+ *
+ * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, d <= 2^20, strides <= 2^21, k <= 2048,
+ * n * k <= 2^31. */
+#define TT_DTYPE_F32  0
+#define TT_DTYPE_BF16 1
+#define TT_DTYPE_F16  2
+#define TT_REDUCE_NONE 0
+#define TT_REDUCE_MEAN 1
+#define TT_REDUCE_SUM  2
+
+typedef struct tt_loss_desc {
+    int64_t n, v, d;                       /* positions, vocabulary, width              */
+    int64_t hidden_stride, weight_stride;  /* elements between rows, >= d               */
+    int64_t ignore_index;                  /* cross entropy                             */
+    int32_t dtype;                         /* TT_DTYPE_* of hidden, weight, gradients   */
+    int32_t teacher_dtype;                 /* TT_DTYPE_* of the teacher's logits        */
+    int32_t reduction;                     /* TT_REDUCE_*                               */
+    int32_t k;                             /* 0: cross entropy; entries per position    */
+    float label_smoothing;                 /* in [0, 1]; 0 with distillation            */
+    float temperature;                     /* > 0; 1 with cross entropy                 */
+} tt_loss_desc;
+
+/* Bytes of `saved` (written by the forward, read by the backward) and of the workspace of
+ * one call (backward != 0: of the backward); `weight` because rows that do not start on 16
+ * bytes are laid out anew, a piece at a time.  0: the descriptor is rejected. */
+size_t tt_loss_saved_size(const tt_loss_desc *desc);
+size_t tt_loss_workspace_size(const tt_loss_desc *desc, const void *weight, int backward);
+
+/* loss [n] (TT_REDUCE_NONE) or [1].  targets: int64 [n], or the teacher's indices int64
+ * [n][k] with its logits [n][k].  saved and ws: 256-byte aligned. */
+int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *weight,
+                    const int64_t *targets, const void *teacher_logits, float *loss, void *saved,
+                    size_t saved_bytes, void *ws, size_t ws_bytes, int32_t *dev_status,
+                    void *stream);
+
+/* grad_hidden [n][d] and grad_weight [v][d], fully overwritten (either may be NULL), of
+ * sum_i grad_loss_i loss_i (TT_REDUCE_NONE: grad_loss [n]) or grad_loss[0] * loss.  hidden
+ * and weight as in the forward that filled `saved`. */
+int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *weight,
+                     const void *saved, size_t saved_bytes, const float *grad_loss,
+                     void *grad_hidden, void *grad_weight, void *ws, size_t ws_bytes,
+                     void *stream);
+
 /* ---------------------------------------------------------------- backward over distinct indices
  * The loss is linear in the rows, so the gradient of a batch equals that of a virtual
  * batch with one element per distinct (table, index) u, weight 1, alone in its bag, whose

@@ -12,11 +12,11 @@ Importing this package does not load the HIP library; the first call into
 """
 from . import metrics, workloads  # noqa: F401
 
-__all__ = ["metrics", "workloads", "abi", "module"]
+__all__ = ["metrics", "workloads", "abi", "module", "loss"]
 
 
 def __getattr__(name):
-    if name in ("abi", "module"):
+    if name in ("abi", "module", "loss"):
         import importlib
         return importlib.import_module("." + name, __name__)
     raise AttributeError(name)

@@ -33,12 +33,22 @@ TT_INIT_UNIFORM = 0
 TT_INIT_NORMAL = 1
 TT_INIT_APPROX_UNIFORM = 2
 TT_INIT_APPROX_NORMAL = 3
+TT_DTYPE_F32 = 0
+TT_DTYPE_BF16 = 1
+TT_DTYPE_F16 = 2
+TT_REDUCE_NONE = 0
+TT_REDUCE_MEAN = 1
+TT_REDUCE_SUM = 2
 
 
 class TTError(RuntimeError):
     def __init__(self, fn: str, code: int):
         super().__init__("%s failed: %d (%s)" % (fn, code, status_string(code)))
         self.code = code
+
+
+_P = ctypes.c_void_p
+_I64 = ctypes.c_int64
 
 
 class TTDesc(ctypes.Structure):
@@ -57,13 +67,19 @@ class TTDescD(ctypes.Structure):
                 ("ranks", ctypes.c_int32 * (TT_MAX_CORES - 1)), ("pooling", ctypes.c_int32)]
 
 
+class TTLossDesc(ctypes.Structure):
+    _fields_ = [("n", _I64), ("v", _I64), ("d", _I64), ("hidden_stride", _I64),
+                ("weight_stride", _I64), ("ignore_index", _I64), ("dtype", ctypes.c_int32),
+                ("teacher_dtype", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("label_smoothing", ctypes.c_float),
+                ("temperature", ctypes.c_float)]
+
+
 class TTCacheView(ctypes.Structure):
     _fields_ = [("slots", ctypes.c_void_p), ("rows", ctypes.c_void_p),
                 ("cache_size", ctypes.c_int64)]
 
 
-_P = ctypes.c_void_p
-_I64 = ctypes.c_int64
 _SIG = {
     "tt_bag_workspace_size": (ctypes.c_size_t, [_P, _I64, _I64, _I64]),
     "tt_bag_forward": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, ctypes.c_size_t,
@@ -133,6 +149,12 @@ _SIG = {
     "tt_profile_kernel_name": (ctypes.c_char_p, [ctypes.c_int]),
     "tt_profile_read": (ctypes.c_int, [ctypes.c_int, _P, _P]),
     "tt_debug_sync_poll_limit": (ctypes.c_int, [_I64]),
+    "tt_loss_saved_size": (ctypes.c_size_t, [_P]),
+    "tt_loss_workspace_size": (ctypes.c_size_t, [_P, _P, ctypes.c_int]),
+    "tt_loss_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P,
+                                       ctypes.c_size_t, _P, _P]),
+    "tt_loss_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_size_t, _P, _P, _P, _P,
+                                        ctypes.c_size_t, _P]),
     "tt_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 EXPORTS = tuple(_SIG)
@@ -1003,3 +1025,128 @@ def prepare_backward(desc: TTDesc, cores, indices, offsets, num_bags: int, grad_
     else:
         raise ValueError("update must be sgd, adagrad or grad")
     return Prepared(name, head + mid + tail, keep)
+
+
+# ---------------------------------------------------------------- vocabulary-head losses
+_DTYPE = {torch.float32: TT_DTYPE_F32, torch.bfloat16: TT_DTYPE_BF16, torch.float16: TT_DTYPE_F16}
+_loss_sizes = {}
+
+
+def make_loss_desc(hidden: torch.Tensor, weight: torch.Tensor, k: int = 0,
+                   reduction: int = TT_REDUCE_MEAN, ignore_index: int = -100,
+                   label_smoothing: float = 0.0, temperature: float = 1.0,
+                   teacher_dtype: Optional[torch.dtype] = None) -> TTLossDesc:
+    """hidden [n, d] and weight [v, d]: unit stride inside a row, any stride between rows."""
+    for t, name in ((hidden, "hidden"), (weight, "weight")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if not t.is_cuda:
+            raise ValueError("%s must be on the GPU" % name)
+        if t.dtype not in _DTYPE:
+            raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+        if t.dim() != 2:
+            raise ValueError("%s must have two dimensions" % name)
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError("the rows of %s must be contiguous" % name)
+    if hidden.dtype != weight.dtype:
+        raise TypeError("hidden is %s, weight %s" % (hidden.dtype, weight.dtype))
+    if hidden.device != weight.device:
+        raise ValueError("hidden is on %s, weight on %s" % (hidden.device, weight.device))
+    if hidden.shape[1] != weight.shape[1]:
+        raise ValueError("hidden has rows of %d, weight of %d" % (hidden.shape[1],
+                                                                  weight.shape[1]))
+    n, d = hidden.shape
+    v = weight.shape[0]
+    if v < 1 or d < 1:
+        raise ValueError("weight is empty")
+    # the stride of a tensor of one row says nothing
+    hs = hidden.stride(0) if n > 1 else d
+    vs = weight.stride(0) if v > 1 else d
+    if hs < d or vs < d:
+        raise ValueError("the rows of hidden and weight must not overlap")
+    return TTLossDesc(n, v, d, hs, vs, int(ignore_index), _DTYPE[hidden.dtype],
+                      _DTYPE[teacher_dtype if teacher_dtype is not None else torch.float32],
+                      reduction, k, label_smoothing, temperature)
+
+
+def tt_loss_sizes(desc: TTLossDesc, weight: torch.Tensor):
+    """(bytes of saved, of the forward's workspace, of the backward's)."""
+    p = weight.data_ptr()
+    key = (bytes(desc), p & 15)
+    got = _loss_sizes.get(key)
+    if got is None:
+        L, r = lib(), ctypes.byref(desc)
+        got = (L.tt_loss_saved_size(r), L.tt_loss_workspace_size(r, p, 0),
+               L.tt_loss_workspace_size(r, p, 1))
+        if not got[0]:
+            raise TTError("tt_loss_saved_size", -2)
+        if len(_loss_sizes) > 4096:
+            _loss_sizes.clear()
+        _loss_sizes[key] = got
+    return got
+
+
+def tt_loss_forward(desc: TTLossDesc, hidden, weight, targets, teacher_logits=None, loss=None,
+                    saved=None, ws=None, dev_status=None, stream=None):
+    """(loss, saved).  targets: int64 [n], or the teacher's indices int64 [n, k] beside its
+    logits [n, k]."""
+    sizes = tt_loss_sizes(desc, weight)
+    dev = hidden.device
+    _need(targets, torch.int64, "targets")
+    _numel(targets, desc.n * max(desc.k, 1), "targets")
+    if desc.k:
+        if teacher_logits is None:
+            raise ValueError("distillation needs teacher_logits")
+        if _DTYPE.get(teacher_logits.dtype) != desc.teacher_dtype:
+            raise TypeError("teacher_logits is %s" % teacher_logits.dtype)
+        _need(teacher_logits, teacher_logits.dtype, "teacher_logits")
+        _numel(teacher_logits, desc.n * desc.k, "teacher_logits")
+    nl = desc.n if desc.reduction == TT_REDUCE_NONE else 1
+    if loss is None:
+        loss = torch.empty(nl, dtype=torch.float32, device=dev)
+    else:
+        _need(loss, torch.float32, "loss")
+        _numel(loss, nl, "loss")
+    if saved is None:
+        saved = torch.empty(sizes[0], dtype=torch.uint8, device=dev)
+    if ws is None:
+        ws = torch.empty(sizes[1], dtype=torch.uint8, device=dev)
+    if dev_status is not None:
+        _need(dev_status, torch.int32, "dev_status")
+    for t in (targets, teacher_logits, loss, saved, ws, dev_status):
+        if t is not None and t.device != dev:
+            raise ValueError("a buffer is on %s, hidden on %s" % (t.device, dev))
+    _check("tt_loss_forward", lib().tt_loss_forward(
+        ctypes.byref(desc), hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+        _ptr(teacher_logits), loss.data_ptr(), saved.data_ptr(), saved.numel(), ws.data_ptr(),
+        ws.numel(), _ptr(dev_status), _stream(stream, hidden)))
+    return loss, saved
+
+
+def tt_loss_backward(desc: TTLossDesc, hidden, weight, saved, grad_loss, grad_hidden=None,
+                     grad_weight=None, need=(True, True), ws=None, stream=None):
+    """(grad_hidden or None, grad_weight or None); need: which of the two."""
+    sizes = tt_loss_sizes(desc, weight)
+    dev = hidden.device
+    _need(grad_loss, torch.float32, "grad_loss")
+    _numel(grad_loss, desc.n if desc.reduction == TT_REDUCE_NONE else 1, "grad_loss")
+    _need(saved, torch.uint8, "saved")
+    if need[0] and grad_hidden is None:
+        grad_hidden = torch.empty(desc.n, desc.d, dtype=hidden.dtype, device=dev)
+    if need[1] and grad_weight is None:
+        grad_weight = torch.empty(desc.v, desc.d, dtype=weight.dtype, device=dev)
+    for t, rows, name in ((grad_hidden, desc.n, "grad_hidden"),
+                          (grad_weight, desc.v, "grad_weight")):
+        if t is not None:
+            _need(t, hidden.dtype, name)
+            _numel(t, rows * desc.d, name)
+    if ws is None:
+        ws = torch.empty(sizes[2], dtype=torch.uint8, device=dev)
+    for t in (grad_loss, saved, grad_hidden, grad_weight, ws):
+        if t is not None and t.device != dev:
+            raise ValueError("a buffer is on %s, hidden on %s" % (t.device, dev))
+    _check("tt_loss_backward", lib().tt_loss_backward(
+        ctypes.byref(desc), hidden.data_ptr(), weight.data_ptr(), saved.data_ptr(),
+        saved.numel(), grad_loss.data_ptr(), _ptr(grad_hidden), _ptr(grad_weight),
+        ws.data_ptr(), ws.numel(), _stream(stream, hidden)))
+    return grad_hidden, grad_weight

@@ -1,0 +1,127 @@
+// tt_loss.h -- shared declarations of the vocabulary-head losses (not installed).
+//
+// Losses of hidden [N, D] against a weight [V, D] whose [N, V] logits are never kept:
+//   z_iv = <hidden_i, weight_v> / T,  lse_i = log sum_v exp z_iv
+//   cross entropy  loss_i = lse_i - (1 - e) z_i,t - (e / V) sum_v z_iv
+//   distillation   loss_i = T^2 (sum_j q_ij log q_ij - sum_j q_ij z_i,idx(ij) + lse_i)
+//   dloss_i/d<hidden_i, weight_v> = s g_iv,  g_iv = exp(z_iv - lse_i) - e / V - sum of the
+//   position's q on v (the target's q is 1 - e), s = 1 or T.
+//
+// forward:  k_entries (distillation: q, duplicates merged) -> k_pack (positions that count,
+//           packed) -> k_logits (running maximum and sum per position and 128 or 256 rows of
+//           the weight) -> k_loss (lse, the entries' logits, loss)
+// backward: k_pack, then per piece of the vocabulary k_logits (G = row factor * g, in 16
+//           bits), k_entries_g (distillation: the entries of G), k_dhidden (split over the
+//           vocabulary, fp32), k_dweight; k_dhidden_out adds the splits.
+#pragma once
+#include "tt_gemm.h"
+#include "tt_internal.h"
+
+namespace ttb {
+
+constexpr int PACK_ROWS = 16;   // positions per block of k_pack
+constexpr int AMAX_BLOCKS = 256;
+
+// scalars that the device works out, at the head of the workspace
+struct LossScalars {
+  float zs;        // logits from sums of products: log2(e) / T over the planes' scales
+  float c_dh, c_dw;  // what the sums of the gradients are multiplied by
+  int ticket;      // blocks of k_loss that are done
+};
+
+// saved by the forward for the backward (one buffer, see saved_layout)
+struct LossSaved {
+  int *count;      // positions that count
+  int *slot;       // [N] position -> packed row, or -1 - (a packed row of zeros)
+  int *tgt;        // [N] packed row -> target row of the weight (cross entropy)
+  float *lse;      // [N] packed row -> lse in base 2
+  int *eidx;       // [N][k] distillation entries: row of the weight or -1
+  float *eq, *ez;  // their q and their logit in base 2
+  float *ent;      // [N] sum_j q log q
+};
+
+struct LossArgs {
+  // problem
+  int64_t N, V, D, hld, wld;  // ld in elements
+  int dtype, tdtype, reduction, k;
+  int64_t ignore;
+  float smoothing, temp;
+  const void *hidden, *weight;
+  const int64_t *tgt;      // targets [N] or teacher indices [N][k]
+  const void *tlogits;     // teacher logits [N][k]
+  float *loss;
+  const float *up;         // gradient of the loss
+  void *dh, *dw;
+  int32_t *status;
+  // plan
+  int64_t Npad, Dp;        // packed rows and their pitch (elements)
+  int planes;              // 2 for fp32
+  int pack_w;              // the weight is packed too (fp32, or rows not on 16 bytes)
+  int64_t piece;           // rows of the weight per piece
+  int ptiles;              // running statistics per position
+  int splits;              // of the vocabulary in k_dhidden
+  LossSaved sv;
+  // workspace
+  LossScalars *sc;
+  float *amax;             // [2 * AMAX_BLOCKS] block maxima of |weight| and |hidden| (fp32)
+  char *hp, *wp;           // packed positions, packed piece of the weight
+  int64_t hplane, wplane;  // bytes
+  float2 *part;            // [Npad][ptiles] (max, sum) in base 2
+  float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)
+  float *rowloss;          // [N]
+  float *rowf;             // [Npad] factor of a packed row's g
+  char *G;                 // [planes][Npad][piece]
+  int64_t ldG, Gplane;     // bytes
+  float *dhp;              // [splits][Npad][Dp]
+};
+
+// G is held times 2^14 in fp16 and times 2^32 in bf16: the matrix cores take subnormal inputs
+// as zeros, and small probabilities are most of a vocabulary (|g| <= 1 keeps both in range).
+__host__ __device__ inline int g_exp(int dtype) { return dtype == TT_DTYPE_BF16 ? 32 : 14; }
+
+// tile shapes: 0 = 256 x 256, 1 = 128 x 128, 2 = 128 x 64 (x by y)
+struct GemmShape {
+  int cfg, bx, by;
+};
+GemmShape gemm_shape(int64_t x, int64_t y);
+
+hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
+                         hipStream_t s);
+hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s);
+hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s);
+
+// the weight's rows [v0, v0 + nv) as an operand: the caller's memory or the packed piece
+inline Operand weight_operand(const LossArgs &a, int64_t v0, int64_t nv) {
+  Operand o;
+  if (a.pack_w) {
+    o.p = a.wp; o.ld = a.Dp * 2; o.plane = a.wplane; o.rows = nv; o.cols = a.Dp;
+  } else {
+    o.p = (const char *)a.weight + v0 * a.wld * 2; o.ld = a.wld * 2; o.plane = 0;
+    o.rows = a.V - v0; o.cols = a.D;
+  }
+  return o;
+}
+inline Operand hidden_operand(const LossArgs &a) {
+  Operand o;
+  o.p = a.hp; o.ld = a.Dp * 2; o.plane = a.hplane; o.rows = a.Npad; o.cols = a.Dp;
+  return o;
+}
+inline Operand g_operand(const LossArgs &a, int64_t nv) {
+  Operand o;
+  o.p = a.G; o.ld = a.ldG; o.plane = a.Gplane; o.rows = a.Npad;
+  o.cols = (nv + GK - 1) / GK * GK;
+  return o;
+}
+
+template <class T, class F>
+inline hipError_t lds_limit(F *f) {
+  static const hipError_t e = hipFuncSetAttribute(
+      (const void *)f, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+  return e;
+}
+
+typedef Tile<256, 256, 128, 64, 2> TileL;
+typedef Tile<128, 128, 64, 64, 2> TileM;
+typedef Tile<128, 64, 32, 64, 3> TileS;
+
+}  // namespace ttb

@@ -1,0 +1,697 @@
+// tt_loss.hip -- vocabulary-head losses: the kernels around the products, and the C entry points.
+#include "tt_loss.h"
+
+#include <algorithm>
+
+namespace ttb {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------- rows of any alignment
+// 8 elements from p (p on an element's boundary only), `left` of them real, the rest 0
+template <class S>
+__device__ __forceinline__ void load8(const S *p, int64_t left, S (&v)[8]) {
+  struct __attribute__((packed, aligned(2))) any { S x[8]; };
+  if (left >= 8) {
+    const any a = *(const any *)p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = a.x[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : (S)0.f;
+  }
+}
+
+// 8 source elements -> planes of 16-bit elements (fp32: x s = hi + lo; an infinity or NaN
+// stays in hi alone)
+template <class S, class E, int PL>
+__device__ __forceinline__ void store8(const S (&v)[8], float scale, char *dst, int64_t plane) {
+  typename E::v8 h;
+  if constexpr (PL == 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = (typename E::e)v[e];
+  } else {
+    typename E::v8 l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = (float)v[e] * scale;
+      h[e] = (typename E::e)x;
+      const float r = x - (float)h[e];
+      l[e] = (typename E::e)(r == r && fabsf(x) < INFINITY ? r : 0.f);
+    }
+    *(typename E::v8 *)(dst + plane) = l;
+  }
+  *(typename E::v8 *)dst = h;
+}
+
+// exponent b of the power of two that puts |x| <= amax below 2^15 (0 for an empty tensor)
+__device__ __forceinline__ int plane_exp(float amax) {
+  if (!(amax > 0.f)) return 0;
+  int e;
+  frexpf(amax, &e);  // amax < 2^e
+  return min(15 - e, 120);
+}
+// block maxima -> exponent, in every lane of a wave
+__device__ __forceinline__ int planes_exp(const float *amax, int lane) {
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < AMAX_BLOCKS / 64; ++u) m = fmaxf(m, amax[u * 64 + lane]);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  return plane_exp(m);
+}
+
+// ---------------------------------------------------------------- distillation entries
+// One wave per position: q = softmax(teacher / T) over its entries (index >= 0 and logit
+// above -inf); entries of one row of the weight are added into the first of them, so that
+// every (position, row) is written once.  sv.tgt[i]: whether position i has entries.
+template <class S>
+__global__ __launch_bounds__(256) void k_entries(LossArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char dyn[];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, k = a.k;
+  const int64_t i = (int64_t)blockIdx.x * 4 + wv;
+  if (i >= a.N) return;  // no workgroup barrier below: waves keep to their own LDS
+  int *id = (int *)dyn + wv * 2 * k;
+  float *q = (float *)(id + k);
+  const float it = 1.f / a.temp;
+  float m = -INFINITY;
+  bool bad = false, any = false, nan = false;
+  for (int j = lane; j < k; j += 64) {
+    const int64_t v = a.tgt[i * k + j];
+    float t = (float)((const S *)a.tlogits)[i * k + j] * it;
+    bad |= v >= a.V;
+    const bool in = v >= 0 && v < a.V && !(t == -INFINITY);
+    id[j] = in ? (int)v : -1;
+    q[j] = in ? t : -INFINITY;
+    any |= in;
+    nan |= in && t != t;
+    m = fmaxf(m, q[j]);
+  }
+  if (__any(bad) && lane == 0) set_status(a.status, TT_DEV_BAD_INDEX);
+  any = __any(any);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if (__any(nan)) m = __builtin_nanf("");
+  float s = 0.f;
+  for (int j = lane; j < k; j += 64)
+    if (id[j] >= 0) s += expf(q[j] - m);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  const float ls = logf(s);
+  float ent = 0.f;
+  for (int j = lane; j < k; j += 64) {
+    if (id[j] < 0) continue;
+    const float lq = q[j] - m - ls, p = expf(lq);
+    q[j] = p;
+    if (!(p == 0.f)) ent += p * lq;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) ent += __shfl_xor(ent, o);
+  __builtin_amdgcn_wave_barrier();
+  __threadfence_block();
+  for (int j = lane; j < k; j += 64) {
+    int own = id[j];
+    float p = 0.f;
+    if (own >= 0) {
+      for (int u = 0; u < k; ++u) {
+        if (id[u] != own) continue;
+        if (u < j) {
+          own = -1;
+          break;
+        }
+        p += q[u];
+      }
+    }
+    a.sv.eidx[i * k + j] = own;
+    a.sv.eq[i * k + j] = own < 0 ? 0.f : p;
+  }
+  if (lane == 0) {
+    a.sv.ent[i] = ent;
+    a.sv.tgt[i] = any;
+  }
+}
+
+// ---------------------------------------------------------------- packing
+__device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
+  if (a.k) return a.sv.tgt[i] != 0;
+  const int64_t t = a.tgt[i];
+  return t != a.ignore && t >= 0 && t < a.V;
+}
+
+// largest finite |x| of the weight (blocks 0 ..) and of the positions that count, per block
+__global__ __launch_bounds__(256) void k_amax(LossArgs a, int grad) {
+  const bool w = blockIdx.x < AMAX_BLOCKS;
+  const int b = blockIdx.x % AMAX_BLOCKS, tid = threadIdx.x;
+  const float *x = (const float *)(w ? a.weight : a.hidden);
+  const int64_t rows = w ? a.V : a.N, ld = w ? a.wld : a.hld;
+  const int64_t cpr = (a.D + 7) / 8, n = rows * cpr;
+  float m = 0.f;
+  int64_t i = (int64_t)b * 256 + tid;
+  int64_t r = i / cpr, q = i % cpr;
+  const int64_t dr = AMAX_BLOCKS * 256 / cpr, dq = AMAX_BLOCKS * 256 % cpr;
+  for (; i < n; i += AMAX_BLOCKS * 256) {
+    if (w || (grad ? a.sv.slot[r] >= 0 : counts(a, r))) {
+      float v[8];
+      load8(x + r * ld + q * 8, a.D - q * 8, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = fabsf(v[e]);
+        if (y < INFINITY) m = fmaxf(m, y);
+      }
+    }
+    r += dr;
+    q += dq;
+    if (q >= cpr) q -= cpr, ++r;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  __shared__ float s[4];
+  if ((tid & 63) == 0) s[tid >> 6] = m;
+  __syncthreads();
+  if (tid == 0) a.amax[blockIdx.x] = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+}
+
+// Rows of the hidden states that count, in order, from row 0 of hp on; the rest of hp's Npad
+// rows are zeros (every position that does not count clears one of them).  A block counts
+// the positions before its own by itself: N / 16 blocks read N / 2 flags on average, which
+// up to some 10^5 positions costs less than another launch to scan them.  The backward takes
+// the places from `saved`.
+template <class S, class E, int PL>
+__global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
+  __shared__ int s_n[4], s_slot[PACK_ROWS];
+  __shared__ float s_m[4];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int64_t i0 = (int64_t)blockIdx.x * PACK_ROWS, ib = min(i0, a.N);
+  int base = 0;
+  float cm = 1.f;  // power of two that the factors of the rows are divided by
+  if (!grad) {
+    int n = 0;
+    for (int64_t i = tid; i < ib; i += 256) n += counts(a, i);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+    if (lane == 0) s_n[wv] = n;
+    __syncthreads();
+    base = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+  } else if (a.reduction == TT_REDUCE_NONE && a.dtype != TT_DTYPE_BF16) {
+    // fp16 G: the largest factor is brought to 1, so 2^14 g fits and small factors keep bits
+    float m = 0.f;
+    for (int64_t i = tid; i < a.N; i += 256) {
+      const float u = fabsf(a.up[i]);
+      if (u < INFINITY && a.sv.slot[i] >= 0) m = fmaxf(m, u);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (lane == 0) s_m[wv] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    if (m > 0.f) {
+      int e;
+      frexpf(m, &e);
+      cm = ldexpf(1.f, max(e, -120));
+    }
+  }
+  int ew = 0, eh = 0;
+  if (PL > 1) {
+    ew = planes_exp(a.amax, lane);
+    eh = planes_exp(a.amax + AMAX_BLOCKS, lane);
+  }
+  if (wv == 0) {
+    const int64_t i = i0 + lane;
+    const bool own = lane < PACK_ROWS, in = own && i < a.N;
+    int slot = (int)min<int64_t>(i, INT32_MAX);  // a row past the last position: zeros
+    if (grad) {
+      if (in) slot = a.sv.slot[i];
+      if (in && slot >= 0) a.rowf[slot] = a.reduction == TT_REDUCE_NONE ? a.up[i] / cm : 1.f;
+    } else {
+      const bool ok = in && counts(a, i);
+      const uint64_t mask = __ballot(ok);
+      const int rank = base + __popcll(mask & ((1ull << lane) - 1));
+      if (in) {
+        slot = ok ? rank : -1 - (int)(a.N - 1 - (i - rank));
+        a.sv.slot[i] = slot;
+        if (!a.k) {
+          const int64_t t = a.tgt[i];
+          if (ok) a.sv.tgt[rank] = (int)t;
+          else if (t != a.ignore) set_status(a.status, TT_DEV_BAD_INDEX);
+        }
+        if (i == a.N - 1) *a.sv.count = rank + ok;
+      }
+    }
+    if (own) s_slot[lane] = in ? slot : -1 - slot;
+    if (blockIdx.x == 0 && lane == 0) {
+      a.sc->zs = ldexpf(LOG2E / a.temp, -(ew + eh));
+      a.sc->ticket = 0;
+      if (grad) {
+        float c = a.k ? a.temp : 1.f;
+        if (a.reduction == TT_REDUCE_NONE) c *= cm;
+        else c *= a.up[0] / (a.reduction == TT_REDUCE_MEAN ? (float)max(*a.sv.count, 1) : 1.f);
+        a.sc->c_dh = ldexpf(c, -ew - g_exp(a.dtype));
+        a.sc->c_dw = ldexpf(c, -eh - g_exp(a.dtype));
+      }
+    }
+  }
+  __syncthreads();
+  const float scale = ldexpf(1.f, eh);
+  const int cpr = (int)(a.Dp / 8);
+  for (int q = tid; q < PACK_ROWS * cpr; q += 256) {
+    const int r = q / cpr, c = (q - r * cpr) * 8, slot = s_slot[r];
+    const int64_t row = slot < 0 ? -1 - slot : slot;
+    if (row >= a.Npad) continue;
+    S v[8];
+    load8((const S *)a.hidden + (i0 + r) * a.hld + c, slot < 0 ? 0 : a.D - c, v);
+    store8<S, E, PL>(v, scale, a.hp + (row * a.Dp + c) * 2, a.hplane);
+  }
+}
+
+// rows [v0, v0 + nv) of the weight -> wp
+template <class S, class E, int PL>
+__global__ __launch_bounds__(256) void k_pack_w(LossArgs a, int64_t v0, int64_t nv) {
+  const float scale = PL > 1 ? ldexpf(1.f, planes_exp(a.amax, threadIdx.x & 63)) : 1.f;
+  const int64_t cpr = a.Dp / 8, n = nv * cpr, st = (int64_t)gridDim.x * 256;
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n; q += st) {
+    const int64_t r = q / cpr, c = (q - r * cpr) * 8;
+    S v[8];
+    load8((const S *)a.weight + (v0 + r) * a.wld + c, a.D - c, v);
+    store8<S, E, PL>(v, scale, a.wp + (r * a.Dp + c) * 2, a.wplane);
+  }
+}
+
+// ---------------------------------------------------------------- loss
+// One block per position: the tiles' statistics become its lse; the logits of its entries
+// are dot products of their own (fp32 sums of the inputs' products), a wave each.
+template <class S>
+__global__ __launch_bounds__(256) void k_loss(LossArgs a) {
+  __shared__ float s_m[4], s_s[4], s_z[4], s_q[4];
+  __shared__ double s_d[4];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int64_t i = blockIdx.x;
+  const int slot = a.sv.slot[i];
+  float out = 0.f;
+  if (slot >= 0) {
+    const float2 *p = a.part + (int64_t)slot * a.ptiles;
+    float m = -INFINITY, s = 0.f, z = 0.f;
+    for (int t = tid; t < a.ptiles; t += 256) {
+      const float2 v = p[t];
+      const float n = fmaxf(m, v.x), n0 = n == -INFINITY ? 0.f : n;
+      s = s * __builtin_amdgcn_exp2f(m - n0) + v.y * __builtin_amdgcn_exp2f(v.x - n0);
+      m = n;
+      if (a.smoothing > 0.f) z += a.zpart[(int64_t)slot * a.ptiles + t];
+    }
+    float wm = m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor(wm, o));
+    s *= __builtin_amdgcn_exp2f(m - (wm == -INFINITY ? 0.f : wm));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      s += __shfl_xor(s, o);
+      z += __shfl_xor(z, o);
+    }
+    float qz = 0.f;
+    const int ne = a.k ? a.k : 1;
+    const S *h = (const S *)a.hidden + i * a.hld;
+    for (int j = wv; j < ne; j += 4) {
+      const int v = a.k ? a.sv.eidx[i * a.k + j] : a.sv.tgt[slot];
+      if (v < 0) continue;
+      const S *w = (const S *)a.weight + v * a.wld;
+      float d = 0.f;
+      for (int64_t c = lane * 8; c < a.D; c += 512) {
+        S x[8], y[8];
+        load8(h + c, a.D - c, x);
+        load8(w + c, a.D - c, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d += (float)x[e] * (float)y[e];
+      }
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o);
+      d *= LOG2E / a.temp;
+      if (a.k) {
+        qz += a.sv.eq[i * a.k + j] * d;
+        if (lane == 0) a.sv.ez[i * a.k + j] = d;
+      } else {
+        qz = d;
+      }
+    }
+    if (lane == 0) s_m[wv] = wm, s_s[wv] = s, s_z[wv] = z, s_q[wv] = qz;
+    __syncthreads();
+    if (tid == 0) {
+      float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+      const float M0 = M == -INFINITY ? 0.f : M;
+      float sum = 0.f, zs = 0.f, q = 0.f;
+      for (int w = 0; w < 4; ++w) {
+        sum += s_s[w] * __builtin_amdgcn_exp2f(s_m[w] - M0);
+        zs += s_z[w];
+        q += s_q[w];
+      }
+      const float lse = M0 + log2f(sum);
+      a.sv.lse[slot] = lse;
+      if (a.k)
+        out = a.temp * a.temp * (a.sv.ent[i] + (lse - q) * LN2);
+      else
+        out = (lse - (1.f - a.smoothing) * q - a.smoothing * (zs / (float)a.V)) * LN2;
+    }
+  }
+  if (a.reduction == TT_REDUCE_NONE) {
+    if (tid == 0) a.loss[i] = out;
+    return;
+  }
+  // the block that ends last adds the rows up, in the rows' order, in fp64
+  if (tid == 0) {
+    __hip_atomic_store(&a.rowloss[i], out, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __threadfence();
+    s_last = atomicAdd(&a.sc->ticket, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double d = 0.0;
+  for (int64_t r = tid; r < a.N; r += 256)
+    d += (double)__hip_atomic_load(&a.rowloss[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o);
+  if (lane == 0) s_d[wv] = d;
+  __syncthreads();
+  if (tid == 0) {
+    d = s_d[0] + s_d[1] + s_d[2] + s_d[3];
+    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? d / max(*a.sv.count, 1) : d);
+  }
+}
+
+// ---------------------------------------------------------------- backward, around the products
+// G at the entries of this piece: (p - q) from the entry's own logit, rounded like the rest
+template <class E, int PL>
+__global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64_t nv) {
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.N * a.k) return;
+  const int64_t i = t / a.k;
+  const int slot = a.sv.slot[i];
+  const int64_t v = a.sv.eidx[t] - v0;
+  if (slot < 0 || a.sv.eidx[t] < 0 || v < 0 || v >= nv) return;
+  const int x = g_exp(a.dtype);
+  const float q = ldexpf(__builtin_amdgcn_exp2f(0.5f * (a.sv.ez[t] - a.sv.lse[slot])), x / 2);
+  const float g = (q * q - ldexpf(a.sv.eq[t], x)) * a.rowf[slot];
+  char *o = a.G + slot * a.ldG + v * 2;
+  const typename E::e h = (typename E::e)g;
+  *(typename E::e *)o = h;
+  if (PL > 1) *(typename E::e *)(o + a.Gplane) = (typename E::e)(g - (float)h);
+}
+
+// dh: the splits added in order, scaled, rounded once, put back at the position's row
+template <class O>
+__global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a) {
+  const int per = (int)((a.D + 1023) / 1024);
+  for (int64_t b = blockIdx.x; b < a.N * per; b += gridDim.x) {
+  const int64_t i = b / per, c = ((b - i * per) * 256 + threadIdx.x) * 4;
+  if (c >= a.D) continue;
+  const int slot = a.sv.slot[i];
+  f4 v = zero4();
+  if (slot >= 0) {
+    const float *p = a.dhp + (int64_t)slot * a.Dp + c;
+    const int64_t st = a.Npad * a.Dp;
+#pragma unroll 4
+    for (int k = 0; k < a.splits; ++k) v += *(const f4 *)(p + k * st);
+    v *= a.sc->c_dh;
+  }
+  O *o = (O *)a.dh + i * a.D + c;
+  typedef O o4 __attribute__((ext_vector_type(4)));
+  o4 w;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) w[r] = (O)v[r];
+  if (a.D % 4 == 0 && ((uintptr_t)a.dh & (4 * sizeof(O) - 1)) == 0) {
+    *(o4 *)o = w;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (c + r < a.D) o[r] = w[r];
+  }
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_fill0(T *x, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    x[i] = (T)0.f;
+}
+
+// ---------------------------------------------------------------- plan
+GemmShape gemm_shape(int64_t x, int64_t y) {
+  const int64_t big = ((x + 255) / 256) * ((y + 255) / 256);
+  if (y > 128 && x > 128 && big >= 128) return {0, 256, 256};
+  if (y > 64) return {1, 128, 128};
+  return {2, 128, 64};
+}
+
+// Memory for one piece of the vocabulary: G of every position, and the packed weight.  256
+// MiB each keeps a piece about the size of the last-level cache; it is the whole of what the
+// backward holds beside its outputs, whatever V is.
+constexpr int64_t PIECE_BYTES = 256ll << 20;
+
+static int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+struct Bump {
+  char *base;
+  int64_t off = 0;
+  template <class T>
+  void take(T *&p, int64_t n) {
+    p = (T *)(base + off);
+    off = round_up(off + n * (int64_t)sizeof(T), 256);
+  }
+};
+
+static int64_t saved_layout(LossArgs &a, void *saved) {
+  Bump b{(char *)saved};
+  b.take(a.sv.count, 1);
+  b.take(a.sv.slot, a.N);
+  b.take(a.sv.tgt, a.N);
+  b.take(a.sv.lse, a.N);
+  if (a.k) {
+    b.take(a.sv.ent, a.N);
+    b.take(a.sv.eidx, a.N * a.k);
+    b.take(a.sv.eq, a.N * a.k);
+    b.take(a.sv.ez, a.N * a.k);
+  }
+  return b.off;
+}
+
+static int64_t elem_size(int dtype) { return dtype == TT_DTYPE_F32 ? 4 : 2; }
+
+static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
+  Bump b{(char *)ws};
+  b.take(a.sc, 1);
+  b.take(a.amax, 2 * AMAX_BLOCKS);
+  a.hplane = a.Npad * a.Dp * 2;
+  b.take(a.hp, a.hplane * a.planes);
+  int64_t rows = a.V;
+  const int64_t wrow = a.Dp * 2 * a.planes, grow = a.Npad * 2 * a.planes;
+  int64_t lim = (1ll << 38) / std::max<int64_t>(a.Npad, 256);  // tiles of one launch
+  if (a.pack_w) lim = std::min(lim, PIECE_BYTES / wrow);
+  if (grad) lim = std::min(lim, PIECE_BYTES / grow);
+  if (lim < rows) {  // pieces of near-equal size, whole tiles each
+    const int64_t n = (rows + std::max<int64_t>(lim, 256) - 1) / std::max<int64_t>(lim, 256);
+    rows = round_up((rows + n - 1) / n, 256);
+  }
+  a.piece = rows;
+  a.wplane = rows * a.Dp * 2;
+  if (a.pack_w) b.take(a.wp, a.wplane * a.planes);
+  if (grad) {
+    b.take(a.rowf, a.Npad);
+    a.ldG = round_up(std::min(rows, a.V), 256) * 2;
+    a.Gplane = a.Npad * a.ldG;
+    b.take(a.G, a.Gplane * a.planes);
+    const GemmShape t = gemm_shape(a.D, a.N);
+    const int64_t tiles = ((a.D + t.bx - 1) / t.bx) * ((a.Npad + t.by - 1) / t.by);
+    // enough workgroups for every CU, at least 8 tiles of k each
+    a.splits = (int)std::max<int64_t>(1, std::min((256 + tiles - 1) / tiles, rows / 512));
+    b.take(a.dhp, (int64_t)a.splits * a.Npad * a.Dp);
+  } else {
+    const GemmShape t = gemm_shape(std::min(a.V, a.piece), a.N);
+    a.ptiles = (int)((a.V + t.bx - 1) / t.bx);
+    b.take(a.part, a.Npad * a.ptiles);
+    b.take(a.zpart, a.smoothing > 0.f ? a.Npad * a.ptiles : 0);
+    b.take(a.rowloss, a.N);
+  }
+  return b.off;
+}
+
+static int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
+  if (!d) return TT_EINVAL;
+  if (d->n < 0 || d->v < 1 || d->d < 1 || d->k < 0) return TT_EINVAL;
+  if (d->dtype < TT_DTYPE_F32 || d->dtype > TT_DTYPE_F16) return TT_EINVAL;
+  if (d->teacher_dtype < TT_DTYPE_F32 || d->teacher_dtype > TT_DTYPE_F16) return TT_EINVAL;
+  if (d->reduction < TT_REDUCE_NONE || d->reduction > TT_REDUCE_SUM) return TT_EINVAL;
+  if (!(d->label_smoothing >= 0.f && d->label_smoothing <= 1.f)) return TT_EINVAL;
+  if (!(d->temperature > 0.f && d->temperature < INFINITY)) return TT_EINVAL;
+  if (d->k ? d->label_smoothing != 0.f : d->temperature != 1.f) return TT_EINVAL;
+  if (d->hidden_stride < d->d || d->weight_stride < d->d) return TT_EINVAL;
+  // 32-bit places of positions, rows and entries; a tile's rows inside one descriptor
+  if (d->n > (1 << 23) || d->v > (1 << 30) || d->d > (1 << 20) || d->k > 2048) return TT_ESHAPE;
+  if (d->hidden_stride > (1 << 21) || d->weight_stride > (1 << 21)) return TT_ESHAPE;
+  if (d->n * std::max(d->k, 1) > (1ll << 31)) return TT_ESHAPE;
+  a = {};
+  a.N = d->n; a.V = d->v; a.D = d->d; a.hld = d->hidden_stride; a.wld = d->weight_stride;
+  a.dtype = d->dtype; a.tdtype = d->teacher_dtype; a.reduction = d->reduction; a.k = d->k;
+  a.ignore = d->ignore_index; a.smoothing = d->label_smoothing; a.temp = d->temperature;
+  a.weight = weight;
+  a.Npad = round_up(std::max<int64_t>(a.N, 1), a.N > 128 ? 256 : a.N > 64 ? 128 : 64);
+  a.Dp = round_up(a.D, 64);
+  a.planes = a.dtype == TT_DTYPE_F32 ? 2 : 1;
+  a.pack_w = a.planes > 1 || a.D % 8 || a.wld % 8 || ((uintptr_t)weight & 15);
+  return TT_OK;
+}
+
+template <class S, class E, int PL>
+static hipError_t pack_h(const LossArgs &a, int grad, hipStream_t s) {
+  tt_launch(K_LOSS_PACK, k_pack<S, E, PL>, dim3((unsigned)((a.Npad + PACK_ROWS - 1) / PACK_ROWS)),
+            dim3(256), 0, s, a, grad);
+  return hipGetLastError();
+}
+template <class S, class E, int PL>
+static hipError_t pack_w(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
+  const int64_t n = nv * (a.Dp / 8);
+  tt_launch(K_LOSS_PACK, k_pack_w<S, E, PL>, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)),
+            dim3(256), 0, s, a, v0, nv);
+  return hipGetLastError();
+}
+static hipError_t launch_pack(const LossArgs &a, int grad, hipStream_t s) {
+  if (a.dtype == TT_DTYPE_F32) {
+    tt_launch(K_LOSS_PACK, k_amax, dim3(2 * AMAX_BLOCKS), dim3(256), 0, s, a, grad);
+    return pack_h<float, Fp16, 2>(a, grad, s);
+  }
+  if (a.dtype == TT_DTYPE_BF16) return pack_h<__bf16, Bf16, 1>(a, grad, s);
+  return pack_h<_Float16, Fp16, 1>(a, grad, s);
+}
+static hipError_t launch_pack_w(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
+  if (!a.pack_w) return hipSuccess;
+  if (a.dtype == TT_DTYPE_F32) return pack_w<float, Fp16, 2>(a, v0, nv, s);
+  if (a.dtype == TT_DTYPE_BF16) return pack_w<__bf16, Bf16, 1>(a, v0, nv, s);
+  return pack_w<_Float16, Fp16, 1>(a, v0, nv, s);
+}
+
+static hipError_t launch_entries(const LossArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N + 3) / 4));
+  const size_t lds = (size_t)a.k * 32;  // at most 64 KiB
+  if (a.tdtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_entries<float>, grid, dim3(256), lds, s, a);
+  else if (a.tdtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_entries<__bf16>, grid, dim3(256), lds, s, a);
+  else tt_launch(K_LOSS_ROWS, k_entries<_Float16>, grid, dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+
+static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)a.N);
+  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_loss<float>, grid, dim3(256), 0, s, a);
+  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_loss<__bf16>, grid, dim3(256), 0, s, a);
+  else tt_launch(K_LOSS_ROWS, k_loss<_Float16>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+static hipError_t launch_entries_g(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
+  if (!a.k) return hipSuccess;
+  const dim3 grid((unsigned)((a.N * a.k + 255) / 256));
+  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_entries_g<Fp16, 2>, grid, dim3(256), 0, s, a, v0, nv);
+  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_entries_g<Bf16, 1>, grid, dim3(256), 0, s, a, v0, nv);
+  else tt_launch(K_LOSS_ROWS, k_entries_g<Fp16, 1>, grid, dim3(256), 0, s, a, v0, nv);
+  return hipGetLastError();
+}
+
+static hipError_t launch_dhidden_out(const LossArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>(a.N * ((a.D + 1023) / 1024), 1 << 20));
+  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_dhidden_out<float>, grid, dim3(256), 0, s, a);
+  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_dhidden_out<__bf16>, grid, dim3(256), 0, s, a);
+  else tt_launch(K_LOSS_ROWS, k_dhidden_out<_Float16>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+static hipError_t fill0(void *x, int64_t bytes, hipStream_t s) {
+  if (bytes == 0) return hipSuccess;
+  const int64_t n = bytes / 2;  // every output here has elements of 2 or 4 bytes
+  hipLaunchKernelGGL(k_fill0<_Float16>, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)),
+                     dim3(256), 0, s, (_Float16 *)x, n);
+  return hipGetLastError();
+}
+
+}  // namespace ttb
+
+using namespace ttb;
+
+extern "C" {
+
+size_t tt_loss_saved_size(const tt_loss_desc *desc) {
+  LossArgs a;
+  return loss_args(desc, nullptr, a) == TT_OK ? (size_t)saved_layout(a, nullptr) : 0;
+}
+
+size_t tt_loss_workspace_size(const tt_loss_desc *desc, const void *weight, int backward) {
+  LossArgs a;
+  return loss_args(desc, weight, a) == TT_OK ? (size_t)ws_layout(a, nullptr, backward != 0) : 0;
+}
+
+int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *weight,
+                    const int64_t *targets, const void *teacher_logits, float *loss, void *saved,
+                    size_t saved_bytes, void *ws, size_t ws_bytes, int32_t *dev_status,
+                    void *stream) {
+  LossArgs a;
+  const int rc = loss_args(desc, weight, a);
+  if (rc != TT_OK) return rc;
+  if (!weight || !saved || !ws) return TT_EINVAL;
+  if (!loss && (a.N || a.reduction != TT_REDUCE_NONE)) return TT_EINVAL;
+  if (a.N && (!hidden || !targets || (a.k && !teacher_logits))) return TT_EINVAL;
+  if ((uintptr_t)weight % elem_size(a.dtype) || (uintptr_t)hidden % elem_size(a.dtype)) return TT_EINVAL;
+  if ((uintptr_t)saved % 256 || (uintptr_t)ws % 256) return TT_EWORKSPACE;
+  if ((size_t)saved_layout(a, saved) > saved_bytes) return TT_EWORKSPACE;
+  if ((size_t)ws_layout(a, ws, false) > ws_bytes) return TT_EWORKSPACE;
+  a.hidden = hidden; a.tgt = targets; a.tlogits = teacher_logits; a.loss = loss;
+  a.status = dev_status;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (a.N == 0) {  // no position: a sum or mean of nothing is 0
+    if (a.reduction != TT_REDUCE_NONE) e = fill0(loss, 4, s);
+    return e == hipSuccess ? TT_OK : TT_EHIP;
+  }
+  if (a.k) e = launch_entries(a, s);
+  if (e == hipSuccess) e = launch_pack(a, 0, s);
+  const GemmShape t = gemm_shape(std::min(a.V, a.piece), a.N);
+  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
+    const int64_t nv = std::min(a.piece, a.V - v0);
+    e = launch_pack_w(a, v0, nv, s);
+    if (e == hipSuccess) e = launch_logits(a, v0, nv, (int)(v0 / t.bx), false, s);
+  }
+  if (e == hipSuccess) e = launch_loss(a, s);
+  return e == hipSuccess ? TT_OK : TT_EHIP;
+}
+
+int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *weight,
+                     const void *saved, size_t saved_bytes, const float *grad_loss,
+                     void *grad_hidden, void *grad_weight, void *ws, size_t ws_bytes,
+                     void *stream) {
+  LossArgs a;
+  const int rc = loss_args(desc, weight, a);
+  if (rc != TT_OK) return rc;
+  if (!weight || !saved || !ws || (a.N && (!hidden || !grad_loss))) return TT_EINVAL;
+  if ((uintptr_t)weight % elem_size(a.dtype) || (uintptr_t)hidden % elem_size(a.dtype) ||
+      (uintptr_t)grad_hidden % elem_size(a.dtype) || (uintptr_t)grad_weight % elem_size(a.dtype))
+    return TT_EINVAL;
+  if ((uintptr_t)saved % 256 || (uintptr_t)ws % 256) return TT_EWORKSPACE;
+  if ((size_t)saved_layout(a, (void *)saved) > saved_bytes) return TT_EWORKSPACE;
+  if ((size_t)ws_layout(a, ws, true) > ws_bytes) return TT_EWORKSPACE;
+  a.hidden = hidden; a.up = grad_loss; a.dh = grad_hidden; a.dw = grad_weight;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (a.N == 0) {
+    if (grad_weight) e = fill0(grad_weight, a.V * a.D * elem_size(a.dtype), s);
+    return e == hipSuccess ? TT_OK : TT_EHIP;
+  }
+  if (!grad_hidden && !grad_weight) return TT_OK;
+  e = launch_pack(a, 1, s);
+  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
+    const int64_t nv = std::min(a.piece, a.V - v0);
+    e = launch_pack_w(a, v0, nv, s);
+    if (e == hipSuccess) e = launch_logits(a, v0, nv, 0, true, s);
+    if (e == hipSuccess) e = launch_entries_g(a, v0, nv, s);
+    if (e == hipSuccess && grad_hidden) e = launch_dhidden(a, v0, nv, s);
+    if (e == hipSuccess && grad_weight) e = launch_dweight(a, v0, nv, s);
+  }
+  if (e == hipSuccess && grad_hidden) e = launch_dhidden_out(a, s);
+  return e == hipSuccess ? TT_OK : TT_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,148 @@
+// tt_loss_grad.hip -- the two products of the backward, on the piece's G as it lies:
+//   dh[i][d] = sum_v G_iv W_vd   x = d (columns of the weight), y = positions, k = v
+//   dW[v][d] = sum_i G_iv h_id   x = d (columns of the packed positions), y = v, k = positions
+// dh is summed in fp32 over the splits and pieces of the vocabulary (each tile owned by one
+// workgroup, so the order is fixed); dW is complete in one piece and rounded once.
+#include "tt_loss.h"
+
+namespace ttb {
+
+template <class E, class T>
+__global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
+                                                   int64_t split, const int *count, int add) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  int ix, iy, is;
+  tile_of(a, ix, iy, is);
+  f4 acc[T::MI][T::NI];
+  if (!gemm_tile<E, T, true, false>(a, lds, ix, iy, is, acc)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int x = ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
+  const int y = iy * T::Y + (wv / T::NWX) * T::wy + c;
+  const int n = *count;
+#pragma unroll
+  for (int j = 0; j < T::NI; ++j) {
+    if (y + 16 * j >= n) continue;
+    float *o = out + is * split + (y + 16 * j) * ld + x;
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i) {
+      if (x + 16 * i >= ld) continue;  // ld is a multiple of 64: whole groups of four
+      f4 v = acc[i][j];
+      if (add) v += *(const f4 *)(o + 16 * i);
+      *(f4 *)(o + 16 * i) = v;
+    }
+  }
+}
+
+template <class O>
+struct DwOut {
+  O *out;             // dW of the piece's first row
+  int64_t ld, nv;     // = D, rows of the piece
+  const LossScalars *sc;
+  int vec;            // rows of whole, aligned groups of four
+};
+
+template <class E, class T, class O>
+__global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  int ix, iy, is;
+  tile_of(a, ix, iy, is);
+  f4 acc[T::MI][T::NI];
+  if (!gemm_tile<E, T, true, true>(a, lds, ix, iy, is, acc)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int x = ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
+  const int64_t y = (int64_t)iy * T::Y + (wv / T::NWX) * T::wy + c;
+  const float s = ep.sc->c_dw;
+  typedef O o4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int j = 0; j < T::NI; ++j) {
+    if (y + 16 * j >= ep.nv) continue;
+    O *o = ep.out + (y + 16 * j) * ep.ld + x;
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i) {
+      const int64_t left = ep.ld - (x + 16 * i);
+      o4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = (O)(acc[i][j][r] * s);
+      if (ep.vec) {
+        if (left > 0) *(o4 *)(o + 16 * i) = v;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (r < left) o[16 * i + r] = v[r];
+      }
+    }
+  }
+}
+
+template <class E, class T>
+static hipError_t go_dh(const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
+  const hipError_t e = lds_limit<T>(&k_dhidden<E, T>);
+  if (e != hipSuccess) return e;
+  tt_launch(K_LOSS_DH, k_dhidden<E, T>, dim3(g.tx * g.ty * g.splits), dim3(T::NT), T::LDS, s, g,
+            a.dhp, a.Dp, a.Npad * a.Dp, (const int *)a.sv.count, add);
+  return hipGetLastError();
+}
+
+template <class E, class T, class O>
+static hipError_t go_dw(const GemmArgs &g, const LossArgs &a, int64_t v0, int64_t nv,
+                        hipStream_t s) {
+  const hipError_t e = lds_limit<T>(&k_dweight<E, T, O>);
+  if (e != hipSuccess) return e;
+  DwOut<O> ep;
+  ep.out = (O *)a.dw + v0 * a.D;
+  ep.ld = a.D; ep.nv = nv; ep.sc = a.sc;
+  ep.vec = a.D % 4 == 0 && ((uintptr_t)a.dw & (4 * sizeof(O) - 1)) == 0;
+  tt_launch(K_LOSS_DW, k_dweight<E, T, O>, dim3(g.tx * g.ty), dim3(T::NT), T::LDS, s, g, ep);
+  return hipGetLastError();
+}
+
+hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
+  GemmArgs g = {};
+  g.P = weight_operand(a, v0, nv);
+  g.Q = g_operand(a, nv);
+  g.K = (nv + GK - 1) / GK * GK;
+  const int64_t per = (g.K + a.splits - 1) / a.splits;
+  g.kper = (per + GK - 1) / GK * GK;
+  g.ycount = a.sv.count;
+  g.nseg = a.planes > 1 ? 3 : 1;
+  const GemmShape t = gemm_shape(a.D, a.N);
+  g.tx = (int)((a.D + t.bx - 1) / t.bx);
+  g.ty = (int)((a.N + t.by - 1) / t.by);
+  g.splits = a.splits;
+  const int add = v0 > 0;
+  if (a.dtype == TT_DTYPE_BF16) {
+    if (t.cfg == 0) return go_dh<Bf16, TileL>(g, a, add, s);
+    if (t.cfg == 1) return go_dh<Bf16, TileM>(g, a, add, s);
+    return go_dh<Bf16, TileS>(g, a, add, s);
+  }
+  if (t.cfg == 0) return go_dh<Fp16, TileL>(g, a, add, s);
+  if (t.cfg == 1) return go_dh<Fp16, TileM>(g, a, add, s);
+  return go_dh<Fp16, TileS>(g, a, add, s);
+}
+
+template <class E, class O>
+static hipError_t pick_dw(int cfg, const GemmArgs &g, const LossArgs &a, int64_t v0, int64_t nv,
+                          hipStream_t s) {
+  if (cfg == 0) return go_dw<E, TileL, O>(g, a, v0, nv, s);
+  if (cfg == 1) return go_dw<E, TileM, O>(g, a, v0, nv, s);
+  return go_dw<E, TileS, O>(g, a, v0, nv, s);
+}
+
+hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
+  GemmArgs g = {};
+  g.P = hidden_operand(a);
+  g.Q = g_operand(a, nv);
+  g.K = a.Npad;
+  g.kper = a.Npad;
+  g.kcount = a.sv.count;
+  g.nseg = a.planes > 1 ? 3 : 1;
+  const GemmShape t = gemm_shape(a.D, nv);
+  g.tx = (int)((a.D + t.bx - 1) / t.bx);
+  g.ty = (int)((nv + t.by - 1) / t.by);
+  g.splits = 1;
+  if (a.dtype == TT_DTYPE_BF16) return pick_dw<Bf16, __bf16>(t.cfg, g, a, v0, nv, s);
+  if (a.dtype == TT_DTYPE_F16) return pick_dw<Fp16, _Float16>(t.cfg, g, a, v0, nv, s);
+  return pick_dw<Fp16, float>(t.cfg, g, a, v0, nv, s);
+}
+
+}  // namespace ttb
