@@ -20,18 +20,20 @@
 namespace ttb {
 
 constexpr int PACK_ROWS = 16;   // positions per block of k_pack
-constexpr int AMAX_BLOCKS = 256;
+constexpr int AMAX_BLOCKS = 1024;
 
 // scalars that the device works out, at the head of the workspace
 struct LossScalars {
   float zs;        // logits from sums of products: log2(e) / T over the planes' scales
   float c_dh, c_dw;  // what the sums of the gradients are multiplied by
   int ticket;      // blocks of k_loss that are done
+  int splits;      // of the vocabulary in k_dhidden
 };
 
 // saved by the forward for the backward (one buffer, see saved_layout)
 struct LossSaved {
   int *count;      // positions that count
+  int *exps;       // fp32: exponents of the planes' scales, weight and hidden states
   int *slot;       // [N] position -> packed row, or -1 - (a packed row of zeros)
   int *tgt;        // [N] packed row -> target row of the weight (cross entropy)
   float *lse;      // [N] packed row -> lse in base 2
@@ -59,7 +61,7 @@ struct LossArgs {
   int pack_w;              // the weight is packed too (fp32, or rows not on 16 bytes)
   int64_t piece;           // rows of the weight per piece
   int ptiles;              // running statistics per position
-  int splits;              // of the vocabulary in k_dhidden
+  int dh_bx, dh_by, cus;   // k_dhidden's tile, compute units
   LossSaved sv;
   // workspace
   LossScalars *sc;
@@ -72,8 +74,34 @@ struct LossArgs {
   float *rowf;             // [Npad] factor of a packed row's g
   char *G;                 // [planes][Npad][piece]
   int64_t ldG, Gplane;     // bytes
-  float *dhp;              // [splits][Npad][Dp]
+  float *dhp;              // [splits][tiles of positions that count][Dp]
 };
+
+constexpr int DH_SPLITS = 64 /* a lane each */, DH_TILES = 1024;  // most splits; most tiles where there are several
+
+// floats between two splits of dh
+__host__ __device__ inline int64_t dh_split_stride(const LossArgs &a, int count) {
+  return (int64_t)((count + a.dh_by - 1) / a.dh_by) * a.dh_by * a.Dp;
+}
+
+// Splits of the vocabulary in k_dhidden for `count` positions (known on the device only): the
+// number with the least estimated time.  A tile of 256 x 256 does 64 k in about 1.8 us on one
+// CU, the tiles come in rounds over the CUs (smaller tiles: two workgroups per CU, at half
+// the rate each), and each split's sums cost a write and a read at some 4 TB/s.
+__device__ __forceinline__ int dh_splits(const LossArgs &a, int count, int lane) {
+  const int tiles = (int)((a.D + a.dh_bx - 1) / a.dh_bx) * ((count + a.dh_by - 1) / a.dh_by);
+  const int K = (int)(a.piece < a.V ? a.piece : a.V), s = lane + 1;
+  const int slots = a.dh_bx == 256 ? a.cus : 2 * a.cus;
+  const float area = a.dh_bx * a.dh_by / 65536.f;
+  const float step = 1.8f * area * (a.planes > 1 ? 3.f : 1.f) * (a.dh_bx == 256 ? 1.f : 2.f);
+  float t = (float)((s * tiles + slots - 1) / slots) * step * ((K + 64 * s - 1) / (64 * s)) +
+            0.13f * s * tiles * area;
+  if (s > 1 && (s * tiles > DH_TILES || K / s < 512)) t = INFINITY;
+  float least = t;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) least = fminf(least, __shfl_xor(least, o));
+  return __ffsll((unsigned long long)__ballot(t == least));  // lane s - 1 holds s
+}
 
 // G is held times 2^14 in fp16 and times 2^32 in bf16: the matrix cores take subnormal inputs
 // as zeros, and small probabilities are most of a vocabulary (|g| <= 1 keeps both in range).
@@ -84,6 +112,7 @@ struct GemmShape {
   int cfg, bx, by;
 };
 GemmShape gemm_shape(int64_t x, int64_t y);
+GemmShape dh_shape(const LossArgs &a);
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
                          hipStream_t s);

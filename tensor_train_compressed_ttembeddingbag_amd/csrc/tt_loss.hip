@@ -139,7 +139,7 @@ __device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
 }
 
 // largest finite |x| of the weight (blocks 0 ..) and of the positions that count, per block
-__global__ __launch_bounds__(256) void k_amax(LossArgs a, int grad) {
+__global__ __launch_bounds__(256) void k_amax(LossArgs a) {
   const bool w = blockIdx.x < AMAX_BLOCKS;
   const int b = blockIdx.x % AMAX_BLOCKS, tid = threadIdx.x;
   const float *x = (const float *)(w ? a.weight : a.hidden);
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a, int grad) {
   int64_t r = i / cpr, q = i % cpr;
   const int64_t dr = AMAX_BLOCKS * 256 / cpr, dq = AMAX_BLOCKS * 256 % cpr;
   for (; i < n; i += AMAX_BLOCKS * 256) {
-    if (w || (grad ? a.sv.slot[r] >= 0 : counts(a, r))) {
+    if (w || counts(a, r)) {
       float v[8];
       load8(x + r * ld + q * 8, a.D - q * 8, v);
 #pragma unroll
@@ -212,8 +212,8 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
   }
   int ew = 0, eh = 0;
   if (PL > 1) {
-    ew = planes_exp(a.amax, lane);
-    eh = planes_exp(a.amax + AMAX_BLOCKS, lane);
+    ew = grad ? a.sv.exps[0] : planes_exp(a.amax, lane);
+    eh = grad ? a.sv.exps[1] : planes_exp(a.amax + AMAX_BLOCKS, lane);
   }
   if (wv == 0) {
     const int64_t i = i0 + lane;
@@ -238,13 +238,17 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
       }
     }
     if (own) s_slot[lane] = in ? slot : -1 - slot;
+    int splits = 1;
+    if (grad && blockIdx.x == 0) splits = dh_splits(a, max(*a.sv.count, 1), lane);
     if (blockIdx.x == 0 && lane == 0) {
       a.sc->zs = ldexpf(LOG2E / a.temp, -(ew + eh));
       a.sc->ticket = 0;
+      if (!grad) a.sv.exps[0] = ew, a.sv.exps[1] = eh;
       if (grad) {
         float c = a.k ? a.temp : 1.f;
         if (a.reduction == TT_REDUCE_NONE) c *= cm;
         else c *= a.up[0] / (a.reduction == TT_REDUCE_MEAN ? (float)max(*a.sv.count, 1) : 1.f);
+        a.sc->splits = splits;
         a.sc->c_dh = ldexpf(c, -ew - g_exp(a.dtype));
         a.sc->c_dw = ldexpf(c, -eh - g_exp(a.dtype));
       }
@@ -266,7 +270,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
 // rows [v0, v0 + nv) of the weight -> wp
 template <class S, class E, int PL>
 __global__ __launch_bounds__(256) void k_pack_w(LossArgs a, int64_t v0, int64_t nv) {
-  const float scale = PL > 1 ? ldexpf(1.f, planes_exp(a.amax, threadIdx.x & 63)) : 1.f;
+  const float scale = PL > 1 ? ldexpf(1.f, a.sv.exps[0]) : 1.f;
   const int64_t cpr = a.Dp / 8, n = nv * cpr, st = (int64_t)gridDim.x * 256;
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n; q += st) {
     const int64_t r = q / cpr, c = (q - r * cpr) * 8;
@@ -310,26 +314,42 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a) {
     float qz = 0.f;
     const int ne = a.k ? a.k : 1;
     const S *h = (const S *)a.hidden + i * a.hld;
-    for (int j = wv; j < ne; j += 4) {
-      const int v = a.k ? a.sv.eidx[i * a.k + j] : a.sv.tgt[slot];
-      if (v < 0) continue;
-      const S *w = (const S *)a.weight + v * a.wld;
-      float d = 0.f;
-      for (int64_t c = lane * 8; c < a.D; c += 512) {
-        S x[8], y[8];
-        load8(h + c, a.D - c, x);
-        load8(w + c, a.D - c, y);
+    // four entries at once: one read of the position's row, five loads in flight
+    for (int j0 = wv * 4; j0 < ne; j0 += 16) {
+      const S *w[4];
+      bool on[4];
+      float d[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d += (float)x[e] * (float)y[e];
+      for (int u = 0; u < 4; ++u) {
+        const int j = min(j0 + u, ne - 1), v = a.k ? a.sv.eidx[i * a.k + j] : a.sv.tgt[slot];
+        on[u] = j0 + u < ne && v >= 0;
+        w[u] = (const S *)a.weight + (v < 0 ? 0 : v) * a.wld;
+        d[u] = 0.f;
+      }
+      for (int64_t c = lane * 8; c < a.D; c += 512) {
+        S x[8];
+        load8(h + c, a.D - c, x);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (!on[u]) continue;
+          S y[8];
+          load8(w[u] + c, a.D - c, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[u] += (float)x[e] * (float)y[e];
+        }
       }
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o);
-      d *= LOG2E / a.temp;
-      if (a.k) {
-        qz += a.sv.eq[i * a.k + j] * d;
-        if (lane == 0) a.sv.ez[i * a.k + j] = d;
-      } else {
-        qz = d;
+      for (int u = 0; u < 4; ++u) {
+        if (!on[u]) continue;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) d[u] += __shfl_xor(d[u], o);
+        d[u] *= LOG2E / a.temp;
+        if (a.k) {
+          qz += a.sv.eq[i * a.k + j0 + u] * d[u];
+          if (lane == 0) a.sv.ez[i * a.k + j0 + u] = d[u];
+        } else {
+          qz = d[u];
+        }
       }
     }
     if (lane == 0) s_m[wv] = wm, s_s[wv] = s, s_z[wv] = z, s_q[wv] = qz;
@@ -358,12 +378,13 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a) {
   // the block that ends last adds the rows up, in the rows' order, in fp64
   if (tid == 0) {
     __hip_atomic_store(&a.rowloss[i], out, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __threadfence();
+    // the row is written through to memory by its own scope; the ticket waits for that store
+    // alone (a fence would write back the XCD's whole L2, in every block)
+    vmem_drain();
     s_last = atomicAdd(&a.sc->ticket, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   double d = 0.0;
   for (int64_t r = tid; r < a.N; r += 256)
     d += (double)__hip_atomic_load(&a.rowloss[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -407,9 +428,10 @@ __global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a) {
   f4 v = zero4();
   if (slot >= 0) {
     const float *p = a.dhp + (int64_t)slot * a.Dp + c;
-    const int64_t st = a.Npad * a.Dp;
+    const int64_t st = dh_split_stride(a, *a.sv.count);
+    const int ns = a.sc->splits;
 #pragma unroll 4
-    for (int k = 0; k < a.splits; ++k) v += *(const f4 *)(p + k * st);
+    for (int k = 0; k < ns; ++k) v += *(const f4 *)(p + k * st);
     v *= a.sc->c_dh;
   }
   O *o = (O *)a.dh + i * a.D + c;
@@ -441,6 +463,14 @@ GemmShape gemm_shape(int64_t x, int64_t y) {
   return {2, 128, 64};
 }
 
+// dh's tiles are few where positions and width are; the vocabulary is split then
+GemmShape dh_shape(const LossArgs &a) {
+  const int64_t big = ((a.D + 255) / 256) * ((a.N + 255) / 256);
+  if (a.N > 128 && a.D > 128 && big * std::min<int64_t>(DH_SPLITS, a.piece / 512) >= 128)
+    return {0, 256, 256};
+  return a.N > 64 ? GemmShape{1, 128, 128} : GemmShape{2, 128, 64};
+}
+
 // Memory for one piece of the vocabulary: G of every position, and the packed weight.  256
 // MiB each keeps a piece about the size of the last-level cache; it is the whole of what the
 // backward holds beside its outputs, whatever V is.
@@ -461,6 +491,7 @@ struct Bump {
 static int64_t saved_layout(LossArgs &a, void *saved) {
   Bump b{(char *)saved};
   b.take(a.sv.count, 1);
+  b.take(a.sv.exps, 2);
   b.take(a.sv.slot, a.N);
   b.take(a.sv.tgt, a.N);
   b.take(a.sv.lse, a.N);
@@ -478,7 +509,7 @@ static int64_t elem_size(int dtype) { return dtype == TT_DTYPE_F32 ? 4 : 2; }
 static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
   Bump b{(char *)ws};
   b.take(a.sc, 1);
-  b.take(a.amax, 2 * AMAX_BLOCKS);
+  b.take(a.amax, grad || a.planes == 1 ? 0 : 2 * AMAX_BLOCKS);
   a.hplane = a.Npad * a.Dp * 2;
   b.take(a.hp, a.hplane * a.planes);
   int64_t rows = a.V;
@@ -498,11 +529,12 @@ static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
     a.ldG = round_up(std::min(rows, a.V), 256) * 2;
     a.Gplane = a.Npad * a.ldG;
     b.take(a.G, a.Gplane * a.planes);
-    const GemmShape t = gemm_shape(a.D, a.N);
-    const int64_t tiles = ((a.D + t.bx - 1) / t.bx) * ((a.Npad + t.by - 1) / t.by);
-    // enough workgroups for every CU, at least 8 tiles of k each
-    a.splits = (int)std::max<int64_t>(1, std::min((256 + tiles - 1) / tiles, rows / 512));
-    b.take(a.dhp, (int64_t)a.splits * a.Npad * a.Dp);
+    const GemmShape t = dh_shape(a);
+    a.dh_bx = t.bx; a.dh_by = t.by;
+    a.cus = std::max(device_cus(), 1);
+    const int64_t ty = (a.N + t.by - 1) / t.by, tx = (a.D + t.bx - 1) / t.bx;
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(DH_SPLITS, rows / 512));
+    b.take(a.dhp, std::max(ty, std::min<int64_t>(DH_TILES / tx, most * ty)) * t.by * a.Dp);
   } else {
     const GemmShape t = gemm_shape(std::min(a.V, a.piece), a.N);
     a.ptiles = (int)((a.V + t.bx - 1) / t.bx);
@@ -554,7 +586,7 @@ static hipError_t pack_w(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t 
 }
 static hipError_t launch_pack(const LossArgs &a, int grad, hipStream_t s) {
   if (a.dtype == TT_DTYPE_F32) {
-    tt_launch(K_LOSS_PACK, k_amax, dim3(2 * AMAX_BLOCKS), dim3(256), 0, s, a, grad);
+    if (!grad) tt_launch(K_LOSS_PACK, k_amax, dim3(2 * AMAX_BLOCKS), dim3(256), 0, s, a);
     return pack_h<float, Fp16, 2>(a, grad, s);
   }
   if (a.dtype == TT_DTYPE_BF16) return pack_h<__bf16, Bf16, 1>(a, grad, s);

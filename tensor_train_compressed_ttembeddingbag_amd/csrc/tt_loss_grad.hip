@@ -5,20 +5,23 @@
 // workgroup, so the order is fixed); dW is complete in one piece and rounded once.
 #include "tt_loss.h"
 
+#include <algorithm>
+
 namespace ttb {
 
 template <class E, class T>
 __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
-                                                   int64_t split, const int *count, int add) {
+                                                   const int *count, int add) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   int ix, iy, is;
-  tile_of(a, ix, iy, is);
+  if (!tile_of<T::Y>(a, ix, iy, is)) return;
   f4 acc[T::MI][T::NI];
   if (!gemm_tile<E, T, true, false>(a, lds, ix, iy, is, acc)) return;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int x = ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
   const int y = iy * T::Y + (wv / T::NWX) * T::wy + c;
   const int n = *count;
+  const int64_t split = (int64_t)a.ty * T::Y * ld;
 #pragma unroll
   for (int j = 0; j < T::NI; ++j) {
     if (y + 16 * j >= n) continue;
@@ -45,7 +48,7 @@ template <class E, class T, class O>
 __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   int ix, iy, is;
-  tile_of(a, ix, iy, is);
+  if (!tile_of<T::Y>(a, ix, iy, is)) return;
   f4 acc[T::MI][T::NI];
   if (!gemm_tile<E, T, true, true>(a, lds, ix, iy, is, acc)) return;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
@@ -78,8 +81,8 @@ template <class E, class T>
 static hipError_t go_dh(const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
   const hipError_t e = lds_limit<T>(&k_dhidden<E, T>);
   if (e != hipSuccess) return e;
-  tt_launch(K_LOSS_DH, k_dhidden<E, T>, dim3(g.tx * g.ty * g.splits), dim3(T::NT), T::LDS, s, g,
-            a.dhp, a.Dp, a.Npad * a.Dp, (const int *)a.sv.count, add);
+  tt_launch(K_LOSS_DH, k_dhidden<E, T>, dim3(std::max(g.tx * g.ty, DH_TILES)), dim3(T::NT), T::LDS,
+            s, g, a.dhp, a.Dp, (const int *)a.sv.count, add);
   return hipGetLastError();
 }
 
@@ -101,14 +104,12 @@ hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   g.P = weight_operand(a, v0, nv);
   g.Q = g_operand(a, nv);
   g.K = (nv + GK - 1) / GK * GK;
-  const int64_t per = (g.K + a.splits - 1) / a.splits;
-  g.kper = (per + GK - 1) / GK * GK;
   g.ycount = a.sv.count;
   g.nseg = a.planes > 1 ? 3 : 1;
-  const GemmShape t = gemm_shape(a.D, a.N);
+  const GemmShape t = dh_shape(a);
   g.tx = (int)((a.D + t.bx - 1) / t.bx);
   g.ty = (int)((a.N + t.by - 1) / t.by);
-  g.splits = a.splits;
+  g.dsplits = &a.sc->splits;
   const int add = v0 > 0;
   if (a.dtype == TT_DTYPE_BF16) {
     if (t.cfg == 0) return go_dh<Bf16, TileL>(g, a, add, s);

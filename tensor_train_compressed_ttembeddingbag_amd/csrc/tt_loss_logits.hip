@@ -28,7 +28,7 @@ template <class E, class T, bool GRAD>
 __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   int ix, iy, is;
-  tile_of(a, ix, iy, is);
+  if (!tile_of<T::Y>(a, ix, iy, is)) return;
   f4 acc[T::MI][T::NI];
   if (!gemm_tile<E, T, false, false>(a, lds, ix, iy, is, acc)) return;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;

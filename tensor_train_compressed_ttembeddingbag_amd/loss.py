@@ -12,6 +12,7 @@ Argument marshalling only; the computation runs in libttbag (``tt_loss_forward``
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -21,22 +22,74 @@ from . import abi
 _REDUCTION = {"none": abi.TT_REDUCE_NONE, "mean": abi.TT_REDUCE_MEAN, "sum": abi.TT_REDUCE_SUM}
 
 
+class _Plan:
+    """The checked descriptor of one kind of call and the buffer sizes that go with it."""
+
+    def __init__(self, hidden, weight, k, reduction, kw):
+        self.desc = abi.make_loss_desc(hidden, weight, k=k, reduction=_REDUCTION[reduction], **kw)
+        self.saved, self.fwd, self.bwd = abi.tt_loss_sizes(self.desc, weight)
+        self.ref = ctypes.byref(self.desc)
+        self.dtype = hidden.dtype
+        self.n, self.d = hidden.shape
+        self.v = weight.shape[0]
+
+
+_plans = {}
+
+
+def _bytes(n: int, device) -> torch.Tensor:
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+# What abi.tt_loss_forward and tt_loss_backward check of every buffer is known here by
+# construction, so the two calls go to the library directly: a small loss is bound by the
+# host, and the checks were a third of its calls.
+def _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status):
+    dev = hidden.device
+    loss = torch.empty(shape, dtype=torch.float32, device=dev)
+    saved, ws = _bytes(plan.saved, dev), _bytes(plan.fwd, dev)
+    rc = abi.lib().tt_loss_forward(
+        plan.ref, hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+        None if teacher_logits is None else teacher_logits.data_ptr(), loss.data_ptr(),
+        saved.data_ptr(), plan.saved, ws.data_ptr(), plan.fwd,
+        None if dev_status is None else dev_status.data_ptr(), abi._stream(None, hidden))
+    if rc:
+        raise abi.TTError("tt_loss_forward", rc)
+    return loss, saved
+
+
+def _backward(ctx, grad_loss):
+    hidden, weight, saved = ctx.saved_tensors
+    plan, dev = ctx.plan, hidden.device
+    grad_loss = grad_loss.contiguous()
+    need_h, need_w = ctx.needs_input_grad[:2]
+    dh = torch.empty((plan.n, plan.d), dtype=plan.dtype, device=dev) if need_h else None
+    dw = torch.empty((plan.v, plan.d), dtype=plan.dtype, device=dev) if need_w else None
+    ws = _bytes(plan.bwd, dev)
+    rc = abi.lib().tt_loss_backward(
+        plan.ref, hidden.data_ptr(), weight.data_ptr(), saved.data_ptr(), plan.saved,
+        grad_loss.data_ptr(), dh.data_ptr() if need_h else None,
+        dw.data_ptr() if need_w else None, ws.data_ptr(), plan.bwd, abi._stream(None, hidden))
+    if rc:
+        raise abi.TTError("tt_loss_backward", rc)
+    return dh, dw, None, None, None, None, None
+
+
+_backward_once = torch.autograd.function.once_differentiable(_backward)
+
+
 class _LossFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, hidden, weight, desc, targets, teacher_logits, dev_status):
-        loss, saved = abi.tt_loss_forward(desc, hidden, weight, targets, teacher_logits,
-                                          dev_status=dev_status)
-        ctx.desc = desc
+    def forward(ctx, hidden, weight, plan, targets, teacher_logits, shape, dev_status):
+        loss, saved = _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status)
+        ctx.plan = plan
         ctx.save_for_backward(hidden, weight, saved)
         return loss
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
-        hidden, weight, saved = ctx.saved_tensors
-        dh, dw = abi.tt_loss_backward(ctx.desc, hidden, weight, saved, grad_loss.contiguous(),
-                                      need=ctx.needs_input_grad[:2])
-        return dh, dw, None, None, None, None
+        # gradients of gradients are refused; only create_graph=True runs with them enabled
+        return (_backward_once if torch.is_grad_enabled() else _backward)(ctx, grad_loss)
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -49,16 +102,31 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
 
 
 def _loss(hidden, weight, targets, teacher_logits, shape, k, reduction, dev_status, **kw):
-    if reduction not in _REDUCTION:
-        raise ValueError("reduction must be one of %s" % sorted(_REDUCTION))
     hidden, weight = _rows(hidden), _rows(weight)
-    desc = abi.make_loss_desc(hidden, weight, k=k, reduction=_REDUCTION[reduction], **kw)
+    key = (hidden.shape, hidden.stride(), weight.shape, weight.stride(), hidden.dtype,
+           weight.dtype, hidden.device, weight.device, weight.data_ptr() & 15, k, reduction,
+           *kw.values())
+    plan = _plans.get(key)
+    if plan is None:
+        if reduction not in _REDUCTION:
+            raise ValueError("reduction must be one of %s" % sorted(_REDUCTION))
+        if len(_plans) > 1024:
+            _plans.clear()
+        plan = _plans[key] = _Plan(hidden, weight, k, reduction, kw)
+    if targets.dtype != torch.int64:
+        raise TypeError("indices must be int64 or int32, got %s" % targets.dtype)
+    for t in (targets, teacher_logits, dev_status):
+        if t is not None and t.device != hidden.device:
+            raise ValueError("a buffer is on %s, hidden on %s" % (t.device, hidden.device))
+    if dev_status is not None:
+        abi._need(dev_status, torch.int32, "dev_status")
+        abi._numel(dev_status, 1, "dev_status")
+    if reduction != "none":
+        shape = ()
     if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
-        loss = _LossFunction.apply(hidden, weight, desc, targets, teacher_logits, dev_status)
-    else:
-        loss = abi.tt_loss_forward(desc, hidden, weight, targets, teacher_logits,
-                                   dev_status=dev_status)[0]
-    return loss.view(shape if reduction == "none" else ())
+        return _LossFunction.apply(hidden, weight, plan, targets, teacher_logits, shape,
+                                   dev_status)
+    return _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status)[0]
 
 
 def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
