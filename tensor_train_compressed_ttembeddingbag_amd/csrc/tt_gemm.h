@@ -11,9 +11,7 @@
 // logits W h^T, dh = G W, dW = G^T h -- read W, h and G as they lie, with no transposed copy.
 //
 // Tiles of 64 k go from memory to LDS by bounds-checked buffer loads that bypass registers
-// (rows past the end arrive as zeros), S tiles deep, with one barrier per tile: the load of
-// tile k + S - 1 goes into the buffer of tile k - 1 once every wave has passed the barrier
-// of step k.  These loads fill LDS in lane order, 16 bytes a lane, so the swizzle that keeps
+// (rows past the end arrive as zeros), S tiles deep, with one barrier per tile.  These loads fill LDS in lane order, 16 bytes a lane, so the swizzle that keeps
 // the reads free of bank conflicts is put on the memory side: a lane fetches the chunk that
 // its LDS place stands for.
 //
@@ -35,6 +33,14 @@ typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef _Float16 hf4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// the thread's index, as a value that the compiler takes to be new at each place: what is
+// derived from it for one stage of a kernel does not occupy registers in the others
+__device__ __forceinline__ int own_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
 
 struct Bf16 {
   typedef __bf16 e;
@@ -68,7 +74,6 @@ struct Operand {
 struct GemmArgs {
   Operand P, Q;
   int64_t K;            // k in all
-  int64_t kper;         // k per split (a multiple of 64)
   const int *kcount;    // device word that bounds K (rounded up to 64), or null
   const int *ycount;    // device word: tiles of y from it on have nothing to do, or null
   int nseg;             // 1, or 3 for two-plane operands
@@ -188,78 +193,105 @@ __device__ __forceinline__ typename E::v8 frag(const char *t, int x0, int kk, in
   }
 }
 
-// tile index -> (x tile, y tile, split).  Workgroups go to the 8 XCDs in turn, so the ids of
-// one XCD are made consecutive; within them 8 x-tiles by all y-tiles are walked together, so
-// the 32 CUs of an XCD share the rows of few tiles of both operands in its L2.
-// Returns false for a workgroup without a tile.
-template <int BY>
-__device__ __forceinline__ bool tile_of(GemmArgs &a, int &ix, int &iy, int &is) {
-  if (a.dsplits) {
-    a.splits = *a.dsplits;
-    a.ty = (*a.ycount + BY - 1) / BY;
-    a.kper = ((a.K + a.splits - 1) / a.splits + GK - 1) / GK * GK;
+// One tile of the result: (x tile, y tile, split) and its 64-k tiles.
+struct TileAt {
+  int ix, iy, is, nk;
+  int64_t k0;
+};
+
+// The walk of a workgroup over the tiles.  Ids go round the XCDs (workgroup b runs on XCD
+// b mod 8), so the ids of one XCD are made consecutive; within them 8 x-tiles by all y-tiles
+// are walked together, so the 32 CUs of an XCD share the rows of few tiles of both operands
+// in its L2.
+struct TileWalk {
+  int tx, ty, splits, total;
+  int64_t K, kper;
+
+  template <int BY>
+  __device__ __forceinline__ void init(const GemmArgs &a) {
+    tx = a.tx;
+    ty = a.ycount ? min(a.ty, (*a.ycount + BY - 1) / BY) : a.ty;
+    splits = a.dsplits ? *a.dsplits : a.splits;
+    K = a.kcount ? (int64_t)((*a.kcount + GK - 1) / GK) * GK : a.K;
+    kper = ((K + splits - 1) / splits + GK - 1) / GK * GK;
+    total = tx * ty * splits;
   }
-  const int total = a.tx * a.ty * a.splits;
-  int id = blockIdx.x;
-  if (id >= total) return false;
-  const int q = total / 8, r = total % 8, xcd = id % 8, loc = id / 8;
-  id = xcd * q + min(xcd, r) + loc;
-  const int per = a.tx * a.ty;
-  is = id / per;
-  id -= is * per;
-  const int grp = id / (8 * a.ty), x0 = grp * 8, w = min(8, a.tx - x0), in = id - grp * 8 * a.ty;
-  ix = x0 + in % w;
-  iy = in / w;
-  return true;
-}
+  __device__ __forceinline__ bool at(int id, TileAt &t) const {
+    if (id >= total) return false;
+    const int q = total / 8, r = total % 8, xcd = id % 8;
+    id = xcd * q + min(xcd, r) + id / 8;
+    const int per = tx * ty;
+    t.is = id / per;
+    id -= t.is * per;
+    const int grp = id / (8 * ty), x0 = grp * 8, w = min(8, tx - x0), in = id - grp * 8 * ty;
+    t.ix = x0 + in % w;
+    t.iy = in / w;
+    t.k0 = t.is * kper;
+    const int64_t n = min(kper, K - t.k0);
+    t.nk = n > 0 ? (int)((n + GK - 1) / GK) : 0;
+    return true;
+  }
+};
 
 template <int BX, int BY, int WX, int WY, int S>
 struct Tile {
   static constexpr int X = BX, Y = BY, NWX = BX / WX, NWY = BY / WY;
   static constexpr int NT = NWX * NWY * 64, MI = WX / 16, NI = WY / 16, STAGES = S;
-  static constexpr int LDS = (BX + BY) * GK * 2 * S;
+  static constexpr int EXTRA = NWX * BY * 12;  // scratch for the results
+  static constexpr int LDS = (BX + BY) * GK * 2 * S + EXTRA;
   static constexpr int wx = WX, wy = WY;
 };
 
-// The sums of this workgroup's tile; returns false if it has nothing to do.
-template <class E, class T, bool PC, bool QC>
-__device__ __forceinline__ bool gemm_tile(const GemmArgs &a, char *lds, int ix, int iy, int is,
-                                          f4 (&acc)[T::MI][T::NI]) {
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+// All tiles of this workgroup (id blockIdx.x, + gridDim.x, ...): the sums of each are handed
+// to done(tile, sums, scratch), scratch being T::EXTRA bytes of LDS beside the tiles'.  The
+// loads run on from one tile into the next, so the next tile's first data travel while this
+// one's results are worked off; done() may use its scratch freely between two of its own
+// barriers.
+template <class E, class T, bool PC, bool QC, class Done>
+__device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done done) {
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
-  if (a.ycount && iy * T::Y >= *a.ycount) return false;
-  int64_t K = a.K;
-  if (a.kcount) K = (int64_t)((*a.kcount + GK - 1) / GK) * GK;
-  const int64_t k0 = is * a.kper, k1 = k0 + a.kper < K ? k0 + a.kper : K;
-  const int nk = k1 > k0 ? (int)((k1 - k0 + GK - 1) / GK) : 0, steps = nk * a.nseg;
-#pragma unroll
-  for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-    for (int j = 0; j < T::NI; ++j) acc[i][j] = zero4();
+  TileWalk walk;
+  walk.init<T::Y>(a);
+  TileAt now, ahead;
+  int id = blockIdx.x, ida = id;
+  if (!walk.at(id, now)) return;
 
   Feed<T::X, PC, T::NT> fp;
   Feed<T::Y, QC, T::NT> fq;
-  fp.init(a.P, (int64_t)ix * T::X, k0, tid);
-  fq.init(a.Q, (int64_t)iy * T::Y, k0, tid);
   constexpr int PB = T::X * GK * 2, QB = T::Y * GK * 2, SB = PB + QB;
   const unsigned lbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)lds +
                          wv * 1024;
-  int ik = 0, seg = 0;  // the next tile to load
+  int ik = 0, seg = 0;  // the next 64-k tile to load, of tile `ahead`
+  bool live = true;
+  auto aim = [&]() {  // at the first tile from ida on that has any k
+    while ((live = walk.at(ida, ahead)) && ahead.nk == 0) ida += gridDim.x;
+    if (live) {
+      const int tid = own_thread();
+      fp.init(a.P, (int64_t)ahead.ix * T::X, ahead.k0, tid);
+      fq.init(a.Q, (int64_t)ahead.iy * T::Y, ahead.k0, tid);
+    }
+  };
   auto load = [&](int buf) {
     if (ik == 0 && a.nseg > 1) {  // lo hi, hi lo, hi hi: the small terms first
       fp.seek(seg == 0 ? a.P.plane : 0);
       fq.seek(seg == 1 ? a.Q.plane : 0);
     }
-    const bool live = seg < a.nseg && nk > 0;
     const unsigned l = __builtin_amdgcn_readfirstlane(lbase + buf * SB);
-    fp.issue(l, live);
+    fp.issue(l, live);  // past the last tile: zeros
     fq.issue(l + PB, live);
-    if (++ik >= nk) {
+    if (live && ++ik >= ahead.nk) {
       ik = 0;
-      ++seg;
+      if (++seg == a.nseg) {
+        seg = 0;
+        ida += gridDim.x;
+        aim();
+      }
     }
   };
+  aim();
   constexpr int LPT = Feed<T::X, PC, T::NT>::L + Feed<T::Y, QC, T::NT>::L;
+  f4 acc[T::MI][T::NI];
   typename E::v8 p[2][T::MI], q[2][T::NI];
   auto read = [&](int set, int buf, int kk) {
     const char *tp = lds + buf * SB, *tq = tp + PB;
@@ -288,22 +320,54 @@ __device__ __forceinline__ bool gemm_tile(const GemmArgs &a, char *lds, int ix, 
   // 1.35 in all three layouts.)
 #pragma unroll
   for (int s = 0; s < T::STAGES; ++s) load(s);
-  wait_barrier<(T::STAGES - 1) * LPT>();
-  read(0, 0, 0);
   int buf = 0;
-  for (int st = 0; st < steps; ++st) {
-    const int next = buf + 1 == T::STAGES ? 0 : buf + 1;
-    read(1, buf, 1);
-    mul(0);
-    wait_barrier<(T::STAGES - 2) * LPT>();
-    load(buf);
-    read(0, next, 0);
-    mul(1);
-    buf = next;
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < T::NI; ++j) acc[i][j] = zero4();
+    const int steps = now.nk * a.nseg;
+    if (steps > 0) {
+      wait_barrier<(T::STAGES - 1) * LPT>();
+      read(0, buf, 0);
+    }
+    for (int st = 0; st < steps; ++st) {
+      const int next = buf + 1 == T::STAGES ? 0 : buf + 1;
+      read(1, buf, 1);
+      mul(0);
+      wait_barrier<(T::STAGES - 2) * LPT>();
+      load(buf);
+      read(0, next, 0);
+      mul(1);
+      buf = next;
+    }
+    done(now, acc, lds + T::STAGES * SB);
+    id += gridDim.x;
+    if (!walk.at(id, now)) break;
   }
-  // loads issued past the end write zeros: none may land in LDS that an epilogue uses
+  // the zeros of loads past the last tile must not land in another workgroup's LDS
   wait_barrier<0>();
-  return true;
+}
+
+// 4 + 4 sixteen-bit values of a lane, from two result tiles 16 x apart, to 8 consecutive ones
+// per lane: swapping the odd 16-lane rows of one register with the even ones of the other
+// leaves lane groups 0..3 with x = 0, 16, 8, 24 and on.  o: x = 0 of the pair.
+template <class V4>
+__device__ __forceinline__ void store_pair_if(bool in, char *o, V4 a, V4 b, int g) {
+  union {
+    V4 v[2];
+    unsigned u[4];
+  } s;
+  s.v[0] = a;
+  s.v[1] = b;
+  const auto lo = __builtin_amdgcn_permlane16_swap(s.u[0], s.u[2], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(s.u[1], s.u[3], false, false);
+  i32x4 v = {(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]};
+  if (in) *(i32x4 *)(o + ((g & 1) * 16 + (g >> 1) * 8) * 2) = v;
+}
+template <class V4>
+__device__ __forceinline__ void store_pair(char *o, V4 a, V4 b, int g) {
+  store_pair_if(true, o, a, b, g);
 }
 
 }  // namespace ttb

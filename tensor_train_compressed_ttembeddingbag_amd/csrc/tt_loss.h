@@ -149,6 +149,13 @@ inline hipError_t lds_limit(F *f) {
   return e;
 }
 
+// workgroups of a product with that many tiles: as many as the CUs hold at once
+template <class T>
+inline unsigned gemm_grid(const LossArgs &a, int64_t tiles) {
+  const int64_t most = (int64_t)a.cus * (160 * 1024 / T::LDS);
+  return (unsigned)(tiles < most ? tiles : most);
+}
+
 typedef Tile<256, 256, 128, 64, 2> TileL;
 typedef Tile<128, 128, 64, 64, 2> TileM;
 typedef Tile<128, 64, 32, 64, 3> TileS;

@@ -531,7 +531,6 @@ static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
     b.take(a.G, a.Gplane * a.planes);
     const GemmShape t = dh_shape(a);
     a.dh_bx = t.bx; a.dh_by = t.by;
-    a.cus = std::max(device_cus(), 1);
     const int64_t ty = (a.N + t.by - 1) / t.by, tx = (a.D + t.bx - 1) / t.bx;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(DH_SPLITS, rows / 512));
     b.take(a.dhp, std::max(ty, std::min<int64_t>(DH_TILES / tx, most * ty)) * t.by * a.Dp);
@@ -567,6 +566,7 @@ static int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
   a.Npad = round_up(std::max<int64_t>(a.N, 1), a.N > 128 ? 256 : a.N > 64 ? 128 : 64);
   a.Dp = round_up(a.D, 64);
   a.planes = a.dtype == TT_DTYPE_F32 ? 2 : 1;
+  a.cus = std::max(device_cus(), 1);
   a.pack_w = a.planes > 1 || a.D % 8 || a.wld % 8 || ((uintptr_t)weight & 15);
   return TT_OK;
 }

@@ -13,19 +13,16 @@ template <class E, class T>
 __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
                                                    const int *count, int add) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  int ix, iy, is;
-  if (!tile_of<T::Y>(a, ix, iy, is)) return;
-  f4 acc[T::MI][T::NI];
-  if (!gemm_tile<E, T, true, false>(a, lds, ix, iy, is, acc)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int x = ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
-  const int y = iy * T::Y + (wv / T::NWX) * T::wy + c;
   const int n = *count;
-  const int64_t split = (int64_t)a.ty * T::Y * ld;
+  const int64_t split = (int64_t)((n + T::Y - 1) / T::Y) * T::Y * ld;
+  gemm_tiles<E, T, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int x = t.ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
+  const int y = t.iy * T::Y + (wv / T::NWX) * T::wy + c;
 #pragma unroll
   for (int j = 0; j < T::NI; ++j) {
     if (y + 16 * j >= n) continue;
-    float *o = out + is * split + (y + 16 * j) * ld + x;
+    float *o = out + t.is * split + (y + 16 * j) * ld + x;
 #pragma unroll
     for (int i = 0; i < T::MI; ++i) {
       if (x + 16 * i >= ld) continue;  // ld is a multiple of 64: whole groups of four
@@ -34,6 +31,7 @@ __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64
       *(f4 *)(o + 16 * i) = v;
     }
   }
+  });
 }
 
 template <class O>
@@ -41,47 +39,58 @@ struct DwOut {
   O *out;             // dW of the piece's first row
   int64_t ld, nv;     // = D, rows of the piece
   const LossScalars *sc;
-  int vec;            // rows of whole, aligned groups of four
+  int vec;            // rows of whole groups of 16 bytes (and so aligned)
 };
 
 template <class E, class T, class O>
 __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  int ix, iy, is;
-  if (!tile_of<T::Y>(a, ix, iy, is)) return;
-  f4 acc[T::MI][T::NI];
-  if (!gemm_tile<E, T, true, true>(a, lds, ix, iy, is, acc)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int x = ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
-  const int64_t y = (int64_t)iy * T::Y + (wv / T::NWX) * T::wy + c;
   const float s = ep.sc->c_dw;
   typedef O o4 __attribute__((ext_vector_type(4)));
+  gemm_tiles<E, T, true, true>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int x = t.ix * T::X + (wv % T::NWX) * T::wx;
+    const int64_t y = (int64_t)t.iy * T::Y + (wv / T::NWX) * T::wy + c;
 #pragma unroll
-  for (int j = 0; j < T::NI; ++j) {
-    if (y + 16 * j >= ep.nv) continue;
-    O *o = ep.out + (y + 16 * j) * ep.ld + x;
+    for (int j = 0; j < T::NI; ++j) {
+      O *o = ep.out + (y + 16 * j) * ep.ld + x;
+      const bool in = y + 16 * j < ep.nv;
 #pragma unroll
-    for (int i = 0; i < T::MI; ++i) {
-      const int64_t left = ep.ld - (x + 16 * i);
-      o4 v;
+      for (int i = 0; i < T::MI; i += 2) {
+        o4 v[2];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = (O)(acc[i][j][r] * s);
-      if (ep.vec) {
-        if (left > 0) *(o4 *)(o + 16 * i) = v;
-      } else {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r < left) o[16 * i + r] = v[r];
+          for (int r = 0; r < 4; ++r) v[u][r] = (O)(acc[i + u][j][r] * s);
+        const int64_t left = ep.ld - (x + 16 * i);  // columns from this pair on
+        if constexpr (sizeof(O) == 2) {
+          if (ep.vec && left >= 32) {  // whole pair: 16 bytes a lane (uniform: no lane diverges)
+            store_pair_if(in, (char *)(o + 16 * i), v[0], v[1], g);
+            continue;
+          }
+        }
+        if (!in) continue;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int e = 16 * u + 4 * g;
+          if (ep.vec && left >= e + 4) {
+            *(o4 *)(o + 16 * i + e) = v[u];
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (e + r < left) o[16 * i + e + r] = v[u][r];
+          }
+        }
       }
     }
-  }
+  });
 }
 
 template <class E, class T>
 static hipError_t go_dh(const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
   const hipError_t e = lds_limit<T>(&k_dhidden<E, T>);
   if (e != hipSuccess) return e;
-  tt_launch(K_LOSS_DH, k_dhidden<E, T>, dim3(std::max(g.tx * g.ty, DH_TILES)), dim3(T::NT), T::LDS,
+  tt_launch(K_LOSS_DH, k_dhidden<E, T>, dim3(gemm_grid<T>(a, std::max(g.tx * g.ty, DH_TILES))), dim3(T::NT), T::LDS,
             s, g, a.dhp, a.Dp, (const int *)a.sv.count, add);
   return hipGetLastError();
 }
@@ -94,8 +103,8 @@ static hipError_t go_dw(const GemmArgs &g, const LossArgs &a, int64_t v0, int64_
   DwOut<O> ep;
   ep.out = (O *)a.dw + v0 * a.D;
   ep.ld = a.D; ep.nv = nv; ep.sc = a.sc;
-  ep.vec = a.D % 4 == 0 && ((uintptr_t)a.dw & (4 * sizeof(O) - 1)) == 0;
-  tt_launch(K_LOSS_DW, k_dweight<E, T, O>, dim3(g.tx * g.ty), dim3(T::NT), T::LDS, s, g, ep);
+  ep.vec = a.D % (16 / sizeof(O)) == 0 && ((uintptr_t)a.dw & 15) == 0;
+  tt_launch(K_LOSS_DW, k_dweight<E, T, O>, dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT), T::LDS, s, g, ep);
   return hipGetLastError();
 }
 
@@ -134,7 +143,6 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   g.P = hidden_operand(a);
   g.Q = g_operand(a, nv);
   g.K = a.Npad;
-  g.kper = a.Npad;
   g.kcount = a.sv.count;
   g.nseg = a.planes > 1 ? 3 : 1;
   const GemmShape t = gemm_shape(a.D, nv);

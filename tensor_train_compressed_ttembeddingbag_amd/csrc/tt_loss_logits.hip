@@ -20,39 +20,47 @@ struct LogitsEpi {
   int64_t ldG, Gplane;
   const float *lse, *rowf;
   const int *tgt;          // null with distillation
-  float one_e, e_v, ghalf; // (1 - e) and e / V times G's factor 2^g_exp; the root of that
+  float one_e, e_v, gs;    // 1 - e, e / V, G's factor 2^g_exp
   int planes;
 };
 
 template <class E, class T, bool GRAD>
 __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  int ix, iy, is;
-  if (!tile_of<T::Y>(a, ix, iy, is)) return;
-  f4 acc[T::MI][T::NI];
-  if (!gemm_tile<E, T, false, false>(a, lds, ix, iy, is, acc)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+  gemm_tiles<E, T, false, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
+  const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
   const float zs = ep.sc->zs;
   const int count = *ep.count;
+  const int ix = t.ix, iy = t.iy;
   const int xl = (int)min<int64_t>(ep.nv - (int64_t)ix * T::X, T::X);  // rows of this tile
   const int xb = px + 4 * g;
+  const bool full = xl == T::X;  // no rows of the tile past the vocabulary
   if constexpr (!GRAD) {
-    float2 *sm = (float2 *)lds;                       // [NWX][Y]
-    float *sz = (float *)(lds + T::NWX * T::Y * 8);   // [NWX][Y]
+    float2 *sm = (float2 *)tmp;                       // [NWX][Y]
+    float *sz = (float *)(tmp + T::NWX * T::Y * 8);   // [NWX][Y]
 #pragma unroll
     for (int j = 0; j < T::NI; ++j) {
       float m = -INFINITY, zsum = 0.f;
+      if (ep.zpart) {
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) zsum += xb + 16 * i + r < xl ? acc[i][j][r] : 0.f;
+        zsum *= zs;
+      }
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (xb + 16 * i + r >= xl) acc[i][j][r] = -INFINITY;
+      }
 #pragma unroll
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool in = xb + 16 * i + r < xl;
-          const float u = acc[i][j][r] * zs;
-          zsum += in ? u : 0.f;
-          acc[i][j][r] = in ? u : -INFINITY;
-          m = fmaxf(m, acc[i][j][r]);
-        }
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
+      m *= zs;  // zs > 0
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
       const float m0 = m == -INFINITY ? 0.f : m;  // nothing but -inf: every term is 0
@@ -60,7 +68,8 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
 #pragma unroll
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(acc[i][j][r] - m0);
+        for (int r = 0; r < 4; ++r)
+          s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zs, -m0));
       s = sum_lane_groups(s);
       if (ep.zpart) zsum = sum_lane_groups(zsum);
       if (g == 0) {
@@ -68,10 +77,10 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
         if (ep.zpart) sz[(wv % T::NWX) * T::Y + qy + 16 * j + c] = zsum;
       }
     }
-    __syncthreads();
+    lds_barrier();
     for (int y = tid; y < T::Y; y += T::NT) {
       const int pos = iy * T::Y + y;
-      if (pos >= count) break;
+      if (pos >= count) continue;
       float m = -INFINITY, s = 0.f, z = 0.f;
 #pragma unroll
       for (int w = 0; w < T::NWX; ++w) m = fmaxf(m, sm[w * T::Y + y].x);
@@ -86,56 +95,72 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
       ep.part[at] = make_float2(m, s);
       if (ep.zpart) ep.zpart[at] = z;
     }
+    lds_barrier();
   } else {
+    // p 2^g_exp as the square of exp2 of half the logit, times the row's factor: v_exp_f32
+    // itself ends at 2^-126, bf16 and the gradients do not
     const float zh = 0.5f * zs;
 #pragma unroll
     for (int j = 0; j < T::NI; ++j) {
       const int pos = iy * T::Y + qy + 16 * j + c;
       const bool live = pos < count;
-      const float lse = live ? 0.5f * ep.lse[pos] : 0.f, f = live ? ep.rowf[pos] : 0.f;
+      const float lse = live ? 0.5f * ep.lse[pos] : 0.f, f = live ? ep.rowf[pos] * ep.gs : 0.f;
+      const float ef = ep.e_v * f;
       const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
       const int d = live && ep.tgt ? (int)(ep.tgt[pos] - first) : -1;
-      char *o = ep.G + pos * ep.ldG + ((int64_t)ix * T::X + xb) * 2;
+      // few tiles hold the target of one of a wave's 16 positions
+      const bool hit = __any(d >= 0 && d < 16 * T::MI);
+      char *o = ep.G + pos * ep.ldG + ((int64_t)ix * T::X + px) * 2;
 #pragma unroll
-      for (int i = 0; i < T::MI; ++i) {
-        float v[4];
+      for (int i0 = 0; i0 < T::MI; i0 += 2) {
+        typename E::v4 h[2], l[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          // as the square of exp2 of half: v_exp_f32 itself ends at 2^-126
-          const float q = __builtin_amdgcn_exp2f(acc[i][j][r] * zh - lse) * ep.ghalf;
-          float p = q * q - ep.e_v;
-          if (d == 16 * i + r) p -= ep.one_e;
-          v[r] = live && xb + 16 * i + r < xl ? p * f : 0.f;
+        for (int u = 0; u < 2; ++u) {
+          const int i = i0 + u;
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zh, -lse));
+            v[r] = __builtin_fmaf(q * q, f, -ef);
+          }
+          if (hit) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (d == 16 * i + r) v[r] -= ep.one_e * f;
+          }
+          if (!full) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (xb + 16 * i + r >= xl) v[r] = 0.f;
+          }
+          if (!live) v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) h[u][r] = (typename E::e)v[r];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) l[u][r] = (typename E::e)(v[r] - (float)h[u][r]);
         }
-        typename E::v4 h;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) h[r] = (typename E::e)v[r];
-        *(typename E::v4 *)(o + 32 * i) = h;
-        if (ep.planes > 1) {
-          typename E::v4 l;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) l[r] = (typename E::e)(v[r] - (float)h[r]);
-          *(typename E::v4 *)(o + ep.Gplane + 32 * i) = l;
-        }
+        store_pair(o + 32 * i0, h[0], h[1], g);
+        if (ep.planes > 1) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
       }
     }
   }
+  });
 }
 
 template <class E, class T, bool GRAD>
-static hipError_t go(const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
+static hipError_t go(const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
   const hipError_t e = lds_limit<T>(&k_logits<E, T, GRAD>);
   if (e != hipSuccess) return e;
-  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, GRAD>, dim3(g.tx * g.ty), dim3(T::NT),
+  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, GRAD>, dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT),
             T::LDS, s, g, ep);
   return hipGetLastError();
 }
 
 template <class E, bool GRAD>
-static hipError_t pick(int cfg, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
-  if (cfg == 0) return go<E, TileL, GRAD>(g, ep, s);
-  if (cfg == 1) return go<E, TileM, GRAD>(g, ep, s);
-  return go<E, TileS, GRAD>(g, ep, s);
+static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
+  if (cfg == 0) return go<E, TileL, GRAD>(a, g, ep, s);
+  if (cfg == 1) return go<E, TileM, GRAD>(a, g, ep, s);
+  return go<E, TileS, GRAD>(a, g, ep, s);
 }
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
@@ -143,8 +168,7 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   GemmArgs g = {};
   g.P = weight_operand(a, v0, nv);
   g.Q = hidden_operand(a);
-  g.K = g.kper = a.pack_w ? a.Dp : a.D;
-  g.kper = (g.K + GK - 1) / GK * GK;
+  g.K = a.pack_w ? a.Dp : a.D;
   g.ycount = a.sv.count;
   g.nseg = a.planes > 1 ? 3 : 1;
   const GemmShape t = gemm_shape(a.V < a.piece ? a.V : a.piece, a.N);
@@ -159,13 +183,13 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.G = a.G; ep.ldG = a.ldG; ep.Gplane = a.Gplane;
   ep.lse = a.sv.lse; ep.rowf = a.rowf;
   ep.tgt = a.k ? nullptr : a.sv.tgt;
-  ep.ghalf = ldexpf(1.f, g_exp(a.dtype) / 2);
-  ep.one_e = ldexpf(1.f - a.smoothing, g_exp(a.dtype));
-  ep.e_v = ldexpf(a.smoothing / (float)a.V, g_exp(a.dtype));
+  ep.gs = ldexpf(1.f, g_exp(a.dtype));
+  ep.one_e = 1.f - a.smoothing;
+  ep.e_v = a.smoothing / (float)a.V;
   ep.planes = a.planes;
   if (a.dtype == TT_DTYPE_BF16)
-    return grad ? pick<Bf16, true>(t.cfg, g, ep, s) : pick<Bf16, false>(t.cfg, g, ep, s);
-  return grad ? pick<Fp16, true>(t.cfg, g, ep, s) : pick<Fp16, false>(t.cfg, g, ep, s);
+    return grad ? pick<Bf16, true>(t.cfg, a, g, ep, s) : pick<Bf16, false>(t.cfg, a, g, ep, s);
+  return grad ? pick<Fp16, true>(t.cfg, a, g, ep, s) : pick<Fp16, false>(t.cfg, a, g, ep, s);
 }
 
 }  // namespace ttb
