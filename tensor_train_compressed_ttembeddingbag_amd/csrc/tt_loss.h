@@ -107,7 +107,7 @@ __device__ __forceinline__ int dh_splits(const LossArgs &a, int count, int lane)
 // as zeros, and small probabilities are most of a vocabulary (|g| <= 1 keeps both in range).
 __host__ __device__ inline int g_exp(int dtype) { return dtype == TT_DTYPE_BF16 ? 32 : 14; }
 
-// tile shapes: 0 = 256 x 256, 1 = 128 x 128, 2 = 128 x 64 (x by y)
+// tile shapes: 0 = 256 x 256, 1 = 128 x 128, 2 = 128 x 64, 3 = 64 x 128 (x by y)
 struct GemmShape {
   int cfg, bx, by;
 };
@@ -159,5 +159,6 @@ inline unsigned gemm_grid(const LossArgs &a, int64_t tiles) {
 typedef Tile<256, 256, 128, 64, 2> TileL;
 typedef Tile<128, 128, 64, 64, 2> TileM;
 typedef Tile<128, 64, 32, 64, 3> TileS;
+typedef Tile<64, 128, 32, 64, 3> TileN;  // gradients of narrow tables (d <= 64)
 
 }  // namespace ttb

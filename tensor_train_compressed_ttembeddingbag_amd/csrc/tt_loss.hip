@@ -171,8 +171,10 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
   if (tid == 0) a.amax[blockIdx.x] = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 }
 
-// Rows of the hidden states that count, in order, from row 0 of hp on; the rest of hp's Npad
-// rows are zeros (every position that does not count clears one of them).  A block counts
+// Rows of the hidden states that count, in order, from row 0 of hp on.  The backward sums over
+// the packed rows 64 at a time, so there the rows up to the next multiple of 64 are zeros (a
+// position that does not count has one of the rows past the counting ones as its own); the
+// forward takes a row's results for itself, and what is past the counting rows is not used.  A block counts
 // the positions before its own by itself: N / 16 blocks read N / 2 flags on average, which
 // up to some 10^5 positions costs less than another launch to scan them.  The backward takes
 // the places from `saved`.
@@ -257,10 +259,11 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
   __syncthreads();
   const float scale = ldexpf(1.f, eh);
   const int cpr = (int)(a.Dp / 8);
+  const int64_t zero_to = grad ? ((int64_t)*a.sv.count + GK - 1) / GK * GK : 0;
   for (int q = tid; q < PACK_ROWS * cpr; q += 256) {
     const int r = q / cpr, c = (q - r * cpr) * 8, slot = s_slot[r];
     const int64_t row = slot < 0 ? -1 - slot : slot;
-    if (row >= a.Npad) continue;
+    if (slot < 0 && row >= zero_to) continue;
     S v[8];
     load8((const S *)a.hidden + (i0 + r) * a.hld + c, slot < 0 ? 0 : a.D - c, v);
     store8<S, E, PL>(v, scale, a.hp + (row * a.Dp + c) * 2, a.hplane);
@@ -281,10 +284,28 @@ __global__ __launch_bounds__(256) void k_pack_w(LossArgs a, int64_t v0, int64_t 
 }
 
 // ---------------------------------------------------------------- loss
+// the rows' losses added in a fixed order, in fp64; NT threads, s_d: a double per wave
+template <int NT>
+__device__ __forceinline__ void sum_rows(const LossArgs &a, double *s_d) {
+  const int tid = threadIdx.x;
+  double d = 0.0;
+  for (int64_t r = tid; r < a.N; r += NT)
+    d += (double)__hip_atomic_load(&a.rowloss[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o);
+  if ((tid & 63) == 0) s_d[tid >> 6] = d;
+  __syncthreads();
+  if (tid == 0) {
+    d = 0.0;
+    for (int w = 0; w < NT / 64; ++w) d += s_d[w];
+    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? d / max(*a.sv.count, 1) : d);
+  }
+}
+
 // One block per position: the tiles' statistics become its lse; the logits of its entries
 // are dot products of their own (fp32 sums of the inputs' products), a wave each.
 template <class S>
-__global__ __launch_bounds__(256) void k_loss(LossArgs a) {
+__global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   __shared__ float s_m[4], s_s[4], s_z[4], s_q[4];
   __shared__ double s_d[4];
   __shared__ int s_last;
@@ -375,27 +396,26 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a) {
     if (tid == 0) a.loss[i] = out;
     return;
   }
-  // the block that ends last adds the rows up, in the rows' order, in fp64
+  if (!ticket) {
+    if (tid == 0) a.rowloss[i] = out;
+    return;
+  }
+  // the block that ends last adds the rows up
   if (tid == 0) {
-    __hip_atomic_store(&a.rowloss[i], out, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // the row is written through to memory by its own scope; the ticket waits for that store
     // alone (a fence would write back the XCD's whole L2, in every block)
+    __hip_atomic_store(&a.rowloss[i], out, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     vmem_drain();
     s_last = atomicAdd(&a.sc->ticket, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
-  if (!s_last) return;
-  double d = 0.0;
-  for (int64_t r = tid; r < a.N; r += 256)
-    d += (double)__hip_atomic_load(&a.rowloss[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o);
-  if (lane == 0) s_d[wv] = d;
-  __syncthreads();
-  if (tid == 0) {
-    d = s_d[0] + s_d[1] + s_d[2] + s_d[3];
-    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? d / max(*a.sv.count, 1) : d);
-  }
+  if (s_last) sum_rows<256>(a, s_d);
+}
+
+// the rows' sum in a launch of its own
+__global__ __launch_bounds__(1024) void k_loss_sum(LossArgs a) {
+  __shared__ double s_d[16];
+  sum_rows<1024>(a, s_d);
 }
 
 // ---------------------------------------------------------------- backward, around the products
@@ -458,6 +478,7 @@ __global__ __launch_bounds__(256) void k_fill0(T *x, int64_t n) {
 // ---------------------------------------------------------------- plan
 GemmShape gemm_shape(int64_t x, int64_t y) {
   const int64_t big = ((x + 255) / 256) * ((y + 255) / 256);
+  if (x <= 64 && y > 64) return {3, 64, 128};
   if (y > 128 && x > 128 && big >= 128) return {0, 256, 256};
   if (y > 64) return {1, 128, 128};
   return {2, 128, 64};
@@ -468,6 +489,7 @@ GemmShape dh_shape(const LossArgs &a) {
   const int64_t big = ((a.D + 255) / 256) * ((a.N + 255) / 256);
   if (a.N > 128 && a.D > 128 && big * std::min<int64_t>(DH_SPLITS, a.piece / 512) >= 128)
     return {0, 256, 256};
+  if (a.D <= 64 && a.N > 64) return {3, 64, 128};
   return a.N > 64 ? GemmShape{1, 128, 128} : GemmShape{2, 128, 64};
 }
 
@@ -608,11 +630,19 @@ static hipError_t launch_entries(const LossArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// A sum of up to LOSS_TICKETS rows is taken by k_loss's last block; the tickets of all blocks
+// go through one address at some 13 ns each (8192 rows: 140 us, of which 100 waited for
+// them), so more rows are added in a launch of its own (about 5 us).
+constexpr int64_t LOSS_TICKETS = 256;
+
 static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)a.N);
-  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_loss<float>, grid, dim3(256), 0, s, a);
-  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_loss<__bf16>, grid, dim3(256), 0, s, a);
-  else tt_launch(K_LOSS_ROWS, k_loss<_Float16>, grid, dim3(256), 0, s, a);
+  const int ticket = a.N <= LOSS_TICKETS;
+  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_loss<float>, grid, dim3(256), 0, s, a, ticket);
+  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_loss<__bf16>, grid, dim3(256), 0, s, a, ticket);
+  else tt_launch(K_LOSS_ROWS, k_loss<_Float16>, grid, dim3(256), 0, s, a, ticket);
+  if (a.reduction != TT_REDUCE_NONE && !ticket)
+    tt_launch(K_LOSS_ROWS, k_loss_sum, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

@@ -123,10 +123,12 @@ hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   if (a.dtype == TT_DTYPE_BF16) {
     if (t.cfg == 0) return go_dh<Bf16, TileL>(g, a, add, s);
     if (t.cfg == 1) return go_dh<Bf16, TileM>(g, a, add, s);
+    if (t.cfg == 3) return go_dh<Bf16, TileN>(g, a, add, s);
     return go_dh<Bf16, TileS>(g, a, add, s);
   }
   if (t.cfg == 0) return go_dh<Fp16, TileL>(g, a, add, s);
   if (t.cfg == 1) return go_dh<Fp16, TileM>(g, a, add, s);
+  if (t.cfg == 3) return go_dh<Fp16, TileN>(g, a, add, s);
   return go_dh<Fp16, TileS>(g, a, add, s);
 }
 
@@ -135,6 +137,7 @@ static hipError_t pick_dw(int cfg, const GemmArgs &g, const LossArgs &a, int64_t
                           hipStream_t s) {
   if (cfg == 0) return go_dw<E, TileL, O>(g, a, v0, nv, s);
   if (cfg == 1) return go_dw<E, TileM, O>(g, a, v0, nv, s);
+  if (cfg == 3) return go_dw<E, TileN, O>(g, a, v0, nv, s);
   return go_dw<E, TileS, O>(g, a, v0, nv, s);
 }
 

@@ -160,6 +160,7 @@ template <class E, bool GRAD>
 static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
   if (cfg == 0) return go<E, TileL, GRAD>(a, g, ep, s);
   if (cfg == 1) return go<E, TileM, GRAD>(a, g, ep, s);
+  if (cfg == 3) return go<E, TileN, GRAD>(a, g, ep, s);  // vocabularies of up to 64 rows
   return go<E, TileS, GRAD>(a, g, ep, s);
 }
 
