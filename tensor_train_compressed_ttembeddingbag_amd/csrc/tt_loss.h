@@ -19,7 +19,7 @@
 
 namespace ttb {
 
-constexpr int PACK_ROWS = 16;   // positions per block of k_pack
+constexpr int PACK_ROWS = 4;    // positions per block of k_pack
 constexpr int AMAX_BLOCKS = 1024;
 
 // scalars that the device works out, at the head of the workspace

@@ -2,6 +2,7 @@
 #include "tt_loss.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace ttb {
 
@@ -19,6 +20,21 @@ __device__ __forceinline__ void load8(const S *p, int64_t left, S (&v)[8]) {
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : (S)0.f;
+  }
+}
+
+// the same where rows are whole groups of eight (WHOLE): without a branch, so that several
+// loads of a thread travel together; p0 is the row's start
+template <bool WHOLE, class S>
+__device__ __forceinline__ void load8_at(const S *p0, int64_t c, int64_t d, bool on, S (&v)[8]) {
+  if constexpr (WHOLE) {
+    on = on && c < d;
+    struct __attribute__((packed, aligned(2))) any { S x[8]; };
+    const any a = *(const any *)(p0 + (c < d ? c : 0));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = on ? a.x[e] : (S)0.f;
+  } else {
+    load8(p0 + c, on ? d - c : 0, v);
   }
 }
 
@@ -175,7 +191,7 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
 // the packed rows 64 at a time, so there the rows up to the next multiple of 64 are zeros (a
 // position that does not count has one of the rows past the counting ones as its own); the
 // forward takes a row's results for itself, and what is past the counting rows is not used.  A block counts
-// the positions before its own by itself: N / 16 blocks read N / 2 flags on average, which
+// the positions before its own by itself: N / 4 blocks read N / 2 flags on average, which
 // up to some 10^5 positions costs less than another launch to scan them.  The backward takes
 // the places from `saved`.
 template <class S, class E, int PL>
@@ -260,14 +276,30 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
   const float scale = ldexpf(1.f, eh);
   const int cpr = (int)(a.Dp / 8);
   const int64_t zero_to = grad ? ((int64_t)*a.sv.count + GK - 1) / GK * GK : 0;
-  for (int q = tid; q < PACK_ROWS * cpr; q += 256) {
-    const int r = q / cpr, c = (q - r * cpr) * 8, slot = s_slot[r];
-    const int64_t row = slot < 0 ? -1 - slot : slot;
-    if (slot < 0 && row >= zero_to) continue;
-    S v[8];
-    load8((const S *)a.hidden + (i0 + r) * a.hld + c, slot < 0 ? 0 : a.D - c, v);
-    store8<S, E, PL>(v, scale, a.hp + (row * a.Dp + c) * 2, a.hplane);
-  }
+  auto copy = [&](auto whole) {
+    constexpr int U = 4;  // groups of eight in flight per thread
+    for (int q0 = tid; q0 < PACK_ROWS * cpr; q0 += 256 * U) {
+      S v[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = min(q0 + 256 * u, PACK_ROWS * cpr - 1), r = q / cpr, c = (q - r * cpr) * 8;
+        // a block of past-the-end rows copies none: any row's address will do
+        load8_at<decltype(whole)::value>((const S *)a.hidden + min(i0 + r, a.N - 1) * a.hld, c,
+                                         a.D, s_slot[r] >= 0, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = q0 + 256 * u, r = q / cpr, c = (q - r * cpr) * 8;
+        if (q >= PACK_ROWS * cpr) continue;
+        const int slot = s_slot[r];
+        const int64_t row = slot < 0 ? -1 - slot : slot;
+        if (slot < 0 && row >= zero_to) continue;
+        store8<S, E, PL>(v[u], scale, a.hp + (row * a.Dp + c) * 2, a.hplane);
+      }
+    }
+  };
+  if (a.D % 8 == 0) copy(std::true_type());
+  else copy(std::false_type());
 }
 
 // rows [v0, v0 + nv) of the weight -> wp
@@ -344,21 +376,24 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
       for (int u = 0; u < 4; ++u) {
         const int j = min(j0 + u, ne - 1), v = a.k ? a.sv.eidx[i * a.k + j] : a.sv.tgt[slot];
         on[u] = j0 + u < ne && v >= 0;
-        w[u] = (const S *)a.weight + (v < 0 ? 0 : v) * a.wld;
+        w[u] = (const S *)a.weight + max(v, 0) * a.wld;  // no entry: any row, not counted
         d[u] = 0.f;
       }
-      for (int64_t c = lane * 8; c < a.D; c += 512) {
-        S x[8];
-        load8(h + c, a.D - c, x);
+      auto dots = [&](auto whole) {
+        for (int64_t c = lane * 8; c < a.D; c += 512) {
+          S x[8], y[4][8];
+          load8_at<decltype(whole)::value>(h, c, a.D, true, x);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (!on[u]) continue;
-          S y[8];
-          load8(w[u] + c, a.D - c, y);
+          for (int u = 0; u < 4; ++u)
+            load8_at<decltype(whole)::value>(w[u], c, a.D, true, y[u]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[u] += (float)x[e] * (float)y[e];
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[u] += (float)x[e] * (float)y[u][e];
         }
-      }
+      };
+      if (a.D % 8 == 0) dots(std::true_type());
+      else dots(std::false_type());
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (!on[u]) continue;
