@@ -111,8 +111,27 @@ __host__ __device__ inline int g_exp(int dtype) { return dtype == TT_DTYPE_BF16 
 struct GemmShape {
   int cfg, bx, by;
 };
-GemmShape gemm_shape(int64_t x, int64_t y);
+GemmShape gemm_shape(int64_t x, int64_t y);  // of products without large tiles
 GemmShape dh_shape(const LossArgs &a);
+// of `along` large tiles by `across` others, how many of the first to take in large tiles
+int64_t large_tiles(int64_t along, int64_t across, int cus);
+
+// A piece of nv rows of the vocabulary in k_logits: the first `large` rows in large tiles, the
+// rest in tiles of `rest`; tiles in all.
+struct LogitsCut {
+  int64_t large;
+  GemmShape rest;
+  int tiles;
+};
+inline LogitsCut logits_cut(const LossArgs &a, int64_t nv) {
+  LogitsCut c = {0, gemm_shape(nv, a.N), 0};
+  if (a.N > 128 && nv > 128) {
+    const int64_t n = large_tiles((nv + 255) / 256, (a.N + 255) / 256, a.cus) * 256;
+    c.large = n < nv ? n : nv;
+  }
+  c.tiles = (int)((c.large + 255) / 256 + (nv - c.large + c.rest.bx - 1) / c.rest.bx);
+  return c;
+}
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
                          hipStream_t s);

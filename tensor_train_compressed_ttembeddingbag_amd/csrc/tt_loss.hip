@@ -511,10 +511,21 @@ __global__ __launch_bounds__(256) void k_fill0(T *x, int64_t n) {
 }
 
 // ---------------------------------------------------------------- plan
+// Which tiles, by the rounds they take on the CUs.  A round of 256 x 256 tiles (one per CU)
+// runs at about 1.45 PFLOP/s; 128 x 128 tiles do a fourth of that work at 0.67 of the rate
+// with two on every CU and at 0.45 with one (4096 x 4096 x 2048: 1407 TFLOP/s, against 1013
+// and 675 for the products of 512 and 256 small tiles).  So a last round of few large tiles
+// is cheaper in small ones: 784 tiles on 256 CUs take 3 + 0.55 rounds instead of 4.
+int64_t large_tiles(int64_t along, int64_t across, int cus) {
+  auto rounds = [&](int64_t n) { return (double)((n + cus - 1) / cus); };
+  const int64_t keep = along * across / cus * cus / across;  // tiles of the whole rounds
+  const int64_t small = 4 * (along - keep) * across;
+  const double cut = rounds(keep * across) + (small <= cus ? 0.55 : 0.73 * rounds((small + 1) / 2));
+  return cut + 0.05 < rounds(along * across) ? keep : along;
+}
+
 GemmShape gemm_shape(int64_t x, int64_t y) {
-  const int64_t big = ((x + 255) / 256) * ((y + 255) / 256);
   if (x <= 64 && y > 64) return {3, 64, 128};
-  if (y > 128 && x > 128 && big >= 128) return {0, 256, 256};
   if (y > 64) return {1, 128, 128};
   return {2, 128, 64};
 }
@@ -592,8 +603,9 @@ static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(DH_SPLITS, rows / 512));
     b.take(a.dhp, std::max(ty, std::min<int64_t>(DH_TILES / tx, most * ty)) * t.by * a.Dp);
   } else {
-    const GemmShape t = gemm_shape(std::min(a.V, a.piece), a.N);
-    a.ptiles = (int)((a.V + t.bx - 1) / t.bx);
+    a.ptiles = 0;
+    for (int64_t v0 = 0; v0 < a.V; v0 += a.piece)
+      a.ptiles += logits_cut(a, std::min(a.piece, a.V - v0)).tiles;
     b.take(a.part, a.Npad * a.ptiles);
     b.take(a.zpart, a.smoothing > 0.f ? a.Npad * a.ptiles : 0);
     b.take(a.rowloss, a.N);
@@ -746,11 +758,12 @@ int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *we
   }
   if (a.k) e = launch_entries(a, s);
   if (e == hipSuccess) e = launch_pack(a, 0, s);
-  const GemmShape t = gemm_shape(std::min(a.V, a.piece), a.N);
+  int tile0 = 0;
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
     const int64_t nv = std::min(a.piece, a.V - v0);
     e = launch_pack_w(a, v0, nv, s);
-    if (e == hipSuccess) e = launch_logits(a, v0, nv, (int)(v0 / t.bx), false, s);
+    if (e == hipSuccess) e = launch_logits(a, v0, nv, tile0, false, s);
+    tile0 += logits_cut(a, nv).tiles;
   }
   if (e == hipSuccess) e = launch_loss(a, s);
   return e == hipSuccess ? TT_OK : TT_EHIP;

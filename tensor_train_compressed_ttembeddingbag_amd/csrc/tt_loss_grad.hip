@@ -142,19 +142,31 @@ static hipError_t pick_dw(int cfg, const GemmArgs &g, const LossArgs &a, int64_t
 }
 
 hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
-  GemmArgs g = {};
-  g.P = hidden_operand(a);
-  g.Q = g_operand(a, nv);
-  g.K = a.Npad;
-  g.kcount = a.sv.count;
-  g.nseg = a.planes > 1 ? 3 : 1;
-  const GemmShape t = gemm_shape(a.D, nv);
-  g.tx = (int)((a.D + t.bx - 1) / t.bx);
-  g.ty = (int)((nv + t.by - 1) / t.by);
-  g.splits = 1;
-  if (a.dtype == TT_DTYPE_BF16) return pick_dw<Bf16, __bf16>(t.cfg, g, a, v0, nv, s);
-  if (a.dtype == TT_DTYPE_F16) return pick_dw<Fp16, _Float16>(t.cfg, g, a, v0, nv, s);
-  return pick_dw<Fp16, float>(t.cfg, g, a, v0, nv, s);
+  int64_t large = 0;
+  if (a.D > 128 && nv > 128)
+    large = std::min(nv, large_tiles((nv + 255) / 256, (a.D + 255) / 256, a.cus) * 256);
+  hipError_t e = hipSuccess;
+  // rows [r0, r0 + n) of the piece in tiles of t
+  auto part = [&](int64_t r0, int64_t n, GemmShape t) {
+    if (n <= 0 || e != hipSuccess) return;
+    GemmArgs g = {};
+    g.P = hidden_operand(a);
+    g.Q = g_operand(a, nv);
+    g.Q.p += r0 * 2;
+    g.Q.cols -= r0;
+    g.K = a.Npad;
+    g.kcount = a.sv.count;
+    g.nseg = a.planes > 1 ? 3 : 1;
+    g.tx = (int)((a.D + t.bx - 1) / t.bx);
+    g.ty = (int)((n + t.by - 1) / t.by);
+    g.splits = 1;
+    if (a.dtype == TT_DTYPE_BF16) e = pick_dw<Bf16, __bf16>(t.cfg, g, a, v0 + r0, n, s);
+    else if (a.dtype == TT_DTYPE_F16) e = pick_dw<Fp16, _Float16>(t.cfg, g, a, v0 + r0, n, s);
+    else e = pick_dw<Fp16, float>(t.cfg, g, a, v0 + r0, n, s);
+  };
+  part(0, large, {0, 256, 256});
+  part(large, nv - large, gemm_shape(a.D, nv - large));
+  return e;
 }
 
 }  // namespace ttb

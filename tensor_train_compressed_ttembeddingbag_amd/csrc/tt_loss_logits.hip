@@ -166,31 +166,45 @@ static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const Logi
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
                          hipStream_t s) {
-  GemmArgs g = {};
-  g.P = weight_operand(a, v0, nv);
-  g.Q = hidden_operand(a);
-  g.K = a.pack_w ? a.Dp : a.D;
-  g.ycount = a.sv.count;
-  g.nseg = a.planes > 1 ? 3 : 1;
-  const GemmShape t = gemm_shape(a.V < a.piece ? a.V : a.piece, a.N);
-  g.tx = (int)((nv + t.bx - 1) / t.bx);
-  g.ty = (int)((a.N + t.by - 1) / t.by);
-  g.splits = 1;
   LogitsEpi ep = {};
   ep.sc = a.sc; ep.count = a.sv.count;
-  ep.v0 = v0; ep.nv = nv;
   ep.part = a.part; ep.zpart = a.smoothing > 0.f ? a.zpart : nullptr;
   ep.ptiles = a.ptiles; ep.tile0 = tile0;
-  ep.G = a.G; ep.ldG = a.ldG; ep.Gplane = a.Gplane;
+  ep.ldG = a.ldG; ep.Gplane = a.Gplane;
   ep.lse = a.sv.lse; ep.rowf = a.rowf;
   ep.tgt = a.k ? nullptr : a.sv.tgt;
   ep.gs = ldexpf(1.f, g_exp(a.dtype));
   ep.one_e = 1.f - a.smoothing;
   ep.e_v = a.smoothing / (float)a.V;
   ep.planes = a.planes;
-  if (a.dtype == TT_DTYPE_BF16)
-    return grad ? pick<Bf16, true>(t.cfg, a, g, ep, s) : pick<Bf16, false>(t.cfg, a, g, ep, s);
-  return grad ? pick<Fp16, true>(t.cfg, a, g, ep, s) : pick<Fp16, false>(t.cfg, a, g, ep, s);
+  const LogitsCut cut = logits_cut(a, nv);
+  hipError_t e = hipSuccess;
+  // rows [r0, r0 + n) of the piece in tiles of t
+  auto part = [&](int64_t r0, int64_t n, GemmShape t) {
+    if (n <= 0 || e != hipSuccess) return;
+    GemmArgs g = {};
+    g.P = weight_operand(a, v0, nv);
+    g.P.p += r0 * g.P.ld;
+    g.P.rows -= r0;
+    g.Q = hidden_operand(a);
+    g.K = a.pack_w ? a.Dp : a.D;
+    g.ycount = a.sv.count;
+    g.nseg = a.planes > 1 ? 3 : 1;
+    g.tx = (int)((n + t.bx - 1) / t.bx);
+    g.ty = (int)((a.N + t.by - 1) / t.by);
+    g.splits = 1;
+    ep.v0 = v0 + r0;
+    ep.nv = n;
+    ep.G = a.G + r0 * 2;
+    if (a.dtype == TT_DTYPE_BF16)
+      e = grad ? pick<Bf16, true>(t.cfg, a, g, ep, s) : pick<Bf16, false>(t.cfg, a, g, ep, s);
+    else
+      e = grad ? pick<Fp16, true>(t.cfg, a, g, ep, s) : pick<Fp16, false>(t.cfg, a, g, ep, s);
+    ep.tile0 += g.tx;
+  };
+  part(0, cut.large, {0, 256, 256});
+  part(cut.large, nv - cut.large, cut.rest);
+  return e;
 }
 
 }  // namespace ttb
