@@ -168,6 +168,44 @@ struct Feed {
     rem -= step;
     kleft -= GK;
   }
+
+  // What the loads get wrong in the last tile of k where the rows of o are of any alignment,
+  // put right in LDS (all threads; the tile has arrived, its readers wait for a barrier):
+  //  - "row": the group of eight across the end of k holds the next row's first elements,
+  //    which have to be zeros (the other operand is zero there, but 0 x inf is not);
+  //  - the bounds check goes by dwords from the load's start, so the very last element of an
+  //    operand of odd length is dropped.
+  static __device__ __forceinline__ void mend(const Operand &o, char *t, int64_t x0, int64_t k0) {
+    const int tid = own_thread();
+    if constexpr (!COL) {
+      const int in = (int)(o.cols - k0);  // elements of k in this tile
+      for (int r = tid; r < ROWS; r += NT) {
+        union {
+          i32x4 v;
+          unsigned short e[8];
+        } u;
+        i32x4 *at = (i32x4 *)(t + r * 128 + (((in >> 3) ^ (r & 7)) << 4));
+        u.v = *at;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e >= (in & 7)) u.e[e] = 0;
+        if ((in & 1) && x0 + r == o.rows - 1) {
+          const unsigned short last =
+              *(const unsigned short *)(o.p + (o.rows - 1) * o.ld + (o.cols - 1) * 2);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e == (in & 7) - 1) u.e[e] = last;
+        }
+        *at = u.v;
+      }
+    } else if (tid == 0 && (o.cols & 1)) {
+      const int64_t k = o.rows - 1 - k0, x = o.cols - 1 - x0;
+      if (k >= 0 && k < GK && x >= 0 && x < ROWS)
+        *(unsigned short *)(t + k * ROWS * 2 + (((int)(x >> 3)) ^ col_swz<ROWS>((int)k)) * 16 +
+                            (x & 7) * 2) =
+            *(const unsigned short *)(o.p + (o.rows - 1) * o.ld + (o.cols - 1) * 2);
+    }
+  }
 };
 
 // ---------------------------------------------------------------- LDS -> registers
@@ -247,7 +285,9 @@ struct Tile {
 // loads run on from one tile into the next, so the next tile's first data travel while this
 // one's results are worked off; done() may use its scratch freely between two of its own
 // barriers.
-template <class E, class T, bool PC, bool QC, class Done>
+// MEND: P's rows do not end with whole 16-byte groups (see Feed::mend); a variant of its own,
+// because the test for it in the loop cost the others 1 to 7 %.
+template <class E, class T, bool PC, bool QC, bool MEND, class Done>
 __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done done) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
@@ -327,8 +367,14 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
 #pragma unroll
       for (int j = 0; j < T::NI; ++j) acc[i][j] = zero4();
     const int steps = now.nk * a.nseg;
+    auto mend = [&](int b) {
+      Feed<T::X, PC, T::NT>::mend(a.P, lds + b * SB, (int64_t)now.ix * T::X,
+                                  now.k0 + (int64_t)(now.nk - 1) * GK);
+      lds_barrier();
+    };
     if (steps > 0) {
       wait_barrier<(T::STAGES - 1) * LPT>();
+      if (MEND && steps == 1) mend(buf);
       read(0, buf, 0);
     }
     for (int st = 0; st < steps; ++st) {
@@ -336,6 +382,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
       read(1, buf, 1);
       mul(0);
       wait_barrier<(T::STAGES - 2) * LPT>();
+      if (MEND && st + 2 == steps) mend(next);
       load(buf);
       read(0, next, 0);
       mul(1);
@@ -352,6 +399,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
 // 4 + 4 sixteen-bit values of a lane, from two result tiles 16 x apart, to 8 consecutive ones
 // per lane: swapping the odd 16-lane rows of one register with the even ones of the other
 // leaves lane groups 0..3 with x = 0, 16, 8, 24 and on.  o: x = 0 of the pair.
+// o may lie on any boundary of two bytes.
 template <class V4>
 __device__ __forceinline__ void store_pair_if(bool in, char *o, V4 a, V4 b, int g) {
   union {
@@ -362,8 +410,9 @@ __device__ __forceinline__ void store_pair_if(bool in, char *o, V4 a, V4 b, int 
   s.v[1] = b;
   const auto lo = __builtin_amdgcn_permlane16_swap(s.u[0], s.u[2], false, false);
   const auto hi = __builtin_amdgcn_permlane16_swap(s.u[1], s.u[3], false, false);
-  i32x4 v = {(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]};
-  if (in) *(i32x4 *)(o + ((g & 1) * 16 + (g >> 1) * 8) * 2) = v;
+  struct __attribute__((packed, aligned(2))) any { i32x4 v; };
+  any v = {{(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]}};
+  if (in) *(any *)(o + ((g & 1) * 16 + (g >> 1) * 8) * 2) = v;
 }
 template <class V4>
 __device__ __forceinline__ void store_pair(char *o, V4 a, V4 b, int g) {

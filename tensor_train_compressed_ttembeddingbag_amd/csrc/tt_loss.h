@@ -58,7 +58,7 @@ struct LossArgs {
   // plan
   int64_t Npad, Dp;        // packed rows and their pitch (elements)
   int planes;              // 2 for fp32
-  int pack_w;              // the weight is packed too (fp32, or rows not on 16 bytes)
+  int pack_w;              // the weight is packed too (fp32, odd widths)
   int64_t piece;           // rows of the weight per piece
   int ptiles;              // running statistics per position
   int dh_bx, dh_by, cus;   // k_dhidden's tile, compute units
@@ -168,6 +168,11 @@ inline hipError_t lds_limit(F *f) {
   return e;
 }
 
+// tile shape for the launch: the deep variants where there are at most as many tiles as CUs
+inline int deep_cfg(const LossArgs &a, int cfg, int64_t tiles) {
+  return tiles > a.cus || (cfg != 1 && cfg != 2) ? cfg : cfg + 3;
+}
+
 // workgroups of a product with that many tiles: as many as the CUs hold at once
 template <class T>
 inline unsigned gemm_grid(const LossArgs &a, int64_t tiles) {
@@ -178,6 +183,10 @@ inline unsigned gemm_grid(const LossArgs &a, int64_t tiles) {
 typedef Tile<256, 256, 128, 64, 2> TileL;
 typedef Tile<128, 128, 64, 64, 2> TileM;
 typedef Tile<128, 64, 32, 64, 3> TileS;
+// Deeper loads where every workgroup has a CU for itself: there nothing else covers the
+// latency of a step.
+typedef Tile<128, 128, 64, 64, 4> TileM4;
+typedef Tile<128, 64, 32, 64, 6> TileS6;
 typedef Tile<64, 128, 32, 64, 3> TileN;  // gradients of narrow tables (d <= 64)
 
 }  // namespace ttb

@@ -491,15 +491,16 @@ __global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a) {
   }
   O *o = (O *)a.dh + i * a.D + c;
   typedef O o4 __attribute__((ext_vector_type(4)));
-  o4 w;
+  struct __attribute__((packed, aligned(2))) any { o4 v; };
+  any w;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) w[r] = (O)v[r];
-  if (a.D % 4 == 0 && ((uintptr_t)a.dh & (4 * sizeof(O) - 1)) == 0) {
-    *(o4 *)o = w;
+  for (int r = 0; r < 4; ++r) w.v[r] = (O)v[r];
+  if (c + 4 <= a.D) {
+    *(any *)o = w;
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (c + r < a.D) o[r] = w[r];
+      if (c + r < a.D) o[r] = w.v[r];
   }
   }
 }
@@ -636,7 +637,11 @@ static int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
   a.Dp = round_up(a.D, 64);
   a.planes = a.dtype == TT_DTYPE_F32 ? 2 : 1;
   a.cus = std::max(device_cus(), 1);
-  a.pack_w = a.planes > 1 || a.D % 8 || a.wld % 8 || ((uintptr_t)weight & 15);
+  // 16-bit rows of odd length are read as they lie, and the last tile of k is put right in LDS
+  // for every tile of positions; where positions are many for the width, packing the weight
+  // is cheaper (1294 x 99003 x 1389: 1205 us as they lie, 1420 packed; 3855 x 41825 x 124:
+  // 312 and 298)
+  a.pack_w = a.planes > 1 || (a.D % 8 && a.N >= 16 * a.D);
   return TT_OK;
 }
 

@@ -9,13 +9,13 @@
 
 namespace ttb {
 
-template <class E, class T>
+template <class E, class T, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
                                                    const int *count, int add) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int n = *count;
   const int64_t split = (int64_t)((n + T::Y - 1) / T::Y) * T::Y * ld;
-  gemm_tiles<E, T, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  gemm_tiles<E, T, true, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int x = t.ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
   const int y = t.iy * T::Y + (wv / T::NWX) * T::wy + c;
@@ -39,7 +39,6 @@ struct DwOut {
   O *out;             // dW of the piece's first row
   int64_t ld, nv;     // = D, rows of the piece
   const LossScalars *sc;
-  int vec;            // rows of whole groups of 16 bytes (and so aligned)
 };
 
 template <class E, class T, class O>
@@ -47,7 +46,7 @@ __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const float s = ep.sc->c_dw;
   typedef O o4 __attribute__((ext_vector_type(4)));
-  gemm_tiles<E, T, true, true>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  gemm_tiles<E, T, true, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
     const int x = t.ix * T::X + (wv % T::NWX) * T::wx;
     const int64_t y = (int64_t)t.iy * T::Y + (wv / T::NWX) * T::wy + c;
@@ -64,17 +63,19 @@ __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
           for (int r = 0; r < 4; ++r) v[u][r] = (O)(acc[i + u][j][r] * s);
         const int64_t left = ep.ld - (x + 16 * i);  // columns from this pair on
         if constexpr (sizeof(O) == 2) {
-          if (ep.vec && left >= 32) {  // whole pair: 16 bytes a lane (uniform: no lane diverges)
+          if (left >= 32) {  // a whole pair: 16 bytes a lane (the same for every lane)
             store_pair_if(in, (char *)(o + 16 * i), v[0], v[1], g);
             continue;
           }
         }
         if (!in) continue;
+        struct __attribute__((packed, aligned(2))) any { o4 v; };
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int e = 16 * u + 4 * g;
-          if (ep.vec && left >= e + 4) {
-            *(o4 *)(o + 16 * i + e) = v[u];
+          if (left >= e + 4) {
+            const any w = {v[u]};
+            *(any *)(o + 16 * i + e) = w;
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -86,11 +87,11 @@ __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   });
 }
 
-template <class E, class T>
+template <class E, class T, bool MEND>
 static hipError_t go_dh(const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
-  const hipError_t e = lds_limit<T>(&k_dhidden<E, T>);
+  const hipError_t e = lds_limit<T>(&k_dhidden<E, T, MEND>);
   if (e != hipSuccess) return e;
-  tt_launch(K_LOSS_DH, k_dhidden<E, T>, dim3(gemm_grid<T>(a, std::max(g.tx * g.ty, DH_TILES))), dim3(T::NT), T::LDS,
+  tt_launch(K_LOSS_DH, k_dhidden<E, T, MEND>, dim3(gemm_grid<T>(a, std::max(g.tx * g.ty, DH_TILES))), dim3(T::NT), T::LDS,
             s, g, a.dhp, a.Dp, (const int *)a.sv.count, add);
   return hipGetLastError();
 }
@@ -103,9 +104,18 @@ static hipError_t go_dw(const GemmArgs &g, const LossArgs &a, int64_t v0, int64_
   DwOut<O> ep;
   ep.out = (O *)a.dw + v0 * a.D;
   ep.ld = a.D; ep.nv = nv; ep.sc = a.sc;
-  ep.vec = a.D % (16 / sizeof(O)) == 0 && ((uintptr_t)a.dw & 15) == 0;
   tt_launch(K_LOSS_DW, k_dweight<E, T, O>, dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT), T::LDS, s, g, ep);
   return hipGetLastError();
+}
+
+template <class E, bool MEND>
+static hipError_t pick_dh(int cfg, const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
+  if (cfg == 0) return go_dh<E, TileL, MEND>(g, a, add, s);
+  if (cfg == 1) return go_dh<E, TileM, MEND>(g, a, add, s);
+  if (cfg == 3) return go_dh<E, TileN, MEND>(g, a, add, s);
+  if (cfg == 4) return go_dh<E, TileM4, MEND>(g, a, add, s);
+  if (cfg == 5) return go_dh<E, TileS6, MEND>(g, a, add, s);
+  return go_dh<E, TileS, MEND>(g, a, add, s);
 }
 
 hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
@@ -120,16 +130,10 @@ hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   g.ty = (int)((a.N + t.by - 1) / t.by);
   g.dsplits = &a.sc->splits;
   const int add = v0 > 0;
-  if (a.dtype == TT_DTYPE_BF16) {
-    if (t.cfg == 0) return go_dh<Bf16, TileL>(g, a, add, s);
-    if (t.cfg == 1) return go_dh<Bf16, TileM>(g, a, add, s);
-    if (t.cfg == 3) return go_dh<Bf16, TileN>(g, a, add, s);
-    return go_dh<Bf16, TileS>(g, a, add, s);
-  }
-  if (t.cfg == 0) return go_dh<Fp16, TileL>(g, a, add, s);
-  if (t.cfg == 1) return go_dh<Fp16, TileM>(g, a, add, s);
-  if (t.cfg == 3) return go_dh<Fp16, TileN>(g, a, add, s);
-  return go_dh<Fp16, TileS>(g, a, add, s);
+  const bool mend = !a.pack_w && a.D % 2;
+  if (a.dtype == TT_DTYPE_BF16)
+    return mend ? pick_dh<Bf16, true>(t.cfg, g, a, add, s) : pick_dh<Bf16, false>(t.cfg, g, a, add, s);
+  return mend ? pick_dh<Fp16, true>(t.cfg, g, a, add, s) : pick_dh<Fp16, false>(t.cfg, g, a, add, s);
 }
 
 template <class E, class O>

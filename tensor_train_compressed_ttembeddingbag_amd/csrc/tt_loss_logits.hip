@@ -24,10 +24,10 @@ struct LogitsEpi {
   int planes;
 };
 
-template <class E, class T, bool GRAD>
+template <class E, class T, bool GRAD, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  gemm_tiles<E, T, false, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
+  gemm_tiles<E, T, false, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
   const float zs = ep.sc->zs;
@@ -147,21 +147,34 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   });
 }
 
-template <class E, class T, bool GRAD>
+template <class E, class T, bool GRAD, bool MEND>
 static hipError_t go(const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
-  const hipError_t e = lds_limit<T>(&k_logits<E, T, GRAD>);
+  const hipError_t e = lds_limit<T>(&k_logits<E, T, GRAD, MEND>);
   if (e != hipSuccess) return e;
-  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, GRAD>, dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT),
-            T::LDS, s, g, ep);
+  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, GRAD, MEND>,
+            dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT), T::LDS, s, g, ep);
   return hipGetLastError();
 }
 
-template <class E, bool GRAD>
-static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
-  if (cfg == 0) return go<E, TileL, GRAD>(a, g, ep, s);
-  if (cfg == 1) return go<E, TileM, GRAD>(a, g, ep, s);
-  if (cfg == 3) return go<E, TileN, GRAD>(a, g, ep, s);  // vocabularies of up to 64 rows
-  return go<E, TileS, GRAD>(a, g, ep, s);
+template <class E, bool GRAD, bool MEND>
+static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep,
+                       hipStream_t s) {
+  cfg = deep_cfg(a, cfg, (int64_t)g.tx * g.ty);
+  if (cfg == 0) return go<E, TileL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 1) return go<E, TileM, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 3) return go<E, TileN, GRAD, MEND>(a, g, ep, s);  // vocabularies of up to 64 rows
+  if (cfg == 4) return go<E, TileM4, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 5) return go<E, TileS6, GRAD, MEND>(a, g, ep, s);
+  return go<E, TileS, GRAD, MEND>(a, g, ep, s);
+}
+
+template <class E>
+static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
+                       const LogitsEpi &ep, hipStream_t s) {
+  const bool mend = !a.pack_w && a.D % 8;
+  if (grad)
+    return mend ? pick<E, true, true>(cfg, a, g, ep, s) : pick<E, true, false>(cfg, a, g, ep, s);
+  return mend ? pick<E, false, true>(cfg, a, g, ep, s) : pick<E, false, false>(cfg, a, g, ep, s);
 }
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
@@ -196,10 +209,8 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     ep.v0 = v0 + r0;
     ep.nv = n;
     ep.G = a.G + r0 * 2;
-    if (a.dtype == TT_DTYPE_BF16)
-      e = grad ? pick<Bf16, true>(t.cfg, a, g, ep, s) : pick<Bf16, false>(t.cfg, a, g, ep, s);
-    else
-      e = grad ? pick<Fp16, true>(t.cfg, a, g, ep, s) : pick<Fp16, false>(t.cfg, a, g, ep, s);
+    e = a.dtype == TT_DTYPE_BF16 ? pick<Bf16>(grad, t.cfg, a, g, ep, s)
+                                 : pick<Fp16>(grad, t.cfg, a, g, ep, s);
     ep.tile0 += g.tx;
   };
   part(0, cut.large, {0, 256, 256});
