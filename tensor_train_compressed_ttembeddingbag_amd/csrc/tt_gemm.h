@@ -17,8 +17,9 @@
 //
 // fp32 operands come as two fp16 planes (x s = hi + lo, s a power of two that puts the
 // tensor's largest value below 2^15: 22 bits of every value within 2^17 of the largest, an
-// absolute 2^-39 of the largest below that); lo hi + hi lo + hi hi are three runs over k into
-// the same sums.
+// absolute 2^-39 of the largest below that), side by side in a row.  Their tiles hold 32 k of
+// both planes, and hi hi, hi lo and lo hi go into the same sums: three products for the LDS
+// traffic of two.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -59,12 +60,13 @@ struct Fp16 {
   }
 };
 
-constexpr int GK = 64;                        // k per tile
+constexpr int GK = 64;                        // k per tile (over all planes)
 constexpr unsigned BUF_MAX = 0x7fffffffu;     // largest extent of one buffer descriptor
 constexpr unsigned BUF_OUT = 0x80000000u;     // an offset past every extent: reads as zeros
 
-// One operand in memory: `rows` rows of `cols` elements, ld bytes apart, `planes` copies
-// plane bytes apart.  "row" operands have rows = x or y, cols = k; "col" ones the reverse.
+// One operand in memory: `rows` rows of `cols` elements, ld bytes apart; with two planes, the
+// second one's row lies `plane` bytes behind the first one's.  "row" operands have rows = x or
+// y, cols = k; "col" ones the reverse.
 struct Operand {
   const char *p;
   int64_t ld, plane;
@@ -76,7 +78,6 @@ struct GemmArgs {
   int64_t K;            // k in all
   const int *kcount;    // device word that bounds K (rounded up to 64), or null
   const int *ycount;    // device word: tiles of y from it on have nothing to do, or null
-  int nseg;             // 1, or 3 for two-plane operands
   int tx, ty, splits;   // tiles along x and y, pieces of k
   const int *dsplits;   // device word: the pieces of k (over the tiles of ycount), or null
 };
@@ -115,47 +116,47 @@ __device__ __forceinline__ int col_swz(int k) {
                      : 2 * (((k >> 1) & 1) + 2 * ((k >> 3) & 1));
 }
 
-// The 64-k tile of ROWS x (or y) of one operand: where its lanes read and where it is next.
-template <int ROWS, bool COL, int NT>
+// The tile of ROWS x (or y) by 64 / PL k of one operand: where its lanes read and where it is
+// next.  Two planes: "row" tiles hold k of the first plane in the front half of a row and of
+// the second in the rear half, "col" tiles have the second plane's rows below the first's.
+template <int ROWS, bool COL, int PL, int NT>
 struct Feed {
+  static constexpr int KT = GK / PL;
   static constexpr int L = ROWS * 8 / NT;  // loads per thread and tile
   unsigned voff[L];
-  uint64_t base0, base;
-  int64_t rem0, rem, step;  // bytes from base to the operand's end; bytes per tile of k
-  int64_t kleft0, kleft;    // "row": elements of k left
+  uint64_t base;
+  int64_t rem, step;        // bytes from base to the operand's end; bytes per tile of k
+  int64_t kleft;            // "row": elements of k left
   int chunk;                // "row": this lane's first element of k inside the tile
 
   __device__ __forceinline__ void init(const Operand &o, int64_t x0, int64_t k0, int tid) {
     const int64_t r = COL ? k0 : x0, c = COL ? x0 : k0;
-    base0 = (uint64_t)o.p + r * o.ld + c * 2;
-    rem0 = (o.rows - 1 - r) * o.ld + (o.cols - c) * 2;
-    step = COL ? GK * o.ld : GK * 2;
-    kleft0 = o.cols - k0;
+    base = (uint64_t)o.p + r * o.ld + c * 2;
+    rem = (o.rows - 1 - r) * o.ld + (PL > 1 ? o.plane : 0) + (o.cols - c) * 2;
+    step = COL ? KT * o.ld : KT * 2;
+    kleft = o.cols - k0;
     if constexpr (COL) {
       constexpr int CPR = ROWS / 8;
       const int k = tid / CPR, pc = tid % CPR;
 #pragma unroll
       for (int j = 0; j < L; ++j) {
         const int kk = k + j * (NT / CPR);
-        voff[j] = (unsigned)(kk * o.ld + (pc ^ col_swz<ROWS>(kk)) * 16);
+        voff[j] = (unsigned)((kk % KT) * o.ld + (kk / KT) * o.plane +
+                             (pc ^ col_swz<ROWS>(kk)) * 16);
       }
       chunk = 0;
     } else {
       const int row = tid / 8, c8 = (tid % 8) ^ (row & 7);
 #pragma unroll
-      for (int j = 0; j < L; ++j) voff[j] = (unsigned)((row + j * (NT / 8)) * o.ld + c8 * 16);
-      chunk = c8 * 8;
+      for (int j = 0; j < L; ++j)
+        voff[j] = (unsigned)((row + j * (NT / 8)) * o.ld + (c8 * 8 / KT) * o.plane +
+                             (c8 * 8 % KT) * 2);
+      chunk = c8 * 8 % KT;
     }
-    seek(0);
-  }
-  __device__ __forceinline__ void seek(int64_t plane) {
-    base = base0 + plane;
-    rem = rem0;
-    kleft = kleft0;
   }
   __device__ __forceinline__ void issue(unsigned lds, bool live) {
     const i32x4 d = buf_desc(base, live ? rem : 0);
-    const bool whole = COL || kleft >= GK;
+    const bool whole = COL || kleft >= KT;
     if (whole) {
 #pragma unroll
       for (int j = 0; j < L; ++j) load_lds(d, voff[j], lds + j * (NT * 16));
@@ -166,7 +167,7 @@ struct Feed {
     }
     base += step;
     rem -= step;
-    kleft -= GK;
+    kleft -= KT;
   }
 
   // What the loads get wrong in the last tile of k where the rows of o are of any alignment,
@@ -209,7 +210,8 @@ struct Feed {
 };
 
 // ---------------------------------------------------------------- LDS -> registers
-// Fragments of 16 x (or y) at x0 of the tile at `t`, k = 32 kk + 8 g .. + 8
+// Fragments of 16 x (or y) at x0 of the tile at `t`: k = 32 kk + 8 g .. + 8, with two planes
+// k = 8 g .. + 8 of plane kk
 template <class E, int ROWS, bool COL>
 __device__ __forceinline__ typename E::v8 frag(const char *t, int x0, int kk, int lane) {
   const int g = lane >> 4, c = lane & 15;
@@ -231,7 +233,7 @@ __device__ __forceinline__ typename E::v8 frag(const char *t, int x0, int kk, in
   }
 }
 
-// One tile of the result: (x tile, y tile, split) and its 64-k tiles.
+// One tile of the result: (x tile, y tile, split) and its tiles of k.
 struct TileAt {
   int ix, iy, is, nk;
   int64_t k0;
@@ -242,11 +244,12 @@ struct TileAt {
 // are walked together, so the 32 CUs of an XCD share the rows of few tiles of both operands
 // in its L2.
 struct TileWalk {
-  int tx, ty, splits, total;
+  int tx, ty, splits, total, KT;
   int64_t K, kper;
 
   template <int BY>
-  __device__ __forceinline__ void init(const GemmArgs &a) {
+  __device__ __forceinline__ void init(const GemmArgs &a, int kt) {
+    KT = kt;
     tx = a.tx;
     ty = a.ycount ? min(a.ty, (*a.ycount + BY - 1) / BY) : a.ty;
     splits = a.dsplits ? *a.dsplits : a.splits;
@@ -266,7 +269,7 @@ struct TileWalk {
     t.iy = in / w;
     t.k0 = t.is * kper;
     const int64_t n = min(kper, K - t.k0);
-    t.nk = n > 0 ? (int)((n + GK - 1) / GK) : 0;
+    t.nk = n > 0 ? (int)((n + KT - 1) / KT) : 0;
     return true;
   }
 };
@@ -287,22 +290,22 @@ struct Tile {
 // barriers.
 // MEND: P's rows do not end with whole 16-byte groups (see Feed::mend); a variant of its own,
 // because the test for it in the loop cost the others 1 to 7 %.
-template <class E, class T, bool PC, bool QC, bool MEND, class Done>
+template <class E, class T, int PL, bool PC, bool QC, bool MEND, class Done>
 __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done done) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
   TileWalk walk;
-  walk.init<T::Y>(a);
+  walk.init<T::Y>(a, GK / PL);
   TileAt now, ahead;
   int id = blockIdx.x, ida = id;
   if (!walk.at(id, now)) return;
 
-  Feed<T::X, PC, T::NT> fp;
-  Feed<T::Y, QC, T::NT> fq;
+  Feed<T::X, PC, PL, T::NT> fp;
+  Feed<T::Y, QC, PL, T::NT> fq;
   constexpr int PB = T::X * GK * 2, QB = T::Y * GK * 2, SB = PB + QB;
   const unsigned lbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)lds +
                          wv * 1024;
-  int ik = 0, seg = 0;  // the next 64-k tile to load, of tile `ahead`
+  int ik = 0;  // the next tile of k to load, of tile `ahead`
   bool live = true;
   auto aim = [&]() {  // at the first tile from ida on that has any k
     while ((live = walk.at(ida, ahead)) && ahead.nk == 0) ida += gridDim.x;
@@ -313,47 +316,45 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
     }
   };
   auto load = [&](int buf) {
-    if (ik == 0 && a.nseg > 1) {  // lo hi, hi lo, hi hi: the small terms first
-      fp.seek(seg == 0 ? a.P.plane : 0);
-      fq.seek(seg == 1 ? a.Q.plane : 0);
-    }
     const unsigned l = __builtin_amdgcn_readfirstlane(lbase + buf * SB);
     fp.issue(l, live);  // past the last tile: zeros
     fq.issue(l + PB, live);
     if (live && ++ik >= ahead.nk) {
       ik = 0;
-      if (++seg == a.nseg) {
-        seg = 0;
-        ida += gridDim.x;
-        aim();
-      }
+      ida += gridDim.x;
+      aim();
     }
   };
   aim();
-  constexpr int LPT = Feed<T::X, PC, T::NT>::L + Feed<T::Y, QC, T::NT>::L;
+  constexpr int LPT = Feed<T::X, PC, PL, T::NT>::L + Feed<T::Y, QC, PL, T::NT>::L;
   f4 acc[T::MI][T::NI];
   typename E::v8 p[2][T::MI], q[2][T::NI];
-  auto read = [&](int set, int buf, int kk) {
-    const char *tp = lds + buf * SB, *tq = tp + PB;
+  auto read_p = [&](int set, int buf) {
 #pragma unroll
-    for (int j = 0; j < T::NI; ++j) q[set][j] = frag<E, T::Y, QC>(tq, qy + 16 * j, kk, lane);
-#pragma unroll
-    for (int i = 0; i < T::MI; ++i) p[set][i] = frag<E, T::X, PC>(tp, px + 16 * i, kk, lane);
+    for (int i = 0; i < T::MI; ++i)
+      p[set][i] = frag<E, T::X, PC>(lds + buf * SB, px + 16 * i, set, lane);
   };
-  auto mul = [&](int set) {
+  auto read_q = [&](int set, int buf) {
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j)
+      q[set][j] = frag<E, T::Y, QC>(lds + buf * SB + PB, qy + 16 * j, set, lane);
+  };
+  auto mul = [&](int sp, int sq) {
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-      for (int j = 0; j < T::NI; ++j) acc[i][j] = E::mfma(p[set][i], q[set][j], acc[i][j]);
-    // one LDS read to every few products, so that neither unit waits for the other's burst
+      for (int j = 0; j < T::NI; ++j) acc[i][j] = E::mfma(p[sp][i], q[sq][j], acc[i][j]);
+  };
+  // one LDS read to every few products, so that neither unit waits for the other's burst
+  auto pace = [&]() {
 #pragma unroll
     for (int u = 0; u < T::MI + T::NI; ++u) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, T::MI * T::NI / (T::MI + T::NI), 0);
     }
   };
-  // The two halves of a tile (32 k each) take turns in two register sets: while one is
-  // multiplied the other is read.  The barrier sits between them: there every wave has read
+  // The two halves of a tile (32 k each, or the two planes of 32 k) take turns in two register
+  // sets: while one is multiplied the other is read.  The barrier sits between them: there every wave has read
   // all of this tile, whose buffer the next load may take, and the next tile is complete, so
   // its first half is read under the second half's products.  (Reads right behind the
   // barrier, with one register set, ran at 1.25 PFLOP/s on 16384 x 8192 x 4096; this runs at
@@ -366,26 +367,38 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
       for (int j = 0; j < T::NI; ++j) acc[i][j] = zero4();
-    const int steps = now.nk * a.nseg;
+    const int steps = now.nk;
     auto mend = [&](int b) {
-      Feed<T::X, PC, T::NT>::mend(a.P, lds + b * SB, (int64_t)now.ix * T::X,
-                                  now.k0 + (int64_t)(now.nk - 1) * GK);
+      Feed<T::X, PC, PL, T::NT>::mend(a.P, lds + b * SB, (int64_t)now.ix * T::X,
+                                  now.k0 + (int64_t)(now.nk - 1) * (GK / PL));
       lds_barrier();
     };
     if (steps > 0) {
       wait_barrier<(T::STAGES - 1) * LPT>();
       if (MEND && steps == 1) mend(buf);
-      read(0, buf, 0);
+      read_q(0, buf);
+      read_p(0, buf);
     }
     for (int st = 0; st < steps; ++st) {
       const int next = buf + 1 == T::STAGES ? 0 : buf + 1;
-      read(1, buf, 1);
-      mul(0);
+      read_q(1, buf);
+      read_p(1, buf);
+      mul(0, 0);
+      pace();
       wait_barrier<(T::STAGES - 2) * LPT>();
       if (MEND && st + 2 == steps) mend(next);
       load(buf);
-      read(0, next, 0);
-      mul(1);
+      if constexpr (PL == 1) {
+        read_q(0, next);
+        read_p(0, next);
+        mul(1, 1);
+        pace();
+      } else {  // hi lo and lo hi; each operand's next front half follows its last use
+        mul(0, 1);
+        read_p(0, next);
+        mul(1, 0);
+        read_q(0, next);
+      }
       buf = next;
     }
     done(now, acc, lds + T::STAGES * SB);

@@ -66,13 +66,12 @@ struct LossArgs {
   // workspace
   LossScalars *sc;
   float *amax;             // [2 * AMAX_BLOCKS] block maxima of |weight| and |hidden| (fp32)
-  char *hp, *wp;           // packed positions, packed piece of the weight
-  int64_t hplane, wplane;  // bytes
+  char *hp, *wp;           // packed positions, packed piece of the weight: [row][plane][Dp]
   float2 *part;            // [Npad][ptiles] (max, sum) in base 2
   float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)
   float *rowloss;          // [N]
   float *rowf;             // [Npad] factor of a packed row's g
-  char *G;                 // [planes][Npad][piece]
+  char *G;                 // [Npad][planes][piece]
   int64_t ldG, Gplane;     // bytes
   float *dhp;              // [splits][tiles of positions that count][Dp]
 };
@@ -107,7 +106,7 @@ __device__ __forceinline__ int dh_splits(const LossArgs &a, int count, int lane)
 // as zeros, and small probabilities are most of a vocabulary (|g| <= 1 keeps both in range).
 __host__ __device__ inline int g_exp(int dtype) { return dtype == TT_DTYPE_BF16 ? 32 : 14; }
 
-// tile shapes: 0 = 256 x 256, 1 = 128 x 128, 2 = 128 x 64, 3 = 64 x 128 (x by y)
+// tile shapes: 0 = 256 x 256, 1 = 128 x 128, 2 = 128 x 64, 3 = 64 x 128, 4 = 64 x 64 (x by y)
 struct GemmShape {
   int cfg, bx, by;
 };
@@ -125,6 +124,10 @@ struct LogitsCut {
 };
 inline LogitsCut logits_cut(const LossArgs &a, int64_t nv) {
   LogitsCut c = {0, gemm_shape(nv, a.N), 0};
+  // very few tiles: half as high, so that more CUs read the weight (38 x 1960 x 1792 fp32: 65
+  // us, 79 in full tiles; past half the CUs it loses: 60 x 20568 x 2176 fp16 48 us, 38 full)
+  if (c.rest.bx == 128 && (nv + 127) / 128 * ((a.N + c.rest.by - 1) / c.rest.by) <= a.cus / 2)
+    c.rest = a.N > 64 ? GemmShape{3, 64, 128} : GemmShape{4, 64, 64};
   if (a.N > 128 && nv > 128) {
     const int64_t n = large_tiles((nv + 255) / 256, (a.N + 255) / 256, a.cus) * 256;
     c.large = n < nv ? n : nv;
@@ -142,7 +145,7 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
 inline Operand weight_operand(const LossArgs &a, int64_t v0, int64_t nv) {
   Operand o;
   if (a.pack_w) {
-    o.p = a.wp; o.ld = a.Dp * 2; o.plane = a.wplane; o.rows = nv; o.cols = a.Dp;
+    o.p = a.wp; o.ld = a.Dp * 2 * a.planes; o.plane = a.Dp * 2; o.rows = nv; o.cols = a.Dp;
   } else {
     o.p = (const char *)a.weight + v0 * a.wld * 2; o.ld = a.wld * 2; o.plane = 0;
     o.rows = a.V - v0; o.cols = a.D;
@@ -151,7 +154,7 @@ inline Operand weight_operand(const LossArgs &a, int64_t v0, int64_t nv) {
 }
 inline Operand hidden_operand(const LossArgs &a) {
   Operand o;
-  o.p = a.hp; o.ld = a.Dp * 2; o.plane = a.hplane; o.rows = a.Npad; o.cols = a.Dp;
+  o.p = a.hp; o.ld = a.Dp * 2 * a.planes; o.plane = a.Dp * 2; o.rows = a.Npad; o.cols = a.Dp;
   return o;
 }
 inline Operand g_operand(const LossArgs &a, int64_t nv) {
@@ -168,11 +171,6 @@ inline hipError_t lds_limit(F *f) {
   return e;
 }
 
-// tile shape for the launch: the deep variants where there are at most as many tiles as CUs
-inline int deep_cfg(const LossArgs &a, int cfg, int64_t tiles) {
-  return tiles > a.cus || (cfg != 1 && cfg != 2) ? cfg : cfg + 3;
-}
-
 // workgroups of a product with that many tiles: as many as the CUs hold at once
 template <class T>
 inline unsigned gemm_grid(const LossArgs &a, int64_t tiles) {
@@ -183,10 +181,7 @@ inline unsigned gemm_grid(const LossArgs &a, int64_t tiles) {
 typedef Tile<256, 256, 128, 64, 2> TileL;
 typedef Tile<128, 128, 64, 64, 2> TileM;
 typedef Tile<128, 64, 32, 64, 3> TileS;
-// Deeper loads where every workgroup has a CU for itself: there nothing else covers the
-// latency of a step.
-typedef Tile<128, 128, 64, 64, 4> TileM4;
-typedef Tile<128, 64, 32, 64, 6> TileS6;
 typedef Tile<64, 128, 32, 64, 3> TileN;  // gradients of narrow tables (d <= 64)
+typedef Tile<64, 64, 32, 32, 4> TileT;   // logits of few positions and a small vocabulary
 
 }  // namespace ttb

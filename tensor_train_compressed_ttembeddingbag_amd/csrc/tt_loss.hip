@@ -294,7 +294,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
         const int slot = s_slot[r];
         const int64_t row = slot < 0 ? -1 - slot : slot;
         if (slot < 0 && row >= zero_to) continue;
-        store8<S, E, PL>(v[u], scale, a.hp + (row * a.Dp + c) * 2, a.hplane);
+        store8<S, E, PL>(v[u], scale, a.hp + (row * PL * a.Dp + c) * 2, a.Dp * 2);
       }
     }
   };
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(256) void k_pack_w(LossArgs a, int64_t v0, int64_t 
     const int64_t r = q / cpr, c = (q - r * cpr) * 8;
     S v[8];
     load8((const S *)a.weight + (v0 + r) * a.wld + c, a.D - c, v);
-    store8<S, E, PL>(v, scale, a.wp + (r * a.Dp + c) * 2, a.wplane);
+    store8<S, E, PL>(v, scale, a.wp + (r * PL * a.Dp + c) * 2, a.Dp * 2);
   }
 }
 
@@ -579,8 +579,7 @@ static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
   Bump b{(char *)ws};
   b.take(a.sc, 1);
   b.take(a.amax, grad || a.planes == 1 ? 0 : 2 * AMAX_BLOCKS);
-  a.hplane = a.Npad * a.Dp * 2;
-  b.take(a.hp, a.hplane * a.planes);
+  b.take(a.hp, a.Npad * a.Dp * 2 * a.planes);
   int64_t rows = a.V;
   const int64_t wrow = a.Dp * 2 * a.planes, grow = a.Npad * 2 * a.planes;
   int64_t lim = (1ll << 38) / std::max<int64_t>(a.Npad, 256);  // tiles of one launch
@@ -591,13 +590,12 @@ static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
     rows = round_up((rows + n - 1) / n, 256);
   }
   a.piece = rows;
-  a.wplane = rows * a.Dp * 2;
-  if (a.pack_w) b.take(a.wp, a.wplane * a.planes);
+  if (a.pack_w) b.take(a.wp, rows * wrow);
   if (grad) {
     b.take(a.rowf, a.Npad);
-    a.ldG = round_up(std::min(rows, a.V), 256) * 2;
-    a.Gplane = a.Npad * a.ldG;
-    b.take(a.G, a.Gplane * a.planes);
+    a.Gplane = round_up(std::min(rows, a.V), 256) * 2;
+    a.ldG = a.Gplane * a.planes;
+    b.take(a.G, a.Npad * a.ldG);
     const GemmShape t = dh_shape(a);
     a.dh_bx = t.bx; a.dh_by = t.by;
     const int64_t ty = (a.N + t.by - 1) / t.by, tx = (a.D + t.bx - 1) / t.bx;

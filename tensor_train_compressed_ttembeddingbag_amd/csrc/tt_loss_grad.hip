@@ -9,13 +9,13 @@
 
 namespace ttb {
 
-template <class E, class T, bool MEND>
+template <class E, class T, int PL, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
                                                    const int *count, int add) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int n = *count;
   const int64_t split = (int64_t)((n + T::Y - 1) / T::Y) * T::Y * ld;
-  gemm_tiles<E, T, true, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  gemm_tiles<E, T, PL, true, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int x = t.ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
   const int y = t.iy * T::Y + (wv / T::NWX) * T::wy + c;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const float s = ep.sc->c_dw;
   typedef O o4 __attribute__((ext_vector_type(4)));
-  gemm_tiles<E, T, true, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  gemm_tiles<E, T, sizeof(O) / 2, true, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
     const int x = t.ix * T::X + (wv % T::NWX) * T::wx;
     const int64_t y = (int64_t)t.iy * T::Y + (wv / T::NWX) * T::wy + c;
@@ -87,11 +87,11 @@ __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   });
 }
 
-template <class E, class T, bool MEND>
+template <class E, class T, int PL, bool MEND>
 static hipError_t go_dh(const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
-  const hipError_t e = lds_limit<T>(&k_dhidden<E, T, MEND>);
+  const hipError_t e = lds_limit<T>(&k_dhidden<E, T, PL, MEND>);
   if (e != hipSuccess) return e;
-  tt_launch(K_LOSS_DH, k_dhidden<E, T, MEND>, dim3(gemm_grid<T>(a, std::max(g.tx * g.ty, DH_TILES))), dim3(T::NT), T::LDS,
+  tt_launch(K_LOSS_DH, k_dhidden<E, T, PL, MEND>, dim3(gemm_grid<T>(a, std::max(g.tx * g.ty, DH_TILES))), dim3(T::NT), T::LDS,
             s, g, a.dhp, a.Dp, (const int *)a.sv.count, add);
   return hipGetLastError();
 }
@@ -108,14 +108,12 @@ static hipError_t go_dw(const GemmArgs &g, const LossArgs &a, int64_t v0, int64_
   return hipGetLastError();
 }
 
-template <class E, bool MEND>
+template <class E, int PL, bool MEND>
 static hipError_t pick_dh(int cfg, const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
-  if (cfg == 0) return go_dh<E, TileL, MEND>(g, a, add, s);
-  if (cfg == 1) return go_dh<E, TileM, MEND>(g, a, add, s);
-  if (cfg == 3) return go_dh<E, TileN, MEND>(g, a, add, s);
-  if (cfg == 4) return go_dh<E, TileM4, MEND>(g, a, add, s);
-  if (cfg == 5) return go_dh<E, TileS6, MEND>(g, a, add, s);
-  return go_dh<E, TileS, MEND>(g, a, add, s);
+  if (cfg == 0) return go_dh<E, TileL, PL, MEND>(g, a, add, s);
+  if (cfg == 1) return go_dh<E, TileM, PL, MEND>(g, a, add, s);
+  if (cfg == 3) return go_dh<E, TileN, PL, MEND>(g, a, add, s);
+  return go_dh<E, TileS, PL, MEND>(g, a, add, s);
 }
 
 hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
@@ -124,16 +122,16 @@ hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   g.Q = g_operand(a, nv);
   g.K = (nv + GK - 1) / GK * GK;
   g.ycount = a.sv.count;
-  g.nseg = a.planes > 1 ? 3 : 1;
   const GemmShape t = dh_shape(a);
   g.tx = (int)((a.D + t.bx - 1) / t.bx);
   g.ty = (int)((a.N + t.by - 1) / t.by);
   g.dsplits = &a.sc->splits;
   const int add = v0 > 0;
+  if (a.planes > 1) return pick_dh<Fp16, 2, false>(t.cfg, g, a, add, s);
   const bool mend = !a.pack_w && a.D % 2;
   if (a.dtype == TT_DTYPE_BF16)
-    return mend ? pick_dh<Bf16, true>(t.cfg, g, a, add, s) : pick_dh<Bf16, false>(t.cfg, g, a, add, s);
-  return mend ? pick_dh<Fp16, true>(t.cfg, g, a, add, s) : pick_dh<Fp16, false>(t.cfg, g, a, add, s);
+    return mend ? pick_dh<Bf16, 1, true>(t.cfg, g, a, add, s) : pick_dh<Bf16, 1, false>(t.cfg, g, a, add, s);
+  return mend ? pick_dh<Fp16, 1, true>(t.cfg, g, a, add, s) : pick_dh<Fp16, 1, false>(t.cfg, g, a, add, s);
 }
 
 template <class E, class O>
@@ -147,7 +145,8 @@ static hipError_t pick_dw(int cfg, const GemmArgs &g, const LossArgs &a, int64_t
 
 hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
   int64_t large = 0;
-  if (a.D > 128 && nv > 128)
+  // with few positions the launch is one of stores: two workgroups on a CU, one of them storing
+  if (a.D > 128 && nv > 128 && a.N > 128)
     large = std::min(nv, large_tiles((nv + 255) / 256, (a.D + 255) / 256, a.cus) * 256);
   hipError_t e = hipSuccess;
   // rows [r0, r0 + n) of the piece in tiles of t
@@ -160,8 +159,7 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
     g.Q.cols -= r0;
     g.K = a.Npad;
     g.kcount = a.sv.count;
-    g.nseg = a.planes > 1 ? 3 : 1;
-    g.tx = (int)((a.D + t.bx - 1) / t.bx);
+      g.tx = (int)((a.D + t.bx - 1) / t.bx);
     g.ty = (int)((n + t.by - 1) / t.by);
     g.splits = 1;
     if (a.dtype == TT_DTYPE_BF16) e = pick_dw<Bf16, __bf16>(t.cfg, g, a, v0 + r0, n, s);

@@ -21,13 +21,12 @@ struct LogitsEpi {
   const float *lse, *rowf;
   const int *tgt;          // null with distillation
   float one_e, e_v, gs;    // 1 - e, e / V, G's factor 2^g_exp
-  int planes;
 };
 
-template <class E, class T, bool GRAD, bool MEND>
+template <class E, class T, int PL, bool GRAD, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  gemm_tiles<E, T, false, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
+  gemm_tiles<E, T, PL, false, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
   const float zs = ep.sc->zs;
@@ -140,41 +139,39 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
           for (int r = 0; r < 4; ++r) l[u][r] = (typename E::e)(v[r] - (float)h[u][r]);
         }
         store_pair(o + 32 * i0, h[0], h[1], g);
-        if (ep.planes > 1) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
+        if constexpr (PL > 1) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
       }
     }
   }
   });
 }
 
-template <class E, class T, bool GRAD, bool MEND>
+template <class E, class T, int PL, bool GRAD, bool MEND>
 static hipError_t go(const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
-  const hipError_t e = lds_limit<T>(&k_logits<E, T, GRAD, MEND>);
+  const hipError_t e = lds_limit<T>(&k_logits<E, T, PL, GRAD, MEND>);
   if (e != hipSuccess) return e;
-  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, GRAD, MEND>,
+  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, PL, GRAD, MEND>,
             dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT), T::LDS, s, g, ep);
   return hipGetLastError();
 }
 
-template <class E, bool GRAD, bool MEND>
+template <class E, int PL, bool GRAD, bool MEND>
 static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep,
                        hipStream_t s) {
-  cfg = deep_cfg(a, cfg, (int64_t)g.tx * g.ty);
-  if (cfg == 0) return go<E, TileL, GRAD, MEND>(a, g, ep, s);
-  if (cfg == 1) return go<E, TileM, GRAD, MEND>(a, g, ep, s);
-  if (cfg == 3) return go<E, TileN, GRAD, MEND>(a, g, ep, s);  // vocabularies of up to 64 rows
-  if (cfg == 4) return go<E, TileM4, GRAD, MEND>(a, g, ep, s);
-  if (cfg == 5) return go<E, TileS6, GRAD, MEND>(a, g, ep, s);
-  return go<E, TileS, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 0) return go<E, TileL, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 1) return go<E, TileM, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 3) return go<E, TileN, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 4) return go<E, TileT, PL, GRAD, MEND>(a, g, ep, s);
+  return go<E, TileS, PL, GRAD, MEND>(a, g, ep, s);
 }
 
-template <class E>
+template <class E, int PL>
 static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
                        const LogitsEpi &ep, hipStream_t s) {
-  const bool mend = !a.pack_w && a.D % 8;
-  if (grad)
-    return mend ? pick<E, true, true>(cfg, a, g, ep, s) : pick<E, true, false>(cfg, a, g, ep, s);
-  return mend ? pick<E, false, true>(cfg, a, g, ep, s) : pick<E, false, false>(cfg, a, g, ep, s);
+  if constexpr (PL == 1)
+    if (!a.pack_w && a.D % 8)
+      return grad ? pick<E, PL, true, true>(cfg, a, g, ep, s) : pick<E, PL, false, true>(cfg, a, g, ep, s);
+  return grad ? pick<E, PL, true, false>(cfg, a, g, ep, s) : pick<E, PL, false, false>(cfg, a, g, ep, s);
 }
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
@@ -189,7 +186,6 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.gs = ldexpf(1.f, g_exp(a.dtype));
   ep.one_e = 1.f - a.smoothing;
   ep.e_v = a.smoothing / (float)a.V;
-  ep.planes = a.planes;
   const LogitsCut cut = logits_cut(a, nv);
   hipError_t e = hipSuccess;
   // rows [r0, r0 + n) of the piece in tiles of t
@@ -202,15 +198,15 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     g.Q = hidden_operand(a);
     g.K = a.pack_w ? a.Dp : a.D;
     g.ycount = a.sv.count;
-    g.nseg = a.planes > 1 ? 3 : 1;
     g.tx = (int)((n + t.bx - 1) / t.bx);
     g.ty = (int)((a.N + t.by - 1) / t.by);
     g.splits = 1;
     ep.v0 = v0 + r0;
     ep.nv = n;
     ep.G = a.G + r0 * 2;
-    e = a.dtype == TT_DTYPE_BF16 ? pick<Bf16>(grad, t.cfg, a, g, ep, s)
-                                 : pick<Fp16>(grad, t.cfg, a, g, ep, s);
+    if (a.dtype == TT_DTYPE_BF16) e = pick<Bf16, 1>(grad, t.cfg, a, g, ep, s);
+    else if (a.dtype == TT_DTYPE_F16) e = pick<Fp16, 1>(grad, t.cfg, a, g, ep, s);
+    else e = pick<Fp16, 2>(grad, t.cfg, a, g, ep, s);
     ep.tile0 += g.tx;
   };
   part(0, cut.large, {0, 256, 256});
