@@ -76,8 +76,9 @@ struct Operand {
 struct GemmArgs {
   Operand P, Q;
   int64_t K;            // k in all
+  int xn, yn;           // x and y in all
   const int *kcount;    // device word that bounds K (rounded up to 64), or null
-  const int *ycount;    // device word: tiles of y from it on have nothing to do, or null
+  const int *ycount;    // device word that bounds yn, or null
   int tx, ty, splits;   // tiles along x and y, pieces of k
   const int *dsplits;   // device word: the pieces of k (over the tiles of ycount), or null
 };
@@ -244,14 +245,15 @@ struct TileAt {
 // are walked together, so the 32 CUs of an XCD share the rows of few tiles of both operands
 // in its L2.
 struct TileWalk {
-  int tx, ty, splits, total, KT;
+  int tx, ty, splits, total, KT, yn;
   int64_t K, kper;
 
   template <int BY>
   __device__ __forceinline__ void init(const GemmArgs &a, int kt) {
     KT = kt;
     tx = a.tx;
-    ty = a.ycount ? min(a.ty, (*a.ycount + BY - 1) / BY) : a.ty;
+    yn = a.ycount ? min(a.yn, *a.ycount) : a.yn;
+    ty = min(a.ty, (yn + BY - 1) / BY);
     splits = a.dsplits ? *a.dsplits : a.splits;
     K = a.kcount ? (int64_t)((*a.kcount + GK - 1) / GK) * GK : a.K;
     kper = ((K + splits - 1) / splits + GK - 1) / GK * GK;
@@ -373,33 +375,49 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
                                   now.k0 + (int64_t)(now.nk - 1) * (GK / PL));
       lds_barrier();
     };
-    if (steps > 0) {
-      wait_barrier<(T::STAGES - 1) * LPT>();
-      if (MEND && steps == 1) mend(buf);
-      read_q(0, buf);
-      read_p(0, buf);
-    }
-    for (int st = 0; st < steps; ++st) {
-      const int next = buf + 1 == T::STAGES ? 0 : buf + 1;
-      read_q(1, buf);
-      read_p(1, buf);
-      mul(0, 0);
-      pace();
-      wait_barrier<(T::STAGES - 2) * LPT>();
-      if (MEND && st + 2 == steps) mend(next);
-      load(buf);
-      if constexpr (PL == 1) {
-        read_q(0, next);
-        read_p(0, next);
-        mul(1, 1);
-        pace();
-      } else {  // hi lo and lo hi; each operand's next front half follows its last use
-        mul(0, 1);
-        read_p(0, next);
-        mul(1, 0);
-        read_q(0, next);
+    // a wave whose part of a ragged tile lies outside has its loads and barriers only (1800
+    // positions: the eighth row of tiles, with 8 of 256, costs half)
+    if (now.ix * T::X + px >= a.xn || now.iy * T::Y + qy >= walk.yn) {
+      if (steps > 0) {
+        wait_barrier<(T::STAGES - 1) * LPT>();
+        if (MEND && steps == 1) mend(buf);
       }
-      buf = next;
+      for (int st = 0; st < steps; ++st) {
+        const int next = buf + 1 == T::STAGES ? 0 : buf + 1;
+        wait_barrier<(T::STAGES - 2) * LPT>();
+        if (MEND && st + 2 == steps) mend(next);
+        load(buf);
+        buf = next;
+      }
+    } else {
+      if (steps > 0) {
+        wait_barrier<(T::STAGES - 1) * LPT>();
+        if (MEND && steps == 1) mend(buf);
+        read_q(0, buf);
+        read_p(0, buf);
+      }
+      for (int st = 0; st < steps; ++st) {
+        const int next = buf + 1 == T::STAGES ? 0 : buf + 1;
+        read_q(1, buf);
+        read_p(1, buf);
+        mul(0, 0);
+        pace();
+        wait_barrier<(T::STAGES - 2) * LPT>();
+        if (MEND && st + 2 == steps) mend(next);
+        load(buf);
+        if constexpr (PL == 1) {
+          read_q(0, next);
+          read_p(0, next);
+          mul(1, 1);
+          pace();
+        } else {  // hi lo and lo hi; each operand's next front half follows its last use
+          mul(0, 1);
+          read_p(0, next);
+          mul(1, 0);
+          read_q(0, next);
+        }
+        buf = next;
+      }
     }
     done(now, acc, lds + T::STAGES * SB);
     id += gridDim.x;

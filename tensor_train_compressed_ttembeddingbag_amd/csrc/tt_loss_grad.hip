@@ -121,6 +121,8 @@ hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   g.P = weight_operand(a, v0, nv);
   g.Q = g_operand(a, nv);
   g.K = (nv + GK - 1) / GK * GK;
+  g.xn = (int)a.D;
+  g.yn = (int)a.N;
   g.ycount = a.sv.count;
   const GemmShape t = dh_shape(a);
   g.tx = (int)((a.D + t.bx - 1) / t.bx);
@@ -158,6 +160,8 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
     g.Q.p += r0 * 2;
     g.Q.cols -= r0;
     g.K = a.Npad;
+    g.xn = (int)a.D;
+    g.yn = (int)n;
     g.kcount = a.sv.count;
       g.tx = (int)((a.D + t.bx - 1) / t.bx);
     g.ty = (int)((n + t.by - 1) / t.by);

@@ -197,6 +197,8 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     g.P.rows -= r0;
     g.Q = hidden_operand(a);
     g.K = a.pack_w ? a.Dp : a.D;
+    g.xn = (int)n;
+    g.yn = (int)a.N;
     g.ycount = a.sv.count;
     g.tx = (int)((n + t.bx - 1) / t.bx);
     g.ty = (int)((a.N + t.by - 1) / t.by);
