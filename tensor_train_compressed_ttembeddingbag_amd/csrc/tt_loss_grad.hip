@@ -171,7 +171,10 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
     else e = pick_dw<Fp16, float>(t.cfg, g, a, v0 + r0, n, s);
   };
   part(0, large, {0, 256, 256});
-  part(large, nv - large, gemm_shape(a.D, nv - large));
+  // narrow tables have few tiles: half as many rows each where that leaves CUs idle
+  GemmShape rest = gemm_shape(a.D, nv - large);
+  if (rest.cfg == 1 && (a.D + 127) / 128 * ((nv - large + 127) / 128) <= a.cus) rest = {2, 128, 64};
+  part(large, nv - large, rest);
   return e;
 }
 
