@@ -106,11 +106,12 @@ __device__ __forceinline__ int dh_splits(const LossArgs &a, int count, int lane)
 // as zeros, and small probabilities are most of a vocabulary (|g| <= 1 keeps both in range).
 __host__ __device__ inline int g_exp(int dtype) { return dtype == TT_DTYPE_BF16 ? 32 : 14; }
 
-// tile shapes: 0 = 256 x 256, 1 = 128 x 128, 2 = 128 x 64, 3 = 64 x 128, 4 = 64 x 64 (x by y)
+// tile shapes (x by y): 0 = 256 x 256, 1 = 128 x 128 for two on a CU, 2 = 128 x 64,
+// 3 = 64 x 128, 4 = 64 x 64, 5 = 128 x 128 for one on a CU
 struct GemmShape {
   int cfg, bx, by;
 };
-GemmShape gemm_shape(int64_t x, int64_t y);  // of products without large tiles
+GemmShape gemm_shape(int64_t x, int64_t y, int cus);  // of products without large tiles
 GemmShape dh_shape(const LossArgs &a);
 // of `along` large tiles by `across` others, how many of the first to take in large tiles
 int64_t large_tiles(int64_t along, int64_t across, int cus);
@@ -123,15 +124,12 @@ struct LogitsCut {
   int tiles;
 };
 inline LogitsCut logits_cut(const LossArgs &a, int64_t nv) {
-  LogitsCut c = {0, gemm_shape(nv, a.N), 0};
-  // very few tiles: half as high, so that more CUs read the weight (38 x 1960 x 1792 fp32: 65
-  // us, 79 in full tiles; past half the CUs it loses: 60 x 20568 x 2176 fp16 48 us, 38 full)
-  if (c.rest.bx == 128 && (nv + 127) / 128 * ((a.N + c.rest.by - 1) / c.rest.by) <= a.cus / 2)
-    c.rest = a.N > 64 ? GemmShape{3, 64, 128} : GemmShape{4, 64, 64};
+  LogitsCut c = {0, {}, 0};
   if (a.N > 128 && nv > 128) {
     const int64_t n = large_tiles((nv + 255) / 256, (a.N + 255) / 256, a.cus) * 256;
     c.large = n < nv ? n : nv;
   }
+  c.rest = gemm_shape(nv - c.large, a.N, a.cus);
   c.tiles = (int)((c.large + 255) / 256 + (nv - c.large + c.rest.bx - 1) / c.rest.bx);
   return c;
 }
@@ -179,9 +177,10 @@ inline unsigned gemm_grid(const LossArgs &a, int64_t tiles) {
 }
 
 typedef Tile<256, 256, 128, 64, 2> TileL;
-typedef Tile<128, 128, 64, 64, 2> TileM;
+typedef Tile<128, 128, 64, 32, 2> TileM;
 typedef Tile<128, 64, 32, 64, 3> TileS;
-typedef Tile<64, 128, 32, 64, 3> TileN;  // gradients of narrow tables (d <= 64)
-typedef Tile<64, 64, 32, 32, 4> TileT;   // logits of few positions and a small vocabulary
+typedef Tile<64, 128, 32, 64, 3> TileN;
+typedef Tile<64, 64, 32, 32, 4> TileT;
+typedef Tile<128, 128, 32, 64, 3> TileM1;
 
 }  // namespace ttb

@@ -513,22 +513,26 @@ __global__ __launch_bounds__(256) void k_fill0(T *x, int64_t n) {
 
 // ---------------------------------------------------------------- plan
 // Which tiles, by the rounds they take on the CUs.  A round of 256 x 256 tiles (one per CU)
-// runs at about 1.45 PFLOP/s; 128 x 128 tiles do a fourth of that work at 0.67 of the rate
-// with two on every CU and at 0.45 with one (4096 x 4096 x 2048: 1407 TFLOP/s, against 1013
-// and 675 for the products of 512 and 256 small tiles).  So a last round of few large tiles
-// is cheaper in small ones: 784 tiles on 256 CUs take 3 + 0.55 rounds instead of 4.
+// runs at about 1.45 PFLOP/s; 128 x 128 tiles reach 1.03 with two on every CU and 0.86 with
+// one (the products 4096 x 2048 x 2048 and 2048 x 2048 x 2048: half a round and a fourth).  So
+// a last round of few large tiles is cheaper in small ones: 784 tiles on 256 CUs take 3 + 0.42
+// rounds instead of 4.
 int64_t large_tiles(int64_t along, int64_t across, int cus) {
   auto rounds = [&](int64_t n) { return (double)((n + cus - 1) / cus); };
   const int64_t keep = along * across / cus * cus / across;  // tiles of the whole rounds
   const int64_t small = 4 * (along - keep) * across;
-  const double cut = rounds(keep * across) + (small <= cus ? 0.55 : 0.73 * rounds((small + 1) / 2));
+  const double cut = rounds(keep * across) + (small <= cus ? 0.42 : 0.7 * rounds((small + 1) / 2));
   return cut + 0.05 < rounds(along * across) ? keep : along;
 }
 
-GemmShape gemm_shape(int64_t x, int64_t y) {
-  if (x <= 64 && y > 64) return {3, 64, 128};
-  if (y > 64) return {1, 128, 128};
-  return {2, 128, 64};
+// Smaller ones, so that few tiles still fill the CUs: 1024 x 1024 x 2048 runs at 0.23 PFLOP/s
+// in 64 tiles of 128 x 128, 0.24 in 128 of half that and 0.29 in 256 of a fourth.
+GemmShape gemm_shape(int64_t x, int64_t y, int cus) {
+  const int64_t m = ((x + 127) / 128) * ((y + 127) / 128);
+  if (y <= 64) return m > cus / 2 ? GemmShape{2, 128, 64} : GemmShape{4, 64, 64};
+  if (m <= cus / 4) return {4, 64, 64};
+  if (x <= 64 || m <= cus / 2) return {3, 64, 128};
+  return m <= cus ? GemmShape{5, 128, 128} : GemmShape{1, 128, 128};
 }
 
 // dh's tiles are few where positions and width are; the vocabulary is split then

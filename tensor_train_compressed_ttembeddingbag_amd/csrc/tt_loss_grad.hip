@@ -142,6 +142,8 @@ static hipError_t pick_dw(int cfg, const GemmArgs &g, const LossArgs &a, int64_t
   if (cfg == 0) return go_dw<E, TileL, O>(g, a, v0, nv, s);
   if (cfg == 1) return go_dw<E, TileM, O>(g, a, v0, nv, s);
   if (cfg == 3) return go_dw<E, TileN, O>(g, a, v0, nv, s);
+  if (cfg == 4) return go_dw<E, TileT, O>(g, a, v0, nv, s);
+  if (cfg == 5) return go_dw<E, TileM1, O>(g, a, v0, nv, s);
   return go_dw<E, TileS, O>(g, a, v0, nv, s);
 }
 
@@ -171,10 +173,7 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
     else e = pick_dw<Fp16, float>(t.cfg, g, a, v0 + r0, n, s);
   };
   part(0, large, {0, 256, 256});
-  // narrow tables have few tiles: half as many rows each where that leaves CUs idle
-  GemmShape rest = gemm_shape(a.D, nv - large);
-  if (rest.cfg == 1 && (a.D + 127) / 128 * ((nv - large + 127) / 128) <= a.cus) rest = {2, 128, 64};
-  part(large, nv - large, rest);
+  part(large, nv - large, gemm_shape(a.D, nv - large, a.cus));
   return e;
 }
 

@@ -162,6 +162,7 @@ static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const Logi
   if (cfg == 1) return go<E, TileM, PL, GRAD, MEND>(a, g, ep, s);
   if (cfg == 3) return go<E, TileN, PL, GRAD, MEND>(a, g, ep, s);
   if (cfg == 4) return go<E, TileT, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 5) return go<E, TileM1, PL, GRAD, MEND>(a, g, ep, s);
   return go<E, TileS, PL, GRAD, MEND>(a, g, ep, s);
 }
 
