@@ -80,7 +80,6 @@ struct GemmArgs {
   const int *kcount;    // device word that bounds K (rounded up to 64), or null
   const int *ycount;    // device word that bounds yn, or null
   int tx, ty, splits;   // tiles along x and y, pieces of k
-  const int *dsplits;   // device word: the pieces of k (over the tiles of ycount), or null
 };
 
 // ---------------------------------------------------------------- memory -> LDS
@@ -254,7 +253,7 @@ struct TileWalk {
     tx = a.tx;
     yn = a.ycount ? min(a.yn, *a.ycount) : a.yn;
     ty = min(a.ty, (yn + BY - 1) / BY);
-    splits = a.dsplits ? *a.dsplits : a.splits;
+    splits = a.splits;
     K = a.kcount ? (int64_t)((*a.kcount + GK - 1) / GK) * GK : a.K;
     kper = ((K + splits - 1) / splits + GK - 1) / GK * GK;
     total = tx * ty * splits;

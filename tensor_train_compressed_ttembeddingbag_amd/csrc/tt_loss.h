@@ -22,19 +22,19 @@ namespace ttb {
 constexpr int PACK_ROWS = 4;    // positions per block of k_pack
 constexpr int AMAX_BLOCKS = 1024;
 
-// scalars that the device works out, at the head of the workspace
+// scalars that the device works out in the forward
 struct LossScalars {
+  int count;       // positions that count
+  int ew, eh;      // exponents of the planes' scales, weight and hidden states (fp32; else 0)
   float zs;        // logits from sums of products: log2(e) / T over the planes' scales
-  float c_dh, c_dw;  // what the sums of the gradients are multiplied by
   int ticket;      // blocks of k_loss that are done
-  int splits;      // of the vocabulary in k_dhidden
 };
 
 // saved by the forward for the backward (one buffer, see saved_layout)
 struct LossSaved {
-  int *count;      // positions that count
-  int *exps;       // fp32: exponents of the planes' scales, weight and hidden states
+  LossScalars *sc;
   int *slot;       // [N] position -> packed row, or -1 - (a packed row of zeros)
+  char *hp;        // packed positions: [row][plane][Dp]
   int *tgt;        // [N] packed row -> target row of the weight (cross entropy)
   float *lse;      // [N] packed row -> lse in base 2
   int *eidx;       // [N][k] distillation entries: row of the weight or -1
@@ -64,13 +64,13 @@ struct LossArgs {
   int dh_bx, dh_by, cus;   // k_dhidden's tile, compute units
   LossSaved sv;
   // workspace
-  LossScalars *sc;
   float *amax;             // [2 * AMAX_BLOCKS] block maxima of |weight| and |hidden| (fp32)
-  char *hp, *wp;           // packed positions, packed piece of the weight: [row][plane][Dp]
+  char *wp;                // packed piece of the weight: [row][plane][Dp]
   float2 *part;            // [Npad][ptiles] (max, sum) in base 2
   float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)
   float *rowloss;          // [N]
-  float *rowf;             // [Npad] factor of a packed row's g
+  float *rowf;             // [Npad] factor of a packed row's g (a gradient per row; else null)
+  float *cm;               // what the factors were divided by
   char *G;                 // [Npad][planes][piece]
   int64_t ldG, Gplane;     // bytes
   float *dhp;              // [splits][tiles of positions that count][Dp]
@@ -78,33 +78,58 @@ struct LossArgs {
 
 constexpr int DH_SPLITS = 64 /* a lane each */, DH_TILES = 1024;  // most splits; most tiles where there are several
 
-// floats between two splits of dh
-__host__ __device__ inline int64_t dh_split_stride(const LossArgs &a, int count) {
-  return (int64_t)((count + a.dh_by - 1) / a.dh_by) * a.dh_by * a.Dp;
-}
-
 // Splits of the vocabulary in k_dhidden for `count` positions (known on the device only): the
 // number with the least estimated time.  A tile of 256 x 256 does 64 k in about 1.8 us on one
 // CU, the tiles come in rounds over the CUs (smaller tiles: two workgroups per CU, at half
 // the rate each), and each split's sums cost a write and a read at some 4 TB/s.
-__device__ __forceinline__ int dh_splits(const LossArgs &a, int count, int lane) {
-  const int tiles = (int)((a.D + a.dh_bx - 1) / a.dh_bx) * ((count + a.dh_by - 1) / a.dh_by);
-  const int K = (int)(a.piece < a.V ? a.piece : a.V), s = lane + 1;
-  const int slots = a.dh_bx == 256 ? a.cus : 2 * a.cus;
-  const float area = a.dh_bx * a.dh_by / 65536.f;
-  const float step = 1.8f * area * (a.planes > 1 ? 3.f : 1.f) * (a.dh_bx == 256 ? 1.f : 2.f);
+struct DhPlan {
+  int tx, bx, by, K, cus, planes;  // tiles along the width, tile, rows per piece, ...
+};
+__device__ __forceinline__ int dh_splits(const DhPlan &d, int count, int lane) {
+  const int tiles = d.tx * ((max(count, 1) + d.by - 1) / d.by), K = d.K, s = lane + 1;
+  const int slots = d.bx == 256 ? d.cus : 2 * d.cus;
+  const float area = d.bx * d.by / 65536.f;
+  const float step = 1.8f * area * (d.planes > 1 ? 3.f : 1.f) * (d.bx == 256 ? 1.f : 2.f);
   float t = (float)((s * tiles + slots - 1) / slots) * step * ((K + 64 * s - 1) / (64 * s)) +
             0.13f * s * tiles * area;
   if (s > 1 && (s * tiles > DH_TILES || K / s < 512)) t = INFINITY;
   float least = t;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) least = fminf(least, __shfl_xor(least, o));
-  return __ffsll((unsigned long long)__ballot(t == least));  // lane s - 1 holds s
+  // lane s - 1 holds s
+  return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(t == least)));
+}
+
+inline DhPlan dh_plan(const LossArgs &a) {
+  return {(int)((a.D + a.dh_bx - 1) / a.dh_bx), a.dh_bx, a.dh_by,
+          (int)(a.piece < a.V ? a.piece : a.V), a.cus, a.planes};
+}
+// floats between two splits of dh
+__device__ __forceinline__ int64_t dh_split_stride(int count, int by, int64_t ld) {
+  return (int64_t)((count + by - 1) / by) * by * ld;
 }
 
 // G is held times 2^14 in fp16 and times 2^32 in bf16: the matrix cores take subnormal inputs
 // as zeros, and small probabilities are most of a vocabulary (|g| <= 1 keeps both in range).
 __host__ __device__ inline int g_exp(int dtype) { return dtype == TT_DTYPE_BF16 ? 32 : 14; }
+
+// What the gradients' sums of products are multiplied by: the gradient of the loss (a mean's
+// over the positions that count; with a gradient per row, what the factors were divided by)
+// over the scales that G and the other operand carry.
+struct GradScale {
+  const float *up;
+  const LossScalars *sc;
+  float base;
+  int mean, gexp;
+  __device__ __forceinline__ float get(int e) const {
+    const float c = base * *up / (mean ? (float)max(sc->count, 1) : 1.f);
+    return ldexpf(c, -e - gexp);
+  }
+};
+inline GradScale grad_scale(const LossArgs &a) {
+  return {a.reduction == TT_REDUCE_NONE ? a.cm : a.up, a.sv.sc, a.k ? a.temp : 1.f,
+          a.reduction == TT_REDUCE_MEAN, g_exp(a.dtype)};
+}
 
 // tile shapes (x by y): 0 = 256 x 256, 1 = 128 x 128 for two on a CU, 2 = 128 x 64,
 // 3 = 64 x 128, 4 = 64 x 64, 5 = 128 x 128 for one on a CU
@@ -152,7 +177,7 @@ inline Operand weight_operand(const LossArgs &a, int64_t v0, int64_t nv) {
 }
 inline Operand hidden_operand(const LossArgs &a) {
   Operand o;
-  o.p = a.hp; o.ld = a.Dp * 2 * a.planes; o.plane = a.Dp * 2; o.rows = a.Npad; o.cols = a.Dp;
+  o.p = a.sv.hp; o.ld = a.Dp * 2 * a.planes; o.plane = a.Dp * 2; o.rows = a.Npad; o.cols = a.Dp;
   return o;
 }
 inline Operand g_operand(const LossArgs &a, int64_t nv) {

@@ -194,88 +194,63 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
 // the positions before its own by itself: N / 4 blocks read N / 2 flags on average, which
 // up to some 10^5 positions costs less than another launch to scan them.  The backward takes
 // the places from `saved`.
+// Rows of the hidden states that count, in order, from row 0 of hp on; the rest of hp's first N
+// rows are zeros (every position that does not count clears one of them; the backward sums
+// over the packed rows 64 at a time), and so are the rows from N to the next multiple of 64.
+// A block counts the positions before its own by itself: N / 4 blocks read N / 2 flags on
+// average, which up to some 10^5 positions costs less than another launch to scan them.
+// Rows of the hidden states that count, in order, from row 0 of hp on; the rest of hp's first N
+// rows are zeros (every position that does not count clears one of them; the backward sums
+// over the packed rows 64 at a time), and so are the rows from N to the next multiple of 64.
+// A block counts the positions before its own by itself: N / 4 blocks read N / 2 flags on
+// average, which up to some 10^5 positions costs less than another launch to scan them.
 template <class S, class E, int PL>
-__global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
+__global__ __launch_bounds__(256) void k_pack(LossArgs a) {
   __shared__ int s_n[4], s_slot[PACK_ROWS];
-  __shared__ float s_m[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t i0 = (int64_t)blockIdx.x * PACK_ROWS, ib = min(i0, a.N);
-  int base = 0;
-  float cm = 1.f;  // power of two that the factors of the rows are divided by
-  if (!grad) {
-    int n = 0;
-    for (int64_t i = tid; i < ib; i += 256) n += counts(a, i);
+  int n = 0;
+#pragma unroll 4
+  for (int64_t i = tid; i < ib; i += 256) n += counts(a, i);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    if (lane == 0) s_n[wv] = n;
-    __syncthreads();
-    base = s_n[0] + s_n[1] + s_n[2] + s_n[3];
-  } else if (a.reduction == TT_REDUCE_NONE && a.dtype != TT_DTYPE_BF16) {
-    // fp16 G: the largest factor is brought to 1, so 2^14 g fits and small factors keep bits
-    float m = 0.f;
-    for (int64_t i = tid; i < a.N; i += 256) {
-      const float u = fabsf(a.up[i]);
-      if (u < INFINITY && a.sv.slot[i] >= 0) m = fmaxf(m, u);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if (lane == 0) s_m[wv] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    if (m > 0.f) {
-      int e;
-      frexpf(m, &e);
-      cm = ldexpf(1.f, max(e, -120));
-    }
-  }
+  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+  if (lane == 0) s_n[wv] = n;
+  __syncthreads();
+  const int base = s_n[0] + s_n[1] + s_n[2] + s_n[3];
   int ew = 0, eh = 0;
   if (PL > 1) {
-    ew = grad ? a.sv.exps[0] : planes_exp(a.amax, lane);
-    eh = grad ? a.sv.exps[1] : planes_exp(a.amax + AMAX_BLOCKS, lane);
+    ew = planes_exp(a.amax, lane);
+    eh = planes_exp(a.amax + AMAX_BLOCKS, lane);
   }
   if (wv == 0) {
     const int64_t i = i0 + lane;
     const bool own = lane < PACK_ROWS, in = own && i < a.N;
-    int slot = (int)min<int64_t>(i, INT32_MAX);  // a row past the last position: zeros
-    if (grad) {
-      if (in) slot = a.sv.slot[i];
-      if (in && slot >= 0) a.rowf[slot] = a.reduction == TT_REDUCE_NONE ? a.up[i] / cm : 1.f;
-    } else {
-      const bool ok = in && counts(a, i);
-      const uint64_t mask = __ballot(ok);
-      const int rank = base + __popcll(mask & ((1ull << lane) - 1));
-      if (in) {
-        slot = ok ? rank : -1 - (int)(a.N - 1 - (i - rank));
-        a.sv.slot[i] = slot;
-        if (!a.k) {
-          const int64_t t = a.tgt[i];
-          if (ok) a.sv.tgt[rank] = (int)t;
-          else if (t != a.ignore) set_status(a.status, TT_DEV_BAD_INDEX);
-        }
-        if (i == a.N - 1) *a.sv.count = rank + ok;
+    const bool ok = in && counts(a, i);
+    const uint64_t mask = __ballot(ok);
+    const int rank = base + __popcll(mask & ((1ull << lane) - 1));
+    int slot = -1 - (int)i;  // a row past the last position: zeros
+    if (in) {
+      slot = ok ? rank : -1 - (int)(a.N - 1 - (i - rank));
+      a.sv.slot[i] = slot;
+      if (!a.k) {
+        const int64_t t = a.tgt[i];
+        if (ok) a.sv.tgt[rank] = (int)t;
+        else if (t != a.ignore) set_status(a.status, TT_DEV_BAD_INDEX);
       }
+      if (i == a.N - 1) a.sv.sc->count = rank + ok;
     }
-    if (own) s_slot[lane] = in ? slot : -1 - slot;
-    int splits = 1;
-    if (grad && blockIdx.x == 0) splits = dh_splits(a, max(*a.sv.count, 1), lane);
+    if (own) s_slot[lane] = slot;
     if (blockIdx.x == 0 && lane == 0) {
-      a.sc->zs = ldexpf(LOG2E / a.temp, -(ew + eh));
-      a.sc->ticket = 0;
-      if (!grad) a.sv.exps[0] = ew, a.sv.exps[1] = eh;
-      if (grad) {
-        float c = a.k ? a.temp : 1.f;
-        if (a.reduction == TT_REDUCE_NONE) c *= cm;
-        else c *= a.up[0] / (a.reduction == TT_REDUCE_MEAN ? (float)max(*a.sv.count, 1) : 1.f);
-        a.sc->splits = splits;
-        a.sc->c_dh = ldexpf(c, -ew - g_exp(a.dtype));
-        a.sc->c_dw = ldexpf(c, -eh - g_exp(a.dtype));
-      }
+      a.sv.sc->zs = ldexpf(LOG2E / a.temp, -(ew + eh));
+      a.sv.sc->ew = ew;
+      a.sv.sc->eh = eh;
+      a.sv.sc->ticket = 0;
     }
   }
   __syncthreads();
   const float scale = ldexpf(1.f, eh);
   const int cpr = (int)(a.Dp / 8);
-  const int64_t zero_to = grad ? ((int64_t)*a.sv.count + GK - 1) / GK * GK : 0;
+  const int64_t last = (a.N + GK - 1) / GK * GK;
   auto copy = [&](auto whole) {
     constexpr int U = 4;  // groups of eight in flight per thread
     for (int q0 = tid; q0 < PACK_ROWS * cpr; q0 += 256 * U) {
@@ -293,8 +268,8 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
         if (q >= PACK_ROWS * cpr) continue;
         const int slot = s_slot[r];
         const int64_t row = slot < 0 ? -1 - slot : slot;
-        if (slot < 0 && row >= zero_to) continue;
-        store8<S, E, PL>(v[u], scale, a.hp + (row * PL * a.Dp + c) * 2, a.Dp * 2);
+        if (row >= last) continue;
+        store8<S, E, PL>(v[u], scale, a.sv.hp + (row * PL * a.Dp + c) * 2, a.Dp * 2);
       }
     }
   };
@@ -305,7 +280,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a, int grad) {
 // rows [v0, v0 + nv) of the weight -> wp
 template <class S, class E, int PL>
 __global__ __launch_bounds__(256) void k_pack_w(LossArgs a, int64_t v0, int64_t nv) {
-  const float scale = PL > 1 ? ldexpf(1.f, a.sv.exps[0]) : 1.f;
+  const float scale = PL > 1 ? ldexpf(1.f, a.sv.sc->ew) : 1.f;
   const int64_t cpr = a.Dp / 8, n = nv * cpr, st = (int64_t)gridDim.x * 256;
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n; q += st) {
     const int64_t r = q / cpr, c = (q - r * cpr) * 8;
@@ -330,32 +305,32 @@ __device__ __forceinline__ void sum_rows(const LossArgs &a, double *s_d) {
   if (tid == 0) {
     d = 0.0;
     for (int w = 0; w < NT / 64; ++w) d += s_d[w];
-    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? d / max(*a.sv.count, 1) : d);
+    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? d / max(a.sv.sc->count, 1) : d);
   }
 }
 
-// One block per position: the tiles' statistics become its lse; the logits of its entries
-// are dot products of their own (fp32 sums of the inputs' products), a wave each.
-template <class S>
+// NW waves per position: the tiles' statistics become its lse; the logits of its entries are
+// dot products of their own (fp32 sums of the inputs' products), a wave each, U at once.
+template <class S, int NW, int U>
 __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   __shared__ float s_m[4], s_s[4], s_z[4], s_q[4];
   __shared__ double s_d[4];
   __shared__ int s_last;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int64_t i = blockIdx.x;
-  const int slot = a.sv.slot[i];
-  float out = 0.f;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, part = wv % NW;
+  const int64_t i = (int64_t)blockIdx.x * (4 / NW) + wv / NW;
+  const int slot = i < a.N ? a.sv.slot[i] : -1;
+  float out = 0.f, wm = -INFINITY, s = 0.f, z = 0.f, qz = 0.f;
   if (slot >= 0) {
     const float2 *p = a.part + (int64_t)slot * a.ptiles;
-    float m = -INFINITY, s = 0.f, z = 0.f;
-    for (int t = tid; t < a.ptiles; t += 256) {
+    float m = -INFINITY;
+    for (int t = part * 64 + lane; t < a.ptiles; t += 64 * NW) {
       const float2 v = p[t];
       const float n = fmaxf(m, v.x), n0 = n == -INFINITY ? 0.f : n;
       s = s * __builtin_amdgcn_exp2f(m - n0) + v.y * __builtin_amdgcn_exp2f(v.x - n0);
       m = n;
       if (a.smoothing > 0.f) z += a.zpart[(int64_t)slot * a.ptiles + t];
     }
-    float wm = m;
+    wm = m;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor(wm, o));
     s *= __builtin_amdgcn_exp2f(m - (wm == -INFINITY ? 0.f : wm));
@@ -364,16 +339,15 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
       s += __shfl_xor(s, o);
       z += __shfl_xor(z, o);
     }
-    float qz = 0.f;
     const int ne = a.k ? a.k : 1;
     const S *h = (const S *)a.hidden + i * a.hld;
-    // four entries at once: one read of the position's row, five loads in flight
-    for (int j0 = wv * 4; j0 < ne; j0 += 16) {
-      const S *w[4];
-      bool on[4];
-      float d[4];
+    // U entries: one read of the position's row, U + 1 loads in flight
+    for (int j0 = part * U; j0 < ne; j0 += U * NW) {
+      const S *w[U];
+      bool on[U];
+      float d[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int j = min(j0 + u, ne - 1), v = a.k ? a.sv.eidx[i * a.k + j] : a.sv.tgt[slot];
         on[u] = j0 + u < ne && v >= 0;
         w[u] = (const S *)a.weight + max(v, 0) * a.wld;  // no entry: any row, not counted
@@ -381,13 +355,13 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
       }
       auto dots = [&](auto whole) {
         for (int64_t c = lane * 8; c < a.D; c += 512) {
-          S x[8], y[4][8];
+          S x[8], y[U][8];
           load8_at<decltype(whole)::value>(h, c, a.D, true, x);
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < U; ++u)
             load8_at<decltype(whole)::value>(w[u], c, a.D, true, y[u]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[u] += (float)x[e] * (float)y[u][e];
         }
@@ -395,7 +369,7 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
       if (a.D % 8 == 0) dots(std::true_type());
       else dots(std::false_type());
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         if (!on[u]) continue;
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) d[u] += __shfl_xor(d[u], o);
@@ -408,41 +382,43 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
         }
       }
     }
+  }
+  if constexpr (NW > 1) {
     if (lane == 0) s_m[wv] = wm, s_s[wv] = s, s_z[wv] = z, s_q[wv] = qz;
     __syncthreads();
-    if (tid == 0) {
-      float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-      const float M0 = M == -INFINITY ? 0.f : M;
-      float sum = 0.f, zs = 0.f, q = 0.f;
-      for (int w = 0; w < 4; ++w) {
-        sum += s_s[w] * __builtin_amdgcn_exp2f(s_m[w] - M0);
-        zs += s_z[w];
-        q += s_q[w];
-      }
-      const float lse = M0 + log2f(sum);
-      a.sv.lse[slot] = lse;
-      if (a.k)
-        out = a.temp * a.temp * (a.sv.ent[i] + (lse - q) * LN2);
-      else
-        out = (lse - (1.f - a.smoothing) * q - a.smoothing * (zs / (float)a.V)) * LN2;
+    wm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    const float m0 = wm == -INFINITY ? 0.f : wm;
+    s = z = qz = 0.f;
+    for (int w = 0; w < 4; ++w) {
+      s += s_s[w] * __builtin_amdgcn_exp2f(s_m[w] - m0);
+      z += s_z[w];
+      qz += s_q[w];
     }
   }
+  const bool first = lane == 0 && part == 0 && i < a.N;
+  if (slot >= 0 && first) {
+    const float lse = (wm == -INFINITY ? 0.f : wm) + log2f(s);
+    a.sv.lse[slot] = lse;
+    if (a.k)
+      out = a.temp * a.temp * (a.sv.ent[i] + (lse - qz) * LN2);
+    else
+      out = (lse - (1.f - a.smoothing) * qz - a.smoothing * (z / (float)a.V)) * LN2;
+  }
   if (a.reduction == TT_REDUCE_NONE) {
-    if (tid == 0) a.loss[i] = out;
+    if (first) a.loss[i] = out;
     return;
   }
   if (!ticket) {
-    if (tid == 0) a.rowloss[i] = out;
+    if (first) a.rowloss[i] = out;
     return;
   }
-  // the block that ends last adds the rows up
-  if (tid == 0) {
-    // the row is written through to memory by its own scope; the ticket waits for that store
-    // alone (a fence would write back the XCD's whole L2, in every block)
-    __hip_atomic_store(&a.rowloss[i], out, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    vmem_drain();
-    s_last = atomicAdd(&a.sc->ticket, 1) == (int)gridDim.x - 1;
-  }
+  // The block that ends last adds the rows up.  A row is written through to memory by its own
+  // scope and the ticket waits for these stores alone (a fence would write back the XCD's
+  // whole L2, in every block).
+  if (first) __hip_atomic_store(&a.rowloss[i], out, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  vmem_drain();
+  __syncthreads();
+  if (tid == 0) s_last = atomicAdd(&a.sv.sc->ticket, 1) == (int)gridDim.x - 1;
   __syncthreads();
   if (s_last) sum_rows<256>(a, s_d);
 }
@@ -454,6 +430,38 @@ __global__ __launch_bounds__(1024) void k_loss_sum(LossArgs a) {
 }
 
 // ---------------------------------------------------------------- backward, around the products
+// With a gradient per position: the factor of every packed row's g.  G in fp16 needs |factor|
+// <= 1 (2^14 g fits, and small factors keep their bits), so the factors are divided by the
+// power of two above the largest finite one, which every block finds for itself.
+__global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
+  __shared__ float s_m[4];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  float cm = 1.f;
+  if (a.dtype != TT_DTYPE_BF16) {
+    float m = 0.f;
+#pragma unroll 4
+    for (int64_t i = tid; i < a.N; i += 256) {
+      const float u = fabsf(a.up[i]);
+      if (u < INFINITY && a.sv.slot[i] >= 0) m = fmaxf(m, u);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (lane == 0) s_m[wv] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    if (m > 0.f) {
+      int e;
+      frexpf(m, &e);
+      cm = ldexpf(1.f, max(e, -120));
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) *a.cm = cm;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < a.N; i += (int64_t)gridDim.x * 256) {
+    const int slot = a.sv.slot[i];
+    if (slot >= 0) a.rowf[slot] = a.up[i] / cm;
+  }
+}
+
 // G at the entries of this piece: (p - q) from the entry's own logit, rounded like the rest
 template <class E, int PL>
 __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64_t nv) {
@@ -465,7 +473,8 @@ __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64
   if (slot < 0 || a.sv.eidx[t] < 0 || v < 0 || v >= nv) return;
   const int x = g_exp(a.dtype);
   const float q = ldexpf(__builtin_amdgcn_exp2f(0.5f * (a.sv.ez[t] - a.sv.lse[slot])), x / 2);
-  const float g = (q * q - ldexpf(a.sv.eq[t], x)) * a.rowf[slot];
+  const float g = (q * q - ldexpf(a.sv.eq[t], x)) *
+                  (a.reduction == TT_REDUCE_NONE ? a.rowf[slot] : 1.f);
   char *o = a.G + slot * a.ldG + v * 2;
   const typename E::e h = (typename E::e)g;
   *(typename E::e *)o = h;
@@ -474,7 +483,10 @@ __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64
 
 // dh: the splits added in order, scaled, rounded once, put back at the position's row
 template <class O>
-__global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a) {
+__global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a, DhPlan plan, GradScale scale) {
+  const int count = a.sv.sc->count, ns = dh_splits(plan, count, threadIdx.x & 63);
+  const int64_t st = dh_split_stride(count, plan.by, a.Dp);
+  const float c_dh = scale.get(a.sv.sc->ew);
   const int per = (int)((a.D + 1023) / 1024);
   for (int64_t b = blockIdx.x; b < a.N * per; b += gridDim.x) {
   const int64_t i = b / per, c = ((b - i * per) * 256 + threadIdx.x) * 4;
@@ -483,11 +495,9 @@ __global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a) {
   f4 v = zero4();
   if (slot >= 0) {
     const float *p = a.dhp + (int64_t)slot * a.Dp + c;
-    const int64_t st = dh_split_stride(a, *a.sv.count);
-    const int ns = a.sc->splits;
 #pragma unroll 4
     for (int k = 0; k < ns; ++k) v += *(const f4 *)(p + k * st);
-    v *= a.sc->c_dh;
+    v *= c_dh;
   }
   O *o = (O *)a.dh + i * a.D + c;
   typedef O o4 __attribute__((ext_vector_type(4)));
@@ -563,8 +573,8 @@ struct Bump {
 
 static int64_t saved_layout(LossArgs &a, void *saved) {
   Bump b{(char *)saved};
-  b.take(a.sv.count, 1);
-  b.take(a.sv.exps, 2);
+  b.take(a.sv.sc, 1);
+  b.take(a.sv.hp, a.Npad * a.Dp * 2 * a.planes);
   b.take(a.sv.slot, a.N);
   b.take(a.sv.tgt, a.N);
   b.take(a.sv.lse, a.N);
@@ -581,9 +591,7 @@ static int64_t elem_size(int dtype) { return dtype == TT_DTYPE_F32 ? 4 : 2; }
 
 static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
   Bump b{(char *)ws};
-  b.take(a.sc, 1);
   b.take(a.amax, grad || a.planes == 1 ? 0 : 2 * AMAX_BLOCKS);
-  b.take(a.hp, a.Npad * a.Dp * 2 * a.planes);
   int64_t rows = a.V;
   const int64_t wrow = a.Dp * 2 * a.planes, grow = a.Npad * 2 * a.planes;
   int64_t lim = (1ll << 38) / std::max<int64_t>(a.Npad, 256);  // tiles of one launch
@@ -596,7 +604,8 @@ static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
   a.piece = rows;
   if (a.pack_w) b.take(a.wp, rows * wrow);
   if (grad) {
-    b.take(a.rowf, a.Npad);
+    b.take(a.cm, 1);
+    b.take(a.rowf, a.reduction == TT_REDUCE_NONE ? a.Npad : 0);
     a.Gplane = round_up(std::min(rows, a.V), 256) * 2;
     a.ldG = a.Gplane * a.planes;
     b.take(a.G, a.Npad * a.ldG);
@@ -648,9 +657,9 @@ static int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
 }
 
 template <class S, class E, int PL>
-static hipError_t pack_h(const LossArgs &a, int grad, hipStream_t s) {
+static hipError_t pack_h(const LossArgs &a, hipStream_t s) {
   tt_launch(K_LOSS_PACK, k_pack<S, E, PL>, dim3((unsigned)((a.Npad + PACK_ROWS - 1) / PACK_ROWS)),
-            dim3(256), 0, s, a, grad);
+            dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <class S, class E, int PL>
@@ -660,13 +669,13 @@ static hipError_t pack_w(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t 
             dim3(256), 0, s, a, v0, nv);
   return hipGetLastError();
 }
-static hipError_t launch_pack(const LossArgs &a, int grad, hipStream_t s) {
+static hipError_t launch_pack(const LossArgs &a, hipStream_t s) {
   if (a.dtype == TT_DTYPE_F32) {
-    if (!grad) tt_launch(K_LOSS_PACK, k_amax, dim3(2 * AMAX_BLOCKS), dim3(256), 0, s, a);
-    return pack_h<float, Fp16, 2>(a, grad, s);
+    tt_launch(K_LOSS_PACK, k_amax, dim3(2 * AMAX_BLOCKS), dim3(256), 0, s, a);
+    return pack_h<float, Fp16, 2>(a, s);
   }
-  if (a.dtype == TT_DTYPE_BF16) return pack_h<__bf16, Bf16, 1>(a, grad, s);
-  return pack_h<_Float16, Fp16, 1>(a, grad, s);
+  if (a.dtype == TT_DTYPE_BF16) return pack_h<__bf16, Bf16, 1>(a, s);
+  return pack_h<_Float16, Fp16, 1>(a, s);
 }
 static hipError_t launch_pack_w(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t s) {
   if (!a.pack_w) return hipSuccess;
@@ -689,12 +698,22 @@ static hipError_t launch_entries(const LossArgs &a, hipStream_t s) {
 // them), so more rows are added in a launch of its own (about 5 us).
 constexpr int64_t LOSS_TICKETS = 256;
 
+template <class S>
+static void launch_loss(const LossArgs &a, int ticket, hipStream_t s) {
+  // one entry and few statistics: a wave per position
+  if (!a.k && a.ptiles <= 256)
+    tt_launch(K_LOSS_ROWS, k_loss<S, 1, 1>, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, ticket);
+  else if (!a.k)
+    tt_launch(K_LOSS_ROWS, k_loss<S, 4, 1>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
+  else
+    tt_launch(K_LOSS_ROWS, k_loss<S, 4, 4>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
+}
+
 static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)a.N);
   const int ticket = a.N <= LOSS_TICKETS;
-  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_loss<float>, grid, dim3(256), 0, s, a, ticket);
-  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_loss<__bf16>, grid, dim3(256), 0, s, a, ticket);
-  else tt_launch(K_LOSS_ROWS, k_loss<_Float16>, grid, dim3(256), 0, s, a, ticket);
+  if (a.dtype == TT_DTYPE_F32) launch_loss<float>(a, ticket, s);
+  else if (a.dtype == TT_DTYPE_BF16) launch_loss<__bf16>(a, ticket, s);
+  else launch_loss<_Float16>(a, ticket, s);
   if (a.reduction != TT_REDUCE_NONE && !ticket)
     tt_launch(K_LOSS_ROWS, k_loss_sum, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
@@ -711,9 +730,9 @@ static hipError_t launch_entries_g(const LossArgs &a, int64_t v0, int64_t nv, hi
 
 static hipError_t launch_dhidden_out(const LossArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)std::min<int64_t>(a.N * ((a.D + 1023) / 1024), 1 << 20));
-  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_dhidden_out<float>, grid, dim3(256), 0, s, a);
-  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_dhidden_out<__bf16>, grid, dim3(256), 0, s, a);
-  else tt_launch(K_LOSS_ROWS, k_dhidden_out<_Float16>, grid, dim3(256), 0, s, a);
+  if (a.dtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_dhidden_out<float>, grid, dim3(256), 0, s, a, dh_plan(a), grad_scale(a));
+  else if (a.dtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_dhidden_out<__bf16>, grid, dim3(256), 0, s, a, dh_plan(a), grad_scale(a));
+  else tt_launch(K_LOSS_ROWS, k_dhidden_out<_Float16>, grid, dim3(256), 0, s, a, dh_plan(a), grad_scale(a));
   return hipGetLastError();
 }
 
@@ -764,7 +783,7 @@ int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *we
     return e == hipSuccess ? TT_OK : TT_EHIP;
   }
   if (a.k) e = launch_entries(a, s);
-  if (e == hipSuccess) e = launch_pack(a, 0, s);
+  if (e == hipSuccess) e = launch_pack(a, s);
   int tile0 = 0;
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
     const int64_t nv = std::min(a.piece, a.V - v0);
@@ -798,7 +817,11 @@ int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *w
     return e == hipSuccess ? TT_OK : TT_EHIP;
   }
   if (!grad_hidden && !grad_weight) return TT_OK;
-  e = launch_pack(a, 1, s);
+  if (a.reduction == TT_REDUCE_NONE) {
+    tt_launch(K_LOSS_ROWS, k_row_factors, dim3((unsigned)std::min<int64_t>((a.N + 255) / 256, 1024)),
+              dim3(256), 0, s, a);
+    e = hipGetLastError();
+  }
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
     const int64_t nv = std::min(a.piece, a.V - v0);
     e = launch_pack_w(a, v0, nv, s);

@@ -11,10 +11,11 @@ namespace ttb {
 
 template <class E, class T, int PL, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
-                                                   const int *count, int add) {
+                                                   DhPlan plan, int add) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int n = *count;
-  const int64_t split = (int64_t)((n + T::Y - 1) / T::Y) * T::Y * ld;
+  const int n = *a.ycount;
+  const int64_t split = dh_split_stride(n, T::Y, ld);
+  a.splits = dh_splits(plan, n, threadIdx.x & 63);
   gemm_tiles<E, T, PL, true, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int x = t.ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
@@ -38,13 +39,13 @@ template <class O>
 struct DwOut {
   O *out;             // dW of the piece's first row
   int64_t ld, nv;     // = D, rows of the piece
-  const LossScalars *sc;
+  GradScale scale;
 };
 
 template <class E, class T, class O>
 __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const float s = ep.sc->c_dw;
+  const float s = ep.scale.get(ep.scale.sc->eh);
   typedef O o4 __attribute__((ext_vector_type(4)));
   gemm_tiles<E, T, sizeof(O) / 2, true, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
@@ -92,7 +93,7 @@ static hipError_t go_dh(const GemmArgs &g, const LossArgs &a, int add, hipStream
   const hipError_t e = lds_limit<T>(&k_dhidden<E, T, PL, MEND>);
   if (e != hipSuccess) return e;
   tt_launch(K_LOSS_DH, k_dhidden<E, T, PL, MEND>, dim3(gemm_grid<T>(a, std::max(g.tx * g.ty, DH_TILES))), dim3(T::NT), T::LDS,
-            s, g, a.dhp, a.Dp, (const int *)a.sv.count, add);
+            s, g, a.dhp, a.Dp, dh_plan(a), add);
   return hipGetLastError();
 }
 
@@ -103,7 +104,7 @@ static hipError_t go_dw(const GemmArgs &g, const LossArgs &a, int64_t v0, int64_
   if (e != hipSuccess) return e;
   DwOut<O> ep;
   ep.out = (O *)a.dw + v0 * a.D;
-  ep.ld = a.D; ep.nv = nv; ep.sc = a.sc;
+  ep.ld = a.D; ep.nv = nv; ep.scale = grad_scale(a);
   tt_launch(K_LOSS_DW, k_dweight<E, T, O>, dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT), T::LDS, s, g, ep);
   return hipGetLastError();
 }
@@ -123,11 +124,10 @@ hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   g.K = (nv + GK - 1) / GK * GK;
   g.xn = (int)a.D;
   g.yn = (int)a.N;
-  g.ycount = a.sv.count;
+  g.ycount = &a.sv.sc->count;
   const GemmShape t = dh_shape(a);
   g.tx = (int)((a.D + t.bx - 1) / t.bx);
   g.ty = (int)((a.N + t.by - 1) / t.by);
-  g.dsplits = &a.sc->splits;
   const int add = v0 > 0;
   if (a.planes > 1) return pick_dh<Fp16, 2, false>(t.cfg, g, a, add, s);
   const bool mend = !a.pack_w && a.D % 2;
@@ -164,7 +164,7 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
     g.K = a.Npad;
     g.xn = (int)a.D;
     g.yn = (int)n;
-    g.kcount = a.sv.count;
+    g.kcount = &a.sv.sc->count;
       g.tx = (int)((a.D + t.bx - 1) / t.bx);
     g.ty = (int)((n + t.by - 1) / t.by);
     g.splits = 1;

@@ -11,7 +11,6 @@ namespace ttb {
 
 struct LogitsEpi {
   const LossScalars *sc;
-  const int *count;
   int64_t v0, nv;          // the piece
   float2 *part;
   float *zpart;
@@ -30,7 +29,7 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
   const float zs = ep.sc->zs;
-  const int count = *ep.count;
+  const int count = ep.sc->count;
   const int ix = t.ix, iy = t.iy;
   const int xl = (int)min<int64_t>(ep.nv - (int64_t)ix * T::X, T::X);  // rows of this tile
   const int xb = px + 4 * g;
@@ -103,7 +102,8 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
     for (int j = 0; j < T::NI; ++j) {
       const int pos = iy * T::Y + qy + 16 * j + c;
       const bool live = pos < count;
-      const float lse = live ? 0.5f * ep.lse[pos] : 0.f, f = live ? ep.rowf[pos] * ep.gs : 0.f;
+      const float lse = live ? 0.5f * ep.lse[pos] : 0.f, 
+                  f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * ep.gs : 0.f;
       const float ef = ep.e_v * f;
       const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
       const int d = live && ep.tgt ? (int)(ep.tgt[pos] - first) : -1;
@@ -178,11 +178,11 @@ static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
                          hipStream_t s) {
   LogitsEpi ep = {};
-  ep.sc = a.sc; ep.count = a.sv.count;
+  ep.sc = a.sv.sc;
   ep.part = a.part; ep.zpart = a.smoothing > 0.f ? a.zpart : nullptr;
   ep.ptiles = a.ptiles; ep.tile0 = tile0;
   ep.ldG = a.ldG; ep.Gplane = a.Gplane;
-  ep.lse = a.sv.lse; ep.rowf = a.rowf;
+  ep.lse = a.sv.lse; ep.rowf = a.reduction == TT_REDUCE_NONE ? a.rowf : nullptr;
   ep.tgt = a.k ? nullptr : a.sv.tgt;
   ep.gs = ldexpf(1.f, g_exp(a.dtype));
   ep.one_e = 1.f - a.smoothing;
@@ -200,7 +200,7 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     g.K = a.pack_w ? a.Dp : a.D;
     g.xn = (int)n;
     g.yn = (int)a.N;
-    g.ycount = a.sv.count;
+    g.ycount = &a.sv.sc->count;
     g.tx = (int)((n + t.bx - 1) / t.bx);
     g.ty = (int)((a.N + t.by - 1) / t.by);
     g.splits = 1;
