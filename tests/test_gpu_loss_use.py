@@ -1,0 +1,126 @@
+"""The vocabulary-head losses as a model uses them: through autograd with parameters, other
+index and teacher types, refused second derivatives, and the example that trains a TT embedding
+bag with both."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+from tensor_train_compressed_ttembeddingbag_amd import abi, loss as L
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _inputs(n=50, v=300, d=40, dt=torch.float32, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    h = torch.randn(n, d, device="cuda", generator=g).to(dt)
+    w = (torch.randn(v, d, device="cuda", generator=g) * d ** -0.5).to(dt)
+    t = torch.randint(0, v, (n,), device="cuda", generator=g)
+    return h, w, t
+
+
+def test_backward_through_a_layer_accumulates_into_parameters():
+    """dL/dx and dL/dW through linear_cross_entropy against torch's own layers in float64.
+    Bound: the loss's own error in its fp32 gradients (products of two rounded operands, 2^-21
+    of the sums' absolute terms) and one fp32 product behind it; 2^-17 of the largest entry is
+    16 times their sum."""
+    print("case layer", flush=True)
+    h, w, t = _inputs()
+    layer = torch.nn.Linear(40, 40, device="cuda")
+    head = torch.nn.Parameter(w.clone())
+    for _ in range(2):  # gradients add up
+        L.linear_cross_entropy(layer(h), head, t, reduction="none").sum().backward()
+    ref = torch.nn.Linear(40, 40, device="cuda", dtype=torch.float64)
+    ref.load_state_dict({k: x.double() for k, x in layer.state_dict().items()})
+    w64 = w.double().requires_grad_(True)
+    out = torch.nn.functional.cross_entropy(ref(h.double()) @ w64.t(), t, reduction="sum")
+    (2 * out).backward()
+    for a, b in ((head.grad, w64.grad), (layer.weight.grad, ref.weight.grad),
+                 (layer.bias.grad, ref.bias.grad)):
+        assert float((a.double() - b).abs().max() / b.abs().max()) <= 2.0 ** -17
+
+
+def test_int32_indices_and_other_teacher_types():
+    print("case types", flush=True)
+    h, w, t = _inputs(dt=torch.bfloat16)
+    a = L.linear_cross_entropy(h, w, t, reduction="none")
+    assert torch.equal(a, L.linear_cross_entropy(h, w, t.int(), reduction="none"))
+    idx = torch.stack([t, (t + 7) % 300], 1)
+    tl = torch.randn(50, 2, device="cuda")
+    for tdt in (torch.float32, torch.bfloat16, torch.float16):
+        x = tl.to(tdt)
+        b = L.linear_distillation(h, w, x, idx, temperature=1.5, reduction="none")
+        c = L.linear_distillation(h, w, x.float(), idx.int(), temperature=1.5, reduction="none")
+        assert torch.equal(b, c)
+
+
+def test_one_teacher_entry_is_cross_entropy():
+    """A teacher of one entry: KL divergence from a point mass is the cross entropy.  The two
+    take the same steps up to the order of one subtraction: 4 ulp of the terms."""
+    print("case point mass", flush=True)
+    h, w, t = _inputs(dt=torch.bfloat16)
+    a = L.linear_cross_entropy(h, w, t, reduction="none")
+    b = L.linear_distillation(h, w, torch.zeros(50, 1, device="cuda"), t[:, None],
+                              reduction="none")
+    assert float((a - b).abs().max()) <= 4 * 2.0 ** -23 * (1 + float(a.abs().max()))
+
+
+def test_second_derivatives_are_refused():
+    print("case second derivative", flush=True)
+    h, w, t = _inputs()
+    h.requires_grad_(True)
+    dh, = torch.autograd.grad(L.linear_cross_entropy(h, w, t), h, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dh.sum(), h)
+
+
+def test_gpu_refusals():
+    print("case refusals", flush=True)
+    h, w, t = _inputs()
+    with pytest.raises(TypeError, match="hidden is"):
+        L.linear_cross_entropy(h, w.bfloat16(), t)
+    with pytest.raises(TypeError, match="float32, bfloat16 or float16"):
+        L.linear_cross_entropy(h.double(), w.double(), t)
+    with pytest.raises(ValueError, match="rows of"):
+        L.linear_cross_entropy(h, w[:, :20], t)
+    with pytest.raises(ValueError, match="empty"):
+        L.linear_cross_entropy(h, w[:0], t)
+    with pytest.raises(TypeError, match="int64"):
+        L.linear_cross_entropy(h, w, t.float())
+    with pytest.raises(ValueError, match="a buffer is on"):
+        L.linear_cross_entropy(h, w, t.cpu())
+    with pytest.raises(ValueError, match="overlap"):
+        abi.make_loss_desc(h.as_strided((10, 40), (20, 1)), w)
+    with pytest.raises(TypeError, match="dev_status"):
+        L.linear_cross_entropy(h, w, t, dev_status=torch.zeros(1, device="cuda"))
+    desc = abi.make_loss_desc(h, w)
+    with pytest.raises(abi.TTError) as e:
+        abi.tt_loss_forward(desc, h, w, t, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == -3
+    with pytest.raises(ValueError, match="expected"):
+        abi.tt_loss_forward(desc, h, w, t[:-1])
+
+
+def test_abi_calls_match_the_public_functions():
+    print("case abi", flush=True)
+    h, w, t = _inputs(dt=torch.float16)
+    desc = abi.make_loss_desc(h, w, label_smoothing=0.1)
+    loss, saved = abi.tt_loss_forward(desc, h, w, t)
+    dh, dw = abi.tt_loss_backward(desc, h, w, saved, torch.ones(1, device="cuda"))
+    x, y = h.requires_grad_(True), w.requires_grad_(True)
+    out = L.linear_cross_entropy(x, y, t, label_smoothing=0.1)
+    gh, gw = torch.autograd.grad(out, (x, y))
+    assert torch.equal(loss[0], out.detach()) and torch.equal(dh, gh) and torch.equal(dw, gw)
+
+
+def test_example_trains():
+    print("case example", flush=True)
+    sp = importlib.util.spec_from_file_location("next_item",
+                                                os.path.join(ROOT, "examples", "next_item.py"))
+    m = importlib.util.module_from_spec(sp)
+    sp.loader.exec_module(m)
+    hard, soft = m.main(items=5000, steps=40, sessions=512)
+    assert hard[1] < 0.9 * hard[0] and soft[1] < 0.9 * soft[0]
