@@ -447,14 +447,21 @@ typedef struct tt_loss_desc {
     float temperature;                     /* > 0; 1 with cross entropy                 */
 } tt_loss_desc;
 
-/* Bytes of `saved` (written by the forward, read by the backward) and of the workspace of
- * one call (backward != 0: of the backward); `weight` because rows that do not start on 16
- * bytes are laid out anew, a piece at a time.  0: the descriptor is rejected. */
+#define TT_LOSS_FORWARD  0  /* of a forward that a backward follows */
+#define TT_LOSS_BACKWARD 1
+#define TT_LOSS_ONLY     2  /* of a forward with saved == NULL       */
+
+/* Bytes of `saved` (written by the forward, read by the backward: the positions that count,
+ * packed, and a few words for each) and of the workspace of one call.  The workspace is that
+ * of one piece of the vocabulary, whatever v is: at most 256 MiB each for the logits'
+ * gradient and for packed rows of the weight (fp32, or odd widths of many positions), beside
+ * fp32 sums of dhidden.  0: the descriptor is rejected. */
 size_t tt_loss_saved_size(const tt_loss_desc *desc);
-size_t tt_loss_workspace_size(const tt_loss_desc *desc, const void *weight, int backward);
+size_t tt_loss_workspace_size(const tt_loss_desc *desc, const void *weight, int mode);
 
 /* loss [n] (TT_REDUCE_NONE) or [1].  targets: int64 [n], or the teacher's indices int64
- * [n][k] with its logits [n][k].  saved and ws: 256-byte aligned. */
+ * [n][k] with its logits [n][k].  saved and ws: 256-byte aligned; saved may be NULL where no
+ * backward follows. */
 int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *weight,
                     const int64_t *targets, const void *teacher_logits, float *loss, void *saved,
                     size_t saved_bytes, void *ws, size_t ws_bytes, int32_t *dev_status,

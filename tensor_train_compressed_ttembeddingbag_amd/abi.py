@@ -39,6 +39,9 @@ TT_DTYPE_F16 = 2
 TT_REDUCE_NONE = 0
 TT_REDUCE_MEAN = 1
 TT_REDUCE_SUM = 2
+TT_LOSS_FORWARD = 0
+TT_LOSS_BACKWARD = 1
+TT_LOSS_ONLY = 2
 
 
 class TTError(RuntimeError):
@@ -1070,14 +1073,15 @@ def make_loss_desc(hidden: torch.Tensor, weight: torch.Tensor, k: int = 0,
 
 
 def tt_loss_sizes(desc: TTLossDesc, weight: torch.Tensor):
-    """(bytes of saved, of the forward's workspace, of the backward's)."""
+    """(bytes of saved, of the workspace of a forward, of a backward, of a forward alone)."""
     p = weight.data_ptr()
     key = (bytes(desc), p & 15)
     got = _loss_sizes.get(key)
     if got is None:
         L, r = lib(), ctypes.byref(desc)
-        got = (L.tt_loss_saved_size(r), L.tt_loss_workspace_size(r, p, 0),
-               L.tt_loss_workspace_size(r, p, 1))
+        got = (L.tt_loss_saved_size(r), L.tt_loss_workspace_size(r, p, TT_LOSS_FORWARD),
+               L.tt_loss_workspace_size(r, p, TT_LOSS_BACKWARD),
+               L.tt_loss_workspace_size(r, p, TT_LOSS_ONLY))
         if not got[0]:
             raise TTError("tt_loss_saved_size", -2)
         if len(_loss_sizes) > 4096:

@@ -59,6 +59,7 @@ struct LossArgs {
   int64_t Npad, Dp;        // packed rows and their pitch (elements)
   int planes;              // 2 for fp32
   int pack_w;              // the weight is packed too (fp32, odd widths)
+  int direct;              // loss alone, few positions: the hidden rows as they lie, all of them
   int64_t piece;           // rows of the weight per piece
   int ptiles;              // running statistics per position
   int dh_bx, dh_by, cus;   // k_dhidden's tile, compute units
@@ -177,6 +178,10 @@ inline Operand weight_operand(const LossArgs &a, int64_t v0, int64_t nv) {
 }
 inline Operand hidden_operand(const LossArgs &a) {
   Operand o;
+  if (a.direct) {
+    o.p = (const char *)a.hidden; o.ld = a.hld * 2; o.plane = 0; o.rows = a.N; o.cols = a.D;
+    return o;
+  }
   o.p = a.sv.hp; o.ld = a.Dp * 2 * a.planes; o.plane = a.Dp * 2; o.rows = a.Npad; o.cols = a.Dp;
   return o;
 }

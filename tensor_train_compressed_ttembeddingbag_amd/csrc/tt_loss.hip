@@ -291,11 +291,21 @@ __global__ __launch_bounds__(256) void k_pack_w(LossArgs a, int64_t v0, int64_t 
 }
 
 // ---------------------------------------------------------------- loss
+// packed row of a position, or below 0
+__device__ __forceinline__ int slot_of(const LossArgs &a, int64_t i) {
+  return a.direct ? (counts(a, i) ? (int)i : -1) : a.sv.slot[i];
+}
+
 // the rows' losses added in a fixed order, in fp64; NT threads, s_d: a double per wave
 template <int NT>
 __device__ __forceinline__ void sum_rows(const LossArgs &a, double *s_d) {
   const int tid = threadIdx.x;
   double d = 0.0;
+  int n = 0;
+  if (a.direct)  // at most 64 positions
+    n = __popcll(__ballot((tid & 63) < a.N && counts(a, tid & 63)));
+  else
+    n = a.sv.sc->count;
   for (int64_t r = tid; r < a.N; r += NT)
     d += (double)__hip_atomic_load(&a.rowloss[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
@@ -305,7 +315,7 @@ __device__ __forceinline__ void sum_rows(const LossArgs &a, double *s_d) {
   if (tid == 0) {
     d = 0.0;
     for (int w = 0; w < NT / 64; ++w) d += s_d[w];
-    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? d / max(a.sv.sc->count, 1) : d);
+    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? d / max(n, 1) : d);
   }
 }
 
@@ -318,7 +328,9 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, part = wv % NW;
   const int64_t i = (int64_t)blockIdx.x * (4 / NW) + wv / NW;
-  const int slot = i < a.N ? a.sv.slot[i] : -1;
+  const int slot = i < a.N ? slot_of(a, i) : -1;
+  if (a.direct && !a.k && slot < 0 && i < a.N && lane == 0 && a.tgt[i] != a.ignore)
+    set_status(a.status, TT_DEV_BAD_INDEX);
   float out = 0.f, wm = -INFINITY, s = 0.f, z = 0.f, qz = 0.f;
   if (slot >= 0) {
     const float2 *p = a.part + (int64_t)slot * a.ptiles;
@@ -348,7 +360,8 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
       float d[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int j = min(j0 + u, ne - 1), v = a.k ? a.sv.eidx[i * a.k + j] : a.sv.tgt[slot];
+        const int j = min(j0 + u, ne - 1), v = a.k ? a.sv.eidx[i * a.k + j]
+                          : a.direct ? (int)a.tgt[i] : a.sv.tgt[slot];
         on[u] = j0 + u < ne && v >= 0;
         w[u] = (const S *)a.weight + max(v, 0) * a.wld;  // no entry: any row, not counted
         d[u] = 0.f;
@@ -574,7 +587,7 @@ struct Bump {
 static int64_t saved_layout(LossArgs &a, void *saved) {
   Bump b{(char *)saved};
   b.take(a.sv.sc, 1);
-  b.take(a.sv.hp, a.Npad * a.Dp * 2 * a.planes);
+  if (!a.direct) b.take(a.sv.hp, a.Npad * a.Dp * 2 * a.planes);
   b.take(a.sv.slot, a.N);
   b.take(a.sv.tgt, a.N);
   b.take(a.sv.lse, a.N);
@@ -589,8 +602,16 @@ static int64_t saved_layout(LossArgs &a, void *saved) {
 
 static int64_t elem_size(int dtype) { return dtype == TT_DTYPE_F32 ? 4 : 2; }
 
-static int64_t ws_layout(LossArgs &a, void *ws, bool grad) {
+// mode: TT_LOSS_FORWARD, _BACKWARD or _ONLY (what is saved otherwise is in the workspace then)
+static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
+  const bool grad = mode == TT_LOSS_BACKWARD;
   Bump b{(char *)ws};
+  if (mode == TT_LOSS_ONLY) {
+    // up to 64 positions fill one tile whether they count or not: nothing to pack, if whole
+    // 16-byte groups make up their rows
+    a.direct = a.N <= 64 && a.D % 8 == 0 && a.planes == 1;
+    b.off = saved_layout(a, ws);
+  }
   b.take(a.amax, grad || a.planes == 1 ? 0 : 2 * AMAX_BLOCKS);
   int64_t rows = a.V;
   const int64_t wrow = a.Dp * 2 * a.planes, grow = a.Npad * 2 * a.planes;
@@ -710,7 +731,7 @@ static void launch_loss(const LossArgs &a, int ticket, hipStream_t s) {
 }
 
 static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
-  const int ticket = a.N <= LOSS_TICKETS;
+  const int ticket = a.N <= LOSS_TICKETS && !a.direct;  // (k_pack clears the ticket)
   if (a.dtype == TT_DTYPE_F32) launch_loss<float>(a, ticket, s);
   else if (a.dtype == TT_DTYPE_BF16) launch_loss<__bf16>(a, ticket, s);
   else launch_loss<_Float16>(a, ticket, s);
@@ -755,9 +776,10 @@ size_t tt_loss_saved_size(const tt_loss_desc *desc) {
   return loss_args(desc, nullptr, a) == TT_OK ? (size_t)saved_layout(a, nullptr) : 0;
 }
 
-size_t tt_loss_workspace_size(const tt_loss_desc *desc, const void *weight, int backward) {
+size_t tt_loss_workspace_size(const tt_loss_desc *desc, const void *weight, int mode) {
   LossArgs a;
-  return loss_args(desc, weight, a) == TT_OK ? (size_t)ws_layout(a, nullptr, backward != 0) : 0;
+  if (mode < TT_LOSS_FORWARD || mode > TT_LOSS_ONLY) return 0;
+  return loss_args(desc, weight, a) == TT_OK ? (size_t)ws_layout(a, nullptr, mode) : 0;
 }
 
 int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *weight,
@@ -767,13 +789,13 @@ int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *we
   LossArgs a;
   const int rc = loss_args(desc, weight, a);
   if (rc != TT_OK) return rc;
-  if (!weight || !saved || !ws) return TT_EINVAL;
+  if (!weight || !ws) return TT_EINVAL;
   if (!loss && (a.N || a.reduction != TT_REDUCE_NONE)) return TT_EINVAL;
   if (a.N && (!hidden || !targets || (a.k && !teacher_logits))) return TT_EINVAL;
   if ((uintptr_t)weight % elem_size(a.dtype) || (uintptr_t)hidden % elem_size(a.dtype)) return TT_EINVAL;
   if ((uintptr_t)saved % 256 || (uintptr_t)ws % 256) return TT_EWORKSPACE;
-  if ((size_t)saved_layout(a, saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)ws_layout(a, ws, false) > ws_bytes) return TT_EWORKSPACE;
+  if (saved && (size_t)saved_layout(a, saved) > saved_bytes) return TT_EWORKSPACE;
+  if ((size_t)ws_layout(a, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY) > ws_bytes) return TT_EWORKSPACE;
   a.hidden = hidden; a.tgt = targets; a.tlogits = teacher_logits; a.loss = loss;
   a.status = dev_status;
   hipStream_t s = (hipStream_t)stream;
@@ -783,7 +805,7 @@ int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *we
     return e == hipSuccess ? TT_OK : TT_EHIP;
   }
   if (a.k) e = launch_entries(a, s);
-  if (e == hipSuccess) e = launch_pack(a, s);
+  if (e == hipSuccess && !a.direct) e = launch_pack(a, s);
   int tile0 = 0;
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
     const int64_t nv = std::min(a.piece, a.V - v0);
@@ -808,7 +830,7 @@ int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *w
     return TT_EINVAL;
   if ((uintptr_t)saved % 256 || (uintptr_t)ws % 256) return TT_EWORKSPACE;
   if ((size_t)saved_layout(a, (void *)saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)ws_layout(a, ws, true) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)ws_layout(a, ws, TT_LOSS_BACKWARD) > ws_bytes) return TT_EWORKSPACE;
   a.hidden = hidden; a.up = grad_loss; a.dh = grad_hidden; a.dw = grad_weight;
   hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;

@@ -10,7 +10,9 @@
 namespace ttb {
 
 struct LogitsEpi {
-  const LossScalars *sc;
+  const LossScalars *sc;   // null: n positions and the scale zs
+  int n;
+  float zs;
   int64_t v0, nv;          // the piece
   float2 *part;
   float *zpart;
@@ -28,8 +30,8 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   gemm_tiles<E, T, PL, false, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
   const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
-  const float zs = ep.sc->zs;
-  const int count = ep.sc->count;
+  const float zs = ep.sc ? ep.sc->zs : ep.zs;
+  const int count = ep.sc ? ep.sc->count : ep.n;
   const int ix = t.ix, iy = t.iy;
   const int xl = (int)min<int64_t>(ep.nv - (int64_t)ix * T::X, T::X);  // rows of this tile
   const int xb = px + 4 * g;
@@ -178,7 +180,9 @@ static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
                          hipStream_t s) {
   LogitsEpi ep = {};
-  ep.sc = a.sv.sc;
+  ep.sc = a.direct ? nullptr : a.sv.sc;
+  ep.n = (int)a.N;
+  ep.zs = 1.4426950408889634f / a.temp;
   ep.part = a.part; ep.zpart = a.smoothing > 0.f ? a.zpart : nullptr;
   ep.ptiles = a.ptiles; ep.tile0 = tile0;
   ep.ldG = a.ldG; ep.Gplane = a.Gplane;
@@ -200,7 +204,7 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     g.K = a.pack_w ? a.Dp : a.D;
     g.xn = (int)n;
     g.yn = (int)a.N;
-    g.ycount = &a.sv.sc->count;
+    g.ycount = a.direct ? nullptr : &a.sv.sc->count;
     g.tx = (int)((n + t.bx - 1) / t.bx);
     g.ty = (int)((a.N + t.by - 1) / t.by);
     g.splits = 1;

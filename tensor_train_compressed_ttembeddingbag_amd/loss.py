@@ -27,7 +27,7 @@ class _Plan:
 
     def __init__(self, hidden, weight, k, reduction, kw):
         self.desc = abi.make_loss_desc(hidden, weight, k=k, reduction=_REDUCTION[reduction], **kw)
-        self.saved, self.fwd, self.bwd = abi.tt_loss_sizes(self.desc, weight)
+        self.saved, self.fwd, self.bwd, self.only = abi.tt_loss_sizes(self.desc, weight)
         self.ref = ctypes.byref(self.desc)
         self.dtype = hidden.dtype
         self.n, self.d = hidden.shape
@@ -44,14 +44,16 @@ def _bytes(n: int, device) -> torch.Tensor:
 # What abi.tt_loss_forward and tt_loss_backward check of every buffer is known here by
 # construction, so the two calls go to the library directly: a small loss is bound by the
 # host, and the checks were a third of its calls.
-def _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status):
+def _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status, save):
     dev = hidden.device
     loss = torch.empty(shape, dtype=torch.float32, device=dev)
-    saved, ws = _bytes(plan.saved, dev), _bytes(plan.fwd, dev)
+    saved = _bytes(plan.saved, dev) if save else None
+    size = plan.fwd if save else plan.only
+    ws = _bytes(size, dev)
     rc = abi.lib().tt_loss_forward(
         plan.ref, hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(),
         None if teacher_logits is None else teacher_logits.data_ptr(), loss.data_ptr(),
-        saved.data_ptr(), plan.saved, ws.data_ptr(), plan.fwd,
+        saved.data_ptr() if save else None, plan.saved, ws.data_ptr(), size,
         None if dev_status is None else dev_status.data_ptr(), abi._stream(None, hidden))
     if rc:
         raise abi.TTError("tt_loss_forward", rc)
@@ -81,7 +83,8 @@ _backward_once = torch.autograd.function.once_differentiable(_backward)
 class _LossFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, plan, targets, teacher_logits, shape, dev_status):
-        loss, saved = _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status)
+        loss, saved = _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status,
+                               True)
         ctx.plan = plan
         ctx.save_for_backward(hidden, weight, saved)
         return loss
@@ -126,7 +129,7 @@ def _loss(hidden, weight, targets, teacher_logits, shape, k, reduction, dev_stat
     if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
         return _LossFunction.apply(hidden, weight, plan, targets, teacher_logits, shape,
                                    dev_status)
-    return _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status)[0]
+    return _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status, False)[0]
 
 
 def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,

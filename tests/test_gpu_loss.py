@@ -404,3 +404,36 @@ def test_captured_calls(n):
         torch.cuda.synchronize()
         ref = run(h, w, "mean", one, targets=t)
         assert torch.equal(loss[0], ref[0]) and torch.equal(dh, ref[1]) and torch.equal(dw, ref[2])
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("n,d", [(1, 64), (5, 200), (64, 72), (63, 67), (64, 8), (65, 64)])
+def test_loss_alone(n, d, op):
+    """Without gradients the loss takes a shorter path for few positions; its values stay
+    within the same bound, ignored rows (NaN in them) and flagged ones included."""
+    print("case loss alone", n, d, op, flush=True)
+    v = 500
+    h, w, t, g = make(n, v, d, "bf16", seed=n + d)
+    if n > 2:
+        t[1] = IGN
+        h[1] = float("nan")
+    tl, idx = teacher(n, v, 6, g, torch.bfloat16)
+    if n > 2:
+        idx[1] = -1
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for red in ("none", "mean", "sum"):
+        up = torch.ones(n if red == "none" else (), device="cuda")
+        if op == "xent":
+            got = L.linear_cross_entropy(h, w, t, label_smoothing=0.1, reduction=red,
+                                         dev_status=st)
+            want = definition(torch.nan_to_num(h), w, "bf16", red, up, targets=t, e=0.1)[0]
+        else:
+            got = L.linear_distillation(h, w, tl, idx, temperature=2.0, reduction=red,
+                                        dev_status=st)
+            want = definition(torch.nan_to_num(h), w, "bf16", red, up, tl=tl, idx=idx, T=2.0)[0]
+        check(got, want, red)
+    assert int(st) == 0
+    if op == "xent" and n > 2:
+        t[0] = v
+        got = L.linear_cross_entropy(h, w, t, reduction="none", dev_status=st)
+        assert int(st) == abi.TT_DEV_BAD_INDEX and float(got[0]) == 0 and float(got[1]) == 0

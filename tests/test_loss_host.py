@@ -56,13 +56,16 @@ def test_bad_pointers_and_workspaces():
             a[int(k[1:])] = x
         return lib.tt_loss_forward(ref, *a)
 
-    for i in (0, 1, 2, 4, 5, 7):
+    for i in (0, 1, 2, 4, 7):
         assert fwd(r, **{"a%d" % i: None}) == -1, i
     assert fwd(rk, a3=None) == -1
     assert fwd(r, a0=FAKE + 1) == -1 and fwd(r, a1=FAKE + 1) == -1
     assert fwd(r, a5=FAKE + 16) == -3 and fwd(r, a7=FAKE + 16) == -3
     assert fwd(r, a6=lib.tt_loss_saved_size(r) - 1) == -3
     assert fwd(r, a8=lib.tt_loss_workspace_size(r, FAKE, 0) - 1) == -3
+    # without saved the workspace is another one
+    assert fwd(r, a5=None, a6=0, a8=lib.tt_loss_workspace_size(r, FAKE, 2) - 1) == -3
+    assert lib.tt_loss_workspace_size(r, FAKE, 3) == 0
     assert lib.tt_loss_forward(None, *args) == -1
 
     bargs = [FAKE, FAKE, FAKE, big, FAKE, FAKE, FAKE, FAKE, big, None]
