@@ -59,6 +59,8 @@ struct LossArgs {
   int64_t Npad, Dp;        // packed rows and their pitch (elements)
   int planes;              // 2 for fp32
   int pack_w;              // the weight is packed too (fp32, odd widths)
+  int twin;                // 16-bit, up to 32 positions: G's rows are followed, twin rows on, by
+                           // what their rounding left (hp's by themselves); else 0
   int direct;              // loss alone, few positions: the hidden rows as they lie, all of them
   int64_t piece;           // rows of the weight per piece
   int ptiles;              // running statistics per position
@@ -73,7 +75,7 @@ struct LossArgs {
   float *rowf;             // [Npad] factor of a packed row's g (a gradient per row; else null)
   float *cm;               // what the factors were divided by
   char *G;                 // [Npad][planes][piece]
-  int64_t ldG, Gplane;     // bytes
+  int64_t ldG, Gplane;     // bytes; Gplane: to the second part of a row of G (plane or twin)
   float *dhp;              // [splits][tiles of positions that count][Dp]
 };
 
@@ -101,6 +103,8 @@ __device__ __forceinline__ int dh_splits(const DhPlan &d, int count, int lane) {
   return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(t == least)));
 }
 
+// rows of G that k_dhidden takes
+inline int64_t dh_rows(const LossArgs &a) { return a.twin ? 2 * a.twin : a.N; }
 inline DhPlan dh_plan(const LossArgs &a) {
   return {(int)((a.D + a.dh_bx - 1) / a.dh_bx), a.dh_bx, a.dh_by,
           (int)(a.piece < a.V ? a.piece : a.V), a.cus, a.planes};

@@ -250,7 +250,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
   __syncthreads();
   const float scale = ldexpf(1.f, eh);
   const int cpr = (int)(a.Dp / 8);
-  const int64_t last = (a.N + GK - 1) / GK * GK;
+  const int64_t last = a.twin ? a.twin : (a.N + GK - 1) / GK * GK;
   auto copy = [&](auto whole) {
     constexpr int U = 4;  // groups of eight in flight per thread
     for (int q0 = tid; q0 < PACK_ROWS * cpr; q0 += 256 * U) {
@@ -269,7 +269,9 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
         const int slot = s_slot[r];
         const int64_t row = slot < 0 ? -1 - slot : slot;
         if (row >= last) continue;
-        store8<S, E, PL>(v[u], scale, a.sv.hp + (row * PL * a.Dp + c) * 2, a.Dp * 2);
+        char *o = a.sv.hp + (row * PL * a.Dp + c) * 2;
+        store8<S, E, PL>(v[u], scale, o, a.Dp * 2);
+        if (PL == 1 && a.twin) store8<S, E, PL>(v[u], scale, o + a.twin * a.Dp * 2, 0);
       }
     }
   };
@@ -491,14 +493,15 @@ __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64
   char *o = a.G + slot * a.ldG + v * 2;
   const typename E::e h = (typename E::e)g;
   *(typename E::e *)o = h;
-  if (PL > 1) *(typename E::e *)(o + a.Gplane) = (typename E::e)(g - (float)h);
+  if (PL > 1 || a.twin) *(typename E::e *)(o + a.Gplane) = (typename E::e)(g - (float)h);
 }
 
 // dh: the splits added in order, scaled, rounded once, put back at the position's row
 template <class O>
 __global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a, DhPlan plan, GradScale scale) {
-  const int count = a.sv.sc->count, ns = dh_splits(plan, count, threadIdx.x & 63);
-  const int64_t st = dh_split_stride(count, plan.by, a.Dp);
+  const int rows = a.twin ? 2 * a.twin : a.sv.sc->count;
+  const int ns = dh_splits(plan, rows, threadIdx.x & 63);
+  const int64_t st = dh_split_stride(rows, plan.by, a.Dp);
   const float c_dh = scale.get(a.sv.sc->ew);
   const int per = (int)((a.D + 1023) / 1024);
   for (int64_t b = blockIdx.x; b < a.N * per; b += gridDim.x) {
@@ -510,6 +513,12 @@ __global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a, DhPlan plan, Gr
     const float *p = a.dhp + (int64_t)slot * a.Dp + c;
 #pragma unroll 4
     for (int k = 0; k < ns; ++k) v += *(const f4 *)(p + k * st);
+    if (a.twin) {
+      f4 w = zero4();
+#pragma unroll 4
+      for (int k = 0; k < ns; ++k) w += *(const f4 *)(p + a.twin * a.Dp + k * st);
+      v += w;
+    }
     v *= c_dh;
   }
   O *o = (O *)a.dh + i * a.D + c;
@@ -560,11 +569,11 @@ GemmShape gemm_shape(int64_t x, int64_t y, int cus) {
 
 // dh's tiles are few where positions and width are; the vocabulary is split then
 GemmShape dh_shape(const LossArgs &a) {
-  const int64_t big = ((a.D + 255) / 256) * ((a.N + 255) / 256);
-  if (a.N > 128 && a.D > 128 && big * std::min<int64_t>(DH_SPLITS, a.piece / 512) >= 128)
+  const int64_t rows = dh_rows(a), big = ((a.D + 255) / 256) * ((rows + 255) / 256);
+  if (rows > 128 && a.D > 128 && big * std::min<int64_t>(DH_SPLITS, a.piece / 512) >= 128)
     return {0, 256, 256};
-  if (a.D <= 64 && a.N > 64) return {3, 64, 128};
-  return a.N > 64 ? GemmShape{1, 128, 128} : GemmShape{2, 128, 64};
+  if (a.D <= 64 && rows > 64) return {3, 64, 128};
+  return rows > 64 ? GemmShape{1, 128, 128} : GemmShape{2, 128, 64};
 }
 
 // Memory for one piece of the vocabulary: G of every position, and the packed weight.  256
@@ -629,10 +638,11 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     b.take(a.rowf, a.reduction == TT_REDUCE_NONE ? a.Npad : 0);
     a.Gplane = round_up(std::min(rows, a.V), 256) * 2;
     a.ldG = a.Gplane * a.planes;
+    if (a.twin) a.Gplane = a.twin * a.ldG;
     b.take(a.G, a.Npad * a.ldG);
     const GemmShape t = dh_shape(a);
     a.dh_bx = t.bx; a.dh_by = t.by;
-    const int64_t ty = (a.N + t.by - 1) / t.by, tx = (a.D + t.bx - 1) / t.bx;
+    const int64_t ty = (dh_rows(a) + t.by - 1) / t.by, tx = (a.D + t.bx - 1) / t.bx;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(DH_SPLITS, rows / 512));
     b.take(a.dhp, std::max(ty, std::min<int64_t>(DH_TILES / tx, most * ty)) * t.by * a.Dp);
   } else {
@@ -669,6 +679,10 @@ static int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
   a.Dp = round_up(a.D, 64);
   a.planes = a.dtype == TT_DTYPE_F32 ? 2 : 1;
   a.cus = std::max(device_cus(), 1);
+  // G rounded to 16 bits adds to the gradients' error as much as their own rounding does where
+  // many roundings average out, and half as much again where few do.  Up to 32 positions a
+  // tile of 64 has room for what the rounding left.
+  a.twin = a.planes == 1 && a.N <= 32 ? 32 : 0;
   // 16-bit rows of odd length are read as they lie, and the last tile of k is put right in LDS
   // for every tile of positions; where positions are many for the width, packing the weight
   // is cheaper (1294 x 99003 x 1389: 1205 us as they lie, 1420 packed; 3855 x 41825 x 124:

@@ -13,7 +13,7 @@ template <class E, class T, int PL, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
                                                    DhPlan plan, int add) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int n = *a.ycount;
+  const int n = a.ycount ? *a.ycount : a.yn;
   const int64_t split = dh_split_stride(n, T::Y, ld);
   a.splits = dh_splits(plan, n, threadIdx.x & 63);
   gemm_tiles<E, T, PL, true, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
@@ -123,11 +123,11 @@ hipError_t launch_dhidden(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
   g.Q = g_operand(a, nv);
   g.K = (nv + GK - 1) / GK * GK;
   g.xn = (int)a.D;
-  g.yn = (int)a.N;
-  g.ycount = &a.sv.sc->count;
+  g.yn = (int)dh_rows(a);
+  g.ycount = a.twin ? nullptr : &a.sv.sc->count;
   const GemmShape t = dh_shape(a);
   g.tx = (int)((a.D + t.bx - 1) / t.bx);
-  g.ty = (int)((a.N + t.by - 1) / t.by);
+  g.ty = (int)((dh_rows(a) + t.by - 1) / t.by);
   const int add = v0 > 0;
   if (a.planes > 1) return pick_dh<Fp16, 2, false>(t.cfg, g, a, add, s);
   const bool mend = !a.pack_w && a.D % 2;
@@ -164,7 +164,7 @@ hipError_t launch_dweight(const LossArgs &a, int64_t v0, int64_t nv, hipStream_t
     g.K = a.Npad;
     g.xn = (int)a.D;
     g.yn = (int)n;
-    g.kcount = &a.sv.sc->count;
+    g.kcount = a.twin ? nullptr : &a.sv.sc->count;
       g.tx = (int)((a.D + t.bx - 1) / t.bx);
     g.ty = (int)((n + t.by - 1) / t.by);
     g.splits = 1;

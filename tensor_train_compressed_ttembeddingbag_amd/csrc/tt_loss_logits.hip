@@ -21,6 +21,7 @@ struct LogitsEpi {
   int64_t ldG, Gplane;
   const float *lse, *rowf;
   const int *tgt;          // null with distillation
+  int twin;
   float one_e, e_v, gs;    // 1 - e, e / V, G's factor 2^g_exp
 };
 
@@ -104,6 +105,7 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
     for (int j = 0; j < T::NI; ++j) {
       const int pos = iy * T::Y + qy + 16 * j + c;
       const bool live = pos < count;
+      if (ep.twin && qy + 16 * j >= ep.twin) continue;
       const float lse = live ? 0.5f * ep.lse[pos] : 0.f, 
                   f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * ep.gs : 0.f;
       const float ef = ep.e_v * f;
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
           for (int r = 0; r < 4; ++r) l[u][r] = (typename E::e)(v[r] - (float)h[u][r]);
         }
         store_pair(o + 32 * i0, h[0], h[1], g);
-        if constexpr (PL > 1) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
+        if (PL > 1 || ep.twin) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
       }
     }
   }
@@ -185,6 +187,7 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.zs = 1.4426950408889634f / a.temp;
   ep.part = a.part; ep.zpart = a.smoothing > 0.f ? a.zpart : nullptr;
   ep.ptiles = a.ptiles; ep.tile0 = tile0;
+  ep.twin = a.twin;
   ep.ldG = a.ldG; ep.Gplane = a.Gplane;
   ep.lse = a.sv.lse; ep.rowf = a.reduction == TT_REDUCE_NONE ? a.rowf : nullptr;
   ep.tgt = a.k ? nullptr : a.sv.tgt;
@@ -204,7 +207,8 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     g.K = a.pack_w ? a.Dp : a.D;
     g.xn = (int)n;
     g.yn = (int)a.N;
-    g.ycount = a.direct ? nullptr : &a.sv.sc->count;
+    // twin rows of G are used whole, so all are written
+    g.ycount = a.direct || (grad && a.twin) ? nullptr : &a.sv.sc->count;
     g.tx = (int)((n + t.bx - 1) / t.bx);
     g.ty = (int)((a.N + t.by - 1) / t.by);
     g.splits = 1;

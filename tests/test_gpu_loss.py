@@ -437,3 +437,25 @@ def test_loss_alone(n, d, op):
         t[0] = v
         got = L.linear_cross_entropy(h, w, t, reduction="none", dev_status=st)
         assert int(st) == abi.TT_DEV_BAD_INDEX and float(got[0]) == 0 and float(got[1]) == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("n", [1, 2, 31, 32])
+def test_few_positions_keep_what_rounding_left(n, dt):
+    """Up to 32 positions the gradient of the logits enters the products as two 16-bit parts:
+    dh and dW are then off by their own rounding (u) and the second part's (2 u^2 of a part's
+    terms, with the fp32 terms of `definition`), ignored positions among them or not."""
+    print("case few positions", n, dt, flush=True)
+    h, w, t, g = make(n, 700, 136, dt, seed=n)
+    if n > 3:
+        t[1] = t[n - 1] = IGN
+    up = upstream(n, "none", g)
+    got = run(h, w, "none", up, targets=t, label_smoothing=0.1)
+    keep = U[dt]
+    U[dt] = 2 * keep * keep
+    try:
+        _, (dh, bh), (dw, bw) = definition(h, w, dt, "none", up, targets=t, e=0.1)
+    finally:
+        U[dt] = keep
+    check(got[1], (dh, bh + keep * dh.abs()), "dh")
+    check(got[2], (dw, bw + keep * dw.abs()), "dW")
