@@ -423,8 +423,9 @@ int tt_full_weight(const tt_desc *desc, const float *const cores[3], int table, 
  * their elements; the gradients are contiguous.  Losses and grad_loss are fp32.  Products of
  * 16-bit inputs are exact and summed in fp32; fp32 inputs enter the matrix cores as two fp16
  * parts each (22 bits, scaled by a power of two of the tensor's largest value).  The logits'
- * gradient is rounded once to the inputs' 16-bit type (fp32: two fp16 parts).  dweight and
- * dhidden do not depend on the order of any atomics.
+ * gradient is rounded once to the inputs' 16-bit type (fp32, and up to 32 positions of any
+ * type: two parts).  No result depends on the order of atomics.  The calls enqueue kernels
+ * only and may be captured into a HIP graph (make one call of the kind before).
  *
  * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, d <= 2^20, strides <= 2^21, k <= 2048,
  * n * k <= 2^31. */

@@ -8,11 +8,15 @@
 //   position's q on v (the target's q is 1 - e), s = 1 or T.
 //
 // forward:  k_entries (distillation: q, duplicates merged) -> k_pack (positions that count,
-//           packed) -> k_logits (running maximum and sum per position and 128 or 256 rows of
-//           the weight) -> k_loss (lse, the entries' logits, loss)
-// backward: k_pack, then per piece of the vocabulary k_logits (G = row factor * g, in 16
-//           bits), k_entries_g (distillation: the entries of G), k_dhidden (split over the
-//           vocabulary, fp32), k_dweight; k_dhidden_out adds the splits.
+//           packed) -> k_logits (running maximum and sum per position and tile of the weight)
+//           -> k_loss (lse, the entries' logits, loss).  A loss alone of up to 64 positions
+//           leaves k_pack out.
+// backward: per piece of the vocabulary k_logits (G = row factor * g, in 16 bits), k_entries_g
+//           (distillation: the entries of G), k_dhidden (split over the vocabulary, fp32),
+//           k_dweight; k_dhidden_out adds the splits.
+//
+// The logits are worked out twice (8 N V D operations where 6 would do): keeping them, or the
+// 16-bit G of all pieces, is the [N, V] array that these losses are there to avoid.
 #pragma once
 #include "tt_gemm.h"
 #include "tt_internal.h"

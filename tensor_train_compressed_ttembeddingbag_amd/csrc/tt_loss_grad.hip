@@ -3,6 +3,10 @@
 //   dW[v][d] = sum_i G_iv h_id   x = d (columns of the packed positions), y = v, k = positions
 // dh is summed in fp32 over the splits and pieces of the vocabulary (each tile owned by one
 // workgroup, so the order is fixed); dW is complete in one piece and rounded once.
+//
+// Bound by the matrix cores: 8192 x 4096 x 16384 bf16 (one piece), dh 0.84 ms and dW 0.83 ms,
+// 1.31 and 1.33 PFLOP/s; 2048 x 2048 x 32000 fp16, dh 218 us and dW 247 us.  With few
+// positions dW is its own bytes: 2 x 49768 x 1152 bf16, 35 us = 3.3 TB/s.
 #include "tt_loss.h"
 
 #include <algorithm>

@@ -5,6 +5,13 @@
 // of one position: statistics are sums over a lane's own registers, then over the 4 lane
 // groups, then over the waves that share the positions.  Statistics and exponentials are fp32
 // in base 2 (the logits are scaled by log2 e once).
+//
+// Bound by the matrix cores from some 200 positions on, below that by the weight's bytes.
+// Measured (MI355X): 8192 x 131072 x 4096 bf16, statistics 6.4 ms = 1.37 PFLOP/s; a piece of
+// G (16384 rows of the vocabulary) 0.83 ms = 1.33 PFLOP/s (without its results 1.52: the
+// exponentials and 128 KiB of stores per tile are not hidden); 1024 x 32000 x 1024 fp32, 155
+// and 175 us (1.3 and 1.15 PFLOP/s over three products); 48 x 131072 x 2048 fp16, 107 us = 5.0
+// TB/s of weight.
 #include "tt_loss.h"
 
 namespace ttb {
