@@ -124,3 +124,78 @@ def test_example_trains():
     sp.loader.exec_module(m)
     hard, soft = m.main(items=5000, steps=40, sessions=512)
     assert hard[1] < 0.9 * hard[0] and soft[1] < 0.9 * soft[0]
+
+
+def test_backward_twice_gives_the_same_gradients():
+    print("case twice", flush=True)
+    h, w, t = _inputs(dt=torch.bfloat16)
+    x, y = h.requires_grad_(True), w.requires_grad_(True)
+    out = L.linear_cross_entropy(x, y, t)
+    a = torch.autograd.grad(out, (x, y), retain_graph=True)
+    b = torch.autograd.grad(out, (x, y))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_many_positions():
+    """70001 positions, a third ignored: the packed order and its counts past 65536, against
+    float64 (loss and dW: sums over all of them; dh of the first, last and some between).
+    Bounds: bf16 G and outputs 2^-8 each of the absolute terms' sums, the fp32 terms below."""
+    print("case many positions", flush=True)
+    n, v, d = 70001, 70, 24
+    h, w, t = _inputs(n, v, d, torch.bfloat16, seed=3)
+    t[::3] = -100
+    x, y = h.requires_grad_(True), w.requires_grad_(True)
+    out = L.linear_cross_entropy(x, y, t, reduction="sum")
+    dh, dw = torch.autograd.grad(out, (x, y))
+    with torch.no_grad():
+        H, W = h.double(), w.double()
+        ok = t >= 0
+        z = H @ W.t()
+        lp = torch.log_softmax(z, 1)
+        q = torch.zeros_like(z)
+        q[ok.nonzero()[:, 0], t[ok]] = 1
+        loss = -(q * lp).sum()
+        g = (lp.exp() - q) * ok[:, None]
+        assert abs(float(out) - float(loss)) <= 2.0 ** -18 * float(loss)
+        eps = 2.0 ** -8 + 2.0 ** -12
+        for got, ref, mag in ((dh, g @ W, g.abs() @ W.abs()), (dw, g.t() @ H, g.t().abs() @ H.abs())):
+            assert float(((got.double() - ref).abs() - eps * (mag + ref.abs())).max()) <= 1e-30
+        assert (dh[::3] == 0).all()
+
+
+def test_weight_past_four_gib():
+    """A weight of 4.9 GB: rows whose offsets pass 32 bits are read, scored and given their
+    gradients.  Loss against float64 a block of rows at a time (2^-16: 4096 products in fp32 and
+    the logs); dW rows against the fp64 product of the same probabilities, bf16's 2^-8 and the
+    two roundings of G's parts."""
+    print("case large weight", flush=True)
+    n, v, d = 8, 600_000, 4096
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    w = torch.empty(v, d, device="cuda", dtype=torch.bfloat16)
+    for a in range(0, v, 50_000):
+        w[a:a + 50_000] = (torch.randn(50_000, d, device="cuda", generator=g) * d ** -0.5).bfloat16()
+    t = torch.tensor([0, 1, 299_999, 524_287, 524_288, 599_998, 599_999, -100], device="cuda")
+    h = torch.randn(n, d, device="cuda", generator=g)
+    h[:7] += 5 * w[t[:7]].float()
+    h = h.bfloat16()
+    x, y = h.requires_grad_(True), w.requires_grad_(True)
+    out = L.linear_cross_entropy(x, y, t, reduction="none")
+    dh, dw = torch.autograd.grad(out.sum(), (x, y))
+    with torch.no_grad():
+        z = torch.cat([h.double() @ w[a:a + 50_000].double().t() for a in range(0, v, 50_000)], 1)
+        lse = torch.logsumexp(z, 1)
+        ref = (lse - z.gather(1, t.clamp(min=0)[:, None])[:, 0])[:7]
+        assert float((out[:7].double() - ref).abs().max()) <= 2.0 ** -16 * float(lse.max())
+        p = torch.exp(z - lse[:, None])
+        p[torch.arange(7, device="cuda"), t[:7]] -= 1
+        p[7] = 0
+        rows = torch.tensor([0, 7, 299_999, 524_287, 524_288, 524_289, 599_998, 599_999],
+                            device="cuda")
+        got, want = dw[rows].double(), p[:, rows].t() @ h.double()
+        mag = p[:, rows].t().abs() @ h.double().abs()
+        assert float(((got - want).abs() - 2.0 ** -8 * want.abs() - 2.0 ** -14 * mag).max()) <= 0
+        gh = sum(p[:, a:a + 50_000] @ w[a:a + 50_000].double() for a in range(0, v, 50_000))
+        mh = sum(p[:, a:a + 50_000].abs() @ w[a:a + 50_000].double().abs()
+                 for a in range(0, v, 50_000))
+        assert float(((dh.double() - gh).abs() - 2.0 ** -8 * gh.abs() - 2.0 ** -14 * mh).max()) <= 0
