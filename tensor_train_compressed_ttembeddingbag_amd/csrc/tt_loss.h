@@ -40,9 +40,12 @@ struct LossSaved {
   int *slot;       // [N] position -> packed row, or -1 - (a packed row of zeros)
   char *hp;        // packed positions: [row][plane][Dp]
   int *tgt;        // [N] packed row -> target row of the weight (cross entropy)
-  float *lse;      // [N] packed row -> lse in base 2
+  float *mx, *lg;  // [N] packed row -> its largest sum of products, and log2 of the sum of
+                   // 2^((sum of products - mx) zs): lse in base 2 is mx zs + lg.  In two parts,
+                   // because exp(z - lse) and a small loss lose what their rounded sum loses
+  float *zt;       // [N] packed row -> the target's sum of products (cross entropy)
   int *eidx;       // [N][k] distillation entries: row of the weight or -1
-  float *eq, *ez;  // their q and their logit in base 2
+  float *eq, *ez;  // their q and their log2 p
   float *ent;      // [N] sum_j q log q
 };
 

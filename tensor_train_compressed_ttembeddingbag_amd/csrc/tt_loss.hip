@@ -321,55 +321,72 @@ __device__ __forceinline__ void sum_rows(const LossArgs &a, double *s_d) {
   }
 }
 
-// Gathers one row of the weight per entry: 2048 x 32 entries of 2048 fp16, 38 us = 7 TB/s out
-// of the last-level cache; 4096 x 64 of 2048 bf16, 143 us = 7.5 TB/s; one target each of 1800
-// positions, 7 us.
-// NW waves per position: the tiles' statistics become its lse; the logits of its entries are
-// dot products of their own (fp32 sums of the inputs' products), a wave each, U at once.
+// NW waves per position: the tiles' statistics become its lse.  Distillation: the logits of the
+// entries are dot products of their own, in fp64 (a small divergence is the difference of
+// large terms), a wave each, U at once.
+// Gathers one row of the weight per entry: 2048 x 32 entries of 2048 fp16 in 38 us, 7 TB/s out
+// of the last-level cache.
 template <class S, int NW, int U>
 __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
-  __shared__ float s_m[4], s_s[4], s_z[4], s_q[4];
-  __shared__ double s_d[4];
+  __shared__ float s_m[4], s_s[4], s_z[4];
+  __shared__ double s_d[4], s_q[4];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, part = wv % NW;
   const int64_t i = (int64_t)blockIdx.x * (4 / NW) + wv / NW;
   const int slot = i < a.N ? slot_of(a, i) : -1;
   if (a.direct && !a.k && slot < 0 && i < a.N && lane == 0 && a.tgt[i] != a.ignore)
     set_status(a.status, TT_DEV_BAD_INDEX);
-  float out = 0.f, wm = -INFINITY, s = 0.f, z = 0.f, qz = 0.f;
+  const float zs = a.direct ? LOG2E / a.temp : a.sv.sc->zs;
+  float out = 0.f, wm = -INFINITY, s = 0.f, z = 0.f;
   if (slot >= 0) {
     const float2 *p = a.part + (int64_t)slot * a.ptiles;
     float m = -INFINITY;
     for (int t = part * 64 + lane; t < a.ptiles; t += 64 * NW) {
       const float2 v = p[t];
       const float n = fmaxf(m, v.x), n0 = n == -INFINITY ? 0.f : n;
-      s = s * __builtin_amdgcn_exp2f(m - n0) + v.y * __builtin_amdgcn_exp2f(v.x - n0);
+      s = s * __builtin_amdgcn_exp2f((m - n0) * zs) + v.y * __builtin_amdgcn_exp2f((v.x - n0) * zs);
       m = n;
       if (a.smoothing > 0.f) z += a.zpart[(int64_t)slot * a.ptiles + t];
     }
     wm = m;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor(wm, o));
-    s *= __builtin_amdgcn_exp2f(m - (wm == -INFINITY ? 0.f : wm));
+    s *= __builtin_amdgcn_exp2f((m - (wm == -INFINITY ? 0.f : wm)) * zs);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
       s += __shfl_xor(s, o);
       z += __shfl_xor(z, o);
     }
-    const int ne = a.k ? a.k : 1;
+  }
+  if constexpr (NW > 1) {
+    if (lane == 0) s_m[wv] = wm, s_s[wv] = s, s_z[wv] = z;
+    __syncthreads();
+    wm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    const float m0 = wm == -INFINITY ? 0.f : wm;
+    s = z = 0.f;
+    for (int w = 0; w < 4; ++w) {
+      s += s_s[w] * __builtin_amdgcn_exp2f((s_m[w] - m0) * zs);
+      z += s_z[w];
+    }
+  }
+  const float mx = wm == -INFINITY ? 0.f : wm, lg = log2f(s);
+  double qd = 0.0;  // sum over the entries of q (lse - logit), base 2
+  if (a.k && slot >= 0) {
+    const double lse = (double)mx * zs + lg;
+    // the same scale as in lse, on the inputs themselves
+    const double sc = a.direct ? zs : ldexpf(zs, a.sv.sc->ew + a.sv.sc->eh);
     const S *h = (const S *)a.hidden + i * a.hld;
     // U entries: one read of the position's row, U + 1 loads in flight
-    for (int j0 = part * U; j0 < ne; j0 += U * NW) {
+    for (int j0 = part * U; j0 < a.k; j0 += U * NW) {
       const S *w[U];
       bool on[U];
-      float d[U];
+      double d[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int j = min(j0 + u, ne - 1), v = a.k ? a.sv.eidx[i * a.k + j]
-                          : a.direct ? (int)a.tgt[i] : a.sv.tgt[slot];
-        on[u] = j0 + u < ne && v >= 0;
+        const int j = min(j0 + u, a.k - 1), v = a.sv.eidx[i * a.k + j];
+        on[u] = j0 + u < a.k && v >= 0;
         w[u] = (const S *)a.weight + max(v, 0) * a.wld;  // no entry: any row, not counted
-        d[u] = 0.f;
+        d[u] = 0.0;
       }
       auto dots = [&](auto whole) {
         for (int64_t c = lane * 8; c < a.D; c += 512) {
@@ -381,7 +398,7 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[u] += (float)x[e] * (float)y[u][e];
+            for (int e = 0; e < 8; ++e) d[u] += (double)(float)x[e] * (double)(float)y[u][e];
         }
       };
       if (a.D % 8 == 0) dots(std::true_type());
@@ -391,36 +408,30 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
         if (!on[u]) continue;
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) d[u] += __shfl_xor(d[u], o);
-        d[u] *= LOG2E / a.temp;
-        if (a.k) {
-          qz += a.sv.eq[i * a.k + j0 + u] * d[u];
-          if (lane == 0) a.sv.ez[i * a.k + j0 + u] = d[u];
-        } else {
-          qz = d[u];
-        }
+        const double lp = d[u] * sc - lse;
+        qd -= (double)a.sv.eq[i * a.k + j0 + u] * lp;
+        if (lane == 0) a.sv.ez[i * a.k + j0 + u] = (float)lp;
       }
     }
   }
-  if constexpr (NW > 1) {
-    if (lane == 0) s_m[wv] = wm, s_s[wv] = s, s_z[wv] = z, s_q[wv] = qz;
+  if (NW > 1 && a.k) {
+    if (lane == 0) s_q[wv] = qd;
     __syncthreads();
-    wm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    const float m0 = wm == -INFINITY ? 0.f : wm;
-    s = z = qz = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      s += s_s[w] * __builtin_amdgcn_exp2f(s_m[w] - m0);
-      z += s_z[w];
-      qz += s_q[w];
-    }
+    qd = s_q[0] + s_q[1] + s_q[2] + s_q[3];
   }
   const bool first = lane == 0 && part == 0 && i < a.N;
   if (slot >= 0 && first) {
-    const float lse = (wm == -INFINITY ? 0.f : wm) + log2f(s);
-    a.sv.lse[slot] = lse;
-    if (a.k)
-      out = a.temp * a.temp * (a.sv.ent[i] + (lse - qz) * LN2);
-    else
-      out = (lse - (1.f - a.smoothing) * qz - a.smoothing * (z / (float)a.V)) * LN2;
+    a.sv.mx[slot] = mx;
+    a.sv.lg[slot] = lg;
+    if (a.k) {
+      out = (float)((double)(a.temp * a.temp) * (a.sv.ent[i] + qd * LN2));
+    } else {
+      const float nll = (mx - a.sv.zt[slot]) * zs + lg;  // no difference of large sums
+      out = a.smoothing > 0.f ? (1.f - a.smoothing) * nll +
+                                    a.smoothing * (mx * zs + lg - z / (float)a.V)
+                              : nll;
+      out *= LN2;
+    }
   }
   if (a.reduction == TT_REDUCE_NONE) {
     if (first) a.loss[i] = out;
@@ -490,7 +501,7 @@ __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64
   const int64_t v = a.sv.eidx[t] - v0;
   if (slot < 0 || a.sv.eidx[t] < 0 || v < 0 || v >= nv) return;
   const int x = g_exp(a.dtype);
-  const float q = ldexpf(__builtin_amdgcn_exp2f(0.5f * (a.sv.ez[t] - a.sv.lse[slot])), x / 2);
+  const float q = ldexpf(__builtin_amdgcn_exp2f(0.5f * a.sv.ez[t]), x / 2);
   const float g = (q * q - ldexpf(a.sv.eq[t], x)) *
                   (a.reduction == TT_REDUCE_NONE ? a.rowf[slot] : 1.f);
   char *o = a.G + slot * a.ldG + v * 2;
@@ -602,7 +613,9 @@ static int64_t saved_layout(LossArgs &a, void *saved) {
   if (!a.direct) b.take(a.sv.hp, a.Npad * a.Dp * 2 * a.planes);
   b.take(a.sv.slot, a.N);
   b.take(a.sv.tgt, a.N);
-  b.take(a.sv.lse, a.N);
+  b.take(a.sv.mx, a.N);
+  b.take(a.sv.lg, a.N);
+  b.take(a.sv.zt, a.k ? 0 : a.N);
   if (a.k) {
     b.take(a.sv.ent, a.N);
     b.take(a.sv.eidx, a.N * a.k);

@@ -26,8 +26,10 @@ struct LogitsEpi {
   int ptiles, tile0;
   char *G;
   int64_t ldG, Gplane;
-  const float *lse, *rowf;
+  const float *mx, *lg, *rowf;
   const int *tgt;          // null with distillation
+  const int64_t *tgt64;    // the caller's targets instead (loss alone), or null
+  float *zt;
   int twin;
   float one_e, e_v, gs;    // 1 - e, e / V, G's factor 2^g_exp
 };
@@ -47,9 +49,26 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   if constexpr (!GRAD) {
     float2 *sm = (float2 *)tmp;                       // [NWX][Y]
     float *sz = (float *)(tmp + T::NWX * T::Y * 8);   // [NWX][Y]
+    int d_[T::NI];  // the target's place from this lane's first row, or -1
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j) {
+      const int pos = iy * T::Y + qy + 16 * j + c;
+      const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
+      const int64_t t = !ep.zt || pos >= count ? -1 : ep.tgt64 ? ep.tgt64[pos] : ep.tgt[pos];
+      d_[j] = (int)max<int64_t>(min<int64_t>(t - first, 1 << 20), -1);
+    }
 #pragma unroll
     for (int j = 0; j < T::NI; ++j) {
       float m = -INFINITY, zsum = 0.f;
+      // the target's logit is the one that the sum below has in it
+      if (__any(d_[j] >= 0 && d_[j] < 16 * T::MI)) {
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (d_[j] == 16 * i + r && d_[j] + xb < xl)
+              ep.zt[iy * T::Y + qy + 16 * j + c] = acc[i][j][r];
+      }
       if (ep.zpart) {
 #pragma unroll
         for (int i = 0; i < T::MI; ++i)
@@ -68,16 +87,19 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
-      m *= zs;  // zs > 0
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
       const float m0 = m == -INFINITY ? 0.f : m;  // nothing but -inf: every term is 0
+      // the exponent of the largest term is off 0 by the rounding of m zs alone, and so are all
+      // the others': taken back from the sum
+      const float mz = m0 * zs, off = __builtin_fmaf(m0, zs, -mz);
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zs, -m0));
+          s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zs, -mz));
+      s *= __builtin_amdgcn_exp2f(-off);
       s = sum_lane_groups(s);
       if (ep.zpart) zsum = sum_lane_groups(zsum);
       if (g == 0) {
@@ -96,7 +118,7 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
 #pragma unroll
       for (int w = 0; w < T::NWX; ++w) {
         const float2 q = sm[w * T::Y + y];
-        s += q.y * __builtin_amdgcn_exp2f(q.x - m0);
+        s += q.y * __builtin_amdgcn_exp2f((q.x - m0) * zs);
         if (ep.zpart) z += sz[w * T::Y + y];
       }
       const int64_t at = (int64_t)pos * ep.ptiles + ep.tile0 + ix;
@@ -113,8 +135,12 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
       const int pos = iy * T::Y + qy + 16 * j + c;
       const bool live = pos < count;
       if (ep.twin && qy + 16 * j >= ep.twin) continue;
-      const float lse = live ? 0.5f * ep.lse[pos] : 0.f, 
+      const float mx = live ? ep.mx[pos] : 0.f, lg = live ? 0.5f * ep.lg[pos] : 0.f,
                   f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * ep.gs : 0.f;
+      // half lse, rounded, and what that left of it: 2^(-2 left) into the row's factor
+      const float hz = mx * zh, lse = hz + lg;
+      const float left = __builtin_fmaf(mx, zh, -hz) + ((hz - lse) + lg);
+      const float fp = f * __builtin_amdgcn_exp2f(-2.f * left);
       const float ef = ep.e_v * f;
       const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
       const int d = live && ep.tgt ? (int)(ep.tgt[pos] - first) : -1;
@@ -131,7 +157,7 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zh, -lse));
-            v[r] = __builtin_fmaf(q * q, f, -ef);
+            v[r] = __builtin_fmaf(q * q, fp, -ef);
           }
           if (hit) {
 #pragma unroll
@@ -196,8 +222,10 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.ptiles = a.ptiles; ep.tile0 = tile0;
   ep.twin = a.twin;
   ep.ldG = a.ldG; ep.Gplane = a.Gplane;
-  ep.lse = a.sv.lse; ep.rowf = a.reduction == TT_REDUCE_NONE ? a.rowf : nullptr;
+  ep.mx = a.sv.mx; ep.lg = a.sv.lg; ep.rowf = a.reduction == TT_REDUCE_NONE ? a.rowf : nullptr;
   ep.tgt = a.k ? nullptr : a.sv.tgt;
+  ep.tgt64 = a.direct ? a.tgt : nullptr;
+  ep.zt = a.k || grad ? nullptr : a.sv.zt;
   ep.gs = ldexpf(1.f, g_exp(a.dtype));
   ep.one_e = 1.f - a.smoothing;
   ep.e_v = a.smoothing / (float)a.V;

@@ -459,3 +459,27 @@ def test_few_positions_keep_what_rounding_left(n, dt):
         U[dt] = keep
     check(got[1], (dh, bh + keep * dh.abs()), "dh")
     check(got[2], (dw, bw + keep * dw.abs()), "dW")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("n", [1, 70])
+def test_confident_positions(n, dt):
+    """Losses of 1e-4 to 1e-2, where lse and the target's logit agree in most digits.  The
+    target's logit is the one in the sum, so a loss is off by the sum's own rounding (some 8
+    terms of 2^-24 of a sum near 1) and by its logits' errors times the share of the others:
+    2^-20 + loss * dz."""
+    print("case confident", n, dt, flush=True)
+    v, d = 4000, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    w = (torch.randn(v, d, device="cuda", generator=g) * d ** -0.5).to(DT[dt])
+    t = torch.randint(0, v, (n,), device="cuda", generator=g)
+    h = (w[t].float() * (15.0 + 3 * torch.rand(n, 1, device="cuda", generator=g))).to(DT[dt])
+    got = L.linear_cross_entropy(h, w, t, reduction="none").double()
+    hg = h.detach().requires_grad_(True)
+    assert torch.equal(L.linear_cross_entropy(hg, w, t, reduction="none").detach().double(), got)
+    ref = torch.nn.functional.cross_entropy(h.double() @ w.double().t(), t, reduction="none")
+    dz = 2 * (d * 2.0 ** -24 + (2.0 ** -21 if dt == "fp32" else 0)) * \
+        (h.double().abs() @ w.double().abs().t()).amax(1)
+    assert float(ref.min()) < 2e-2
+    assert float(((got - ref).abs() / (2.0 ** -20 + ref * dz)).max()) <= 1
