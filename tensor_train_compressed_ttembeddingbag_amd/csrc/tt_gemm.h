@@ -11,9 +11,9 @@
 // logits W h^T, dh = G W, dW = G^T h -- read W, h and G as they lie, with no transposed copy.
 //
 // Tiles of 64 k go from memory to LDS by bounds-checked buffer loads that bypass registers
-// (rows past the end arrive as zeros), S tiles deep, with one barrier per tile.  These loads fill LDS in lane order, 16 bytes a lane, so the swizzle that keeps
-// the reads free of bank conflicts is put on the memory side: a lane fetches the chunk that
-// its LDS place stands for.
+// (rows past the end arrive as zeros), S tiles deep, with one barrier per tile.  These loads
+// fill LDS in lane order, 16 bytes a lane, so the swizzle that keeps the reads free of bank
+// conflicts is put on the memory side: a lane fetches the chunk that its LDS place stands for.
 //
 // fp32 operands come as two fp16 planes (x s = hi + lo, s a power of two that puts the
 // tensor's largest value below 2^15: 22 bits of every value within 2^17 of the largest, an

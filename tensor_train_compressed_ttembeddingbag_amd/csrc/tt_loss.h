@@ -86,7 +86,8 @@ struct LossArgs {
   float *dhp;              // [splits][tiles of positions that count][Dp]
 };
 
-constexpr int DH_SPLITS = 64 /* a lane each */, DH_TILES = 1024;  // most splits; most tiles where there are several
+constexpr int DH_SPLITS = 64;   // most splits of the vocabulary in k_dhidden: a lane each
+constexpr int DH_TILES = 1024;  // most tiles of it where there are several splits
 
 // Splits of the vocabulary in k_dhidden for `count` positions (known on the device only): the
 // number with the least estimated time.  A tile of 256 x 256 does 64 k in about 1.8 us on one

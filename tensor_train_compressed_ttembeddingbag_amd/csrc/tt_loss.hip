@@ -519,35 +519,35 @@ __global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a, DhPlan plan, Gr
   const float c_dh = scale.get(a.sv.sc->ew);
   const int per = (int)((a.D + 1023) / 1024);
   for (int64_t b = blockIdx.x; b < a.N * per; b += gridDim.x) {
-  const int64_t i = b / per, c = ((b - i * per) * 256 + threadIdx.x) * 4;
-  if (c >= a.D) continue;
-  const int slot = a.sv.slot[i];
-  f4 v = zero4();
-  if (slot >= 0) {
-    const float *p = a.dhp + (int64_t)slot * a.Dp + c;
+    const int64_t i = b / per, c = ((b - i * per) * 256 + threadIdx.x) * 4;
+    if (c >= a.D) continue;
+    const int slot = a.sv.slot[i];
+    f4 v = zero4();
+    if (slot >= 0) {
+      const float *p = a.dhp + (int64_t)slot * a.Dp + c;
 #pragma unroll 4
-    for (int k = 0; k < ns; ++k) v += *(const f4 *)(p + k * st);
-    if (a.twin) {
-      f4 w = zero4();
+      for (int k = 0; k < ns; ++k) v += *(const f4 *)(p + k * st);
+      if (a.twin) {
+        f4 w = zero4();
 #pragma unroll 4
-      for (int k = 0; k < ns; ++k) w += *(const f4 *)(p + a.twin * a.Dp + k * st);
-      v += w;
+        for (int k = 0; k < ns; ++k) w += *(const f4 *)(p + a.twin * a.Dp + k * st);
+        v += w;
+      }
+      v *= c_dh;
     }
-    v *= c_dh;
-  }
-  O *o = (O *)a.dh + i * a.D + c;
-  typedef O o4 __attribute__((ext_vector_type(4)));
-  struct __attribute__((packed, aligned(2))) any { o4 v; };
-  any w;
+    O *o = (O *)a.dh + i * a.D + c;
+    typedef O o4 __attribute__((ext_vector_type(4)));
+    struct __attribute__((packed, aligned(2))) any { o4 v; };
+    any w;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) w.v[r] = (O)v[r];
-  if (c + 4 <= a.D) {
-    *(any *)o = w;
-  } else {
+    for (int r = 0; r < 4; ++r) w.v[r] = (O)v[r];
+    if (c + 4 <= a.D) {
+      *(any *)o = w;
+    } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (c + r < a.D) o[r] = w.v[r];
-  }
+      for (int r = 0; r < 4; ++r)
+        if (c + r < a.D) o[r] = w.v[r];
+    }
   }
 }
 

@@ -21,21 +21,21 @@ __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64
   const int64_t split = dh_split_stride(n, T::Y, ld);
   a.splits = dh_splits(plan, n, threadIdx.x & 63);
   gemm_tiles<E, T, PL, true, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
-  const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int x = t.ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
-  const int y = t.iy * T::Y + (wv / T::NWX) * T::wy + c;
+    const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int x = t.ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
+    const int y = t.iy * T::Y + (wv / T::NWX) * T::wy + c;
 #pragma unroll
-  for (int j = 0; j < T::NI; ++j) {
-    if (y + 16 * j >= n) continue;
-    float *o = out + t.is * split + (y + 16 * j) * ld + x;
+    for (int j = 0; j < T::NI; ++j) {
+      if (y + 16 * j >= n) continue;
+      float *o = out + t.is * split + (y + 16 * j) * ld + x;
 #pragma unroll
-    for (int i = 0; i < T::MI; ++i) {
-      if (x + 16 * i >= ld) continue;  // ld is a multiple of 64: whole groups of four
-      f4 v = acc[i][j];
-      if (add) v += *(const f4 *)(o + 16 * i);
-      *(f4 *)(o + 16 * i) = v;
+      for (int i = 0; i < T::MI; ++i) {
+        if (x + 16 * i >= ld) continue;  // ld is a multiple of 64: whole groups of four
+        f4 v = acc[i][j];
+        if (add) v += *(const f4 *)(o + 16 * i);
+        *(f4 *)(o + 16 * i) = v;
+      }
     }
-  }
   });
 }
 
@@ -52,43 +52,43 @@ __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   const float s = ep.scale.get(ep.scale.sc->eh);
   typedef O o4 __attribute__((ext_vector_type(4)));
   gemm_tiles<E, T, sizeof(O) / 2, true, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
-  const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
-    const int x = t.ix * T::X + (wv % T::NWX) * T::wx;
-    const int64_t y = (int64_t)t.iy * T::Y + (wv / T::NWX) * T::wy + c;
+    const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+      const int x = t.ix * T::X + (wv % T::NWX) * T::wx;
+      const int64_t y = (int64_t)t.iy * T::Y + (wv / T::NWX) * T::wy + c;
 #pragma unroll
-    for (int j = 0; j < T::NI; ++j) {
-      O *o = ep.out + (y + 16 * j) * ep.ld + x;
-      const bool in = y + 16 * j < ep.nv;
+      for (int j = 0; j < T::NI; ++j) {
+        O *o = ep.out + (y + 16 * j) * ep.ld + x;
+        const bool in = y + 16 * j < ep.nv;
 #pragma unroll
-      for (int i = 0; i < T::MI; i += 2) {
-        o4 v[2];
+        for (int i = 0; i < T::MI; i += 2) {
+          o4 v[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[u][r] = (O)(acc[i + u][j][r] * s);
-        const int64_t left = ep.ld - (x + 16 * i);  // columns from this pair on
-        if constexpr (sizeof(O) == 2) {
-          if (left >= 32) {  // a whole pair: 16 bytes a lane (the same for every lane)
-            store_pair_if(in, (char *)(o + 16 * i), v[0], v[1], g);
-            continue;
+            for (int r = 0; r < 4; ++r) v[u][r] = (O)(acc[i + u][j][r] * s);
+          const int64_t left = ep.ld - (x + 16 * i);  // columns from this pair on
+          if constexpr (sizeof(O) == 2) {
+            if (left >= 32) {  // a whole pair: 16 bytes a lane (the same for every lane)
+              store_pair_if(in, (char *)(o + 16 * i), v[0], v[1], g);
+              continue;
+            }
           }
-        }
-        if (!in) continue;
-        struct __attribute__((packed, aligned(2))) any { o4 v; };
+          if (!in) continue;
+          struct __attribute__((packed, aligned(2))) any { o4 v; };
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int e = 16 * u + 4 * g;
-          if (left >= e + 4) {
-            const any w = {v[u]};
-            *(any *)(o + 16 * i + e) = w;
-          } else {
+          for (int u = 0; u < 2; ++u) {
+            const int e = 16 * u + 4 * g;
+            if (left >= e + 4) {
+              const any w = {v[u]};
+              *(any *)(o + 16 * i + e) = w;
+            } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (e + r < left) o[16 * i + e + r] = v[u][r];
+              for (int r = 0; r < 4; ++r)
+                if (e + r < left) o[16 * i + e + r] = v[u][r];
+            }
           }
         }
       }
-    }
   });
 }
 

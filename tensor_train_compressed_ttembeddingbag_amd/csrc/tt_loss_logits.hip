@@ -38,148 +38,148 @@ template <class E, class T, int PL, bool GRAD, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   gemm_tiles<E, T, PL, false, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
-  const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
-  const float zs = ep.sc ? ep.sc->zs : ep.zs;
-  const int count = ep.sc ? ep.sc->count : ep.n;
-  const int ix = t.ix, iy = t.iy;
-  const int xl = (int)min<int64_t>(ep.nv - (int64_t)ix * T::X, T::X);  // rows of this tile
-  const int xb = px + 4 * g;
-  const bool full = xl == T::X;  // no rows of the tile past the vocabulary
-  if constexpr (!GRAD) {
-    float2 *sm = (float2 *)tmp;                       // [NWX][Y]
-    float *sz = (float *)(tmp + T::NWX * T::Y * 8);   // [NWX][Y]
-    int d_[T::NI];  // the target's place from this lane's first row, or -1
+    const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
+    const float zs = ep.sc ? ep.sc->zs : ep.zs;
+    const int count = ep.sc ? ep.sc->count : ep.n;
+    const int ix = t.ix, iy = t.iy;
+    const int xl = (int)min<int64_t>(ep.nv - (int64_t)ix * T::X, T::X);  // rows of this tile
+    const int xb = px + 4 * g;
+    const bool full = xl == T::X;  // no rows of the tile past the vocabulary
+    if constexpr (!GRAD) {
+      float2 *sm = (float2 *)tmp;                       // [NWX][Y]
+      float *sz = (float *)(tmp + T::NWX * T::Y * 8);   // [NWX][Y]
+      int d_[T::NI];  // the target's place from this lane's first row, or -1
 #pragma unroll
-    for (int j = 0; j < T::NI; ++j) {
-      const int pos = iy * T::Y + qy + 16 * j + c;
-      const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
-      const int64_t t = !ep.zt || pos >= count ? -1 : ep.tgt64 ? ep.tgt64[pos] : ep.tgt[pos];
-      d_[j] = (int)max<int64_t>(min<int64_t>(t - first, 1 << 20), -1);
-    }
-#pragma unroll
-    for (int j = 0; j < T::NI; ++j) {
-      float m = -INFINITY, zsum = 0.f;
-      // the target's logit is the one that the sum below has in it
-      if (__any(d_[j] >= 0 && d_[j] < 16 * T::MI)) {
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (d_[j] == 16 * i + r && d_[j] + xb < xl)
-              ep.zt[iy * T::Y + qy + 16 * j + c] = acc[i][j][r];
-      }
-      if (ep.zpart) {
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) zsum += xb + 16 * i + r < xl ? acc[i][j][r] : 0.f;
-        zsum *= zs;
-      }
-      if (!full) {
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (xb + 16 * i + r >= xl) acc[i][j][r] = -INFINITY;
+      for (int j = 0; j < T::NI; ++j) {
+        const int pos = iy * T::Y + qy + 16 * j + c;
+        const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
+        const int64_t t = !ep.zt || pos >= count ? -1 : ep.tgt64 ? ep.tgt64[pos] : ep.tgt[pos];
+        d_[j] = (int)max<int64_t>(min<int64_t>(t - first, 1 << 20), -1);
       }
 #pragma unroll
-      for (int i = 0; i < T::MI; ++i)
+      for (int j = 0; j < T::NI; ++j) {
+        float m = -INFINITY, zsum = 0.f;
+        // the target's logit is the one that the sum below has in it
+        if (__any(d_[j] >= 0 && d_[j] < 16 * T::MI)) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float m0 = m == -INFINITY ? 0.f : m;  // nothing but -inf: every term is 0
-      // the exponent of the largest term is off 0 by the rounding of m zs alone, and so are all
-      // the others': taken back from the sum
-      const float mz = m0 * zs, off = __builtin_fmaf(m0, zs, -mz);
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zs, -mz));
-      s *= __builtin_amdgcn_exp2f(-off);
-      s = sum_lane_groups(s);
-      if (ep.zpart) zsum = sum_lane_groups(zsum);
-      if (g == 0) {
-        sm[(wv % T::NWX) * T::Y + qy + 16 * j + c] = make_float2(m, s);
-        if (ep.zpart) sz[(wv % T::NWX) * T::Y + qy + 16 * j + c] = zsum;
-      }
-    }
-    lds_barrier();
-    for (int y = tid; y < T::Y; y += T::NT) {
-      const int pos = iy * T::Y + y;
-      if (pos >= count) continue;
-      float m = -INFINITY, s = 0.f, z = 0.f;
-#pragma unroll
-      for (int w = 0; w < T::NWX; ++w) m = fmaxf(m, sm[w * T::Y + y].x);
-      const float m0 = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int w = 0; w < T::NWX; ++w) {
-        const float2 q = sm[w * T::Y + y];
-        s += q.y * __builtin_amdgcn_exp2f((q.x - m0) * zs);
-        if (ep.zpart) z += sz[w * T::Y + y];
-      }
-      const int64_t at = (int64_t)pos * ep.ptiles + ep.tile0 + ix;
-      ep.part[at] = make_float2(m, s);
-      if (ep.zpart) ep.zpart[at] = z;
-    }
-    lds_barrier();
-  } else {
-    // p 2^g_exp as the square of exp2 of half the logit, times the row's factor: v_exp_f32
-    // itself ends at 2^-126, bf16 and the gradients do not
-    const float zh = 0.5f * zs;
-#pragma unroll
-    for (int j = 0; j < T::NI; ++j) {
-      const int pos = iy * T::Y + qy + 16 * j + c;
-      const bool live = pos < count;
-      if (ep.twin && qy + 16 * j >= ep.twin) continue;
-      const float mx = live ? ep.mx[pos] : 0.f, lg = live ? 0.5f * ep.lg[pos] : 0.f,
-                  f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * ep.gs : 0.f;
-      // half lse, rounded, and what that left of it: 2^(-2 left) into the row's factor
-      const float hz = mx * zh, lse = hz + lg;
-      const float left = __builtin_fmaf(mx, zh, -hz) + ((hz - lse) + lg);
-      const float fp = f * __builtin_amdgcn_exp2f(-2.f * left);
-      const float ef = ep.e_v * f;
-      const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
-      const int d = live && ep.tgt ? (int)(ep.tgt[pos] - first) : -1;
-      // few tiles hold the target of one of a wave's 16 positions
-      const bool hit = __any(d >= 0 && d < 16 * T::MI);
-      char *o = ep.G + pos * ep.ldG + ((int64_t)ix * T::X + px) * 2;
-#pragma unroll
-      for (int i0 = 0; i0 < T::MI; i0 += 2) {
-        typename E::v4 h[2], l[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int i = i0 + u;
-          float v[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zh, -lse));
-            v[r] = __builtin_fmaf(q * q, fp, -ef);
-          }
-          if (hit) {
+          for (int i = 0; i < T::MI; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (d == 16 * i + r) v[r] -= ep.one_e * f;
-          }
-          if (!full) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (xb + 16 * i + r >= xl) v[r] = 0.f;
-          }
-          if (!live) v[0] = v[1] = v[2] = v[3] = 0.f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) h[u][r] = (typename E::e)v[r];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) l[u][r] = (typename E::e)(v[r] - (float)h[u][r]);
+              if (d_[j] == 16 * i + r && d_[j] + xb < xl)
+                ep.zt[iy * T::Y + qy + 16 * j + c] = acc[i][j][r];
         }
-        store_pair(o + 32 * i0, h[0], h[1], g);
-        if (PL > 1 || ep.twin) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
+        if (ep.zpart) {
+#pragma unroll
+          for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) zsum += xb + 16 * i + r < xl ? acc[i][j][r] : 0.f;
+          zsum *= zs;
+        }
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (xb + 16 * i + r >= xl) acc[i][j][r] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float m0 = m == -INFINITY ? 0.f : m;  // nothing but -inf: every term is 0
+        // the exponent of the largest term is off 0 by the rounding of m zs alone, and so are all
+        // the others': taken back from the sum
+        const float mz = m0 * zs, off = __builtin_fmaf(m0, zs, -mz);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zs, -mz));
+        s *= __builtin_amdgcn_exp2f(-off);
+        s = sum_lane_groups(s);
+        if (ep.zpart) zsum = sum_lane_groups(zsum);
+        if (g == 0) {
+          sm[(wv % T::NWX) * T::Y + qy + 16 * j + c] = make_float2(m, s);
+          if (ep.zpart) sz[(wv % T::NWX) * T::Y + qy + 16 * j + c] = zsum;
+        }
+      }
+      lds_barrier();
+      for (int y = tid; y < T::Y; y += T::NT) {
+        const int pos = iy * T::Y + y;
+        if (pos >= count) continue;
+        float m = -INFINITY, s = 0.f, z = 0.f;
+#pragma unroll
+        for (int w = 0; w < T::NWX; ++w) m = fmaxf(m, sm[w * T::Y + y].x);
+        const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < T::NWX; ++w) {
+          const float2 q = sm[w * T::Y + y];
+          s += q.y * __builtin_amdgcn_exp2f((q.x - m0) * zs);
+          if (ep.zpart) z += sz[w * T::Y + y];
+        }
+        const int64_t at = (int64_t)pos * ep.ptiles + ep.tile0 + ix;
+        ep.part[at] = make_float2(m, s);
+        if (ep.zpart) ep.zpart[at] = z;
+      }
+      lds_barrier();
+    } else {
+      // p 2^g_exp as the square of exp2 of half the logit, times the row's factor: v_exp_f32
+      // itself ends at 2^-126, bf16 and the gradients do not
+      const float zh = 0.5f * zs;
+#pragma unroll
+      for (int j = 0; j < T::NI; ++j) {
+        const int pos = iy * T::Y + qy + 16 * j + c;
+        const bool live = pos < count;
+        if (ep.twin && qy + 16 * j >= ep.twin) continue;
+        const float mx = live ? ep.mx[pos] : 0.f, lg = live ? 0.5f * ep.lg[pos] : 0.f,
+                    f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * ep.gs : 0.f;
+        // half lse, rounded, and what that left of it: 2^(-2 left) into the row's factor
+        const float hz = mx * zh, lse = hz + lg;
+        const float left = __builtin_fmaf(mx, zh, -hz) + ((hz - lse) + lg);
+        const float fp = f * __builtin_amdgcn_exp2f(-2.f * left);
+        const float ef = ep.e_v * f;
+        const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
+        const int d = live && ep.tgt ? (int)(ep.tgt[pos] - first) : -1;
+        // few tiles hold the target of one of a wave's 16 positions
+        const bool hit = __any(d >= 0 && d < 16 * T::MI);
+        char *o = ep.G + pos * ep.ldG + ((int64_t)ix * T::X + px) * 2;
+#pragma unroll
+        for (int i0 = 0; i0 < T::MI; i0 += 2) {
+          typename E::v4 h[2], l[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int i = i0 + u;
+            float v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zh, -lse));
+              v[r] = __builtin_fmaf(q * q, fp, -ef);
+            }
+            if (hit) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (d == 16 * i + r) v[r] -= ep.one_e * f;
+            }
+            if (!full) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (xb + 16 * i + r >= xl) v[r] = 0.f;
+            }
+            if (!live) v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[u][r] = (typename E::e)v[r];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) l[u][r] = (typename E::e)(v[r] - (float)h[u][r]);
+          }
+          store_pair(o + 32 * i0, h[0], h[1], g);
+          if (PL > 1 || ep.twin) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
+        }
       }
     }
-  }
   });
 }
 
