@@ -5,7 +5,8 @@ three Tensor-Train cores and sum-pooled per bag, with a backward pass that updat
 the cores in place (fused sparse SGD) and an HBM cache of decompressed hot rows.
 The compute runs in hand-written HIP kernels behind the C ABI in
 ``include/tt_bag.h`` (``libttbag.so``); ``abi`` is the thin ctypes binding and
-``module`` a small torch.nn.Module on top of it.
+``module`` a small torch.nn.Module on top of it.  ``loss`` has the losses of a table
+used as an output head over a large vocabulary.
 
 Importing this package does not load the HIP library; the first call into
 ``abi`` does, and raises if the library has not been built.
