@@ -20,6 +20,12 @@
 // absolute 2^-39 of the largest below that), side by side in a row.  Their tiles hold 32 k of
 // both planes, and hi hi, hi lo and lo hi go into the same sums: three products for the LDS
 // traffic of two.
+//
+// What two parts cannot stand for goes through the same tiles WHOLE: the planes hold the upper
+// and the lower halves of the values' bits, which are put together again in registers, and
+// v_mfma_f32_16x16x4 multiplies them, fp32 as it is.  An infinity is such a value: it would
+// meet the other operand's lo part as inf x 0 or inf - inf.  (A step of 1024 x 32000 x 1024:
+// 2.4 ms, of two parts 0.84 ms.)
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -59,6 +65,34 @@ struct Fp16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
+
+// element e of eight fp32 values whose upper and lower halves lie in two fragments
+template <class V8>
+__device__ __forceinline__ float whole(V8 hi, V8 lo, int e) {
+  union {
+    V8 v;
+    unsigned u[4];
+  } a, b;
+  a.v = hi;
+  b.v = lo;
+  return __uint_as_float(
+      __builtin_amdgcn_perm(a.u[e / 2], b.u[e / 2], e % 2 ? 0x07060302u : 0x05040100u));
+}
+// the halves of four fp32 values, as 16-bit patterns
+template <class V4>
+__device__ __forceinline__ void halves(const float (&v)[4], V4 &hi, V4 &lo) {
+  union {
+    V4 v;
+    unsigned short u[4];
+  } a, b;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    a.u[r] = (unsigned short)(__float_as_uint(v[r]) >> 16);
+    b.u[r] = (unsigned short)__float_as_uint(v[r]);
+  }
+  hi = a.v;
+  lo = b.v;
+}
 
 constexpr int GK = 64;                        // k per tile (over all planes)
 constexpr unsigned BUF_MAX = 0x7fffffffu;     // largest extent of one buffer descriptor
@@ -291,7 +325,8 @@ struct Tile {
 // barriers.
 // MEND: P's rows do not end with whole 16-byte groups (see Feed::mend); a variant of its own,
 // because the test for it in the loop cost the others 1 to 7 %.
-template <class E, class T, int PL, bool PC, bool QC, bool MEND, class Done>
+// WHOLE: the two planes are the halves of fp32 values.
+template <class E, class T, int PL, bool PC, bool QC, bool MEND, bool WHOLE, class Done>
 __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done done) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
@@ -346,6 +381,25 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
 #pragma unroll
       for (int j = 0; j < T::NI; ++j) acc[i][j] = E::mfma(p[sp][i], q[sq][j], acc[i][j]);
   };
+  // fp32: lane group g holds k = 8 g + e of both operands, so element e of all four is one
+  // product over four k.  The reads wait for their use here: both register sets beside the
+  // accumulators and the joined values do not fit.
+  auto mul_whole = [&](int buf) {
+    read_q(0, buf);
+    read_q(1, buf);
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i) {
+      const typename E::v8 hi = frag<E, T::X, PC>(lds + buf * SB, px + 16 * i, 0, lane),
+                           lo = frag<E, T::X, PC>(lds + buf * SB, px + 16 * i, 1, lane);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              whole(hi, lo, e), whole(q[0][j], q[1][j], e), acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
   // one LDS read to every few products, so that neither unit waits for the other's burst
   auto pace = [&]() {
 #pragma unroll
@@ -392,15 +446,21 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
       if (steps > 0) {
         wait_barrier<(T::STAGES - 1) * LPT>();
         if (MEND && steps == 1) mend(buf);
-        read_q(0, buf);
-        read_p(0, buf);
+        if constexpr (!WHOLE) {
+          read_q(0, buf);
+          read_p(0, buf);
+        }
       }
       for (int st = 0; st < steps; ++st) {
         const int next = buf + 1 == T::STAGES ? 0 : buf + 1;
-        read_q(1, buf);
-        read_p(1, buf);
-        mul(0, 0);
-        pace();
+        if constexpr (WHOLE) {
+          mul_whole(buf);
+        } else {
+          read_q(1, buf);
+          read_p(1, buf);
+          mul(0, 0);
+          pace();
+        }
         wait_barrier<(T::STAGES - 2) * LPT>();
         if (MEND && st + 2 == steps) mend(next);
         load(buf);
@@ -409,7 +469,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
           read_p(0, next);
           mul(1, 1);
           pace();
-        } else {  // hi lo and lo hi; each operand's next front half follows its last use
+        } else if constexpr (!WHOLE) {  // hi lo and lo hi; each operand's next front half follows its last use
           mul(0, 1);
           read_p(0, next);
           mul(1, 0);

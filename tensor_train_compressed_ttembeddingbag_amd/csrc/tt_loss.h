@@ -29,7 +29,8 @@ constexpr int AMAX_BLOCKS = 1024;
 // scalars that the device works out in the forward
 struct LossScalars {
   int count;       // positions that count
-  int ew, eh;      // exponents of the planes' scales, weight and hidden states (fp32; else 0)
+  int whole;       // fp32: the planes are the halves of the values' bits, see tt_gemm.h
+  int ew, eh;      // exponents of the planes' scales, weight and hidden states (else 0)
   float zs;        // logits from sums of products: log2(e) / T over the planes' scales
   int ticket;      // blocks of k_loss that are done
 };
@@ -74,7 +75,8 @@ struct LossArgs {
   int dh_bx, dh_by, cus;   // k_dhidden's tile, compute units
   LossSaved sv;
   // workspace
-  float *amax;             // [2 * AMAX_BLOCKS] block maxima of |weight| and |hidden| (fp32)
+  float *amax;             // [2 * AMAX_BLOCKS] block maxima of |weight| and |hidden| (fp32; infinite
+                           // where a value is not finite)
   char *wp;                // packed piece of the weight: [row][plane][Dp]
   float2 *part;            // [Npad][ptiles] (max, sum) in base 2
   float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)
@@ -136,7 +138,7 @@ struct GradScale {
   int mean, gexp;
   __device__ __forceinline__ float get(int e) const {
     const float c = base * *up / (mean ? (float)max(sc->count, 1) : 1.f);
-    return ldexpf(c, -e - gexp);
+    return sc->whole ? c : ldexpf(c, -e - gexp);
   }
 };
 inline GradScale grad_scale(const LossArgs &a) {

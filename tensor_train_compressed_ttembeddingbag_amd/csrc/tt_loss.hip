@@ -38,22 +38,32 @@ __device__ __forceinline__ void load8_at(const S *p0, int64_t c, int64_t d, bool
   }
 }
 
-// 8 source elements -> planes of 16-bit elements (fp32: x s = hi + lo; an infinity or NaN
-// stays in hi alone)
+// 8 source elements -> planes of 16-bit elements (fp32: x s = hi + lo, or the halves of x)
 template <class S, class E, int PL>
-__device__ __forceinline__ void store8(const S (&v)[8], float scale, char *dst, int64_t plane) {
+__device__ __forceinline__ void store8(const S (&v)[8], float scale, bool whole, char *dst,
+                                       int64_t plane) {
   typename E::v8 h;
   if constexpr (PL == 1) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = (typename E::e)v[e];
   } else {
     typename E::v8 l;
+    if (whole) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = (float)v[e] * scale;
-      h[e] = (typename E::e)x;
-      const float r = x - (float)h[e];
-      l[e] = (typename E::e)(r == r && fabsf(x) < INFINITY ? r : 0.f);
+      for (int u = 0; u < 8; u += 4) {
+        const float x[4] = {(float)v[u], (float)v[u + 1], (float)v[u + 2], (float)v[u + 3]};
+        typename E::v4 a, b;
+        halves(x, a, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[u + e] = a[e], l[u + e] = b[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = (float)v[e] * scale;
+        h[e] = (typename E::e)x;
+        l[e] = (typename E::e)(x - (float)h[e]);
+      }
     }
     *(typename E::v8 *)(dst + plane) = l;
   }
@@ -67,14 +77,14 @@ __device__ __forceinline__ int plane_exp(float amax) {
   frexpf(amax, &e);  // amax < 2^e
   return min(15 - e, 120);
 }
-// block maxima -> exponent, in every lane of a wave
-__device__ __forceinline__ int planes_exp(const float *amax, int lane) {
+// block maxima -> the tensor's, in every lane of a wave
+__device__ __forceinline__ float largest(const float *amax, int lane) {
   float m = 0.f;
 #pragma unroll
   for (int u = 0; u < AMAX_BLOCKS / 64; ++u) m = fmaxf(m, amax[u * 64 + lane]);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  return plane_exp(m);
+  return m;
 }
 
 // ---------------------------------------------------------------- distillation entries
@@ -154,7 +164,8 @@ __device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
   return t != a.ignore && t >= 0 && t < a.V;
 }
 
-// largest finite |x| of the weight (blocks 0 ..) and of the positions that count, per block
+// largest |x| of the weight (blocks 0 ..) and of the positions that count, per block: infinite
+// where one is NaN
 __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
   const bool w = blockIdx.x < AMAX_BLOCKS;
   const int b = blockIdx.x % AMAX_BLOCKS, tid = threadIdx.x;
@@ -171,8 +182,7 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
       load8(x + r * ld + q * 8, a.D - q * 8, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float y = fabsf(v[e]);
-        if (y < INFINITY) m = fmaxf(m, y);
+        m = fmaxf(m, v[e] == v[e] ? fabsf(v[e]) : INFINITY);
       }
     }
     r += dr;
@@ -218,9 +228,11 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
   __syncthreads();
   const int base = s_n[0] + s_n[1] + s_n[2] + s_n[3];
   int ew = 0, eh = 0;
+  bool whole = false;
   if (PL > 1) {
-    ew = planes_exp(a.amax, lane);
-    eh = planes_exp(a.amax + AMAX_BLOCKS, lane);
+    const float mw = largest(a.amax, lane), mh = largest(a.amax + AMAX_BLOCKS, lane);
+    whole = !(mw < INFINITY && mh < INFINITY);
+    if (!whole) ew = plane_exp(mw), eh = plane_exp(mh);
   }
   if (wv == 0) {
     const int64_t i = i0 + lane;
@@ -242,6 +254,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
     if (own) s_slot[lane] = slot;
     if (blockIdx.x == 0 && lane == 0) {
       a.sv.sc->zs = ldexpf(LOG2E / a.temp, -(ew + eh));
+      a.sv.sc->whole = whole;
       a.sv.sc->ew = ew;
       a.sv.sc->eh = eh;
       a.sv.sc->ticket = 0;
@@ -251,7 +264,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
   const float scale = ldexpf(1.f, eh);
   const int cpr = (int)(a.Dp / 8);
   const int64_t last = a.twin ? a.twin : (a.N + GK - 1) / GK * GK;
-  auto copy = [&](auto whole) {
+  auto copy = [&](auto eights) {  // rows of whole groups of eight
     constexpr int U = 4;  // groups of eight in flight per thread
     for (int q0 = tid; q0 < PACK_ROWS * cpr; q0 += 256 * U) {
       S v[U][8];
@@ -259,7 +272,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
       for (int u = 0; u < U; ++u) {
         const int q = min(q0 + 256 * u, PACK_ROWS * cpr - 1), r = q / cpr, c = (q - r * cpr) * 8;
         // a block of past-the-end rows copies none: any row's address will do
-        load8_at<decltype(whole)::value>((const S *)a.hidden + min(i0 + r, a.N - 1) * a.hld, c,
+        load8_at<decltype(eights)::value>((const S *)a.hidden + min(i0 + r, a.N - 1) * a.hld, c,
                                          a.D, s_slot[r] >= 0, v[u]);
       }
 #pragma unroll
@@ -270,8 +283,8 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
         const int64_t row = slot < 0 ? -1 - slot : slot;
         if (row >= last) continue;
         char *o = a.sv.hp + (row * PL * a.Dp + c) * 2;
-        store8<S, E, PL>(v[u], scale, o, a.Dp * 2);
-        if (PL == 1 && a.twin) store8<S, E, PL>(v[u], scale, o + a.twin * a.Dp * 2, 0);
+        store8<S, E, PL>(v[u], scale, whole, o, a.Dp * 2);
+        if (PL == 1 && a.twin) store8<S, E, PL>(v[u], scale, whole, o + a.twin * a.Dp * 2, 0);
       }
     }
   };
@@ -282,13 +295,14 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
 // rows [v0, v0 + nv) of the weight -> wp (a copy: 32000 x 1024 fp32 in 41 us, 6.4 TB/s)
 template <class S, class E, int PL>
 __global__ __launch_bounds__(256) void k_pack_w(LossArgs a, int64_t v0, int64_t nv) {
+  const bool whole = PL > 1 && a.sv.sc->whole;
   const float scale = PL > 1 ? ldexpf(1.f, a.sv.sc->ew) : 1.f;
   const int64_t cpr = a.Dp / 8, n = nv * cpr, st = (int64_t)gridDim.x * 256;
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n; q += st) {
     const int64_t r = q / cpr, c = (q - r * cpr) * 8;
     S v[8];
     load8((const S *)a.weight + (v0 + r) * a.wld + c, a.D - c, v);
-    store8<S, E, PL>(v, scale, a.wp + (r * PL * a.Dp + c) * 2, a.Dp * 2);
+    store8<S, E, PL>(v, scale, whole, a.wp + (r * PL * a.Dp + c) * 2, a.Dp * 2);
   }
 }
 
@@ -466,7 +480,7 @@ __global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
   __shared__ float s_m[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   float cm = 1.f;
-  if (a.dtype != TT_DTYPE_BF16) {
+  if (a.dtype != TT_DTYPE_BF16 && !a.sv.sc->whole) {
     float m = 0.f;
 #pragma unroll 4
     for (int64_t i = tid; i < a.N; i += 256) {
@@ -500,11 +514,17 @@ __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64
   const int slot = a.sv.slot[i];
   const int64_t v = a.sv.eidx[t] - v0;
   if (slot < 0 || a.sv.eidx[t] < 0 || v < 0 || v >= nv) return;
-  const int x = g_exp(a.dtype);
+  const bool whole = PL > 1 && a.sv.sc->whole;
+  const int x = whole ? 0 : g_exp(a.dtype);
   const float q = ldexpf(__builtin_amdgcn_exp2f(0.5f * a.sv.ez[t]), x / 2);
   const float g = (q * q - ldexpf(a.sv.eq[t], x)) *
                   (a.reduction == TT_REDUCE_NONE ? a.rowf[slot] : 1.f);
   char *o = a.G + slot * a.ldG + v * 2;
+  if (whole) {
+    *(unsigned short *)o = (unsigned short)(__float_as_uint(g) >> 16);
+    *(unsigned short *)(o + a.Gplane) = (unsigned short)__float_as_uint(g);
+    return;
+  }
   const typename E::e h = (typename E::e)g;
   *(typename E::e *)o = h;
   if (PL > 1 || a.twin) *(typename E::e *)(o + a.Gplane) = (typename E::e)(g - (float)h);

@@ -13,14 +13,13 @@
 
 namespace ttb {
 
-template <class E, class T, int PL, bool MEND>
-__global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
-                                                   DhPlan plan, int add) {
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
+template <class E, class T, int PL, bool MEND, bool WHOLE>
+__device__ __forceinline__ void dhidden_tiles(GemmArgs &a, float *out, int64_t ld,
+                                              const DhPlan &plan, int add, char *lds) {
   const int n = a.ycount ? *a.ycount : a.yn;
   const int64_t split = dh_split_stride(n, T::Y, ld);
   a.splits = dh_splits(plan, n, threadIdx.x & 63);
-  gemm_tiles<E, T, PL, true, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  gemm_tiles<E, T, PL, true, false, MEND, WHOLE>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
     const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
     const int x = t.ix * T::X + (wv % T::NWX) * T::wx + 4 * g;
     const int y = t.iy * T::Y + (wv / T::NWX) * T::wy + c;
@@ -39,6 +38,15 @@ __global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64
   });
 }
 
+template <class E, class T, int PL, bool MEND>
+__global__ __launch_bounds__(T::NT) void k_dhidden(GemmArgs a, float *out, int64_t ld,
+                                                   DhPlan plan, int add, const LossScalars *sc) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  if constexpr (PL > 1)
+    if (sc->whole) return dhidden_tiles<E, T, PL, MEND, true>(a, out, ld, plan, add, lds);
+  dhidden_tiles<E, T, PL, MEND, false>(a, out, ld, plan, add, lds);
+}
+
 template <class O>
 struct DwOut {
   O *out;             // dW of the piece's first row
@@ -46,12 +54,11 @@ struct DwOut {
   GradScale scale;
 };
 
-template <class E, class T, class O>
-__global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
+template <class E, class T, class O, bool WHOLE>
+__device__ __forceinline__ void dweight_tiles(const GemmArgs &a, const DwOut<O> &ep, char *lds) {
   const float s = ep.scale.get(ep.scale.sc->eh);
   typedef O o4 __attribute__((ext_vector_type(4)));
-  gemm_tiles<E, T, sizeof(O) / 2, true, true, false>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
+  gemm_tiles<E, T, sizeof(O) / 2, true, true, false, WHOLE>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *) {
     const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
       const int x = t.ix * T::X + (wv % T::NWX) * T::wx;
       const int64_t y = (int64_t)t.iy * T::Y + (wv / T::NWX) * T::wy + c;
@@ -92,12 +99,20 @@ __global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
   });
 }
 
+template <class E, class T, class O>
+__global__ __launch_bounds__(T::NT) void k_dweight(GemmArgs a, DwOut<O> ep) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  if constexpr (sizeof(O) > 2)
+    if (ep.scale.sc->whole) return dweight_tiles<E, T, O, true>(a, ep, lds);
+  dweight_tiles<E, T, O, false>(a, ep, lds);
+}
+
 template <class E, class T, int PL, bool MEND>
 static hipError_t go_dh(const GemmArgs &g, const LossArgs &a, int add, hipStream_t s) {
   const hipError_t e = lds_limit<T>(&k_dhidden<E, T, PL, MEND>);
   if (e != hipSuccess) return e;
   tt_launch(K_LOSS_DH, k_dhidden<E, T, PL, MEND>, dim3(gemm_grid<T>(a, std::max(g.tx * g.ty, DH_TILES))), dim3(T::NT), T::LDS,
-            s, g, a.dhp, a.Dp, dh_plan(a), add);
+            s, g, a.dhp, a.Dp, dh_plan(a), add, a.sv.sc);
   return hipGetLastError();
 }
 

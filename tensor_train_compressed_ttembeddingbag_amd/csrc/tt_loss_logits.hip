@@ -34,10 +34,9 @@ struct LogitsEpi {
   float one_e, e_v, gs;    // 1 - e, e / V, G's factor 2^g_exp
 };
 
-template <class E, class T, int PL, bool GRAD, bool MEND>
-__global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
-  gemm_tiles<E, T, PL, false, false, MEND>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
+template <class E, class T, int PL, bool GRAD, bool MEND, bool WHOLE>
+__device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi &ep, char *lds) {
+  gemm_tiles<E, T, PL, false, false, MEND, WHOLE>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
     const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
     const int px = (wv % T::NWX) * T::wx, qy = (wv / T::NWX) * T::wy;
     const float zs = ep.sc ? ep.sc->zs : ep.zs;
@@ -136,7 +135,7 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
         const bool live = pos < count;
         if (ep.twin && qy + 16 * j >= ep.twin) continue;
         const float mx = live ? ep.mx[pos] : 0.f, lg = live ? 0.5f * ep.lg[pos] : 0.f,
-                    f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * ep.gs : 0.f;
+                    f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * (WHOLE ? 1.f : ep.gs) : 0.f;
         // half lse, rounded, and what that left of it: 2^(-2 left) into the row's factor
         const float hz = mx * zh, lse = hz + lg;
         const float left = __builtin_fmaf(mx, zh, -hz) + ((hz - lse) + lg);
@@ -170,10 +169,14 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
                 if (xb + 16 * i + r >= xl) v[r] = 0.f;
             }
             if (!live) v[0] = v[1] = v[2] = v[3] = 0.f;
+            if constexpr (WHOLE) {
+              halves(v, h[u], l[u]);
+            } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) h[u][r] = (typename E::e)v[r];
+              for (int r = 0; r < 4; ++r) h[u][r] = (typename E::e)v[r];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) l[u][r] = (typename E::e)(v[r] - (float)h[u][r]);
+              for (int r = 0; r < 4; ++r) l[u][r] = (typename E::e)(v[r] - (float)h[u][r]);
+            }
           }
           store_pair(o + 32 * i0, h[0], h[1], g);
           if (PL > 1 || ep.twin) store_pair(o + ep.Gplane + 32 * i0, l[0], l[1], g);
@@ -181,6 +184,14 @@ __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
       }
     }
   });
+}
+
+template <class E, class T, int PL, bool GRAD, bool MEND>
+__global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  if constexpr (PL > 1)
+    if (ep.sc->whole) return logits_tiles<E, T, PL, GRAD, MEND, true>(a, ep, lds);
+  logits_tiles<E, T, PL, GRAD, MEND, false>(a, ep, lds);
 }
 
 template <class E, class T, int PL, bool GRAD, bool MEND>

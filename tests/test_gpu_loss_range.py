@@ -1,0 +1,111 @@
+"""Vocabulary-head losses over the whole range of their types: masked rows (infinities, the
+type's lowest value, large finite ones), outliers, tiny and huge tensors, against float64.
+
+Bounds per element, as in plain fp32 arithmetic (u = 2^-21 for fp32's products and G):
+  logit  dz_iv = (D 2^-24 + u) sum_d |h_id w_vd|
+  g      eg_iv = u |g| + p_iv (dz_iv + max over rows that carry weight of dz_i. + 2^-20)
+               + 2^-39 where a row carries any weight (G's smallest step under its scale)
+  dh     sum_v eg |w| + (V 2^-24 + u) sum_v |g w|, dW alike over positions
+and a loss is off by 2 dz of the rows that carry weight and 2^-20 of its own terms."""
+import math
+
+import pytest
+import torch
+
+from tensor_train_compressed_ttembeddingbag_amd import loss as L
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -21}
+LOW = torch.finfo(torch.float32).min
+
+
+def inputs(n, v, d, seed, dt="fp32"):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    w = torch.randn(v, d, device="cuda", generator=g) * d ** -0.5
+    t = torch.randint(0, v, (n,), device="cuda", generator=g)
+    h = torch.randn(n, d, device="cuda", generator=g) + 5 * w[t]
+    return h.to(DT[dt]), w.to(DT[dt]), t, g
+
+
+def check(h, w, dt="fp32", up=None, t=None, tl=None, idx=None, T=1.0, columns=slice(None)):
+    """The public call and its gradients (reduction "none") against the definition."""
+    up = torch.ones(h.shape[0], device="cuda") if up is None else up
+    x, y = h.detach().requires_grad_(True), w.detach().requires_grad_(True)
+    if t is not None:
+        out = L.linear_cross_entropy(x, y, t, reduction="none")
+    else:
+        out = L.linear_distillation(x, y, tl, idx, temperature=T, reduction="none")
+    dh, dw = torch.autograd.grad(out, (x, y), up)
+    with torch.no_grad():
+        alone = L.linear_cross_entropy(h, w, t, reduction="none") if t is not None else \
+            L.linear_distillation(h, w, tl, idx, temperature=T, reduction="none")
+    u, uo = U[dt], (2.0 ** -24 if dt == "fp32" else U[dt])
+    H, W = h.double(), w.double()
+    n, d = H.shape
+    v = W.shape[0]
+    z = H @ W.t() / T
+    lse = torch.logsumexp(z, 1)
+    p = torch.exp(z - lse[:, None])
+    q = torch.zeros_like(z)
+    if t is not None:
+        q[torch.arange(n, device="cuda"), t] = 1
+        ent = torch.zeros_like(lse)
+    else:
+        lq = torch.log_softmax(tl.double() / T, 1)
+        q.scatter_add_(1, idx, lq.exp())
+        ent = (lq.exp() * lq).sum(1)
+    used = (p > 0) | (q > 0)
+    zq = torch.where(q > 0, q * z, torch.zeros_like(z))
+    scale = T * T if t is None else 1.0
+    rows = scale * (ent + lse - zq.sum(1))
+    abs_w = torch.where(torch.isinf(W), torch.zeros_like(W), W.abs())
+    dz = (d * 2.0 ** -24 + (2.0 ** -21 if dt == "fp32" else 0)) * (H.abs() @ abs_w.t()) / T
+    carry = torch.where((p > 2.0 ** -60) | (q > 0), dz, torch.zeros_like(dz)).amax(1)
+    bound = scale * (2 * carry + 2.0 ** -20 * (1 + ent.abs() + torch.where(
+        torch.isfinite(lse), lse.abs(), torch.zeros_like(lse)) * 2 ** -3))
+    for got in (out.detach(), alone):
+        assert torch.isfinite(got).all()
+        r = (got.double() - rows).abs() / bound
+        assert float(r.max()) <= 1, ("loss", float(r.max()), got[:4], rows[:4])
+    f = up.double() * (1.0 if t is not None else T)
+    g = (p - q) * f[:, None]
+    eg = (u * (p - q).abs() + p * (torch.minimum(dz, carry[:, None]) + carry[:, None] + 2.0 ** -20)
+          + 2.0 ** -22 * q + 2.0 ** -39 * used) * f.abs()[:, None]
+    extra = 2.0 ** -21 if dt == "fp32" else 0.0
+    # 0 x inf is NaN in the definition too: such elements are compared as NaN
+    for got, ref, b, name in ((dh, g @ W, eg @ abs_w + (v * 2.0 ** -24 + extra) * (g.abs() @ abs_w), "dh"),
+                              (dw, g.t() @ H, eg.t() @ H.abs() + (n * 2.0 ** -24 + extra) * (g.abs().t() @ H.abs()), "dW")):
+        got = got.double()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), name
+        b = b + uo * ref.abs() + (2.0 ** -25 if dt == "fp16" else 2.0 ** -133)
+        ok = ~torch.isnan(ref)
+        r = ((got - ref).abs() / b)[ok]
+        assert float(r.max()) <= 1, (name, float(r.max()))
+    return out.detach(), dh, dw
+
+
+def entries(n, v, k, g, allowed):
+    pick = torch.randint(0, allowed.numel(), (n, k), device="cuda", generator=g)
+    return torch.randn(n, k, device="cuda", generator=g) * 2, allowed[pick]
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("n,v,d", [(40, 700, 33), (300, 5000, 136)])
+@pytest.mark.parametrize("mask", [-math.inf])
+def test_rows_of_minus_infinity(mask, n, v, d, op):
+    """A bias column of -inf in half of the weight's rows, met by a hidden column of 1.0 or 0.3."""
+    print("case -inf", n, v, d, op, flush=True)
+    h, w, t, g = inputs(n, v, d, n)
+    h[:, d - 1] = torch.where(torch.arange(n, device="cuda") % 2 == 0, 1.0, 0.3)
+    off = torch.rand(v, device="cuda", generator=g) < 0.5
+    w[off, d - 1] = mask
+    w[~off, d - 1] = 0
+    free = (~off).nonzero()[:, 0]
+    if op == "xent":
+        check(h, w, t=free[torch.randint(0, free.numel(), (n,), device="cuda", generator=g)])
+    else:
+        tl, idx = entries(n, v, 5, g, free)
+        check(h, w, tl=tl, idx=idx, T=1.5)
