@@ -31,6 +31,7 @@ struct LossScalars {
   int count;       // positions that count
   int whole;       // fp32: the planes are the halves of the values' bits, see tt_gemm.h
   int ew, eh;      // exponents of the planes' scales, weight and hidden states (else 0)
+  int ge;          // exponent of the scale of G, see g_exp
   float zs;        // logits from sums of products: log2(e) / T over the planes' scales
   int ticket;      // blocks of k_loss that are done
 };
@@ -124,9 +125,13 @@ __device__ __forceinline__ int64_t dh_split_stride(int count, int by, int64_t ld
   return (int64_t)((count + by - 1) / by) * by * ld;
 }
 
-// G is held times 2^14 in fp16 and times 2^32 in bf16: the matrix cores take subnormal inputs
-// as zeros, and small probabilities are most of a vocabulary (|g| <= 1 keeps both in range).
+// G is held times 2^14 in fp16 and times 2^32 in bf16, as small probabilities are most of a
+// vocabulary and |g| <= 1 keeps both in range.  The matrix cores keep subnormal inputs, so a g
+// is off by half a step of 2^-38 or 2^-165 at least.  (LossScalars::ge: bf16 values near the
+// type's largest would overflow with this scale on G; where a position's largest sum of
+// products or its target's passes G_PLAIN, which tells, G is held as it is.)
 __host__ __device__ inline int g_exp(int dtype) { return dtype == TT_DTYPE_BF16 ? 32 : 14; }
+constexpr float G_PLAIN = 0x1p90f;
 
 // What the gradients' sums of products are multiplied by: the gradient of the loss (a mean's
 // over the positions that count; with a gradient per row, what the factors were divided by)
@@ -135,15 +140,15 @@ struct GradScale {
   const float *up;
   const LossScalars *sc;
   float base;
-  int mean, gexp;
+  int mean;
   __device__ __forceinline__ float get(int e) const {
     const float c = base * *up / (mean ? (float)max(sc->count, 1) : 1.f);
-    return sc->whole ? c : ldexpf(c, -e - gexp);
+    return ldexpf(c, -e - sc->ge);
   }
 };
 inline GradScale grad_scale(const LossArgs &a) {
   return {a.reduction == TT_REDUCE_NONE ? a.cm : a.up, a.sv.sc, a.k ? a.temp : 1.f,
-          a.reduction == TT_REDUCE_MEAN, g_exp(a.dtype)};
+          a.reduction == TT_REDUCE_MEAN};
 }
 
 // tile shapes (x by y): 0 = 256 x 256, 1 = 128 x 128 for two on a CU, 2 = 128 x 64,

@@ -255,6 +255,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
     if (blockIdx.x == 0 && lane == 0) {
       a.sv.sc->zs = ldexpf(LOG2E / a.temp, -(ew + eh));
       a.sv.sc->whole = whole;
+      a.sv.sc->ge = whole ? 0 : g_exp(a.dtype);
       a.sv.sc->ew = ew;
       a.sv.sc->eh = eh;
       a.sv.sc->ticket = 0;
@@ -435,6 +436,9 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   }
   const bool first = lane == 0 && part == 0 && i < a.N;
   if (slot >= 0 && first) {
+    if (std::is_same<S, __bf16>::value && !a.direct &&
+        !(fmaxf(fabsf(mx), a.k ? 0.f : fabsf(a.sv.zt[slot])) < G_PLAIN))
+      atomicMin(&a.sv.sc->ge, 0);
     a.sv.mx[slot] = mx;
     a.sv.lg[slot] = lg;
     if (a.k) {
@@ -515,7 +519,7 @@ __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64
   const int64_t v = a.sv.eidx[t] - v0;
   if (slot < 0 || a.sv.eidx[t] < 0 || v < 0 || v >= nv) return;
   const bool whole = PL > 1 && a.sv.sc->whole;
-  const int x = whole ? 0 : g_exp(a.dtype);
+  const int x = a.sv.sc->ge;
   const float q = ldexpf(__builtin_amdgcn_exp2f(0.5f * a.sv.ez[t]), x / 2);
   const float g = (q * q - ldexpf(a.sv.eq[t], x)) *
                   (a.reduction == TT_REDUCE_NONE ? a.rowf[slot] : 1.f);

@@ -31,7 +31,7 @@ struct LogitsEpi {
   const int64_t *tgt64;    // the caller's targets instead (loss alone), or null
   float *zt;
   int twin;
-  float one_e, e_v, gs;    // 1 - e, e / V, G's factor 2^g_exp
+  float one_e, e_v;        // 1 - e, e / V
 };
 
 template <class E, class T, int PL, bool GRAD, bool MEND, bool WHOLE>
@@ -89,16 +89,12 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         const float m0 = m == -INFINITY ? 0.f : m;  // nothing but -inf: every term is 0
-        // the exponent of the largest term is off 0 by the rounding of m zs alone, and so are all
-        // the others': taken back from the sum
-        const float mz = m0 * zs, off = __builtin_fmaf(m0, zs, -mz);
+        // the difference first: m zs overflows where all rows hold a type's lowest value
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zs, -mz));
-        s *= __builtin_amdgcn_exp2f(-off);
+          for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f((acc[i][j][r] - m0) * zs);
         s = sum_lane_groups(s);
         if (ep.zpart) zsum = sum_lane_groups(zsum);
         if (g == 0) {
@@ -128,18 +124,14 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
     } else {
       // p 2^g_exp as the square of exp2 of half the logit, times the row's factor: v_exp_f32
       // itself ends at 2^-126, bf16 and the gradients do not
-      const float zh = 0.5f * zs;
+      const float zh = 0.5f * zs, gs = ldexpf(1.f, ep.sc->ge);
 #pragma unroll
       for (int j = 0; j < T::NI; ++j) {
         const int pos = iy * T::Y + qy + 16 * j + c;
         const bool live = pos < count;
         if (ep.twin && qy + 16 * j >= ep.twin) continue;
         const float mx = live ? ep.mx[pos] : 0.f, lg = live ? 0.5f * ep.lg[pos] : 0.f,
-                    f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * (WHOLE ? 1.f : ep.gs) : 0.f;
-        // half lse, rounded, and what that left of it: 2^(-2 left) into the row's factor
-        const float hz = mx * zh, lse = hz + lg;
-        const float left = __builtin_fmaf(mx, zh, -hz) + ((hz - lse) + lg);
-        const float fp = f * __builtin_amdgcn_exp2f(-2.f * left);
+                    f = live ? (ep.rowf ? ep.rowf[pos] : 1.f) * gs : 0.f;
         const float ef = ep.e_v * f;
         const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
         const int d = live && ep.tgt ? (int)(ep.tgt[pos] - first) : -1;
@@ -155,8 +147,8 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
             float v[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], zh, -lse));
-              v[r] = __builtin_fmaf(q * q, fp, -ef);
+              const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r] - mx, zh, -lg));
+              v[r] = __builtin_fmaf(q * q, f, -ef);
             }
             if (hit) {
 #pragma unroll
@@ -237,7 +229,6 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.tgt = a.k ? nullptr : a.sv.tgt;
   ep.tgt64 = a.direct ? a.tgt : nullptr;
   ep.zt = a.k || grad ? nullptr : a.sv.zt;
-  ep.gs = ldexpf(1.f, g_exp(a.dtype));
   ep.one_e = 1.f - a.smoothing;
   ep.e_v = a.smoothing / (float)a.V;
   const LogitsCut cut = logits_cut(a, nv);

@@ -47,25 +47,24 @@ def check(h, w, dt="fp32", up=None, t=None, tl=None, idx=None, T=1.0, columns=sl
     n, d = H.shape
     v = W.shape[0]
     z = H @ W.t() / T
-    lse = torch.logsumexp(z, 1)
-    p = torch.exp(z - lse[:, None])
+    lp = torch.log_softmax(z, 1)  # (lse by itself has no digits left beside logits of 1e38)
+    p = lp.exp()
     q = torch.zeros_like(z)
     if t is not None:
         q[torch.arange(n, device="cuda"), t] = 1
-        ent = torch.zeros_like(lse)
+        ent = torch.zeros(n, dtype=torch.float64, device="cuda")
     else:
         lq = torch.log_softmax(tl.double() / T, 1)
         q.scatter_add_(1, idx, lq.exp())
         ent = (lq.exp() * lq).sum(1)
     used = (p > 0) | (q > 0)
-    zq = torch.where(q > 0, q * z, torch.zeros_like(z))
+    ql = torch.where(q > 0, q * lp, torch.zeros_like(z)).sum(1)
     scale = T * T if t is None else 1.0
-    rows = scale * (ent + lse - zq.sum(1))
+    rows = scale * (ent - ql)
     abs_w = torch.where(torch.isinf(W), torch.zeros_like(W), W.abs())
     dz = (d * 2.0 ** -24 + (2.0 ** -21 if dt == "fp32" else 0)) * (H.abs() @ abs_w.t()) / T
     carry = torch.where((p > 2.0 ** -60) | (q > 0), dz, torch.zeros_like(dz)).amax(1)
-    bound = scale * (2 * carry + 2.0 ** -20 * (1 + ent.abs() + torch.where(
-        torch.isfinite(lse), lse.abs(), torch.zeros_like(lse)) * 2 ** -3))
+    bound = scale * (2 * carry + 2.0 ** -20 * (1 + ent.abs() + ql.abs()))
     for got in (out.detach(), alone):
         assert torch.isfinite(got).all()
         r = (got.double() - rows).abs() / bound
@@ -81,8 +80,10 @@ def check(h, w, dt="fp32", up=None, t=None, tl=None, idx=None, T=1.0, columns=sl
         got = got.double()
         assert torch.equal(torch.isnan(got), torch.isnan(ref)), name
         b = b + uo * ref.abs() + (2.0 ** -25 if dt == "fp16" else 2.0 ** -133)
-        ok = ~torch.isnan(ref)
-        r = ((got - ref).abs() / b)[ok]
+        # a result whose bound reaches past the type's largest value may be infinite
+        over = torch.isinf(got) & (got.sign() == ref.sign()) & \
+            (ref.abs() + b >= torch.finfo(DT[dt]).max)
+        r = ((got - ref).abs() / b)[~torch.isnan(ref) & ~over]
         assert float(r.max()) <= 1, (name, float(r.max()))
     return out.detach(), dh, dw
 
@@ -109,3 +110,32 @@ def test_rows_of_minus_infinity(mask, n, v, d, op):
     else:
         tl, idx = entries(n, v, 5, g, free)
         check(h, w, tl=tl, idx=idx, T=1.5)
+
+
+def lowest_values(dt, op):
+    """A column of 1 in the weight meets the type's lowest value in some hidden states: all of
+    their logits are that value (other digits are lost in it, in float64 too but for fp16), and
+    the loss is log V.  So is a weight whose every row holds it."""
+    print("case lowest", dt, op, flush=True)
+    n, v, d = 37, 600, 40
+    h, w, t, g = inputs(n, v, d, 2, dt)
+    low = torch.finfo(DT[dt]).min
+    tl, idx = entries(n, v, 4, g, torch.arange(v, device="cuda"))
+    kw = dict(t=t) if op == "xent" else dict(tl=tl, idx=idx, T=2.0)
+    w1, h1 = w.clone(), h.clone()
+    w1[:, 7], h1[:, 7] = 1, 0
+    h1[::3, 7] = low
+    h1[::3, :7], h1[::3, 8:] = 0, 0
+    out, _, _ = check(h1, w1, dt, **kw)
+    if op == "xent":
+        assert float((out[::3] - math.log(v)).abs().max()) <= 2.0 ** -20 * math.log(v)
+    w2, h2 = w.clone(), h.clone()
+    w2[:, 7], h2[:, 7] = low, 1
+    if dt != "fp16":
+        h2[:, :7], h2[:, 8:] = 0, 0
+    check(h2, w2, dt, **kw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_positions_with_nothing_but_lowest_values(dt):
+    lowest_values(dt, "xent")
