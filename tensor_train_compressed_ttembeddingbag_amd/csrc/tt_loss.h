@@ -25,6 +25,7 @@ namespace ttb {
 
 constexpr int PACK_ROWS = 4;    // positions per block of k_pack
 constexpr int AMAX_BLOCKS = 1024;
+constexpr int RANGE_BITS = 14;  // see TensorRange
 
 // scalars that the device works out in the forward
 struct LossScalars {
@@ -76,8 +77,9 @@ struct LossArgs {
   int dh_bx, dh_by, cus;   // k_dhidden's tile, compute units
   LossSaved sv;
   // workspace
-  float *amax;             // [2 * AMAX_BLOCKS] block maxima of |weight| and |hidden| (fp32; infinite
-                           // where a value is not finite)
+  float *amax;             // [3][2 * AMAX_BLOCKS] (fp32) per block of the weight and of the positions:
+                           // largest |x| (infinite where a value is not finite), sum of the
+                           // exponents of the values that are not 0, how many these are
   char *wp;                // packed piece of the weight: [row][plane][Dp]
   float2 *part;            // [Npad][ptiles] (max, sum) in base 2
   float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)

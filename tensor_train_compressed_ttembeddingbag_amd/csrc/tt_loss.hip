@@ -77,15 +77,36 @@ __device__ __forceinline__ int plane_exp(float amax) {
   frexpf(amax, &e);  // amax < 2^e
   return min(15 - e, 120);
 }
-// block maxima -> the tensor's, in every lane of a wave
-__device__ __forceinline__ float largest(const float *amax, int lane) {
-  float m = 0.f;
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 127; }
+
+// What k_amax found of a tensor, in every lane of a wave.  Two parts hold a value to 22 bits
+// down to 2^-17 of the largest and to 2^-40 of the largest below; so they stand for a tensor
+// whose values lie near its largest, not for one that a mask or an outlier tops by far.
+// `spread` is how many powers of two the values' mean exponent lies below the largest's:
+// 4 to 5 for normal values, 12 with outliers of 1000 times the rest, 18 and more with a mask
+// of -1e4.  Up to RANGE_BITS the values in the middle keep their 22 bits with some to spare.
+struct TensorRange {
+  float top, spread;
+  __device__ __forceinline__ TensorRange(const float *amax, int lane) {
+    float m = 0.f, s = 0.f, n = 0.f;
 #pragma unroll
-  for (int u = 0; u < AMAX_BLOCKS / 64; ++u) m = fmaxf(m, amax[u * 64 + lane]);
+    for (int u = 0; u < AMAX_BLOCKS / 64; ++u) {
+      const float *p = amax + u * 64 + lane;
+      m = fmaxf(m, p[0]);
+      s += p[2 * AMAX_BLOCKS];
+      n += p[4 * AMAX_BLOCKS];
+    }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  return m;
-}
+    for (int o = 32; o > 0; o >>= 1) {
+      m = fmaxf(m, __shfl_xor(m, o));
+      s += __shfl_xor(s, o);
+      n += __shfl_xor(n, o);
+    }
+    top = m;
+    spread = n > 0.f ? exponent(m) - s / n : 0.f;
+  }
+  __device__ __forceinline__ bool in_parts() const { return top < INFINITY && spread <= RANGE_BITS; }
+};
 
 // ---------------------------------------------------------------- distillation entries
 // One wave per position: q = softmax(teacher / T) over its entries (index >= 0 and logit
@@ -164,8 +185,7 @@ __device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
   return t != a.ignore && t >= 0 && t < a.V;
 }
 
-// largest |x| of the weight (blocks 0 ..) and of the positions that count, per block: infinite
-// where one is NaN
+// amax: the weight (blocks 0 ..) and the positions that count
 __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
   const bool w = blockIdx.x < AMAX_BLOCKS;
   const int b = blockIdx.x % AMAX_BLOCKS, tid = threadIdx.x;
@@ -173,6 +193,7 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
   const int64_t rows = w ? a.V : a.N, ld = w ? a.wld : a.hld;
   const int64_t cpr = (a.D + 7) / 8, n = rows * cpr;
   float m = 0.f;
+  int es = 0, en = 0;
   int64_t i = (int64_t)b * 256 + tid;
   int64_t r = i / cpr, q = i % cpr;
   const int64_t dr = AMAX_BLOCKS * 256 / cpr, dq = AMAX_BLOCKS * 256 % cpr;
@@ -183,6 +204,8 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         m = fmaxf(m, v[e] == v[e] ? fabsf(v[e]) : INFINITY);
+        es += v[e] != 0.f ? exponent(v[e]) : 0;
+        en += v[e] != 0.f;
       }
     }
     r += dr;
@@ -191,10 +214,18 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  __shared__ float s[4];
-  if ((tid & 63) == 0) s[tid >> 6] = m;
+  float fs = (float)es, fn = (float)en;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) fs += __shfl_xor(fs, o), fn += __shfl_xor(fn, o);
+  __shared__ float s[3][4];
+  if ((tid & 63) == 0) s[0][tid >> 6] = m, s[1][tid >> 6] = fs, s[2][tid >> 6] = fn;
   __syncthreads();
-  if (tid == 0) a.amax[blockIdx.x] = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+  if (tid == 0) {
+    float *o = a.amax + blockIdx.x;
+    o[0] = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+    o[2 * AMAX_BLOCKS] = s[1][0] + s[1][1] + s[1][2] + s[1][3];
+    o[4 * AMAX_BLOCKS] = s[2][0] + s[2][1] + s[2][2] + s[2][3];
+  }
 }
 
 // Rows of the hidden states that count, in order, from row 0 of hp on.  The backward sums over
@@ -216,7 +247,8 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
 // average, which up to some 10^5 positions costs less than another launch to scan them.
 template <class S, class E, int PL>
 __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
-  __shared__ int s_n[4], s_slot[PACK_ROWS];
+  __shared__ int s_n[4], s_slot[PACK_ROWS], s_parts[2];
+  __shared__ float s_top[2];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t i0 = (int64_t)blockIdx.x * PACK_ROWS, ib = min(i0, a.N);
   int n = 0;
@@ -225,14 +257,17 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
   if (lane == 0) s_n[wv] = n;
+  if (PL > 1 && wv < 2) {  // the weight's range, the positions'
+    const TensorRange t(a.amax + wv * AMAX_BLOCKS, lane);
+    if (lane == 0) s_top[wv] = t.top, s_parts[wv] = t.in_parts();
+  }
   __syncthreads();
   const int base = s_n[0] + s_n[1] + s_n[2] + s_n[3];
   int ew = 0, eh = 0;
   bool whole = false;
   if (PL > 1) {
-    const float mw = largest(a.amax, lane), mh = largest(a.amax + AMAX_BLOCKS, lane);
-    whole = !(mw < INFINITY && mh < INFINITY);
-    if (!whole) ew = plane_exp(mw), eh = plane_exp(mh);
+    whole = !(s_parts[0] && s_parts[1]);
+    if (!whole) ew = plane_exp(s_top[0]), eh = plane_exp(s_top[1]);
   }
   if (wv == 0) {
     const int64_t i = i0 + lane;
@@ -661,7 +696,7 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     a.direct = a.N <= 64 && a.D % 8 == 0 && a.planes == 1;
     b.off = saved_layout(a, ws);
   }
-  b.take(a.amax, grad || a.planes == 1 ? 0 : 2 * AMAX_BLOCKS);
+  b.take(a.amax, grad || a.planes == 1 ? 0 : 3 * 2 * AMAX_BLOCKS);
   int64_t rows = a.V;
   const int64_t wrow = a.Dp * 2 * a.planes, grow = a.Npad * 2 * a.planes;
   int64_t lim = (1ll << 38) / std::max<int64_t>(a.Npad, 256);  // tiles of one launch

@@ -139,3 +139,49 @@ def lowest_values(dt, op):
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_positions_with_nothing_but_lowest_values(dt):
     lowest_values(dt, "xent")
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("n,v,d", [(40, 700, 33), (300, 5000, 136), (40, 700, 6)])
+@pytest.mark.parametrize("mask", [LOW, -1e30, -1e9, -1e6, -1e4, -100.0])
+def test_rows_masked_by_large_finite_values(mask, n, v, d, op):
+    """Masked rows far below the others leave the others' digits alone, whether half or nearly
+    all of the rows are masked."""
+    print("case mask", mask, n, v, d, op, flush=True)
+    for share in (0.5, 0.99):
+        h, w, t, g = inputs(n, v, d, n)
+        h[:, d - 1] = 1.0
+        off = torch.rand(v, device="cuda", generator=g) < share
+        off[:2] = False
+        w[off, d - 1] = mask
+        w[~off, d - 1] = 0
+        free = (~off).nonzero()[:, 0]
+        if op == "xent":
+            check(h, w, t=free[torch.randint(0, free.numel(), (n,), device="cuda", generator=g)])
+        else:
+            tl, idx = entries(n, v, 5, g, free)
+            check(h, w, tl=tl, idx=idx, T=1.5)
+
+
+@pytest.mark.parametrize("factor", [1e3, 1e9, 1e25])
+@pytest.mark.parametrize("where", ["position", "row", "column"])
+def test_outliers(where, factor):
+    """One position, one row of the weight or one column many times the rest (the position and
+    the row with logits to match; the column against as small a one of the weight)."""
+    print("case outlier", where, factor, flush=True)
+    n, v, d = 70, 900, 48
+    h, w, t, g = inputs(n, v, d, 3)
+    if where == "position":
+        h[5] *= factor
+    elif where == "row":
+        w[7] *= factor
+        t[t == 7] = 8
+    else:
+        h[:, 4] *= factor
+        w[:, 4] /= factor
+    check(h, w, t=t)
+    check(h, w, t=t, up=torch.rand(n, device="cuda", generator=g))
+
+
+def test_fp32_positions_with_nothing_but_the_lowest_value():
+    lowest_values("fp32", "xent")
