@@ -424,9 +424,10 @@ int tt_full_weight(const tt_desc *desc, const float *const cores[3], int table, 
  * 16-bit inputs are exact and summed in fp32; fp32 inputs enter the matrix cores as two fp16
  * parts each: 22 bits of a value down to 2^-17 of the tensor's largest, and an absolute 2^-40 of
  * the largest below that.  A tensor that this does not suit -- one with a value that is not
- * finite, or whose values lie on average more than 14 powers of two below the largest (a mask
- * of -1e4 and up, an outlier) -- is multiplied as it is, in fp32 products at about a third of
- * the speed; the device decides.  The logits'
+ * finite, whose largest lies outside 2^-50 .. 2^79 (the product of both tensors' largest outside
+ * 2^-35 .. 2^94), or whose values lie on average more than 14 powers of two below the largest (a
+ * mask of -1e4 and up, an outlier) -- is multiplied as it is, in fp32 products at about a third
+ * of the speed; the device decides.  The logits'
  * gradient is rounded once to the inputs' 16-bit type (fp32, and up to 32 positions of any
  * type: two parts).  No result depends on the order of atomics.  The calls enqueue kernels
  * only and may be captured into a HIP graph (make one call of the kind before).

@@ -75,7 +75,12 @@ __device__ __forceinline__ int plane_exp(float amax) {
   if (!(amax > 0.f)) return 0;
   int e;
   frexpf(amax, &e);  // amax < 2^e
-  return min(15 - e, 120);
+  return 15 - e;
+}
+// Tiny and huge tensors are multiplied as they are: the scales are taken back as zs 2^-(ew + eh)
+// and 2^-(e + ge) of a gradient, which have to be normal numbers whatever T and the gradient.
+__device__ __forceinline__ bool plane_exps_in_range(int ew, int eh) {
+  return max(max(abs(ew), abs(eh)), abs(ew + eh)) <= 64;
 }
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 127; }
 
@@ -268,6 +273,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
   if (PL > 1) {
     whole = !(s_parts[0] && s_parts[1]);
     if (!whole) ew = plane_exp(s_top[0]), eh = plane_exp(s_top[1]);
+    if (!plane_exps_in_range(ew, eh)) whole = true, ew = eh = 0;
   }
   if (wv == 0) {
     const int64_t i = i0 + lane;

@@ -185,3 +185,17 @@ def test_outliers(where, factor):
 
 def test_fp32_positions_with_nothing_but_the_lowest_value():
     lowest_values("fp32", "xent")
+
+
+@pytest.mark.parametrize("sh,sw", [(1e-23, 1e-23), (1e-30, 1e-3), (1e-19, 1e-19), (1e25, 1e-25),
+                                   (1e-28, 1e27)])
+def test_tiny_and_huge_tensors(sh, sw):
+    """The loss of tiny inputs is log V, not NaN; opposite scales cancel."""
+    print("case scale", sh, sw, flush=True)
+    for n, v, d in ((3, 37, 8), (130, 1500, 40)):
+        h, w, t, _ = inputs(n, v, d, n)
+        out, _, _ = check(h * sh, w * sw, t=t)
+        if sh * sw < 1e-20:
+            assert float((out - math.log(v)).abs().max()) <= 2.0 ** -20 * math.log(v)
+        tl, idx = entries(n, v, 4, torch.Generator(device="cuda"), torch.arange(v, device="cuda"))
+        check(h * sh, w * sw, tl=tl, idx=idx, T=2.0)
