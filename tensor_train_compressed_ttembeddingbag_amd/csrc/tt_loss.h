@@ -7,9 +7,9 @@
 //   dloss_i/d<hidden_i, weight_v> = s g_iv,  g_iv = exp(z_iv - lse_i) - e / V - sum of the
 //   position's q on v (the target's q is 1 - e), s = 1 or T.
 //
-// forward:  k_entries (distillation: q, duplicates merged) -> k_pack (positions that count,
-//           packed) -> k_logits (running maximum and sum per position and tile of the weight)
-//           -> k_loss (lse, the entries' logits, loss).  A loss alone of up to 64 positions
+// forward:  k_entries (distillation: q, sorted, repeated rows merged) -> k_pack (positions that
+//           count, packed) -> k_logits (running maximum and sum per position and tile of the
+//           weight; the sums of products of targets and entries) -> k_loss (lse, loss).  A loss alone of up to 64 positions
 //           leaves k_pack out.
 // backward: per piece of the vocabulary k_logits (G = row factor * g, in 16 bits), k_entries_g
 //           (distillation: the entries of G), k_dhidden (split over the vocabulary, fp32),
@@ -47,8 +47,10 @@ struct LossSaved {
                    // 2^((sum of products - mx) zs): lse in base 2 is mx zs + lg.  In two parts,
                    // because exp(z - lse) and a small loss lose what their rounded sum loses
   float *zt;       // [N] packed row -> the target's sum of products (cross entropy)
-  int *eidx;       // [N][k] distillation entries: row of the weight or -1
-  float *eq, *ez;  // their q and their log2 p
+  int *eidx;       // [N][k] distillation entries by row of the weight, the empty ones (-1) last
+  float *eq, *ez;  // their q (of a repeated row at its first entry, 0 behind) and their sums of
+                   // products, which k_loss turns into log2 p
+  int *at;         // [N] packed row -> position (distillation)
   float *ent;      // [N] sum_j q log q
 };
 
@@ -84,12 +86,19 @@ struct LossArgs {
   float2 *part;            // [Npad][ptiles] (max, sum) in base 2
   float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)
   float *rowloss;          // [N]
+  unsigned short *dir;     // [N][groups + 1] distillation: the first entry of each group of 2^gshift
+                           // rows of the weight
+  int gshift, groups;
   float *rowf;             // [Npad] factor of a packed row's g (a gradient per row; else null)
   float *cm;               // what the factors were divided by
   char *G;                 // [Npad][planes][piece]
   int64_t ldG, Gplane;     // bytes; Gplane: to the second part of a row of G (plane or twin)
   float *dhp;              // [splits][tiles of positions that count][Dp]
 };
+
+// Groups of the weight's rows in the entries' directory: at least 256 rows, so that a tile's
+// rows lie in one, and 2 KiB a position at most, so that a group has few entries.
+constexpr int DIR_GROUPS = 1024;
 
 constexpr int DH_SPLITS = 64;   // most splits of the vocabulary in k_dhidden: a lane each
 constexpr int DH_TILES = 1024;  // most tiles of it where there are several splits

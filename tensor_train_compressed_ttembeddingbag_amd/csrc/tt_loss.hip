@@ -115,29 +115,37 @@ struct TensorRange {
 
 // ---------------------------------------------------------------- distillation entries
 // One wave per position: q = softmax(teacher / T) over its entries (index >= 0 and logit
-// above -inf); entries of one row of the weight are added into the first of them, so that
-// every (position, row) is written once.  sv.tgt[i]: whether position i has entries.
+// above -inf), sorted by row, so that repeated rows lie side by side and k_logits finds the
+// entries of a tile in a directory; their q are added into the first, so that every (position,
+// row) of G is written once.  (q is the lower half of the key: the order of a sum, and with it
+// the result, does not depend on the sort's steps.)  sv.tgt[i]: whether position i has entries.
+// pow2: the power of two from k on.
 template <class S>
-__global__ __launch_bounds__(256) void k_entries(LossArgs a) {
+__global__ __launch_bounds__(256) void k_entries(LossArgs a, int pow2) {
   extern __shared__ __attribute__((aligned(16))) char dyn[];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, k = a.k;
   const int64_t i = (int64_t)blockIdx.x * 4 + wv;
   if (i >= a.N) return;  // no workgroup barrier below: waves keep to their own LDS
-  int *id = (int *)dyn + wv * 2 * k;
-  float *q = (float *)(id + k);
+  struct Entry {
+    unsigned q, row;  // bits of q; none: ~0
+  };
+  union Key {
+    Entry e;
+    uint64_t u;
+  };
+  Key *key = (Key *)dyn + wv * pow2;
   const float it = 1.f / a.temp;
   float m = -INFINITY;
   bool bad = false, any = false, nan = false;
-  for (int j = lane; j < k; j += 64) {
-    const int64_t v = a.tgt[i * k + j];
-    float t = (float)((const S *)a.tlogits)[i * k + j] * it;
+  for (int j = lane; j < pow2; j += 64) {
+    const int64_t v = j < k ? a.tgt[i * k + j] : -1;
+    const float t = j < k ? (float)((const S *)a.tlogits)[i * k + j] * it : -INFINITY;
     bad |= v >= a.V;
     const bool in = v >= 0 && v < a.V && !(t == -INFINITY);
-    id[j] = in ? (int)v : -1;
-    q[j] = in ? t : -INFINITY;
+    key[j].e = {__float_as_uint(in ? t : -INFINITY), in ? (unsigned)v : ~0u};
     any |= in;
     nan |= in && t != t;
-    m = fmaxf(m, q[j]);
+    if (in) m = fmaxf(m, t);
   }
   if (__any(bad) && lane == 0) set_status(a.status, TT_DEV_BAD_INDEX);
   any = __any(any);
@@ -146,36 +154,50 @@ __global__ __launch_bounds__(256) void k_entries(LossArgs a) {
   if (__any(nan)) m = __builtin_nanf("");
   float s = 0.f;
   for (int j = lane; j < k; j += 64)
-    if (id[j] >= 0) s += expf(q[j] - m);
+    if (key[j].e.row != ~0u) s += expf(__uint_as_float(key[j].e.q) - m);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
   const float ls = logf(s);
   float ent = 0.f;
   for (int j = lane; j < k; j += 64) {
-    if (id[j] < 0) continue;
-    const float lq = q[j] - m - ls, p = expf(lq);
-    q[j] = p;
+    if (key[j].e.row == ~0u) continue;
+    const float lq = __uint_as_float(key[j].e.q) - m - ls, p = expf(lq);
+    key[j].e.q = __float_as_uint(p);
     if (!(p == 0.f)) ent += p * lq;
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) ent += __shfl_xor(ent, o);
-  __builtin_amdgcn_wave_barrier();
-  __threadfence_block();
-  for (int j = lane; j < k; j += 64) {
-    int own = id[j];
-    float p = 0.f;
-    if (own >= 0) {
-      for (int u = 0; u < k; ++u) {
-        if (id[u] != own) continue;
-        if (u < j) {
-          own = -1;
-          break;
+  auto settle = [] {
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+  };
+  settle();
+  for (int size = 2; size <= pow2; size <<= 1)
+    for (int st = size >> 1; st > 0; st >>= 1) {
+      for (int x = lane; x < pow2 / 2; x += 64) {
+        const int lo = 2 * x - (x & (st - 1)), hi = lo + st;
+        const uint64_t p = key[lo].u, q = key[hi].u;
+        if ((p > q) == ((lo & size) == 0)) {
+          key[lo].u = q;
+          key[hi].u = p;
         }
-        p += q[u];
       }
+      settle();
     }
-    a.sv.eidx[i * k + j] = own;
-    a.sv.eq[i * k + j] = own < 0 ? 0.f : p;
+  for (int j = lane; j < k; j += 64) {
+    const unsigned row = key[j].e.row;
+    float p = 0.f;
+    if (row != ~0u && (j == 0 || key[j - 1].e.row != row))
+      for (int u = j; u < k && key[u].e.row == row; ++u) p += __uint_as_float(key[u].e.q);
+    a.sv.eidx[i * k + j] = (int)row;
+    a.sv.eq[i * k + j] = p;
+  }
+  for (int b = lane; b <= a.groups; b += 64) {
+    const unsigned row = b < a.groups ? (unsigned)b << a.gshift : ~0u;
+    int n = 0;  // entries below it
+    for (int st = pow2; st > 0; st >>= 1)
+      if (n + st <= k && key[n + st - 1].e.row < row) n += st;
+    a.dir[i * (a.groups + 1) + b] = (unsigned short)n;
   }
   if (lane == 0) {
     a.sv.ent[i] = ent;
@@ -285,7 +307,9 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
     if (in) {
       slot = ok ? rank : -1 - (int)(a.N - 1 - (i - rank));
       a.sv.slot[i] = slot;
-      if (!a.k) {
+      if (a.k) {
+        if (ok) a.sv.at[rank] = (int)i;
+      } else {
         const int64_t t = a.tgt[i];
         if (ok) a.sv.tgt[rank] = (int)t;
         else if (t != a.ignore) set_status(a.status, TT_DEV_BAD_INDEX);
@@ -377,12 +401,10 @@ __device__ __forceinline__ void sum_rows(const LossArgs &a, double *s_d) {
   }
 }
 
-// NW waves per position: the tiles' statistics become its lse.  Distillation: the logits of the
-// entries are dot products of their own, in fp64 (a small divergence is the difference of
-// large terms), a wave each, U at once.
-// Gathers one row of the weight per entry: 2048 x 32 entries of 2048 fp16 in 38 us, 7 TB/s out
-// of the last-level cache.
-template <class S, int NW, int U>
+// NW waves per position: the tiles' statistics become its lse.  The logits of the target and
+// of the entries are the ones in these sums (a small loss is the difference of large terms);
+// the sum over the entries is taken in fp64.
+template <int NW>
 __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   __shared__ float s_m[4], s_s[4], s_z[4];
   __shared__ double s_d[4], s_q[4];
@@ -427,48 +449,17 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   }
   const float mx = wm == -INFINITY ? 0.f : wm, lg = log2f(s);
   double qd = 0.0;  // sum over the entries of q (lse - logit), base 2
+  float far = fabsf(mx);
   if (a.k && slot >= 0) {
-    const double lse = (double)mx * zs + lg;
-    // the same scale as in lse, on the inputs themselves
-    const double sc = a.direct ? zs : ldexpf(zs, a.sv.sc->ew + a.sv.sc->eh);
-    const S *h = (const S *)a.hidden + i * a.hld;
-    // U entries: one read of the position's row, U + 1 loads in flight
-    for (int j0 = part * U; j0 < a.k; j0 += U * NW) {
-      const S *w[U];
-      bool on[U];
-      double d[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = min(j0 + u, a.k - 1), v = a.sv.eidx[i * a.k + j];
-        on[u] = j0 + u < a.k && v >= 0;
-        w[u] = (const S *)a.weight + max(v, 0) * a.wld;  // no entry: any row, not counted
-        d[u] = 0.0;
-      }
-      auto dots = [&](auto whole) {
-        for (int64_t c = lane * 8; c < a.D; c += 512) {
-          S x[8], y[U][8];
-          load8_at<decltype(whole)::value>(h, c, a.D, true, x);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            load8_at<decltype(whole)::value>(w[u], c, a.D, true, y[u]);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[u] += (double)(float)x[e] * (double)(float)y[u][e];
-        }
-      };
-      if (a.D % 8 == 0) dots(std::true_type());
-      else dots(std::false_type());
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (!on[u]) continue;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) d[u] += __shfl_xor(d[u], o);
-        const double lp = d[u] * sc - lse;
-        qd -= (double)a.sv.eq[i * a.k + j0 + u] * lp;
-        if (lane == 0) a.sv.ez[i * a.k + j0 + u] = (float)lp;
-      }
+    for (int64_t t = i * a.k + part * 64 + lane; t < (i + 1) * a.k; t += 64 * NW) {
+      if (a.sv.eidx[t] < 0) break;
+      const float z = a.sv.ez[t], q = a.sv.eq[t];
+      const double lp = ((double)z - mx) * zs - lg;
+      if (!(q == 0.f)) qd -= q * lp, far = fmaxf(far, fabsf(z));
+      a.sv.ez[t] = (float)lp;
     }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) qd += __shfl_xor(qd, o);
   }
   if (NW > 1 && a.k) {
     if (lane == 0) s_q[wv] = qd;
@@ -476,10 +467,10 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
     qd = s_q[0] + s_q[1] + s_q[2] + s_q[3];
   }
   const bool first = lane == 0 && part == 0 && i < a.N;
+  if (slot >= 0 && !a.k) far = fmaxf(far, fabsf(a.sv.zt[slot]));
+  if (a.dtype == TT_DTYPE_BF16 && !a.direct && slot >= 0 && !(far < G_PLAIN))
+    atomicMin(&a.sv.sc->ge, 0);
   if (slot >= 0 && first) {
-    if (std::is_same<S, __bf16>::value && !a.direct &&
-        !(fmaxf(fabsf(mx), a.k ? 0.f : fabsf(a.sv.zt[slot])) < G_PLAIN))
-      atomicMin(&a.sv.sc->ge, 0);
     a.sv.mx[slot] = mx;
     a.sv.lg[slot] = lg;
     if (a.k) {
@@ -559,6 +550,7 @@ __global__ __launch_bounds__(256) void k_entries_g(LossArgs a, int64_t v0, int64
   const int slot = a.sv.slot[i];
   const int64_t v = a.sv.eidx[t] - v0;
   if (slot < 0 || a.sv.eidx[t] < 0 || v < 0 || v >= nv) return;
+  if (t > i * a.k && a.sv.eidx[t - 1] == a.sv.eidx[t]) return;  // its row's first has all of q
   const bool whole = PL > 1 && a.sv.sc->whole;
   const int x = a.sv.sc->ge;
   const float q = ldexpf(__builtin_amdgcn_exp2f(0.5f * a.sv.ez[t]), x / 2);
@@ -686,6 +678,7 @@ static int64_t saved_layout(LossArgs &a, void *saved) {
     b.take(a.sv.eidx, a.N * a.k);
     b.take(a.sv.eq, a.N * a.k);
     b.take(a.sv.ez, a.N * a.k);
+    b.take(a.sv.at, a.N);
   }
   return b.off;
 }
@@ -733,6 +726,12 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     b.take(a.part, a.Npad * a.ptiles);
     b.take(a.zpart, a.smoothing > 0.f ? a.Npad * a.ptiles : 0);
     b.take(a.rowloss, a.N);
+    if (a.k) {
+      a.gshift = 8;
+      while ((a.V - 1) >> a.gshift >= DIR_GROUPS) ++a.gshift;
+      a.groups = (int)((a.V - 1) >> a.gshift) + 1;
+      b.take(a.dir, a.N * (a.groups + 1));
+    }
   }
   return b.off;
 }
@@ -802,10 +801,12 @@ static hipError_t launch_pack_w(const LossArgs &a, int64_t v0, int64_t nv, hipSt
 
 static hipError_t launch_entries(const LossArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)((a.N + 3) / 4));
-  const size_t lds = (size_t)a.k * 32;  // at most 64 KiB
-  if (a.tdtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_entries<float>, grid, dim3(256), lds, s, a);
-  else if (a.tdtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_entries<__bf16>, grid, dim3(256), lds, s, a);
-  else tt_launch(K_LOSS_ROWS, k_entries<_Float16>, grid, dim3(256), lds, s, a);
+  int pow2 = 1;
+  while (pow2 < a.k) pow2 *= 2;
+  const size_t lds = (size_t)pow2 * 32;  // at most 64 KiB
+  if (a.tdtype == TT_DTYPE_F32) tt_launch(K_LOSS_ROWS, k_entries<float>, grid, dim3(256), lds, s, a, pow2);
+  else if (a.tdtype == TT_DTYPE_BF16) tt_launch(K_LOSS_ROWS, k_entries<__bf16>, grid, dim3(256), lds, s, a, pow2);
+  else tt_launch(K_LOSS_ROWS, k_entries<_Float16>, grid, dim3(256), lds, s, a, pow2);
   return hipGetLastError();
 }
 
@@ -814,22 +815,12 @@ static hipError_t launch_entries(const LossArgs &a, hipStream_t s) {
 // them), so more rows are added in a launch of its own (about 5 us).
 constexpr int64_t LOSS_TICKETS = 256;
 
-template <class S>
-static void launch_loss(const LossArgs &a, int ticket, hipStream_t s) {
-  // one entry and few statistics: a wave per position
-  if (!a.k && a.ptiles <= 256)
-    tt_launch(K_LOSS_ROWS, k_loss<S, 1, 1>, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, ticket);
-  else if (!a.k)
-    tt_launch(K_LOSS_ROWS, k_loss<S, 4, 1>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
-  else
-    tt_launch(K_LOSS_ROWS, k_loss<S, 4, 4>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
-}
-
 static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
   const int ticket = a.N <= LOSS_TICKETS && !a.direct;  // (k_pack clears the ticket)
-  if (a.dtype == TT_DTYPE_F32) launch_loss<float>(a, ticket, s);
-  else if (a.dtype == TT_DTYPE_BF16) launch_loss<__bf16>(a, ticket, s);
-  else launch_loss<_Float16>(a, ticket, s);
+  if (a.ptiles <= 256 && a.k <= 256)  // few statistics and entries: a wave per position
+    tt_launch(K_LOSS_ROWS, k_loss<1>, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, ticket);
+  else
+    tt_launch(K_LOSS_ROWS, k_loss<4>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
   if (a.reduction != TT_REDUCE_NONE && !ticket)
     tt_launch(K_LOSS_ROWS, k_loss_sum, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();

@@ -30,6 +30,11 @@ struct LogitsEpi {
   const int *tgt;          // null with distillation
   const int64_t *tgt64;    // the caller's targets instead (loss alone), or null
   float *zt;
+  int k;                   // distillation: entries per position
+  const int *eidx, *at;    // at: null where positions are not packed
+  float *ez;
+  const unsigned short *dir;
+  int gshift, groups;
   int twin;
   float one_e, e_v;        // 1 - e, e / V
 };
@@ -55,6 +60,41 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
         const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
         const int64_t t = !ep.zt || pos >= count ? -1 : ep.tgt64 ? ep.tgt64[pos] : ep.tgt[pos];
         d_[j] = (int)max<int64_t>(min<int64_t>(t - first, 1 << 20), -1);
+      }
+      if (ep.k) {
+        // the entries that this wave's rows hold: each lane writes the sums of its rows
+        const unsigned lo = (unsigned)(ep.v0 + (int64_t)ix * T::X + px),
+                       hi = lo + max(min(xl - px, T::wx), 0);
+        int64_t e[T::NI];
+        int n[T::NI], end[T::NI];
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) {
+          const int pos = iy * T::Y + qy + 16 * j + c, row = pos < count ? pos : 0;
+          e[j] = ep.at ? ep.at[row] : row;
+        }
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) {
+          const unsigned short *dir = ep.dir + e[j] * (ep.groups + 1) + (lo >> ep.gshift);
+          n[j] = lo < hi ? dir[0] : 0;
+          end[j] = lo < hi && iy * T::Y + qy + 16 * j + c < count ? dir[1] : 0;
+          e[j] *= ep.k;
+        }
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) {
+          for (int u = n[j]; u < end[j]; ++u) {
+            const unsigned row = ep.eidx[e[j] + u];
+            if (row >= hi) break;
+            if (row < lo) continue;
+            const int d = (int)(row - lo) - 4 * g;
+            if (d < 0 || (d & 12)) continue;
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) z = d == 16 * i + r ? acc[i][j][r] : z;
+            ep.ez[e[j] + u] = z;
+          }
+        }
       }
 #pragma unroll
       for (int j = 0; j < T::NI; ++j) {
@@ -229,6 +269,9 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.tgt = a.k ? nullptr : a.sv.tgt;
   ep.tgt64 = a.direct ? a.tgt : nullptr;
   ep.zt = a.k || grad ? nullptr : a.sv.zt;
+  ep.k = grad ? 0 : a.k;
+  ep.eidx = a.sv.eidx; ep.at = a.direct ? nullptr : a.sv.at; ep.ez = a.sv.ez;
+  ep.dir = a.dir; ep.gshift = a.gshift; ep.groups = a.groups;
   ep.one_e = 1.f - a.smoothing;
   ep.e_v = a.smoothing / (float)a.V;
   const LogitsCut cut = logits_cut(a, nv);
