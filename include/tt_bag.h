@@ -429,7 +429,9 @@ int tt_full_weight(const tt_desc *desc, const float *const cores[3], int table, 
  * mask of -1e4 and up, an outlier) -- is multiplied as it is, in fp32 products at about a third
  * of the speed; the device decides.  The logits'
  * gradient is rounded once to the inputs' 16-bit type (fp32, and up to 32 positions of any
- * type: two parts).  No result depends on the order of atomics.  The calls enqueue kernels
+ * type: two parts).  fp16 parts of it end at steps of 2^-38 (p - q near 1 being 2^0): what is
+ * smaller is off by up to half of that, in grad_hidden relative to the position's own gradient
+ * (2^-33 of it where that is under 1/16 of the largest), in grad_weight to the largest.  No result depends on the order of atomics.  The calls enqueue kernels
  * only and may be captured into a HIP graph (make one call of the kind before).
  *
  * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, d <= 2^20, strides <= 2^21, k <= 2048,

@@ -90,6 +90,7 @@ struct LossArgs {
                            // rows of the weight
   int gshift, groups;
   float *rowf;             // [Npad] factor of a packed row's g (a gradient per row; else null)
+  int *rowe;               // [Npad] exponent that a light row's factor leaves out, see LIGHT
   float *cm;               // what the factors were divided by
   char *G;                 // [Npad][planes][piece]
   int64_t ldG, Gplane;     // bytes; Gplane: to the second part of a row of G (plane or twin)
@@ -99,6 +100,14 @@ struct LossArgs {
 // Groups of the weight's rows in the entries' directory: at least 256 rows, so that a tile's
 // rows lie in one, and 2 KiB a position at most, so that a group has few entries.
 constexpr int DIR_GROUPS = 1024;
+
+// A gradient per position in fp16 G: factors down to 2^-LIGHT of the largest go into G, whose
+// range has that much to spare.  A smaller one would push its row's G below fp16's steps, and
+// with it all of the position's dh: it goes into G times a power of two, which dh's sums take
+// back.  dweight adds the positions up, so there G gets its right size first (k_light_rows,
+// which reads and writes such rows only: 4096 x 32000 x 2048 fp16, 1840 us with none or with
+// factors spread evenly over 0 .. 1, 1871 with half of the rows light, 1907 with all but one).
+constexpr int LIGHT = 4;
 
 constexpr int DH_SPLITS = 64;   // most splits of the vocabulary in k_dhidden: a lane each
 constexpr int DH_TILES = 1024;  // most tiles of it where there are several splits

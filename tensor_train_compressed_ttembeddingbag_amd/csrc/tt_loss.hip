@@ -510,13 +510,14 @@ __global__ __launch_bounds__(1024) void k_loss_sum(LossArgs a) {
 
 // ---------------------------------------------------------------- backward, around the products
 // With a gradient per position: the factor of every packed row's g.  G in fp16 needs |factor|
-// <= 1 (2^14 g fits, and small factors keep their bits), so the factors are divided by the
-// power of two above the largest finite one, which every block finds for itself.
+// <= 1 (2^14 g fits), so the factors are divided by the power of two above the largest finite
+// one, which every block finds for itself; light ones come in two parts, see LIGHT.
 __global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
   __shared__ float s_m[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   float cm = 1.f;
-  if (a.dtype != TT_DTYPE_BF16 && !a.sv.sc->whole) {
+  const bool scaled = a.dtype != TT_DTYPE_BF16 && !a.sv.sc->whole;
+  if (scaled) {
     float m = 0.f;
 #pragma unroll 4
     for (int64_t i = tid; i < a.N; i += 256) {
@@ -537,7 +538,34 @@ __global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
   if (blockIdx.x == 0 && tid == 0) *a.cm = cm;
   for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < a.N; i += (int64_t)gridDim.x * 256) {
     const int slot = a.sv.slot[i];
-    if (slot >= 0) a.rowf[slot] = a.up[i] / cm;
+    if (slot < 0) continue;
+    const float f = a.up[i] / cm;
+    int e = 0;
+    if (scaled && fabsf(f) < INFINITY) {
+      frexpf(f, &e);
+      e = min(e + LIGHT, 0);
+    }
+    a.rowf[slot] = ldexpf(f, -e);
+    a.rowe[slot] = e;
+  }
+}
+
+// G of the light rows at its right size, for dweight
+__global__ __launch_bounds__(256) void k_light_rows(LossArgs a) {
+  const int count = a.sv.sc->count;
+  for (int64_t r = blockIdx.x; r < count; r += gridDim.x) {
+    const int e = a.rowe[r];
+    if (e == 0) continue;
+    const float s = ldexpf(1.f, e);
+    for (int part = 0; part < (a.twin ? 2 : 1); ++part) {
+      hf8 *g = (hf8 *)(a.G + (r + part * a.twin) * a.ldG);
+      for (int64_t c = threadIdx.x; c < a.ldG / 16; c += 256) {
+        hf8 v = g[c];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = (_Float16)((float)v[u] * s);
+        g[c] = v;
+      }
+    }
   }
 }
 
@@ -591,6 +619,12 @@ __global__ __launch_bounds__(256) void k_dhidden_out(LossArgs a, DhPlan plan, Gr
         v += w;
       }
       v *= c_dh;
+      if (a.reduction == TT_REDUCE_NONE) {
+        const int e = a.rowe[slot];
+        if (e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = ldexpf(v[r], e);
+      }
     }
     O *o = (O *)a.dh + i * a.D + c;
     typedef O o4 __attribute__((ext_vector_type(4)));
@@ -710,6 +744,7 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
   if (grad) {
     b.take(a.cm, 1);
     b.take(a.rowf, a.reduction == TT_REDUCE_NONE ? a.Npad : 0);
+    b.take(a.rowe, a.reduction == TT_REDUCE_NONE ? a.Npad : 0);
     a.Gplane = round_up(std::min(rows, a.V), 256) * 2;
     a.ldG = a.Gplane * a.planes;
     if (a.twin) a.Gplane = a.twin * a.ldG;
@@ -843,6 +878,13 @@ static hipError_t launch_dhidden_out(const LossArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+static hipError_t launch_light_rows(const LossArgs &a, hipStream_t s) {
+  if (a.reduction != TT_REDUCE_NONE || a.dtype == TT_DTYPE_BF16) return hipSuccess;
+  tt_launch(K_LOSS_ROWS, k_light_rows, dim3((unsigned)std::min<int64_t>(a.N, 1 << 16)), dim3(256),
+            0, s, a);
+  return hipGetLastError();
+}
+
 static hipError_t fill0(void *x, int64_t bytes, hipStream_t s) {
   if (bytes == 0) return hipSuccess;
   const int64_t n = bytes / 2;  // every output here has elements of 2 or 4 bytes
@@ -936,6 +978,7 @@ int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *w
     if (e == hipSuccess) e = launch_logits(a, v0, nv, 0, true, s);
     if (e == hipSuccess) e = launch_entries_g(a, v0, nv, s);
     if (e == hipSuccess && grad_hidden) e = launch_dhidden(a, v0, nv, s);
+    if (e == hipSuccess && grad_weight) e = launch_light_rows(a, s);
     if (e == hipSuccess && grad_weight) e = launch_dweight(a, v0, nv, s);
   }
   if (e == hipSuccess && grad_hidden) e = launch_dhidden_out(a, s);

@@ -4,7 +4,8 @@ type's lowest value, large finite ones), outliers, tiny and huge tensors, agains
 Bounds per element, as in plain fp32 arithmetic (u = 2^-21 for fp32's products and G):
   logit  dz_iv = (D 2^-24 + u) sum_d |h_id w_vd|
   g      eg_iv = u |g| + p_iv (dz_iv + max over rows that carry weight of dz_i. + 2^-20)
-               + 2^-39 where a row carries any weight (G's smallest step under its scale)
+               + 2^-39 where a row carries any weight (G's smallest step under its scale; with a
+               gradient per position `step` of its own factor for dh, 2^-39 of the largest for dW)
   dh     sum_v eg |w| + (V 2^-24 + u) sum_v |g w|, dW alike over positions
 and a loss is off by 2 dz of the rows that carry weight and 2^-20 of its own terms."""
 import math
@@ -30,7 +31,7 @@ def inputs(n, v, d, seed, dt="fp32"):
     return h.to(DT[dt]), w.to(DT[dt]), t, g
 
 
-def check(h, w, dt="fp32", up=None, t=None, tl=None, idx=None, T=1.0, columns=slice(None)):
+def check(h, w, dt="fp32", up=None, t=None, tl=None, idx=None, T=1.0, step=2.0 ** -39):
     """The public call and its gradients (reduction "none") against the definition."""
     up = torch.ones(h.shape[0], device="cuda") if up is None else up
     x, y = h.detach().requires_grad_(True), w.detach().requires_grad_(True)
@@ -72,11 +73,12 @@ def check(h, w, dt="fp32", up=None, t=None, tl=None, idx=None, T=1.0, columns=sl
     f = up.double() * (1.0 if t is not None else T)
     g = (p - q) * f[:, None]
     eg = (u * (p - q).abs() + p * (torch.minimum(dz, carry[:, None]) + carry[:, None] + 2.0 ** -20)
-          + 2.0 ** -22 * q + 2.0 ** -39 * used) * f.abs()[:, None]
+          + 2.0 ** -22 * q) * f.abs()[:, None]
+    eh, ew = eg + step * used * f.abs()[:, None], eg + 2.0 ** -39 * used * f.abs().max()
     extra = 2.0 ** -21 if dt == "fp32" else 0.0
     # 0 x inf is NaN in the definition too: such elements are compared as NaN
-    for got, ref, b, name in ((dh, g @ W, eg @ abs_w + (v * 2.0 ** -24 + extra) * (g.abs() @ abs_w), "dh"),
-                              (dw, g.t() @ H, eg.t() @ H.abs() + (n * 2.0 ** -24 + extra) * (g.abs().t() @ H.abs()), "dW")):
+    for got, ref, b, name in ((dh, g @ W, eh @ abs_w + (v * 2.0 ** -24 + extra) * (g.abs() @ abs_w), "dh"),
+                              (dw, g.t() @ H, ew.t() @ H.abs() + (n * 2.0 ** -24 + extra) * (g.abs().t() @ H.abs()), "dW")):
         got = got.double()
         assert torch.equal(torch.isnan(got), torch.isnan(ref)), name
         b = b + uo * ref.abs() + (2.0 ** -25 if dt == "fp16" else 2.0 ** -133)
@@ -199,3 +201,23 @@ def test_tiny_and_huge_tensors(sh, sw):
             assert float((out - math.log(v)).abs().max()) <= 2.0 ** -20 * math.log(v)
         tl, idx = entries(n, v, 4, torch.Generator(device="cuda"), torch.arange(v, device="cuda"))
         check(h * sh, w * sw, tl=tl, idx=idx, T=2.0)
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("n,v", [(24, 33000), (70, 33000), (70, 500)])
+def test_gradients_per_position_of_any_size(n, v, dt, op):
+    """A position's dh keeps its digits however small its gradient is beside the others': bounded
+    by its own factor (factors down to 2^-5 of the largest leave steps of 2^-39 in G, 2^-34 of
+    theirs).  Zeros and signs among them."""
+    print("case factors", n, v, dt, op, flush=True)
+    h, w, t, g = inputs(n, v, 64, n, dt)
+    up = 10.0 ** -(9 * torch.rand(n, device="cuda", generator=g))
+    up[::2] *= -1
+    up[0], up[1], up[2] = 1, 1e-9, 0
+    kw = dict(t=t) if op == "xent" else dict(T=0.7)
+    if op == "distill":
+        kw["tl"], kw["idx"] = entries(n, v, 4, g, torch.arange(v, device="cuda"))
+    _, dh, _ = check(h, w, dt, up=up, step=2.0 ** -34, **kw)
+    assert (dh[2] == 0).all()
+    _, dh, _ = check(h, w, dt, up=up * 2.0 ** 12, step=2.0 ** -34, **kw)
