@@ -434,7 +434,7 @@ int tt_full_weight(const tt_desc *desc, const float *const cores[3], int table, 
  * (2^-33 of it where that is under 1/16 of the largest), in grad_weight to the largest.  No result depends on the order of atomics.  The calls enqueue kernels
  * only and may be captured into a HIP graph (make one call of the kind before).
  *
- * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, d <= 2^20, strides <= 2^21, k <= 2048,
+ * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, d <= 2^20, weight_stride <= 2^21, k <= 2048,
  * n * k <= 2^31. */
 #define TT_DTYPE_F32  0
 #define TT_DTYPE_BF16 1

@@ -717,6 +717,9 @@ static int64_t saved_layout(LossArgs &a, void *saved) {
   return b.off;
 }
 
+// elements between rows that tiles are loaded from: 256 of them inside one buffer descriptor
+constexpr int64_t MAX_STRIDE = 1 << 21;
+
 static int64_t elem_size(int dtype) { return dtype == TT_DTYPE_F32 ? 4 : 2; }
 
 // mode: TT_LOSS_FORWARD, _BACKWARD or _ONLY (what is saved otherwise is in the workspace then)
@@ -725,8 +728,8 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
   Bump b{(char *)ws};
   if (mode == TT_LOSS_ONLY) {
     // up to 64 positions fill one tile whether they count or not: nothing to pack, if whole
-    // 16-byte groups make up their rows
-    a.direct = a.N <= 64 && a.D % 8 == 0 && a.planes == 1;
+    // 16-byte groups make up their rows (and a tile of them fits a descriptor)
+    a.direct = a.N <= 64 && a.D % 8 == 0 && a.planes == 1 && a.hld <= MAX_STRIDE;
     b.off = saved_layout(a, ws);
   }
   b.take(a.amax, grad || a.planes == 1 ? 0 : 3 * 2 * AMAX_BLOCKS);
@@ -783,7 +786,7 @@ static int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
   if (d->hidden_stride < d->d || d->weight_stride < d->d) return TT_EINVAL;
   // 32-bit places of positions, rows and entries; a tile's rows inside one descriptor
   if (d->n > (1 << 23) || d->v > (1 << 30) || d->d > (1 << 20) || d->k > 2048) return TT_ESHAPE;
-  if (d->hidden_stride > (1 << 21) || d->weight_stride > (1 << 21)) return TT_ESHAPE;
+  if (d->weight_stride > MAX_STRIDE) return TT_ESHAPE;
   if (d->n * std::max(d->k, 1) > (1ll << 31)) return TT_ESHAPE;
   a = {};
   a.N = d->n; a.V = d->v; a.D = d->d; a.hld = d->hidden_stride; a.wld = d->weight_stride;

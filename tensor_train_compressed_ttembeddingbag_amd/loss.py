@@ -95,17 +95,21 @@ class _LossFunction(torch.autograd.Function):
         return (_backward_once if torch.is_grad_enabled() else _backward)(ctx, grad_loss)
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
+_MAX_WEIGHT_STRIDE = 1 << 21  # the library's limit; hidden states may lie any distance apart
+
+
+def _rows(t: torch.Tensor, far: bool) -> torch.Tensor:
     """[..., D] as [N, D] with contiguous rows (a view where the strides allow it)."""
     if t.dim() != 2:
         t = t.reshape(-1, t.shape[-1])
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and (
+            t.stride(0) < t.shape[1] or not far and t.stride(0) > _MAX_WEIGHT_STRIDE):
         t = t.contiguous()
     return t
 
 
 def _loss(hidden, weight, targets, teacher_logits, shape, k, reduction, dev_status, **kw):
-    hidden, weight = _rows(hidden), _rows(weight)
+    hidden, weight = _rows(hidden, True), _rows(weight, False)
     key = (hidden.shape, hidden.stride(), weight.shape, weight.stride(), hidden.dtype,
            weight.dtype, hidden.device, weight.device, weight.data_ptr() & 15, k, reduction,
            *kw.values())

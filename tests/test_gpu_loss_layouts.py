@@ -1,0 +1,64 @@
+"""Vocabulary-head losses of views: rows far apart, odd offsets and strides, with and without
+gradients, equal bit for bit to those of contiguous copies."""
+import pytest
+import torch
+
+from tensor_train_compressed_ttembeddingbag_amd import loss as L
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def same(h, w, t):
+    """Loss alone and with gradients of the views and of contiguous copies."""
+    hc, wc = h.contiguous(), w.contiguous()
+    for smoothing in (0.0, 0.1):
+        kw = dict(reduction="none", label_smoothing=smoothing)
+        a = L.linear_cross_entropy(h, w, t, **kw)
+        assert torch.equal(a, L.linear_cross_entropy(hc, wc, t, **kw))
+        assert torch.isfinite(a).all()
+    tl, idx = torch.zeros(*t.shape, 3, device="cuda"), (t[..., None] + torch.arange(3, device="cuda")) % len(w)
+    assert torch.equal(L.linear_distillation(h, w, tl, idx), L.linear_distillation(hc, wc, tl, idx))
+    grads = []
+    for x, y in ((h, w), (hc, wc)):
+        x, y = x.detach().requires_grad_(True), y.detach().requires_grad_(True)
+        grads.append(torch.autograd.grad(L.linear_cross_entropy(x, y, t), (x, y)))
+    assert all(torch.equal(p, q) for p, q in zip(*grads))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("last", [-1, slice(-1, None)])
+def test_last_token_of_each_sequence(last, dt):
+    """hidden[B, T, D][:, -1]: rows T D = 2.2 million elements apart."""
+    print("case last token", last, dt, flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    h = torch.randn(3, 1100, 2048, device="cuda", generator=g).to(DT[dt])[:, last]
+    w = (torch.randn(500, 2048, device="cuda", generator=g) / 45).to(DT[dt])
+    same(h, w, torch.randint(0, 500, h.shape[:-1], device="cuda", generator=g))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_weight_rows_far_apart(dt):
+    print("case far weight", dt, flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    w = torch.zeros(20, (1 << 21) + 8, device="cuda", dtype=DT[dt])[:, :64]
+    w.copy_(torch.randn(20, 64, device="cuda", generator=g))
+    h = torch.randn(70, 64, device="cuda", generator=g).to(DT[dt])
+    same(h, w, torch.randint(0, 20, (70,), device="cuda", generator=g))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("n", [1, 33, 64, 65])
+def test_few_positions_of_any_stride_and_offset(n, dt):
+    print("case offsets", n, dt, flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    big_h = torch.randn(n, 117, device="cuda", generator=g).to(DT[dt])
+    big_w = torch.randn(700, 131, device="cuda", generator=g).to(DT[dt])
+    t = torch.randint(0, 700, (n,), device="cuda", generator=g)
+    for d in (8, 64, 96):
+        for a, b in ((0, 0), (3, 0), (0, 5), (1, 7)):
+            same(big_h[:, a:a + d], big_w[:, b:b + d], t)
