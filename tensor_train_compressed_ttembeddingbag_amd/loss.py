@@ -4,8 +4,8 @@
 [V, D] -- an ordinary table, or the rows of a TT table from ``full_weight()`` -- and return the
 loss of the logits ``hidden @ weight.T`` without ever holding the [N, V] logits: the forward
 keeps a running maximum and sum per position, the backward works through the vocabulary in
-pieces.  Both are differentiable in hidden and weight (once), for float32, bfloat16 and
-float16, and return the loss in float32.
+pieces.  Both are differentiable in hidden and weight (once, in reverse mode), for float32,
+bfloat16 and float16, and return the loss in float32.
 
 Argument marshalling only; the computation runs in libttbag (``tt_loss_forward`` and
 ``tt_loss_backward`` of ``include/tt_bag.h``).
@@ -16,6 +16,7 @@ import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import abi
 
@@ -109,6 +110,9 @@ def _rows(t: torch.Tensor, far: bool) -> torch.Tensor:
 
 
 def _loss(hidden, weight, targets, teacher_logits, shape, k, reduction, dev_status, **kw):
+    for t in (hidden, weight):
+        if forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("the vocabulary-head losses have no forward-mode derivative")
     hidden, weight = _rows(hidden, True), _rows(weight, False)
     key = (hidden.shape, hidden.stride(), weight.shape, weight.stride(), hidden.dtype,
            weight.dtype, hidden.device, weight.device, weight.data_ptr() & 15, k, reduction,
