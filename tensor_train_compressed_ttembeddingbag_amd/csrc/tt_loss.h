@@ -25,6 +25,7 @@ namespace ttb {
 
 constexpr int PACK_ROWS = 4;    // positions per block of k_pack
 constexpr int AMAX_BLOCKS = 1024;
+constexpr int CHUNK = 1024;     // positions that k_count counts together
 constexpr int RANGE_BITS = 14;  // see TensorRange
 
 // scalars that the device works out in the forward
@@ -83,6 +84,7 @@ struct LossArgs {
                            // largest |x| (infinite where a value is not finite), sum of the
                            // exponents of the values that are not 0, how many these are
   char *wp;                // packed piece of the weight: [row][plane][Dp]
+  int *chunk;              // [N / CHUNK] positions that count before each chunk, or null, see CHUNKS_AT
   float2 *part;            // [Npad][ptiles] (max, sum) in base 2
   float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)
   float *rowloss;          // [N]
