@@ -25,6 +25,7 @@ namespace ttb {
 
 constexpr int PACK_ROWS = 4;    // positions per block of k_pack
 constexpr int AMAX_BLOCKS = 1024;
+constexpr int FACTOR_BLOCKS = 256;  // of k_row_max
 constexpr int CHUNK = 1024;     // positions that k_count counts together
 constexpr int RANGE_BITS = 14;  // see TensorRange
 
@@ -93,6 +94,7 @@ struct LossArgs {
   int gshift, groups;
   float *rowf;             // [Npad] factor of a packed row's g (a gradient per row; else null)
   int *rowe;               // [Npad] exponent that a light row's factor leaves out, see LIGHT
+  float *upmax;            // [FACTOR_BLOCKS] largest factors, or null, see FACTORS_AT
   float *cm;               // what the factors were divided by
   char *G;                 // [Npad][planes][piece]
   int64_t ldG, Gplane;     // bytes; Gplane: to the second part of a row of G (plane or twin)

@@ -539,24 +539,41 @@ __global__ __launch_bounds__(1024) void k_loss_sum(LossArgs a) {
 // ---------------------------------------------------------------- backward, around the products
 // With a gradient per position: the factor of every packed row's g.  G in fp16 needs |factor|
 // <= 1 (2^14 g fits), so the factors are divided by the power of two above the largest finite
-// one, which every block finds for itself; light ones come in two parts, see LIGHT.
-__global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
+// one; light ones come in two parts, see LIGHT.  The blocks find the largest for themselves, from
+// FACTORS_AT positions on from what k_row_max found.
+__device__ __forceinline__ float block_max_factor(const LossArgs &a, int64_t i0, int64_t step) {
   __shared__ float s_m[4];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int tid = threadIdx.x;
+  float m = 0.f;
+#pragma unroll 4
+  for (int64_t i = i0 + tid; i < a.N; i += step) {
+    const float u = fabsf(a.up[i]);
+    if (u < INFINITY && a.sv.slot[i] >= 0) m = fmaxf(m, u);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((tid & 63) == 0) s_m[tid >> 6] = m;
+  __syncthreads();
+  return fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+}
+__global__ __launch_bounds__(256) void k_row_max(LossArgs a) {
+  const float m = block_max_factor(a, (int64_t)blockIdx.x * 256, 256 * gridDim.x);
+  if (threadIdx.x == 0) a.upmax[blockIdx.x] = m;
+}
+__global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
+  const int tid = threadIdx.x;
   float cm = 1.f;
   const bool scaled = a.dtype != TT_DTYPE_BF16 && !a.sv.sc->whole;
   if (scaled) {
-    float m = 0.f;
-#pragma unroll 4
-    for (int64_t i = tid; i < a.N; i += 256) {
-      const float u = fabsf(a.up[i]);
-      if (u < INFINITY && a.sv.slot[i] >= 0) m = fmaxf(m, u);
-    }
+    float m;
+    if (a.upmax) {
+      m = 0.f;
+      for (int b = tid & 63; b < FACTOR_BLOCKS; b += 64) m = fmaxf(m, a.upmax[b]);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if (lane == 0) s_m[wv] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+      for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    } else {
+      m = block_max_factor(a, 0, 256);
+    }
     if (m > 0.f) {
       int e;
       frexpf(m, &e);
@@ -754,6 +771,9 @@ static int64_t elem_size(int dtype) { return dtype == TT_DTYPE_F32 ? 4 : 2; }
 // with it: 4096 18 and 21 us, 8192 25 and 24, 16384 43 and 31, 131072 1025 and 126, 2^20 76 ms
 // and 0.8 ms.
 constexpr int64_t CHUNKS_AT = 8192;
+// Positions past which k_row_max goes before k_row_factors (the backward of n x 200 x 64 for dhidden:
+// 16384 64 us without and 66 with it, 32768 99 and 77, 131072 426 and 228, 2^20 4.1 and 1.7 ms).
+constexpr int64_t FACTORS_AT = 16384;
 
 // mode: TT_LOSS_FORWARD, _BACKWARD or _ONLY (what is saved otherwise is in the workspace then)
 static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
@@ -781,6 +801,8 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     b.take(a.cm, 1);
     b.take(a.rowf, a.reduction == TT_REDUCE_NONE ? a.Npad : 0);
     b.take(a.rowe, a.reduction == TT_REDUCE_NONE ? a.Npad : 0);
+    if (a.N > FACTORS_AT && a.reduction == TT_REDUCE_NONE && a.dtype != TT_DTYPE_BF16)
+      b.take(a.upmax, FACTOR_BLOCKS);
     a.Gplane = round_up(std::min(rows, a.V), 256) * 2;
     a.ldG = a.Gplane * a.planes;
     if (a.twin) a.Gplane = a.twin * a.ldG;
@@ -1010,6 +1032,7 @@ int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *w
   }
   if (!grad_hidden && !grad_weight) return TT_OK;
   if (a.reduction == TT_REDUCE_NONE) {
+    if (a.upmax) tt_launch(K_LOSS_ROWS, k_row_max, dim3(FACTOR_BLOCKS), dim3(256), 0, s, a);
     tt_launch(K_LOSS_ROWS, k_row_factors, dim3((unsigned)std::min<int64_t>((a.N + 255) / 256, 1024)),
               dim3(256), 0, s, a);
     e = hipGetLastError();
