@@ -460,10 +460,15 @@ typedef struct tt_loss_desc {
 #define TT_LOSS_ONLY     2  /* of a forward with saved == NULL       */
 
 /* Bytes of `saved` (written by the forward, read by the backward: the positions that count,
- * packed, and a few words for each) and of the workspace of one call.  The workspace is that
- * of one piece of the vocabulary, whatever v is: at most 256 MiB each for the logits'
- * gradient and for packed rows of the weight (fp32, or odd widths of many positions), beside
- * fp32 sums of dhidden.  0: the descriptor is rejected. */
+ * packed, and a few words for each position and entry) and of the workspace of one call; 0: the
+ * descriptor is rejected.  The workspace is that of a piece of the vocabulary, whatever v is:
+ *   forward   at most 256 MiB of running statistics, and of the packed rows of the weight (fp32,
+ *             or odd widths of many positions); with k entries at most 2 KiB a position;
+ *   backward  at most 256 MiB, or 256 rows of the weight if that is more, each of the logits'
+ *             gradient (n rounded up to 256 positions, 2 bytes, fp32 4, per row of the weight) and
+ *             of the packed rows of the weight; the fp32 sums of grad_hidden (n x d rounded up to
+ *             tiles of 256 x 64, or 1024 tiles of 256 x 256 where that is more);
+ * and at most 64 bytes a position beside that.  weight is not looked at (NULL will do). */
 size_t tt_loss_saved_size(const tt_loss_desc *desc);
 size_t tt_loss_workspace_size(const tt_loss_desc *desc, const void *weight, int mode);
 

@@ -78,6 +78,7 @@ struct LossArgs {
   int direct;              // loss alone, few positions: the hidden rows as they lie, all of them
   int64_t piece;           // rows of the weight per piece
   int ptiles;              // running statistics per position
+  int fold;                // those of a piece are added up into slot 0
   int dh_bx, dh_by, cus;   // k_dhidden's tile, compute units
   LossSaved sv;
   // workspace

@@ -429,6 +429,51 @@ __device__ __forceinline__ void sum_rows(const LossArgs &a, double *s_d) {
   }
 }
 
+// Statistics of a position over part of the weight's rows: its largest sum of products, the sum
+// of 2^((sum of products - largest) zs), the sum of its logits.
+struct Stats {
+  float m, s, z;
+};
+// slots [t0, t1) of a position, every step-th one from this lane on, and then the wave's lanes
+__device__ __forceinline__ Stats wave_stats(const LossArgs &a, int64_t slot, int t0, int t1,
+                                            int step, float zs) {
+  Stats w = {-INFINITY, 0.f, 0.f};
+  const int64_t row = slot * a.ptiles;
+  for (int t = t0; t < t1; t += step) {
+    const float2 v = a.part[row + t];
+    const float n = fmaxf(w.m, v.x), n0 = n == -INFINITY ? 0.f : n;
+    w.s = w.s * __builtin_amdgcn_exp2f((w.m - n0) * zs) + v.y * __builtin_amdgcn_exp2f((v.x - n0) * zs);
+    w.m = n;
+    if (a.smoothing > 0.f) w.z += a.zpart[row + t];
+  }
+  float m = w.m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  w.s *= __builtin_amdgcn_exp2f((w.m - (m == -INFINITY ? 0.f : m)) * zs);
+  w.m = m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    w.s += __shfl_xor(w.s, o);
+    w.z += __shfl_xor(w.z, o);
+  }
+  return w;
+}
+
+// Where the statistics of all tiles would not fit (see ws_layout): those of a piece of the
+// vocabulary, slots 1 .. tiles, are added to the position's in slot 0.
+__global__ __launch_bounds__(256) void k_fold(LossArgs a, int tiles, int first) {
+  const int lane = threadIdx.x & 63;
+  const int64_t count = a.direct ? a.N : a.sv.sc->count;
+  const float zs = a.direct ? LOG2E / a.temp : a.sv.sc->zs;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < count; r += gridDim.x * 4) {
+    const Stats w = wave_stats(a, r, first + lane, tiles + 1, 64, zs);
+    if (lane == 0) {
+      a.part[r * a.ptiles] = make_float2(w.m, w.s);
+      if (a.smoothing > 0.f) a.zpart[r * a.ptiles] = w.z;
+    }
+  }
+}
+
 // NW waves per position: the tiles' statistics become its lse.  The logits of the target and
 // of the entries are the ones in these sums (a small loss is the difference of large terms);
 // the sum over the entries is taken in fp64.
@@ -445,24 +490,8 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   const float zs = a.direct ? LOG2E / a.temp : a.sv.sc->zs;
   float out = 0.f, wm = -INFINITY, s = 0.f, z = 0.f;
   if (slot >= 0) {
-    const float2 *p = a.part + (int64_t)slot * a.ptiles;
-    float m = -INFINITY;
-    for (int t = part * 64 + lane; t < a.ptiles; t += 64 * NW) {
-      const float2 v = p[t];
-      const float n = fmaxf(m, v.x), n0 = n == -INFINITY ? 0.f : n;
-      s = s * __builtin_amdgcn_exp2f((m - n0) * zs) + v.y * __builtin_amdgcn_exp2f((v.x - n0) * zs);
-      m = n;
-      if (a.smoothing > 0.f) z += a.zpart[(int64_t)slot * a.ptiles + t];
-    }
-    wm = m;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor(wm, o));
-    s *= __builtin_amdgcn_exp2f((m - (wm == -INFINITY ? 0.f : wm)) * zs);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      s += __shfl_xor(s, o);
-      z += __shfl_xor(z, o);
-    }
+    const Stats w = wave_stats(a, slot, part * 64 + lane, a.fold ? 1 : a.ptiles, 64 * NW, zs);
+    wm = w.m, s = w.s, z = w.z;
   }
   if constexpr (NW > 1) {
     if (lane == 0) s_m[wv] = wm, s_s[wv] = s, s_z[wv] = z;
@@ -813,9 +842,24 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(DH_SPLITS, rows / 512));
     b.take(a.dhp, std::max(ty, std::min<int64_t>(DH_TILES / tx, most * ty)) * t.by * a.Dp);
   } else {
-    a.ptiles = 0;
-    for (int64_t v0 = 0; v0 < a.V; v0 += a.piece)
-      a.ptiles += logits_cut(a, std::min(a.piece, a.V - v0)).tiles;
+    // statistics of all tiles where they fit, else of a piece's at a time
+    const int64_t most = PIECE_BYTES / (a.Npad * (a.smoothing > 0.f ? 12 : 8));
+    auto tiles = [&]() {
+      int64_t n = 0;
+      for (int64_t v0 = 0; v0 < a.V; v0 += a.piece) n += logits_cut(a, std::min(a.piece, a.V - v0)).tiles;
+      return n;
+    };
+    int64_t all = tiles();
+    a.fold = all > most;
+    if (a.fold) {
+      auto widest = [&]() {  // of a whole piece and the last one
+        const int64_t last = a.V - (a.V - 1) / a.piece * a.piece;
+        return std::max(logits_cut(a, std::min(a.piece, a.V)).tiles, logits_cut(a, last).tiles);
+      };
+      while (a.piece > 256 && widest() + 1 > most) a.piece = round_up(a.piece / 2, 256);
+      all = widest() + 1;
+    }
+    a.ptiles = (int)all;
     b.take(a.part, a.Npad * a.ptiles);
     b.take(a.zpart, a.smoothing > 0.f ? a.Npad * a.ptiles : 0);
     b.take(a.rowloss, a.N);
@@ -914,9 +958,15 @@ static hipError_t launch_entries(const LossArgs &a, hipStream_t s) {
 // them), so more rows are added in a launch of its own (about 5 us).
 constexpr int64_t LOSS_TICKETS = 256;
 
+static hipError_t launch_fold(const LossArgs &a, int tiles, int first, hipStream_t s) {
+  tt_launch(K_LOSS_ROWS, k_fold, dim3((unsigned)std::min<int64_t>((a.N + 3) / 4, 1 << 16)),
+            dim3(256), 0, s, a, tiles, first);
+  return hipGetLastError();
+}
+
 static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
   const int ticket = a.N <= LOSS_TICKETS && !a.direct;  // (k_pack clears the ticket)
-  if (a.ptiles <= 256 && a.k <= 256)  // few statistics and entries: a wave per position
+  if ((a.fold || a.ptiles <= 256) && a.k <= 256)  // few statistics and entries: a wave per position
     tt_launch(K_LOSS_ROWS, k_loss<1>, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, ticket);
   else
     tt_launch(K_LOSS_ROWS, k_loss<4>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
@@ -1002,8 +1052,10 @@ int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *we
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
     const int64_t nv = std::min(a.piece, a.V - v0);
     e = launch_pack_w(a, v0, nv, s);
-    if (e == hipSuccess) e = launch_logits(a, v0, nv, tile0, false, s);
-    tile0 += logits_cut(a, nv).tiles;
+    const int tiles = logits_cut(a, nv).tiles;
+    if (e == hipSuccess) e = launch_logits(a, v0, nv, a.fold ? 1 : tile0, false, s);
+    if (e == hipSuccess && a.fold) e = launch_fold(a, tiles, v0 == 0, s);
+    tile0 += tiles;
   }
   if (e == hipSuccess) e = launch_loss(a, s);
   return e == hipSuccess ? TT_OK : TT_EHIP;

@@ -137,3 +137,35 @@ def test_time_of_gradients_of_many_positions():
     b.record()
     torch.cuda.synchronize()
     assert a.elapsed_time(b) < 3.0
+
+
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+@pytest.mark.parametrize("n,v,d,dt", [(8192, 1_100_000, 8, "bf16"), (5, 68_000_000, 8, "bf16"),
+                                      (8192, 1_100_000, 12, "fp32")])
+def test_vocabularies_whose_statistics_are_added_up_by_pieces(n, v, d, dt, smoothing):
+    """1000 distinct rows over and over: lse is that of the distinct ones and the log of their
+    number (uneven at the end: counted).  Bound: D + 2 log2 V rounded sums of logits within 30,
+    and the smoothing's mean, V / 256 tiles of fp32 sums within 30 of each."""
+    print("case many tiles", n, v, d, dt, smoothing, flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    some = torch.randn(1000, d, device="cuda", generator=g).to(DT[dt])
+    w = some.repeat((v + 999) // 1000, 1)[:v]
+    h = torch.randn(n, d, device="cuda", generator=g).to(DT[dt])
+    t = torch.randint(0, v, (n,), device="cuda", generator=g)
+    if n > 10:
+        t[7::11] = -100
+    z = h.double() @ some.double().t()
+    many = torch.full((1000,), v // 1000, device="cuda", dtype=torch.float64)
+    many[: v % 1000] += 1
+    lse = torch.logsumexp(z + many.log(), 1)
+    ref = lse - (1 - smoothing) * z.gather(1, (t.clamp(min=0) % 1000)[:, None])[:, 0] \
+        - smoothing * (z * many).sum(1) / v
+    ref = torch.where(t >= 0, ref, torch.zeros_like(ref))
+    bound = 2.0 ** -24 * (d + 50) * 30 + (2.0 ** -21 * 30 if dt == "fp32" else 0) + \
+        smoothing * 2.0 ** -24 * 300 * 30
+    out = L.linear_cross_entropy(h, w, t, reduction="none", label_smoothing=smoothing)
+    assert float((out.double() - ref).abs().max()) <= bound
+    x = h.clone().requires_grad_(True)
+    kept = L.linear_cross_entropy(x, w, t, reduction="none", label_smoothing=smoothing)
+    assert float((kept.detach().double() - ref).abs().max()) <= bound
