@@ -481,8 +481,9 @@ int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *we
                     void *stream);
 
 /* grad_hidden [n][d] and grad_weight [v][d], fully overwritten (either may be NULL), of
- * sum_i grad_loss_i loss_i (TT_REDUCE_NONE: grad_loss [n]) or grad_loss[0] * loss.  hidden
- * and weight as in the forward that filled `saved`. */
+ * sum_i grad_loss_i loss_i (TT_REDUCE_NONE: grad_loss [n]) or grad_loss[0] * loss.  weight as in
+ * the forward that filled `saved`; hidden is not read (`saved` has its rows that count), but
+ * must not be NULL. */
 int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *weight,
                      const void *saved, size_t saved_bytes, const float *grad_loss,
                      void *grad_hidden, void *grad_weight, void *ws, size_t ws_bytes,

@@ -62,17 +62,17 @@ def _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status, s
 
 
 def _backward(ctx, grad_loss):
-    hidden, weight, saved = ctx.saved_tensors
-    plan, dev = ctx.plan, hidden.device
+    weight, saved = ctx.saved_tensors
+    plan, dev = ctx.plan, weight.device
     grad_loss = grad_loss.contiguous()
     need_h, need_w = ctx.needs_input_grad[:2]
     dh = torch.empty((plan.n, plan.d), dtype=plan.dtype, device=dev) if need_h else None
     dw = torch.empty((plan.v, plan.d), dtype=plan.dtype, device=dev) if need_w else None
     ws = _bytes(plan.bwd, dev)
     rc = abi.lib().tt_loss_backward(
-        plan.ref, hidden.data_ptr(), weight.data_ptr(), saved.data_ptr(), plan.saved,
+        plan.ref, saved.data_ptr(), weight.data_ptr(), saved.data_ptr(), plan.saved,
         grad_loss.data_ptr(), dh.data_ptr() if need_h else None,
-        dw.data_ptr() if need_w else None, ws.data_ptr(), plan.bwd, abi._stream(None, hidden))
+        dw.data_ptr() if need_w else None, ws.data_ptr(), plan.bwd, abi._stream(None, weight))
     if rc:
         raise abi.TTError("tt_loss_backward", rc)
     return dh, dw, None, None, None, None, None
@@ -87,7 +87,8 @@ class _LossFunction(torch.autograd.Function):
         loss, saved = _forward(plan, hidden, weight, targets, teacher_logits, shape, dev_status,
                                True)
         ctx.plan = plan
-        ctx.save_for_backward(hidden, weight, saved)
+        # `saved` has the hidden rows that count, packed: the backward does not read hidden itself
+        ctx.save_for_backward(weight, saved)
         return loss
 
     @staticmethod

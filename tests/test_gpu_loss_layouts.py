@@ -169,3 +169,27 @@ def test_vocabularies_whose_statistics_are_added_up_by_pieces(n, v, d, dt, smoot
     x = h.clone().requires_grad_(True)
     kept = L.linear_cross_entropy(x, w, t, reduction="none", label_smoothing=smoothing)
     assert float((kept.detach().double() - ref).abs().max()) <= bound
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_hidden_states_are_not_kept_beside_their_packed_copy(dt):
+    """The backward reads the packed rows alone: hidden states that are overwritten after the
+    forward change nothing, and given up they are freed."""
+    print("case kept", dt, flush=True)
+    h, w, t, _ = inputs(1000, 300, 512, 7, dt)
+    w.requires_grad_(True)
+    want = torch.autograd.grad(L.linear_cross_entropy(x := h.clone().requires_grad_(True), w, t), (x, w))
+    y = x * 1
+    out = L.linear_cross_entropy(y, w, t)
+    size = y.numel() * y.element_size()
+    y.detach().zero_()
+    before = torch.cuda.memory_allocated()
+    del y
+    assert before - torch.cuda.memory_allocated() >= size
+    got = torch.autograd.grad(out, (x, w))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y = x * 1
+    out = L.linear_cross_entropy(y, w, t)
+    y.zero_()
+    got = torch.autograd.grad(out, (x, w))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
