@@ -1073,15 +1073,15 @@ def make_loss_desc(hidden: torch.Tensor, weight: torch.Tensor, k: int = 0,
 
 
 def tt_loss_sizes(desc: TTLossDesc, weight: torch.Tensor):
-    """(bytes of saved, of the workspace of a forward, of a backward, of a forward alone)."""
-    p = weight.data_ptr()
-    key = (bytes(desc), p & 15)
+    """(bytes of saved, of the workspace of a forward, of a backward, of a forward alone); they
+    do not depend on weight."""
+    key = bytes(desc)
     got = _loss_sizes.get(key)
     if got is None:
         L, r = lib(), ctypes.byref(desc)
-        got = (L.tt_loss_saved_size(r), L.tt_loss_workspace_size(r, p, TT_LOSS_FORWARD),
-               L.tt_loss_workspace_size(r, p, TT_LOSS_BACKWARD),
-               L.tt_loss_workspace_size(r, p, TT_LOSS_ONLY))
+        got = (L.tt_loss_saved_size(r), L.tt_loss_workspace_size(r, None, TT_LOSS_FORWARD),
+               L.tt_loss_workspace_size(r, None, TT_LOSS_BACKWARD),
+               L.tt_loss_workspace_size(r, None, TT_LOSS_ONLY))
         if not got[0]:
             raise TTError("tt_loss_saved_size", -2)
         if len(_loss_sizes) > 4096:

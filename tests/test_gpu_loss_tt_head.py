@@ -58,3 +58,16 @@ def test_the_head_learns_through_its_cores():
         opt.step()
         losses.append(float(out.detach()))
     assert losses[-1] < 0.8 * losses[0], losses
+
+
+def test_views_of_one_shape_share_a_plan():
+    """What is kept per kind of call depends on shapes, strides and types, not on an address."""
+    print("case plans", flush=True)
+    big = torch.randn(100, 48, device="cuda").bfloat16()
+    h = torch.randn(5, 32, device="cuda").bfloat16()
+    t = torch.zeros(5, dtype=torch.int64, device="cuda")
+    L.linear_cross_entropy(h, big[:, :32], t)
+    n = len(L._plans)
+    for a in range(1, 16):
+        L.linear_cross_entropy(h, big[:, a:a + 32], t)
+    assert len(L._plans) == n
