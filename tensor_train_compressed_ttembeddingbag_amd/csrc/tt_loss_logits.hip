@@ -39,7 +39,11 @@ struct LogitsEpi {
   float one_e, e_v;        // 1 - e, e / V
 };
 
-template <class E, class T, int PL, bool GRAD, bool MEND, bool WHOLE>
+// What the tiles give: the statistics, these and the sums of the entries' rows (distillation; a
+// variant of its own, because its mere presence cost the others 1 to 3 %), or G.
+enum { STATS, ENTRIES, GRAD };
+
+template <class E, class T, int PL, int OUT, bool MEND, bool WHOLE>
 __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi &ep, char *lds) {
   gemm_tiles<E, T, PL, false, false, MEND, WHOLE>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
     const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
@@ -50,7 +54,7 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
     const int xl = (int)min<int64_t>(ep.nv - (int64_t)ix * T::X, T::X);  // rows of this tile
     const int xb = px + 4 * g;
     const bool full = xl == T::X;  // no rows of the tile past the vocabulary
-    if constexpr (!GRAD) {
+    if constexpr (OUT != GRAD) {
       float2 *sm = (float2 *)tmp;                       // [NWX][Y]
       float *sz = (float *)(tmp + T::NWX * T::Y * 8);   // [NWX][Y]
       int d_[T::NI];  // the target's place from this lane's first row, or -1
@@ -61,7 +65,7 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
         const int64_t t = !ep.zt || pos >= count ? -1 : ep.tgt64 ? ep.tgt64[pos] : ep.tgt[pos];
         d_[j] = (int)max<int64_t>(min<int64_t>(t - first, 1 << 20), -1);
       }
-      if (ep.k) {
+      if constexpr (OUT == ENTRIES) {
         // the entries that this wave's rows hold: each lane writes the sums of its rows
         const unsigned lo = (unsigned)(ep.v0 + (int64_t)ix * T::X + px),
                        hi = lo + max(min(xl - px, T::wx), 0);
@@ -218,41 +222,48 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
   });
 }
 
-template <class E, class T, int PL, bool GRAD, bool MEND>
+template <class E, class T, int PL, int OUT, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   if constexpr (PL > 1)
-    if (ep.sc->whole) return logits_tiles<E, T, PL, GRAD, MEND, true>(a, ep, lds);
-  logits_tiles<E, T, PL, GRAD, MEND, false>(a, ep, lds);
+    if (ep.sc->whole) return logits_tiles<E, T, PL, OUT, MEND, true>(a, ep, lds);
+  logits_tiles<E, T, PL, OUT, MEND, false>(a, ep, lds);
 }
 
-template <class E, class T, int PL, bool GRAD, bool MEND>
+template <class E, class T, int PL, int OUT, bool MEND>
 static hipError_t go(const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
-  const hipError_t e = lds_limit<T>(&k_logits<E, T, PL, GRAD, MEND>);
+  const hipError_t e = lds_limit<T>(&k_logits<E, T, PL, OUT, MEND>);
   if (e != hipSuccess) return e;
-  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, PL, GRAD, MEND>,
+  tt_launch(OUT == GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, PL, OUT, MEND>,
             dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT), T::LDS, s, g, ep);
   return hipGetLastError();
 }
 
-template <class E, int PL, bool GRAD, bool MEND>
+template <class E, int PL, int OUT, bool MEND>
 static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep,
                        hipStream_t s) {
-  if (cfg == 0) return go<E, TileL, PL, GRAD, MEND>(a, g, ep, s);
-  if (cfg == 1) return go<E, TileM, PL, GRAD, MEND>(a, g, ep, s);
-  if (cfg == 3) return go<E, TileN, PL, GRAD, MEND>(a, g, ep, s);
-  if (cfg == 4) return go<E, TileT, PL, GRAD, MEND>(a, g, ep, s);
-  if (cfg == 5) return go<E, TileM1, PL, GRAD, MEND>(a, g, ep, s);
-  return go<E, TileS, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 0) return go<E, TileL, PL, OUT, MEND>(a, g, ep, s);
+  if (cfg == 1) return go<E, TileM, PL, OUT, MEND>(a, g, ep, s);
+  if (cfg == 3) return go<E, TileN, PL, OUT, MEND>(a, g, ep, s);
+  if (cfg == 4) return go<E, TileT, PL, OUT, MEND>(a, g, ep, s);
+  if (cfg == 5) return go<E, TileM1, PL, OUT, MEND>(a, g, ep, s);
+  return go<E, TileS, PL, OUT, MEND>(a, g, ep, s);
+}
+
+template <class E, int PL, bool MEND>
+static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
+                       const LogitsEpi &ep, hipStream_t s) {
+  if (grad) return pick<E, PL, GRAD, MEND>(cfg, a, g, ep, s);
+  return a.k ? pick<E, PL, ENTRIES, MEND>(cfg, a, g, ep, s)
+             : pick<E, PL, STATS, MEND>(cfg, a, g, ep, s);
 }
 
 template <class E, int PL>
 static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
                        const LogitsEpi &ep, hipStream_t s) {
   if constexpr (PL == 1)
-    if (!a.pack_w && a.D % 8)
-      return grad ? pick<E, PL, true, true>(cfg, a, g, ep, s) : pick<E, PL, false, true>(cfg, a, g, ep, s);
-  return grad ? pick<E, PL, true, false>(cfg, a, g, ep, s) : pick<E, PL, false, false>(cfg, a, g, ep, s);
+    if (!a.pack_w && a.D % 8) return pick<E, PL, true>(grad, cfg, a, g, ep, s);
+  return pick<E, PL, false>(grad, cfg, a, g, ep, s);
 }
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
@@ -269,7 +280,7 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.tgt = a.k ? nullptr : a.sv.tgt;
   ep.tgt64 = a.direct ? a.tgt : nullptr;
   ep.zt = a.k || grad ? nullptr : a.sv.zt;
-  ep.k = grad ? 0 : a.k;
+  ep.k = a.k;
   ep.eidx = a.sv.eidx; ep.at = a.direct ? nullptr : a.sv.at; ep.ez = a.sv.ez;
   ep.dir = a.dir; ep.gshift = a.gshift; ep.groups = a.groups;
   ep.one_e = 1.f - a.smoothing;
