@@ -103,8 +103,8 @@ struct LossArgs {
 };
 
 // Groups of the weight's rows in the entries' directory: at least 256 rows, so that a tile's
-// rows lie in one, and 2 KiB a position at most, so that a group has few entries.
-constexpr int DIR_GROUPS = 1024;
+// rows lie in one, and up to 16 an entry, so that a group has few of them (1024 at most).
+inline int dir_groups(int k) { return k < 64 ? 16 * k : 1024; }
 
 // A gradient per position in fp16 G: factors down to 2^-LIGHT of the largest go into G, whose
 // range has that much to spare.  A smaller one would push its row's G below fp16's steps, and

@@ -866,7 +866,7 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     if (a.N > CHUNKS_AT) b.take(a.chunk, (a.N + CHUNK - 1) / CHUNK);
     if (a.k) {
       a.gshift = 8;
-      while ((a.V - 1) >> a.gshift >= DIR_GROUPS) ++a.gshift;
+      while ((a.V - 1) >> a.gshift >= dir_groups(a.k)) ++a.gshift;
       a.groups = (int)((a.V - 1) >> a.gshift) + 1;
       b.take(a.dir, a.N * (a.groups + 1));
     }

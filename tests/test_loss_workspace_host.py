@@ -17,7 +17,7 @@ def up(x, m):
 @pytest.mark.parametrize("kw", [dict(), dict(label_smoothing=0.1), dict(dtype=abi.TT_DTYPE_F32),
                                 dict(dtype=abi.TT_DTYPE_F32, label_smoothing=0.1),
                                 dict(d=63, hidden_stride=63, weight_stride=63),
-                                dict(k=64, temperature=2.0), dict(reduction=abi.TT_REDUCE_NONE)],
+                                dict(k=64, temperature=2.0), dict(k=1), dict(reduction=abi.TT_REDUCE_NONE)],
                          ids=str)
 @pytest.mark.parametrize("n", [1, 64, 100, 8192, 1 << 20, 1 << 23])
 def test_bounds(n, kw):
@@ -30,7 +30,7 @@ def test_bounds(n, kw):
         rows, wide = up(n, 256), up(d.d, 64)
         packed = 256 * MIB + 256 * wide * size  # (pieces are whole groups of 256 rows)
         other = 64 * rows + MIB
-        assert 0 < fwd <= 256 * MIB + packed + (2048 * n if d.k else 0) + other
+        assert 0 < fwd <= 256 * MIB + packed + 32 * n * d.k + other
         assert fwd <= only <= fwd + saved + other
         grad = max(256 * MIB, 256 * rows * size) + 256 * rows * size
         sums = max(4 * rows * up(d.d, 64), 1024 * 4 * 65536)
