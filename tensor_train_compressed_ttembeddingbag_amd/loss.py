@@ -187,8 +187,8 @@ def linear_distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_logi
     k = teacher_indices.shape[-1]
     if k < 1:
         raise ValueError("at least one teacher entry per position is needed")
-    if not 0.0 < temperature < float("inf"):
-        raise ValueError("temperature must be positive and finite")
+    if not 0.0 < ctypes.c_float(temperature).value < float("inf"):  # the library's type
+        raise ValueError("temperature must be positive and finite in float32")
     if teacher_indices.dtype == torch.int32:
         teacher_indices = teacher_indices.to(torch.int64)
     return _loss(hidden, weight, teacher_indices.contiguous(),
