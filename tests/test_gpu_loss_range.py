@@ -221,3 +221,20 @@ def test_gradients_per_position_of_any_size(n, v, dt, op):
     _, dh, _ = check(h, w, dt, up=up, step=2.0 ** -34, **kw)
     assert (dh[2] == 0).all()
     _, dh, _ = check(h, w, dt, up=up * 2.0 ** 12, step=2.0 ** -34, **kw)
+
+
+@pytest.mark.parametrize("mask", [-math.inf, LOW])
+def test_large_tiles_of_masked_rows(mask):
+    """Sizes whose products take the largest tiles, none a multiple of them, and a vocabulary of
+    two pieces."""
+    for n, v, d in ((2100, 4500, 2056), (4100, 33000, 40)):
+        print("case large masked", mask, n, v, d, flush=True)
+        h, w, t, g = inputs(n, v, d, n)
+        h[:, d - 1] = 1.0
+        off = torch.rand(v, device="cuda", generator=g) < 0.5
+        off[0] = False
+        w[off, d - 1], w[~off, d - 1] = mask, 0
+        free = (~off).nonzero()[:, 0]
+        check(h, w, t=free[torch.randint(0, free.numel(), (n,), device="cuda", generator=g)])
+        tl, idx = entries(n, v, 5, g, free)
+        check(h, w, tl=tl, idx=idx, T=1.5)

@@ -1,5 +1,5 @@
-"""What the vocabulary-head losses refuse before any device work: forward-mode derivatives, which would
-be dropped, and temperatures that float32 does not hold."""
+"""What the vocabulary-head losses refuse before any device work: forward-mode derivatives, which
+would be dropped, and temperatures that float32 does not hold."""
 import pytest
 import torch
 from torch.autograd import forward_ad
