@@ -463,7 +463,7 @@ typedef struct tt_loss_desc {
  * packed, and a few words for each position and entry) and of the workspace of one call; 0: the
  * descriptor is rejected.  The workspace is that of a piece of the vocabulary, whatever v is:
  *   forward   at most 256 MiB of running statistics, and of the packed rows of the weight (fp32,
- *             or odd widths of many positions); at most 32 bytes an entry;
+ *             or odd widths of many positions);
  *   backward  at most 256 MiB, or 256 rows of the weight if that is more, each of the logits'
  *             gradient (n rounded up to 256 positions, 2 bytes, fp32 4, per row of the weight) and
  *             of the packed rows of the weight; the fp32 sums of grad_hidden (n x d rounded up to

@@ -9,7 +9,7 @@
 //
 // forward:  k_entries (distillation: q, sorted, repeated rows merged) -> k_pack (positions that
 //           count, packed) -> k_logits (running maximum and sum per position and tile of the
-//           weight; the sums of products of targets and entries) -> k_loss (lse, loss).  A loss alone of up to 64 positions
+//           weight, the targets' logits) -> k_loss (lse, the entries' logits, loss).  A loss alone of up to 64 positions
 //           leaves k_pack out.
 // backward: per piece of the vocabulary k_logits (G = row factor * g, in 16 bits), k_entries_g
 //           (distillation: the entries of G), k_dhidden (split over the vocabulary, fp32),
@@ -50,9 +50,7 @@ struct LossSaved {
                    // because exp(z - lse) and a small loss lose what their rounded sum loses
   float *zt;       // [N] packed row -> the target's sum of products (cross entropy)
   int *eidx;       // [N][k] distillation entries by row of the weight, the empty ones (-1) last
-  float *eq, *ez;  // their q (of a repeated row at its first entry, 0 behind) and their sums of
-                   // products, which k_loss turns into log2 p
-  int *at;         // [N] packed row -> position (distillation)
+  float *eq, *ez;  // their q (of a repeated row at its first entry, 0 behind) and their log2 p
   float *ent;      // [N] sum_j q log q
 };
 
@@ -90,9 +88,6 @@ struct LossArgs {
   float2 *part;            // [Npad][ptiles] (max, sum) in base 2
   float *zpart;            // [Npad][ptiles] sums of logits (label smoothing)
   float *rowloss;          // [N]
-  unsigned short *dir;     // [N][groups + 1] distillation: the first entry of each group of 2^gshift
-                           // rows of the weight
-  int gshift, groups;
   float *rowf;             // [Npad] factor of a packed row's g (a gradient per row; else null)
   int *rowe;               // [Npad] exponent that a light row's factor leaves out, see LIGHT
   float *upmax;            // [FACTOR_BLOCKS] largest factors, or null, see FACTORS_AT
@@ -101,10 +96,6 @@ struct LossArgs {
   int64_t ldG, Gplane;     // bytes; Gplane: to the second part of a row of G (plane or twin)
   float *dhp;              // [splits][tiles of positions that count][Dp]
 };
-
-// Groups of the weight's rows in the entries' directory: at least 256 rows, so that a tile's
-// rows lie in one, and up to 16 an entry, so that a group has few of them (1024 at most).
-inline int dir_groups(int k) { return k < 64 ? 16 * k : 1024; }
 
 // A gradient per position in fp16 G: factors down to 2^-LIGHT of the largest go into G, whose
 // range has that much to spare.  A smaller one would push its row's G below fp16's steps, and

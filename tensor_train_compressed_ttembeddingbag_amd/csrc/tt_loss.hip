@@ -38,7 +38,18 @@ __device__ __forceinline__ void load8_at(const S *p0, int64_t c, int64_t d, bool
   }
 }
 
-// 8 source elements -> planes of 16-bit elements (fp32: x s = hi + lo, or the halves of x)
+// 8 fp32 values -> two planes: x s = hi + lo
+template <class V8, class S>
+__device__ __forceinline__ void two_parts(const S (&v)[8], float scale, V8 &hi, V8 &lo) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = (float)v[e] * scale;
+    hi[e] = (_Float16)x;
+    lo[e] = (_Float16)(x - (float)hi[e]);
+  }
+}
+
+// 8 source elements -> planes of 16-bit elements (fp32: two parts, or the halves of x)
 template <class S, class E, int PL>
 __device__ __forceinline__ void store8(const S (&v)[8], float scale, bool whole, char *dst,
                                        int64_t plane) {
@@ -58,12 +69,7 @@ __device__ __forceinline__ void store8(const S (&v)[8], float scale, bool whole,
         for (int e = 0; e < 4; ++e) h[u + e] = a[e], l[u + e] = b[e];
       }
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = (float)v[e] * scale;
-        h[e] = (typename E::e)x;
-        l[e] = (typename E::e)(x - (float)h[e]);
-      }
+      two_parts(v, scale, h, l);
     }
     *(typename E::v8 *)(dst + plane) = l;
   }
@@ -115,9 +121,8 @@ struct TensorRange {
 
 // ---------------------------------------------------------------- distillation entries
 // One wave per position: q = softmax(teacher / T) over its entries (index >= 0 and logit
-// above -inf), sorted by row, so that repeated rows lie side by side and k_logits finds the
-// entries of a tile in a directory; their q are added into the first, so that every (position,
-// row) of G is written once.  (q is the lower half of the key: the order of a sum, and with it
+// above -inf), sorted by row, so that repeated rows lie side by side; their q are added into the
+// first, so that every (position, row) of G is written once.  (q is the lower half of the key: the order of a sum, and with it
 // the result, does not depend on the sort's steps.)  sv.tgt[i]: whether position i has entries.
 // pow2: the power of two from k on.
 template <class S>
@@ -191,13 +196,6 @@ __global__ __launch_bounds__(256) void k_entries(LossArgs a, int pow2) {
       for (int u = j; u < k && key[u].e.row == row; ++u) p += __uint_as_float(key[u].e.q);
     a.sv.eidx[i * k + j] = (int)row;
     a.sv.eq[i * k + j] = p;
-  }
-  for (int b = lane; b <= a.groups; b += 64) {
-    const unsigned row = b < a.groups ? (unsigned)b << a.gshift : ~0u;
-    int n = 0;  // entries below it
-    for (int st = pow2; st > 0; st >>= 1)
-      if (n + st <= k && key[n + st - 1].e.row < row) n += st;
-    a.dir[i * (a.groups + 1) + b] = (unsigned short)n;
   }
   if (lane == 0) {
     a.sv.ent[i] = ent;
@@ -335,9 +333,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
     if (in) {
       slot = ok ? rank : -1 - (int)(a.N - 1 - (i - rank));
       a.sv.slot[i] = slot;
-      if (a.k) {
-        if (ok) a.sv.at[rank] = (int)i;
-      } else {
+      if (!a.k) {
         const int64_t t = a.tgt[i];
         if (ok) a.sv.tgt[rank] = (int)t;
         else if (t != a.ignore) set_status(a.status, TT_DEV_BAD_INDEX);
@@ -474,10 +470,58 @@ __global__ __launch_bounds__(256) void k_fold(LossArgs a, int tiles, int first) 
   }
 }
 
+// The sums of products of 16 entries of position i, from entry j0 on: lane 16 g + c has those of
+// entries 4 g .. + 3 (the same for every c).  They are the very sums that k_logits has of these
+// rows: the same instructions on the same k in the same order, the rows of the weight gathered
+// in place of 16 that follow each other, and the position's row in all 16 columns.  So what the
+// products' rounding does to a logit is the same in it and in lse, and cancels where an entry
+// holds most of the probability; a dot product of its own, however exact, would not.
+// The gather is its time: 2048 x 32 rows of 2048 fp16 in 41 us, 4096 x 64 of
+// 2048 bf16 in 138 us, out of the last-level cache.  (Entries picked out of the tiles of k_logits
+// cost 30 and 160 us there, and 45 us of 100 with rows of 256.)
+template <class S, class E, int PL, bool EIGHTS>
+__device__ __forceinline__ f4 entry_sums(const LossArgs &a, int64_t i, int j0, int lane,
+                                         bool whole, float sw, float sh) {
+  constexpr int U = PL > 1 ? 4 : 8;  // times 32 k in flight
+  const int g = lane >> 4, v = a.sv.eidx[i * a.k + min(j0 + (lane & 15), a.k - 1)];
+  const S *w = (const S *)a.weight + max(v, 0) * a.wld;  // no entry: any row, not used
+  const S *h = (const S *)a.hidden + i * a.hld;
+  f4 acc = zero4();
+  for (int64_t k0 = 0; k0 < a.D; k0 += 32 * U) {
+    S x[U][8], y[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      load8_at<EIGHTS>(w, k0 + 32 * u + 8 * g, a.D, true, x[u]);
+      load8_at<EIGHTS>(h, k0 + 32 * u + 8 * g, a.D, true, y[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (PL == 1) {
+        typename E::v8 p, q;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = x[u][e], q[e] = y[u][e];
+        acc = E::mfma(p, q, acc);
+      } else if (whole) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[u][e], y[u][e], acc, 0, 0, 0);
+      } else {
+        typename E::v8 p[2], q[2];
+        two_parts(x[u], sw, p[0], p[1]);
+        two_parts(y[u], sh, q[0], q[1]);
+        acc = E::mfma(p[0], q[0], acc);
+        acc = E::mfma(p[0], q[1], acc);
+        acc = E::mfma(p[1], q[0], acc);
+      }
+    }
+  }
+  return acc;
+}
+
 // NW waves per position: the tiles' statistics become its lse.  The logits of the target and
 // of the entries are the ones in these sums (a small loss is the difference of large terms);
 // the sum over the entries is taken in fp64.
-template <int NW>
+template <class S, class E, int PL, int NW>
 __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   __shared__ float s_m[4], s_s[4], s_z[4];
   __shared__ double s_d[4], s_q[4];
@@ -496,10 +540,12 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   if constexpr (NW > 1) {
     if (lane == 0) s_m[wv] = wm, s_s[wv] = s, s_z[wv] = z;
     __syncthreads();
-    wm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    const int w0 = wv - part;
+    wm = s_m[w0];
+    for (int w = 1; w < NW; ++w) wm = fmaxf(wm, s_m[w0 + w]);
     const float m0 = wm == -INFINITY ? 0.f : wm;
     s = z = 0.f;
-    for (int w = 0; w < 4; ++w) {
+    for (int w = w0; w < w0 + NW; ++w) {
       s += s_s[w] * __builtin_amdgcn_exp2f((s_m[w] - m0) * zs);
       z += s_z[w];
     }
@@ -508,9 +554,17 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   double qd = 0.0;  // sum over the entries of q (lse - logit), base 2
   float far = fabsf(mx);
   if (a.k && slot >= 0) {
-    for (int64_t t = i * a.k + part * 64 + lane; t < (i + 1) * a.k; t += 64 * NW) {
-      if (a.sv.eidx[t] < 0) break;
-      const float z = a.sv.ez[t], q = a.sv.eq[t];
+    const bool whole = PL > 1 && a.sv.sc->whole;
+    const float sw = PL > 1 ? ldexpf(1.f, a.sv.sc->ew) : 1.f, sh = PL > 1 ? ldexpf(1.f, a.sv.sc->eh) : 1.f;
+    for (int j0 = part * 16; j0 < a.k; j0 += 16 * NW) {
+      if (a.sv.eidx[i * a.k + j0] < 0) break;  // the empty ones are last
+      const f4 sums = a.D % 8 == 0 ? entry_sums<S, E, PL, true>(a, i, j0, lane, whole, sw, sh)
+                                   : entry_sums<S, E, PL, false>(a, i, j0, lane, whole, sw, sh);
+      const int c = lane & 15, j = j0 + 4 * (lane >> 4) + c;
+      const int64_t t = i * a.k + j;
+      if (c >= 4 || j >= a.k || a.sv.eidx[t] < 0) continue;
+      const float z = c == 0 ? sums[0] : c == 1 ? sums[1] : c == 2 ? sums[2] : sums[3];
+      const float q = a.sv.eq[t];
       const double lp = ((double)z - mx) * zs - lg;
       if (!(q == 0.f)) qd -= q * lp, far = fmaxf(far, fabsf(z));
       a.sv.ez[t] = (float)lp;
@@ -521,7 +575,8 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   if (NW > 1 && a.k) {
     if (lane == 0) s_q[wv] = qd;
     __syncthreads();
-    qd = s_q[0] + s_q[1] + s_q[2] + s_q[3];
+    qd = 0.0;
+    for (int w = 0; w < NW; ++w) qd += s_q[wv - part + w];
   }
   const bool first = lane == 0 && part == 0 && i < a.N;
   if (slot >= 0 && !a.k) far = fmaxf(far, fabsf(a.sv.zt[slot]));
@@ -786,7 +841,6 @@ static int64_t saved_layout(LossArgs &a, void *saved) {
     b.take(a.sv.eidx, a.N * a.k);
     b.take(a.sv.eq, a.N * a.k);
     b.take(a.sv.ez, a.N * a.k);
-    b.take(a.sv.at, a.N);
   }
   return b.off;
 }
@@ -864,12 +918,7 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     b.take(a.zpart, a.smoothing > 0.f ? a.Npad * a.ptiles : 0);
     b.take(a.rowloss, a.N);
     if (a.N > CHUNKS_AT) b.take(a.chunk, (a.N + CHUNK - 1) / CHUNK);
-    if (a.k) {
-      a.gshift = 8;
-      while ((a.V - 1) >> a.gshift >= dir_groups(a.k)) ++a.gshift;
-      a.groups = (int)((a.V - 1) >> a.gshift) + 1;
-      b.take(a.dir, a.N * (a.groups + 1));
-    }
+    if (a.N > CHUNKS_AT) b.take(a.chunk, (a.N + CHUNK - 1) / CHUNK);
   }
   return b.off;
 }
@@ -964,12 +1013,23 @@ static hipError_t launch_fold(const LossArgs &a, int tiles, int first, hipStream
   return hipGetLastError();
 }
 
+template <class S, class E, int PL>
+static void launch_loss(const LossArgs &a, int ticket, hipStream_t s) {
+  // few statistics: a wave per position and group of 16 entries
+  const bool few = a.fold || a.ptiles <= 256;
+  if (few && a.k <= 16)
+    tt_launch(K_LOSS_ROWS, k_loss<S, E, PL, 1>, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, ticket);
+  else if (few && a.k <= 32)
+    tt_launch(K_LOSS_ROWS, k_loss<S, E, PL, 2>, dim3((unsigned)((a.N + 1) / 2)), dim3(256), 0, s, a, ticket);
+  else
+    tt_launch(K_LOSS_ROWS, k_loss<S, E, PL, 4>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
+}
+
 static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
   const int ticket = a.N <= LOSS_TICKETS && !a.direct;  // (k_pack clears the ticket)
-  if ((a.fold || a.ptiles <= 256) && a.k <= 256)  // few statistics and entries: a wave per position
-    tt_launch(K_LOSS_ROWS, k_loss<1>, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, ticket);
-  else
-    tt_launch(K_LOSS_ROWS, k_loss<4>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
+  if (a.dtype == TT_DTYPE_F32) launch_loss<float, Fp16, 2>(a, ticket, s);
+  else if (a.dtype == TT_DTYPE_BF16) launch_loss<__bf16, Bf16, 1>(a, ticket, s);
+  else launch_loss<_Float16, Fp16, 1>(a, ticket, s);
   if (a.reduction != TT_REDUCE_NONE && !ticket)
     tt_launch(K_LOSS_ROWS, k_loss_sum, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();

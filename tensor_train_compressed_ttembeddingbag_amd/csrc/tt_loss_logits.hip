@@ -30,20 +30,11 @@ struct LogitsEpi {
   const int *tgt;          // null with distillation
   const int64_t *tgt64;    // the caller's targets instead (loss alone), or null
   float *zt;
-  int k;                   // distillation: entries per position
-  const int *eidx, *at;    // at: null where positions are not packed
-  float *ez;
-  const unsigned short *dir;
-  int gshift, groups;
   int twin;
   float one_e, e_v;        // 1 - e, e / V
 };
 
-// What the tiles give: the statistics, these and the sums of the entries' rows (distillation; a
-// variant of its own, because its mere presence cost the others 1 to 3 %), or G.
-enum { STATS, ENTRIES, GRAD };
-
-template <class E, class T, int PL, int OUT, bool MEND, bool WHOLE>
+template <class E, class T, int PL, bool GRAD, bool MEND, bool WHOLE>
 __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi &ep, char *lds) {
   gemm_tiles<E, T, PL, false, false, MEND, WHOLE>(a, lds, [&](const TileAt &t, f4 (&acc)[T::MI][T::NI], char *tmp) {
     const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
@@ -54,7 +45,7 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
     const int xl = (int)min<int64_t>(ep.nv - (int64_t)ix * T::X, T::X);  // rows of this tile
     const int xb = px + 4 * g;
     const bool full = xl == T::X;  // no rows of the tile past the vocabulary
-    if constexpr (OUT != GRAD) {
+    if constexpr (!GRAD) {
       float2 *sm = (float2 *)tmp;                       // [NWX][Y]
       float *sz = (float *)(tmp + T::NWX * T::Y * 8);   // [NWX][Y]
       int d_[T::NI];  // the target's place from this lane's first row, or -1
@@ -64,41 +55,6 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
         const int64_t first = ep.v0 + (int64_t)ix * T::X + xb;
         const int64_t t = !ep.zt || pos >= count ? -1 : ep.tgt64 ? ep.tgt64[pos] : ep.tgt[pos];
         d_[j] = (int)max<int64_t>(min<int64_t>(t - first, 1 << 20), -1);
-      }
-      if constexpr (OUT == ENTRIES) {
-        // the entries that this wave's rows hold: each lane writes the sums of its rows
-        const unsigned lo = (unsigned)(ep.v0 + (int64_t)ix * T::X + px),
-                       hi = lo + max(min(xl - px, T::wx), 0);
-        int64_t e[T::NI];
-        int n[T::NI], end[T::NI];
-#pragma unroll
-        for (int j = 0; j < T::NI; ++j) {
-          const int pos = iy * T::Y + qy + 16 * j + c, row = pos < count ? pos : 0;
-          e[j] = ep.at ? ep.at[row] : row;
-        }
-#pragma unroll
-        for (int j = 0; j < T::NI; ++j) {
-          const unsigned short *dir = ep.dir + e[j] * (ep.groups + 1) + (lo >> ep.gshift);
-          n[j] = lo < hi ? dir[0] : 0;
-          end[j] = lo < hi && iy * T::Y + qy + 16 * j + c < count ? dir[1] : 0;
-          e[j] *= ep.k;
-        }
-#pragma unroll
-        for (int j = 0; j < T::NI; ++j) {
-          for (int u = n[j]; u < end[j]; ++u) {
-            const unsigned row = ep.eidx[e[j] + u];
-            if (row >= hi) break;
-            if (row < lo) continue;
-            const int d = (int)(row - lo) - 4 * g;
-            if (d < 0 || (d & 12)) continue;
-            float z = 0.f;
-#pragma unroll
-            for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) z = d == 16 * i + r ? acc[i][j][r] : z;
-            ep.ez[e[j] + u] = z;
-          }
-        }
       }
 #pragma unroll
       for (int j = 0; j < T::NI; ++j) {
@@ -222,40 +178,39 @@ __device__ __forceinline__ void logits_tiles(const GemmArgs &a, const LogitsEpi 
   });
 }
 
-template <class E, class T, int PL, int OUT, bool MEND>
+template <class E, class T, int PL, bool GRAD, bool MEND>
 __global__ __launch_bounds__(T::NT) void k_logits(GemmArgs a, LogitsEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   if constexpr (PL > 1)
-    if (ep.sc->whole) return logits_tiles<E, T, PL, OUT, MEND, true>(a, ep, lds);
-  logits_tiles<E, T, PL, OUT, MEND, false>(a, ep, lds);
+    if (ep.sc->whole) return logits_tiles<E, T, PL, GRAD, MEND, true>(a, ep, lds);
+  logits_tiles<E, T, PL, GRAD, MEND, false>(a, ep, lds);
 }
 
-template <class E, class T, int PL, int OUT, bool MEND>
+template <class E, class T, int PL, bool GRAD, bool MEND>
 static hipError_t go(const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep, hipStream_t s) {
-  const hipError_t e = lds_limit<T>(&k_logits<E, T, PL, OUT, MEND>);
+  const hipError_t e = lds_limit<T>(&k_logits<E, T, PL, GRAD, MEND>);
   if (e != hipSuccess) return e;
-  tt_launch(OUT == GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, PL, OUT, MEND>,
+  tt_launch(GRAD ? K_LOSS_G : K_LOSS_LOGITS, k_logits<E, T, PL, GRAD, MEND>,
             dim3(gemm_grid<T>(a, (int64_t)g.tx * g.ty)), dim3(T::NT), T::LDS, s, g, ep);
   return hipGetLastError();
 }
 
-template <class E, int PL, int OUT, bool MEND>
+template <class E, int PL, bool GRAD, bool MEND>
 static hipError_t pick(int cfg, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep,
                        hipStream_t s) {
-  if (cfg == 0) return go<E, TileL, PL, OUT, MEND>(a, g, ep, s);
-  if (cfg == 1) return go<E, TileM, PL, OUT, MEND>(a, g, ep, s);
-  if (cfg == 3) return go<E, TileN, PL, OUT, MEND>(a, g, ep, s);
-  if (cfg == 4) return go<E, TileT, PL, OUT, MEND>(a, g, ep, s);
-  if (cfg == 5) return go<E, TileM1, PL, OUT, MEND>(a, g, ep, s);
-  return go<E, TileS, PL, OUT, MEND>(a, g, ep, s);
+  if (cfg == 0) return go<E, TileL, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 1) return go<E, TileM, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 3) return go<E, TileN, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 4) return go<E, TileT, PL, GRAD, MEND>(a, g, ep, s);
+  if (cfg == 5) return go<E, TileM1, PL, GRAD, MEND>(a, g, ep, s);
+  return go<E, TileS, PL, GRAD, MEND>(a, g, ep, s);
 }
 
 template <class E, int PL, bool MEND>
 static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
                        const LogitsEpi &ep, hipStream_t s) {
-  if (grad) return pick<E, PL, GRAD, MEND>(cfg, a, g, ep, s);
-  return a.k ? pick<E, PL, ENTRIES, MEND>(cfg, a, g, ep, s)
-             : pick<E, PL, STATS, MEND>(cfg, a, g, ep, s);
+  return grad ? pick<E, PL, true, MEND>(cfg, a, g, ep, s)
+              : pick<E, PL, false, MEND>(cfg, a, g, ep, s);
 }
 
 template <class E, int PL>
@@ -280,9 +235,6 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
   ep.tgt = a.k ? nullptr : a.sv.tgt;
   ep.tgt64 = a.direct ? a.tgt : nullptr;
   ep.zt = a.k || grad ? nullptr : a.sv.zt;
-  ep.k = a.k;
-  ep.eidx = a.sv.eidx; ep.at = a.direct ? nullptr : a.sv.at; ep.ez = a.sv.ez;
-  ep.dir = a.dir; ep.gshift = a.gshift; ep.groups = a.groups;
   ep.one_e = 1.f - a.smoothing;
   ep.e_v = a.smoothing / (float)a.V;
   const LogitsCut cut = logits_cut(a, nv);

@@ -30,7 +30,7 @@ def test_bounds(n, kw):
         rows, wide = up(n, 256), up(d.d, 64)
         packed = 256 * MIB + 256 * wide * size  # (pieces are whole groups of 256 rows)
         other = 64 * rows + MIB
-        assert 0 < fwd <= 256 * MIB + packed + 32 * n * d.k + other
+        assert 0 < fwd <= 256 * MIB + packed + other
         assert fwd <= only <= fwd + saved + other
         grad = max(256 * MIB, 256 * rows * size) + 256 * rows * size
         sums = max(4 * rows * up(d.d, 64), 1024 * 4 * 65536)
