@@ -479,10 +479,9 @@ __global__ __launch_bounds__(256) void k_fold(LossArgs a, int tiles, int first) 
 // The gather is its time: 2048 x 32 rows of 2048 fp16 in 41 us, 4096 x 64 of
 // 2048 bf16 in 138 us, out of the last-level cache.  (Entries picked out of the tiles of k_logits
 // cost 30 and 160 us there, and 45 us of 100 with rows of 256.)
-template <class S, class E, int PL, bool EIGHTS>
-__device__ __forceinline__ f4 entry_sums(const LossArgs &a, int64_t i, int j0, int lane,
-                                         bool whole, float sw, float sh) {
-  constexpr int U = PL > 1 ? 4 : 8;  // times 32 k in flight
+template <class S, class E, bool EIGHTS>
+__device__ __forceinline__ f4 entry_sums(const LossArgs &a, int64_t i, int j0, int lane) {
+  constexpr int U = 8;  // times 32 k in flight
   const int g = lane >> 4, v = a.sv.eidx[i * a.k + min(j0 + (lane & 15), a.k - 1)];
   const S *w = (const S *)a.weight + max(v, 0) * a.wld;  // no entry: any row, not used
   const S *h = (const S *)a.hidden + i * a.hld;
@@ -496,32 +495,85 @@ __device__ __forceinline__ f4 entry_sums(const LossArgs &a, int64_t i, int j0, i
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if constexpr (PL == 1) {
-        typename E::v8 p, q;
+      typename E::v8 p, q;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = x[u][e], q[e] = y[u][e];
-        acc = E::mfma(p, q, acc);
-      } else if (whole) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[u][e], y[u][e], acc, 0, 0, 0);
-      } else {
-        typename E::v8 p[2], q[2];
-        two_parts(x[u], sw, p[0], p[1]);
-        two_parts(y[u], sh, q[0], q[1]);
-        acc = E::mfma(p[0], q[0], acc);
-        acc = E::mfma(p[0], q[1], acc);
-        acc = E::mfma(p[1], q[0], acc);
-      }
+      for (int e = 0; e < 8; ++e) p[e] = x[u][e], q[e] = y[u][e];
+      acc = E::mfma(p, q, acc);
     }
   }
   return acc;
+}
+// fp32: the planes as k_logits reads them, but the rows of the weight from the caller's where the
+// packed ones are of the vocabulary's last piece only
+template <bool EIGHTS>
+__device__ __forceinline__ f4 entry_sums_fp32(const LossArgs &a, int64_t i, int slot, int j0,
+                                              int lane) {
+  constexpr int U = 4;
+  const bool packed = a.piece >= a.V, whole = a.sv.sc->whole;
+  const float scale = ldexpf(1.f, a.sv.sc->ew);
+  const int g = lane >> 4;
+  const int64_t v = max(a.sv.eidx[i * a.k + min(j0 + (lane & 15), a.k - 1)], 0), row = a.Dp * 4;
+  const char *w = packed ? a.wp + v * row : (const char *)a.weight + v * a.wld * 4;
+  const char *h = a.sv.hp + slot * row;
+  union Eight {  // values, or their two planes
+    float x[8];
+    hf8 p[2];
+  };
+  auto load16 = [](const char *p) {
+    struct __attribute__((packed, aligned(2))) any { hf8 v; };
+    return ((const any *)p)->v;
+  };
+  f4 acc = zero4();
+  for (int64_t k0 = 0; k0 < a.D; k0 += 32 * U) {
+    Eight x[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = k0 + 32 * u + 8 * g;
+      const int64_t at = c < a.Dp ? c * 2 : 0;
+      y[u].p[0] = load16(h + at);
+      y[u].p[1] = load16(h + row / 2 + at);
+      if (c >= a.Dp) y[u].p[0] = y[u].p[1] = hf8{};
+      if (EIGHTS || packed) {
+        const bool in = c < (packed ? a.Dp : a.D);
+        const char *p = w + (in ? c * (packed ? 2 : 4) : 0);
+        x[u].p[0] = load16(p);
+        x[u].p[1] = load16(p + (packed ? row / 2 : 16));
+        if (!in) x[u].p[0] = x[u].p[1] = hf8{};
+      } else {
+        load8((const float *)w + c, a.D - c, x[u].x);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (whole) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              packed ? ttb::whole(x[u].p[0], x[u].p[1], e) : x[u].x[e],
+              ttb::whole(y[u].p[0], y[u].p[1], e), acc, 0, 0, 0);
+        continue;
+      }
+      hf8 hi = x[u].p[0], lo = x[u].p[1];
+      if (!packed) two_parts(x[u].x, scale, hi, lo);
+      acc = Fp16::mfma(hi, y[u].p[0], acc);
+      acc = Fp16::mfma(hi, y[u].p[1], acc);
+      acc = Fp16::mfma(lo, y[u].p[0], acc);
+    }
+  }
+  return acc;
+}
+template <class S, class E, int PL, bool EIGHTS>
+__device__ __forceinline__ f4 sums_of(const LossArgs &a, int64_t i, int slot, int j0, int lane) {
+  if constexpr (PL > 1) return entry_sums_fp32<EIGHTS>(a, i, slot, j0, lane);
+  else return entry_sums<S, E, EIGHTS>(a, i, j0, lane);
 }
 
 // NW waves per position: the tiles' statistics become its lse.  The logits of the target and
 // of the entries are the ones in these sums (a small loss is the difference of large terms);
 // the sum over the entries is taken in fp64.
-template <class S, class E, int PL, int NW>
+// ENTRIES (distillation) is a variant of its own, because the gather's registers halve the
+// occupancy.
+template <class S, class E, int PL, int NW, bool ENTRIES>
 __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   __shared__ float s_m[4], s_s[4], s_z[4];
   __shared__ double s_d[4], s_q[4];
@@ -553,13 +605,11 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   const float mx = wm == -INFINITY ? 0.f : wm, lg = log2f(s);
   double qd = 0.0;  // sum over the entries of q (lse - logit), base 2
   float far = fabsf(mx);
-  if (a.k && slot >= 0) {
-    const bool whole = PL > 1 && a.sv.sc->whole;
-    const float sw = PL > 1 ? ldexpf(1.f, a.sv.sc->ew) : 1.f, sh = PL > 1 ? ldexpf(1.f, a.sv.sc->eh) : 1.f;
+  if (ENTRIES && slot >= 0) {
     for (int j0 = part * 16; j0 < a.k; j0 += 16 * NW) {
       if (a.sv.eidx[i * a.k + j0] < 0) break;  // the empty ones are last
-      const f4 sums = a.D % 8 == 0 ? entry_sums<S, E, PL, true>(a, i, j0, lane, whole, sw, sh)
-                                   : entry_sums<S, E, PL, false>(a, i, j0, lane, whole, sw, sh);
+      const f4 sums = a.D % 8 == 0 ? sums_of<S, E, PL, true>(a, i, slot, j0, lane)
+                                   : sums_of<S, E, PL, false>(a, i, slot, j0, lane);
       const int c = lane & 15, j = j0 + 4 * (lane >> 4) + c;
       const int64_t t = i * a.k + j;
       if (c >= 4 || j >= a.k || a.sv.eidx[t] < 0) continue;
@@ -572,20 +622,20 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) qd += __shfl_xor(qd, o);
   }
-  if (NW > 1 && a.k) {
+  if (NW > 1 && ENTRIES) {
     if (lane == 0) s_q[wv] = qd;
     __syncthreads();
     qd = 0.0;
     for (int w = 0; w < NW; ++w) qd += s_q[wv - part + w];
   }
   const bool first = lane == 0 && part == 0 && i < a.N;
-  if (slot >= 0 && !a.k) far = fmaxf(far, fabsf(a.sv.zt[slot]));
+  if (slot >= 0 && !ENTRIES) far = fmaxf(far, fabsf(a.sv.zt[slot]));
   if (a.dtype == TT_DTYPE_BF16 && !a.direct && slot >= 0 && !(far < G_PLAIN))
     atomicMin(&a.sv.sc->ge, 0);
   if (slot >= 0 && first) {
     a.sv.mx[slot] = mx;
     a.sv.lg[slot] = lg;
-    if (a.k) {
+    if (ENTRIES) {
       out = (float)((double)(a.temp * a.temp) * (a.sv.ent[i] + qd * LN2));
     } else {
       const float nll = (mx - a.sv.zt[slot]) * zs + lg;  // no difference of large sums
@@ -1013,23 +1063,25 @@ static hipError_t launch_fold(const LossArgs &a, int tiles, int first, hipStream
   return hipGetLastError();
 }
 
-template <class S, class E, int PL>
+template <class S, class E, int PL, bool ENTRIES>
 static void launch_loss(const LossArgs &a, int ticket, hipStream_t s) {
   // few statistics: a wave per position and group of 16 entries
   const bool few = a.fold || a.ptiles <= 256;
-  if (few && a.k <= 16)
-    tt_launch(K_LOSS_ROWS, k_loss<S, E, PL, 1>, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, ticket);
-  else if (few && a.k <= 32)
-    tt_launch(K_LOSS_ROWS, k_loss<S, E, PL, 2>, dim3((unsigned)((a.N + 1) / 2)), dim3(256), 0, s, a, ticket);
-  else
-    tt_launch(K_LOSS_ROWS, k_loss<S, E, PL, 4>, dim3((unsigned)a.N), dim3(256), 0, s, a, ticket);
+  auto go = [&](auto *kernel, int nw) {
+    tt_launch(K_LOSS_ROWS, kernel, dim3((unsigned)((a.N * nw + 3) / 4)), dim3(256), 0, s, a, ticket);
+  };
+  if (few && a.k <= 16) return go(k_loss<S, E, PL, 1, ENTRIES>, 1);
+  if constexpr (ENTRIES)
+    if (few && a.k <= 32) return go(k_loss<S, E, PL, 2, ENTRIES>, 2);
+  go(k_loss<S, E, PL, 4, ENTRIES>, 4);
 }
 
 static hipError_t launch_loss(const LossArgs &a, hipStream_t s) {
   const int ticket = a.N <= LOSS_TICKETS && !a.direct;  // (k_pack clears the ticket)
-  if (a.dtype == TT_DTYPE_F32) launch_loss<float, Fp16, 2>(a, ticket, s);
-  else if (a.dtype == TT_DTYPE_BF16) launch_loss<__bf16, Bf16, 1>(a, ticket, s);
-  else launch_loss<_Float16, Fp16, 1>(a, ticket, s);
+  if (!a.k) launch_loss<_Float16, Fp16, 1, false>(a, ticket, s);  // (of any type)
+  else if (a.dtype == TT_DTYPE_F32) launch_loss<float, Fp16, 2, true>(a, ticket, s);
+  else if (a.dtype == TT_DTYPE_BF16) launch_loss<__bf16, Bf16, 1, true>(a, ticket, s);
+  else launch_loss<_Float16, Fp16, 1, true>(a, ticket, s);
   if (a.reduction != TT_REDUCE_NONE && !ticket)
     tt_launch(K_LOSS_ROWS, k_loss_sum, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
