@@ -729,16 +729,19 @@ __global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
   }
 }
 
-// G of the light rows at its right size, for dweight
+// G of the light rows at its right size, for dweight: blockIdx.y takes LIGHT_BYTES of a row
+constexpr int LIGHT_BYTES = 16 * 256 * 4;
 __global__ __launch_bounds__(256) void k_light_rows(LossArgs a) {
   const int count = a.sv.sc->count;
+  const int64_t c0 = (int64_t)blockIdx.y * (LIGHT_BYTES / 16), c1 = min(c0 + LIGHT_BYTES / 16, a.ldG / 16);
   for (int64_t r = blockIdx.x; r < count; r += gridDim.x) {
     const int e = a.rowe[r];
     if (e == 0) continue;
     const float s = ldexpf(1.f, e);
     for (int part = 0; part < (a.twin ? 2 : 1); ++part) {
       hf8 *g = (hf8 *)(a.G + (r + part * a.twin) * a.ldG);
-      for (int64_t c = threadIdx.x; c < a.ldG / 16; c += 256) {
+#pragma unroll 4
+      for (int64_t c = c0 + threadIdx.x; c < c1; c += 256) {
         hf8 v = g[c];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] = (_Float16)((float)v[u] * s);
@@ -1106,8 +1109,9 @@ static hipError_t launch_dhidden_out(const LossArgs &a, hipStream_t s) {
 
 static hipError_t launch_light_rows(const LossArgs &a, hipStream_t s) {
   if (a.reduction != TT_REDUCE_NONE || a.dtype == TT_DTYPE_BF16) return hipSuccess;
-  tt_launch(K_LOSS_ROWS, k_light_rows, dim3((unsigned)std::min<int64_t>(a.N, 1 << 16)), dim3(256),
-            0, s, a);
+  const int64_t y = (a.ldG + LIGHT_BYTES - 1) / LIGHT_BYTES;
+  tt_launch(K_LOSS_ROWS, k_light_rows,
+            dim3((unsigned)std::min<int64_t>(a.N, std::max<int64_t>(1, 4096 / y)), (unsigned)y), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
