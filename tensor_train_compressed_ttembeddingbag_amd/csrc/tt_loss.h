@@ -13,10 +13,11 @@
 //           leaves k_pack out.
 // backward: per piece of the vocabulary k_logits (G = row factor * g, in 16 bits), k_entries_g
 //           (distillation: the entries of G), k_dhidden (split over the vocabulary, fp32),
-//           k_dweight; k_dhidden_out adds the splits.
+//           k_light_rows (a gradient per position), k_dweight; k_dhidden_out adds the splits.
 //
 // The logits are worked out twice (8 N V D operations where 6 would do): keeping them, or the
-// 16-bit G of all pieces, is the [N, V] array that these losses are there to avoid.
+// 16-bit G of all pieces, is the [N, V] array that these losses are there to avoid.  (Where G is
+// one piece, it exists for the length of the backward.)
 #pragma once
 #include "tt_gemm.h"
 #include "tt_internal.h"

@@ -9,8 +9,8 @@
 // Bound by the matrix cores from some 200 positions on, below that by the weight's bytes.
 // Measured (MI355X): 8192 x 131072 x 4096 bf16, statistics 6.4 ms = 1.37 PFLOP/s; a piece of
 // G (16384 rows of the vocabulary) 0.83 ms = 1.33 PFLOP/s (without its results 1.52: the
-// exponentials and 128 KiB of stores per tile are not hidden); 1024 x 32000 x 1024 fp32, 155
-// and 175 us (1.3 and 1.15 PFLOP/s over three products); 48 x 131072 x 2048 fp16, 107 us = 5.0
+// exponentials and 128 KiB of stores per tile are not hidden); 1024 x 32000 x 1024 fp32, 160
+// and 175 us (1.26 and 1.15 PFLOP/s over three products); 48 x 131072 x 2048 fp16, 107 us = 5.0
 // TB/s of weight.
 #include "tt_loss.h"
 
