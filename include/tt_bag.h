@@ -439,6 +439,7 @@ int tt_full_weight(const tt_desc *desc, const float *const cores[3], int table, 
 #define TT_DTYPE_F32  0
 #define TT_DTYPE_BF16 1
 #define TT_DTYPE_F16  2
+#define TT_DTYPE_I8   3  /* tables that are looked up or multiplied, see below; not the losses */
 #define TT_REDUCE_NONE 0
 #define TT_REDUCE_MEAN 1
 #define TT_REDUCE_SUM  2
@@ -488,6 +489,40 @@ int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *w
                      const void *saved, size_t saved_bytes, const float *grad_loss,
                      void *grad_hidden, void *grad_weight, void *ws, size_t ws_bytes,
                      void *stream);
+
+/* ---------------------------------------------------------------- rows of a dense table
+ * The rows of an ordinary table weight [v, d] times a scale, and the table's gradient:
+ *   out[n] = scale weight[i_n]
+ *   grad_weight[r] = scale sum over n with i_n = r of grad_out[n], summed in fp32 in a fixed
+ *     order (of n, long runs in pieces), scaled and rounded once; rows no index names are zeros.
+ * An index outside [0, v) gives a row of zeros and no gradient and sets TT_DEV_BAD_INDEX in
+ * *dev_status (may be NULL); the row padding_idx (any value outside [0, v): none) is looked up
+ * like the others but gets no gradient.  Several rows may be asked for any number of times.
+ * weight and grad_weight are of desc->dtype, out and grad_out of desc->out_dtype, any two of fp32,
+ * bf16 and fp16; rows of weight and grad_out have unit stride inside and weight_stride /
+ * grad_stride elements between them, of any alignment of their elements; out and grad_weight
+ * are contiguous.  Products are fp32 and rounded once.
+ * dtype TT_DTYPE_I8: the table is int8 with a scale for each row (tt_int8_quantize), weight[r] =
+ * values[r] row_scales[r], rows a multiple of 16 bytes apart from a multiple of 16 on; no gradient.
+ * The calls enqueue kernels only and may be captured into a HIP graph.  The result does not
+ * depend on the order of atomics.
+ * Limits (TT_ESHAPE): n <= 2^28, v <= 2^30, d <= 2^20, strides <= 2^32. */
+typedef struct tt_embed_desc {
+    int64_t n, v, d;                       /* tokens, rows of the table, width              */
+    int64_t weight_stride, grad_stride;    /* elements between rows, >= d                   */
+    int64_t padding_idx;
+    int32_t dtype, out_dtype;              /* TT_DTYPE_* of the table, of the rows looked up */
+    float scale;                           /* finite                                        */
+} tt_embed_desc;
+
+int tt_embed_forward(const tt_embed_desc *desc, const int64_t *indices, const void *weight,
+                     const float *row_scales, void *out, int32_t *dev_status, void *stream);
+/* workspace of tt_embed_backward (256-byte aligned): at most 16.1 bytes a token and, past 1024
+ * tokens, the fp32 sums of one in 64 of them; 0: the descriptor is rejected */
+size_t tt_embed_workspace_size(const tt_embed_desc *desc);
+int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const void *grad_out,
+                      void *grad_weight, void *ws, size_t ws_bytes, int32_t *dev_status,
+                      void *stream);
 
 /* ---------------------------------------------------------------- backward over distinct indices
  * The loss is linear in the rows, so the gradient of a batch equals that of a virtual

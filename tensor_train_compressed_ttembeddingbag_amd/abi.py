@@ -8,12 +8,14 @@ loudly (``RuntimeError``) when the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libttbag.so")
@@ -36,6 +38,7 @@ TT_INIT_APPROX_NORMAL = 3
 TT_DTYPE_F32 = 0
 TT_DTYPE_BF16 = 1
 TT_DTYPE_F16 = 2
+TT_DTYPE_I8 = 3
 TT_REDUCE_NONE = 0
 TT_REDUCE_MEAN = 1
 TT_REDUCE_SUM = 2
@@ -76,6 +79,12 @@ class TTLossDesc(ctypes.Structure):
                 ("teacher_dtype", ctypes.c_int32), ("reduction", ctypes.c_int32),
                 ("k", ctypes.c_int32), ("label_smoothing", ctypes.c_float),
                 ("temperature", ctypes.c_float)]
+
+
+class TTEmbedDesc(ctypes.Structure):
+    _fields_ = [("n", _I64), ("v", _I64), ("d", _I64), ("weight_stride", _I64),
+                ("grad_stride", _I64), ("padding_idx", _I64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class TTCacheView(ctypes.Structure):
@@ -152,6 +161,9 @@ _SIG = {
     "tt_profile_kernel_name": (ctypes.c_char_p, [ctypes.c_int]),
     "tt_profile_read": (ctypes.c_int, [ctypes.c_int, _P, _P]),
     "tt_debug_sync_poll_limit": (ctypes.c_int, [_I64]),
+    "tt_embed_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P]),
+    "tt_embed_workspace_size": (ctypes.c_size_t, [_P]),
+    "tt_embed_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "tt_loss_saved_size": (ctypes.c_size_t, [_P]),
     "tt_loss_workspace_size": (ctypes.c_size_t, [_P, _P, ctypes.c_int]),
     "tt_loss_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P,
@@ -251,6 +263,23 @@ def _stream(stream, like: Optional[torch.Tensor] = None):
     if _raw_stream is not None:
         return _raw_stream(like.get_device() if like is not None else torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_same_device = contextlib.nullcontext()
+
+
+def _device_of(like: torch.Tensor):
+    """A context in which the device that holds `like` is the current one: a kernel is launched on
+    a stream of the current device."""
+    return _same_device if like.get_device() == _current_device() else torch.cuda.device(like.device)
+
+
+def _no_dual(what: str, *tensors: torch.Tensor):
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("%s has no forward-mode derivative" % what)
 
 
 def _check(fn: str, rc: int):

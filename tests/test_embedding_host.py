@@ -1,0 +1,104 @@
+"""Refusals of the rows of a dense table, on the host: the C entry points reject descriptors,
+pointers and workspaces before any device work, and the public functions their arguments."""
+import ctypes
+
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from tensor_train_compressed_ttembeddingbag_amd import abi
+from tensor_train_compressed_ttembeddingbag_amd.embedding import embedding, embedding_gradient
+from tensor_train_compressed_ttembeddingbag_amd.quant import Int8Rows
+
+FAKE = 0x10000  # 256-byte aligned, never dereferenced
+BIG = 1 << 40
+
+
+def desc(**kw):
+    d = dict(n=10, v=100, d=64, weight_stride=64, grad_stride=64, padding_idx=-1,
+             dtype=abi.TT_DTYPE_BF16, out_dtype=abi.TT_DTYPE_BF16, scale=1.0)
+    d.update(kw)
+    return abi.TTEmbedDesc(*[d[f[0]] for f in abi.TTEmbedDesc._fields_])
+
+
+BAD = [(-1, dict(n=-1)), (-1, dict(v=0)), (-1, dict(d=0)), (-1, dict(dtype=4)), (-1, dict(dtype=-1)),
+       (-1, dict(out_dtype=3)), (-1, dict(out_dtype=-1)), (-1, dict(weight_stride=63)),
+       (-1, dict(grad_stride=63)), (-1, dict(scale=float("inf"))), (-1, dict(scale=float("nan"))),
+       (-2, dict(n=(1 << 28) + 1)), (-2, dict(v=(1 << 30) + 1)),
+       (-2, dict(d=(1 << 20) + 1, weight_stride=1 << 21, grad_stride=1 << 21)),
+       (-2, dict(weight_stride=(1 << 32) + 1)), (-2, dict(grad_stride=(1 << 32) + 1))]
+
+
+@pytest.mark.parametrize("code,kw", BAD, ids=[str(b[1]) for b in BAD])
+def test_bad_descriptors(code, kw):
+    lib, d = abi.lib(), desc(**kw)
+    r = ctypes.byref(d)
+    assert lib.tt_embed_workspace_size(r) == 0
+    assert lib.tt_embed_forward(r, FAKE, FAKE, None, FAKE, None, None) == code
+    assert lib.tt_embed_backward(r, FAKE, FAKE, FAKE, FAKE, BIG, None, None) == code
+
+
+def test_bad_pointers_and_workspaces():
+    lib, d, d8 = abi.lib(), desc(), desc(dtype=abi.TT_DTYPE_I8)
+    r, r8 = ctypes.byref(d), ctypes.byref(d8)
+    assert lib.tt_embed_workspace_size(None) == 0
+    assert lib.tt_embed_forward(None, FAKE, FAKE, None, FAKE, None, None) == -1
+    assert lib.tt_embed_backward(None, FAKE, FAKE, FAKE, FAKE, BIG, None, None) == -1
+    for i in (0, 1, 3):
+        a = [FAKE, FAKE, None, FAKE]
+        a[i] = None
+        assert lib.tt_embed_forward(r, *a, None, None) == -1
+    assert lib.tt_embed_forward(r, FAKE, FAKE + 1, None, FAKE, None, None) == -1
+    assert lib.tt_embed_forward(r, FAKE, FAKE, None, FAKE + 1, None, None) == -1
+    # scales come with int8 rows and with nothing else, which lie 16 bytes apart
+    assert lib.tt_embed_forward(r, FAKE, FAKE, FAKE, FAKE, None, None) == -1
+    assert lib.tt_embed_forward(r8, FAKE, FAKE, None, FAKE, None, None) == -1
+    assert lib.tt_embed_forward(r8, FAKE, FAKE + 8, FAKE, FAKE, None, None) == -1
+    odd = desc(dtype=abi.TT_DTYPE_I8, weight_stride=72)
+    assert lib.tt_embed_forward(ctypes.byref(odd), FAKE, FAKE, FAKE, FAKE, None, None) == -1
+    for i in range(4):
+        a = [FAKE] * 4
+        a[i] = None
+        assert lib.tt_embed_backward(r, *a, BIG, None, None) == -1
+    assert lib.tt_embed_backward(r8, FAKE, FAKE, FAKE, FAKE, BIG, None, None) == -1
+    assert lib.tt_embed_backward(r, FAKE, FAKE + 1, FAKE, FAKE, BIG, None, None) == -1
+    assert lib.tt_embed_backward(r, FAKE, FAKE, FAKE + 1, FAKE, BIG, None, None) == -1
+    assert lib.tt_embed_backward(r, FAKE, FAKE, FAKE, FAKE + 16, BIG, None, None) == -3
+    for n in (10, 5000, 50000):
+        d = desc(n=n)
+        size = lib.tt_embed_workspace_size(ctypes.byref(d))
+        assert 0 < size <= 16.1 * n + n // 64 * 64 * 4 + 8192
+        assert lib.tt_embed_backward(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, size - 1, None,
+                                     None) == -3
+
+
+def test_arguments():
+    w = torch.zeros(20, 8)
+    i = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU"):
+        embedding(i, w)
+    with pytest.raises(TypeError, match="weight"):
+        embedding(i, w.double())
+    with pytest.raises(TypeError, match="weight"):
+        embedding(i, [1.0])
+    with pytest.raises(ValueError, match="two dimensions"):
+        embedding(i, w[0])
+    with pytest.raises(ValueError, match="GPU"):
+        embedding_gradient(torch.zeros(4, 8), i, 20)
+    with pytest.raises(TypeError, match="grad_out"):
+        embedding_gradient(torch.zeros(4, 8, dtype=torch.int8), i, 20)
+    with pytest.raises(TypeError, match="dtype"):
+        embedding_gradient(torch.zeros(4, 8), i, 20, dtype=torch.float64)
+    with pytest.raises(ValueError, match="GPU"):
+        Int8Rows(torch.zeros(3, 16, dtype=torch.int8), torch.zeros(3))
+    with pytest.raises(TypeError, match="values"):
+        Int8Rows(w, torch.zeros(20))
+    with pytest.raises(ValueError, match="scales"):
+        Int8Rows(torch.zeros(3, 16, dtype=torch.int8), torch.zeros(3, 1))
+
+
+def test_dual_tensors_are_refused():
+    with forward_ad.dual_level():
+        w = forward_ad.make_dual(torch.zeros(20, 8), torch.ones(20, 8))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            embedding(torch.zeros(4, dtype=torch.int64), w)

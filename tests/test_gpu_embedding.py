@@ -1,0 +1,339 @@
+"""Rows of a dense table and the table's gradient on the GPU, against float64.
+
+Bounds, element by element.  Forward: one fp32 product (int8 rows: two) and one rounding to the
+output's type.  Gradient: a sum of k fp32 values in any order is off by at most k 2^-24 of the sum
+of their magnitudes, the scale and the rounding to the table's type come on top.  A type's smallest
+step is added for values below its normal range.
+"""
+import pytest
+import torch
+
+from tensor_train_compressed_ttembeddingbag_amd import abi
+from tensor_train_compressed_ttembeddingbag_amd.embedding import embedding, embedding_gradient
+from tensor_train_compressed_ttembeddingbag_amd.quant import Int8Rows
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+FP32 = 2.0 ** -24
+
+
+def step(dtype):
+    f = torch.finfo(dtype)
+    return f.eps / 2, f.tiny * f.eps
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def check_forward(out, indices, table, scale, products=1):
+    want = table[indices].double() * scale
+    rel, least = step(out.dtype)
+    bound = (rel + products * FP32) * 1.01 * want.abs() + least
+    assert out.shape == want.shape
+    assert bool(((out.double() - want).abs() <= bound).all())
+
+
+def check_gradient(dw, indices, up, v, scale, pad=None):
+    i, up = indices.reshape(-1), up.reshape(-1, up.shape[-1]).double()
+    keep = (i >= 0) & (i < v)
+    if pad is not None:
+        keep &= i != pad
+    i, up = i[keep], up[keep]
+    want = torch.zeros(v, up.shape[1], dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    count = torch.zeros(v, dtype=torch.float64, device="cuda")
+    want.index_add_(0, i, up, alpha=scale)
+    size.index_add_(0, i, up.abs(), alpha=abs(scale))
+    count.index_add_(0, i, torch.ones_like(i, dtype=torch.float64))
+    rel, least = step(dw.dtype)
+    # float64's own sums: far below
+    bound = ((count + 1) * FP32 * 1.01)[:, None] * size * (1 + rel) + rel * want.abs() + least
+    bound[count == 0] = 0  # exactly zero
+    assert dw.shape == want.shape
+    err = (dw.double() - want).abs()
+    assert bool((err <= bound).all()), float((err - bound).max())
+
+
+def tokens(n, v, g, hot=0.1):
+    i = (v * torch.rand(n, device="cuda", generator=g) ** 3).long().clamp_(max=v - 1)
+    i[torch.rand(n, device="cuda", generator=g) < hot] = v // 3
+    return i
+
+
+# lengths around the kernels' own borders (1024 tokens found without a sort, 8192 sorted by one
+# workgroup, tiles of 4096), tables of one, two and three digits, odd widths
+SIZES = [(0, 7, 5), (1, 1, 1), (1, 5, 3), (2, 1000, 8), (333, 1007, 515), (1023, 50, 64),
+         (1024, 3, 7), (1025, 50, 64), (1500, 200003, 9), (4096, 1000, 130), (8192, 1023, 33),
+         (8193, 1024, 16), (30000, 70001, 24), (9000, (1 << 20) + 5, 2), (12289, 31, 520),
+         (700, 4096, 4104)]
+
+
+@pytest.mark.parametrize("n,v,d", SIZES)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_sizes(n, v, d, dtype):
+    g = gen(n + v + d)
+    w = torch.randn(v, d, device="cuda", generator=g).to(dtype).requires_grad_()
+    i = tokens(n, v, g)
+    up = torch.randn(n, d, device="cuda", generator=g).to(dtype)
+    out = embedding(i, w, scale=1.7)
+    check_forward(out.detach(), i, w.detach(), 1.7000000476837158)  # as fp32
+    out.backward(up)
+    check_gradient(w.grad, i, up, v, 1.7000000476837158)
+    again = embedding_gradient(up, i, v, scale=1.7)
+    assert torch.equal(again, w.grad)  # a fixed order, the same bits
+
+
+@pytest.mark.parametrize("wt", TYPES)
+@pytest.mark.parametrize("ot", TYPES)
+@pytest.mark.parametrize("n", [100, 3000])
+def test_types(wt, ot, n):
+    g = gen(5)
+    v, d = 301, 77
+    w = torch.randn(v, d, device="cuda", generator=g).to(wt).requires_grad_()
+    i = tokens(n, v, g)
+    out = embedding(i, w, dtype=ot, scale=0.5, padding_idx=-1)
+    assert out.dtype == ot
+    check_forward(out.detach(), i, w.detach(), 0.5)
+    up = torch.randn(n, d, device="cuda", generator=g).to(ot)
+    out.backward(up)
+    assert w.grad.dtype == wt
+    check_gradient(w.grad, i, up, v, 0.5, v - 1)
+
+
+@pytest.mark.parametrize("n", [900, 5000, 20000])
+@pytest.mark.parametrize("v", [1, 17, 5000])
+def test_one_token_all_over(n, v):
+    """A run as long as the batch, with whole pieces in its middle."""
+    g = gen(n)
+    i = torch.full((n,), v - 1, dtype=torch.int64, device="cuda")
+    up = torch.randn(n, 40, device="cuda", generator=g)
+    check_gradient(embedding_gradient(up, i, v), i, up, v, 1.0)
+    up = up.bfloat16()
+    check_gradient(embedding_gradient(up, i, v), i, up, v, 1.0)
+
+
+@pytest.mark.parametrize("before", [0, 1, 37, 63, 64, 65])
+@pytest.mark.parametrize("length", [16, 17, 63, 64, 127, 128, 129, 191, 192, 200])
+def test_runs_and_pieces(before, length):
+    """Runs of every length around a piece's, starting anywhere in one."""
+    g = gen(before * 1000 + length)
+    n, v = 2500, 12
+    i = torch.cat([torch.zeros(before, dtype=torch.int64), torch.full((length,), 3),
+                   torch.randint(4, v, (n - before - length,))]).cuda()
+    i = i[torch.randperm(n, device="cuda", generator=g)]
+    up = torch.randn(n, 24, device="cuda", generator=g)
+    check_gradient(embedding_gradient(up, i, v, scale=-3.0), i, up, v, -3.0)
+
+
+@pytest.mark.parametrize("n", [50, 2000, 10000])
+def test_bad_indices_and_padding(n):
+    g = gen(n)
+    v, d = 90, 20
+    w = torch.randn(v, d, device="cuda", generator=g).requires_grad_()
+    i = tokens(n, v, g)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[::7] = True
+    i[::14] = -1 - torch.arange(len(i[::14]), device="cuda") * 12345678901
+    i[7::14] = v + torch.arange(len(i[7::14]), device="cuda") * (1 << 32)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = embedding(i, w, padding_idx=4, dev_status=status)
+    assert int(status) == abi.TT_DEV_BAD_INDEX
+    assert bool((out[bad] == 0).all())
+    check_forward(out[~bad].detach(), i[~bad], w.detach(), 1.0)
+    up = torch.randn(n, d, device="cuda", generator=g)
+    up[bad] = float("nan")  # not read into anything
+    status.zero_()
+    out.backward(up)
+    assert int(status) == abi.TT_DEV_BAD_INDEX
+    check_gradient(w.grad, i, torch.where(bad[:, None], 0.0, up), v, 1.0, 4)
+    assert bool((w.grad[4] == 0).all())
+    status.zero_()
+    embedding_gradient(up[~bad], i[~bad], v, dev_status=status)
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("n", [64, 3000])
+def test_values_that_are_not_finite(n):
+    """They reach the rows that name them and no others."""
+    g = gen(1)
+    v, d = 40, 24
+    i = tokens(n, v, g)
+    up = torch.randn(n, d, device="cuda", generator=g).half()
+    up[5, 3], up[6, 4], up[n - 1, 0] = float("nan"), float("inf"), float("-inf")
+    dw = embedding_gradient(up, i, v)
+    want = torch.zeros(v, d, device="cuda").index_add_(0, i, up.float())
+    assert torch.equal(torch.isfinite(dw), torch.isfinite(want))
+    assert torch.equal(torch.isnan(dw), torch.isnan(want))
+    w = torch.randn(v, d, device="cuda", generator=g)
+    w[2] = float("inf")
+    w[3, 1] = float("nan")
+    assert torch.equal(torch.isfinite(embedding(i, w, scale=2.0)), torch.isfinite(w[i]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [200, 2000])
+def test_strides_and_shapes(dtype, n):
+    """Rows any distance apart from any element on, indices of several dimensions, int32."""
+    g = gen(n)
+    v, d = 77, 45
+    base = torch.randn(v, d + 14, device="cuda", generator=g).to(dtype)
+    w = base[:, 3:3 + d].requires_grad_()
+    i = tokens(n, v, g).view(2, n // 4, 2).transpose(0, 1).int()
+    assert not i.is_contiguous()
+    out = embedding(i, w)
+    check_forward(out.detach(), i.long(), w.detach(), 1.0)
+    up = torch.randn(n // 4, 2, 2, d + 5, device="cuda", generator=g).to(dtype)[..., 1:1 + d]
+    dw, = torch.autograd.grad(out, w, up)
+    check_gradient(dw, i.long(), up, v, 1.0)
+    rows = torch.randn(n, 2 * d + 1, device="cuda", generator=g).to(dtype)[:, d:2 * d]
+    check_gradient(embedding_gradient(rows, i.reshape(-1), v),
+                   i.reshape(-1).long(), rows, v, 1.0)
+    # a broadcast gradient, a transposed table
+    out = embedding(i, w)
+    dw, = torch.autograd.grad(out.sum(), w)
+    check_gradient(dw, i.long(), torch.ones_like(out), v, 1.0)
+    t = torch.randn(d, v, device="cuda", generator=g).to(dtype).t().requires_grad_()
+    out = embedding(i, t)
+    check_forward(out.detach(), i.long(), t.detach(), 1.0)
+    dw, = torch.autograd.grad(out, t, up)
+    check_gradient(dw, i.long(), up, v, 1.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [1, 7, 16, 513])
+def test_int8_rows(dtype, d):
+    g = gen(d)
+    v, n = 61, 400
+    values = torch.randint(-127, 128, (v, d), device="cuda", generator=g, dtype=torch.int8)
+    scales = torch.rand(v, device="cuda", generator=g)
+    i = tokens(n, v, g)
+    table = values.double() * scales.double()[:, None]
+    padded = torch.full((v, d + 40), 99, dtype=torch.int8, device="cuda")
+    padded[:, 16:16 + d] = values
+    for rows in (Int8Rows(values, scales), Int8Rows(padded[:, 16:16 + d], scales)):
+        out = embedding(i, rows, dtype=dtype, scale=3.0)
+        check_forward(out, i, table, 3.0, 2)
+    assert embedding(i, rows).dtype == torch.float32
+
+
+def test_one_row_tables():
+    values = torch.ones(1, 5, dtype=torch.int8, device="cuda")
+    rows = Int8Rows(values, torch.full((1,), 0.25, device="cuda"))
+    assert bool((embedding(torch.zeros(3, dtype=torch.int64, device="cuda"), rows) == 0.25).all())
+
+
+def test_table_past_four_gigabytes():
+    """Elements of the table and of its gradient are counted in 64 bits."""
+    g = gen(9)
+    v, d = (1 << 20) + 77, 4100
+    w = torch.zeros(v, d, dtype=torch.bfloat16, device="cuda")
+    i = torch.tensor([v - 1, 5, v - 2, v // 2 + 3, v - 1], device="cuda")
+    w[i] = torch.randn(5, d, device="cuda", generator=g).bfloat16()
+    assert torch.equal(embedding(i, w), w[i])
+    del w
+    up = torch.randn(5, d, device="cuda", generator=g).bfloat16()
+    dw = embedding_gradient(up, i, v)
+    assert torch.equal(dw[v - 2], up[2]) and torch.equal(dw[v // 2 + 3], up[3])
+    assert torch.equal(dw[v - 1], (up[0].float() + up[4].float()).bfloat16())
+    touched = torch.zeros(v, dtype=torch.bool, device="cuda")
+    touched[i] = True
+    assert not bool(dw.view(torch.int16).any(1)[~touched].any())
+
+
+def test_gradient_rows_past_four_gigabytes():
+    """Rows of grad_out far apart."""
+    far = torch.empty(3, 1 << 30, dtype=torch.bfloat16, device="cuda")
+    up = far[:, :40]
+    up.copy_(torch.randn(3, 40, device="cuda", generator=gen(3)))
+    i = torch.tensor([2, 0, 2], device="cuda")
+    dw = embedding_gradient(up, i, 4)
+    assert torch.equal(dw[0], up[1])
+    assert torch.equal(dw[2], (up[0].float() + up[2].float()).bfloat16())
+
+
+@pytest.mark.parametrize("n", [500, 5000, 20000])
+def test_captured_and_on_another_stream(n):
+    """A captured forward and gradient replayed with new data between eager work, and calls on two
+    streams at once."""
+    g = gen(n)
+    v, d = 5000, 72
+    w = torch.randn(v, d, device="cuda", generator=g).bfloat16()
+    i, up = tokens(n, v, g), torch.randn(n, d, device="cuda", generator=g).bfloat16()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        embedding(i, w)
+        embedding_gradient(up, i, v)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = embedding(i, w, scale=2.0)
+        dw = embedding_gradient(up, i, v, scale=2.0)
+    for k in range(4):
+        i.copy_(tokens(n, v, g, 0.02 * k))
+        up.copy_(torch.randn(n, d, device="cuda", generator=g))
+        graph.replay()
+        want = embedding_gradient(up, i, v, scale=2.0)
+        torch.cuda.synchronize()
+        assert torch.equal(out, embedding(i, w, scale=2.0))
+        assert torch.equal(dw, want)
+        check_gradient(dw, i, up, v, 2.0)
+    i2 = tokens(n, v, g)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        a = embedding_gradient(up, i2, v)
+    b = embedding_gradient(up, i, v)
+    torch.cuda.synchronize()
+    check_gradient(a, i2, up, v, 1.0)
+    check_gradient(b, i, up, v, 1.0)
+
+
+def test_against_differences():
+    """The gradient of a scalar of the rows against central differences (float32, exact steps)."""
+    g = gen(11)
+    w = torch.randint(-8, 8, (9, 4), device="cuda", generator=g).float().requires_grad_()
+    i = torch.tensor([3, 3, 8, 0, 3, 1], device="cuda")
+    c = torch.randint(-4, 4, (6, 4), device="cuda", generator=g).float()
+    (embedding(i, w, scale=0.5) * c).sum().backward()
+    for r in range(9):
+        for k in range(4):
+            e = torch.zeros_like(w)
+            e[r, k] = 1.0
+            hi = (embedding(i, w.detach() + e, scale=0.5) * c).sum()
+            lo = (embedding(i, w.detach() - e, scale=0.5) * c).sum()
+            assert float(w.grad[r, k]) == float(hi - lo) / 2  # small whole numbers: exact
+
+
+def test_second_derivatives_are_refused():
+    w = torch.randn(5, 4, device="cuda", requires_grad=True)
+    out = embedding(torch.tensor([1, 2], device="cuda"), w)
+    up = torch.ones(2, 4, device="cuda", requires_grad=True)
+    dw, = torch.autograd.grad(out, w, up, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dw.sum().backward()
+
+
+def test_arguments_are_refused():
+    w = torch.zeros(20, 8, device="cuda")
+    i = torch.zeros(4, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError, match="indices"):
+        embedding(i.cpu(), w)
+    with pytest.raises(TypeError, match="int64"):
+        embedding(i.float(), w)
+    with pytest.raises(ValueError, match="padding_idx"):
+        embedding(i, w, padding_idx=20)
+    with pytest.raises(ValueError, match="scale"):
+        embedding(i, w, scale=1e39)
+    with pytest.raises(TypeError, match="dtype"):
+        embedding(i, w, dtype=torch.float64)
+    with pytest.raises(TypeError, match="dev_status"):
+        embedding(i, w, dev_status=i)
+    with pytest.raises(ValueError, match="dev_status"):
+        embedding(i, w, dev_status=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="shape"):
+        embedding_gradient(torch.zeros(5, 8, device="cuda"), i, 20)
+    with pytest.raises(ValueError, match="num_rows"):
+        embedding_gradient(torch.zeros(4, 8, device="cuda"), i, 0)
