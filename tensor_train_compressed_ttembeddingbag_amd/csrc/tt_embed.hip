@@ -23,7 +23,9 @@ typedef unsigned long long u64;
 constexpr int PIECE_T = 64;      // sorted tokens per piece of a long run
 constexpr int LONG_RUN = 2 * PIECE_T;  // from here on a run has a whole piece
 constexpr int ROWS_MAX = 64;     // rows of the table per block, at most
-constexpr int LIST = 1024;       // tokens of a block's rows that are kept in LDS
+constexpr int SHORT = 16;        // tokens of a run that one group of lanes adds up by itself
+constexpr int LIST = 1024;       // tokens that are looked for without a sort
+static_assert(ROWS_MAX * SHORT <= LIST, "all short runs of a block in LDS");
 constexpr int MAX_BITS = 10;     // of a digit
 constexpr int BINS = 1 << MAX_BITS;
 constexpr int SORT_ROUNDS = 8;   // elements per thread
@@ -40,71 +42,92 @@ struct EmbedArgs {
   void *out;
   int32_t *status;
   // backward
-  int lpr, chunks, rows;       // groups of eight columns per block, blocks along a row, rows per block
+  int lpr, chunks;             // groups of eight columns per block, blocks along a row
+  int rows, shift;             // rows per block: 2^shift
+  int *first;                  // [blocks of rows + 1] sorted place of a block's first token
   const u64 *sorted;           // row << 32 | token; tokens without a row last, as row v
   float *part;                 // [n / PIECE_T][d] sums of the whole pieces
 };
 
+// Eight elements of a row, on an element's boundary (int8: on a group's).  A row's last group
+// takes its last eight, whatever its width: two lanes then work the same columns out from the
+// same values in the same order and store the same bits, and no load hides behind a branch.
+// Rows narrower than eight are a variant of their own (NARROW).
 template <class T>
 struct Eight {
   T x[8];
 };
-// eight elements at p, of which `left` are there (p on an element's boundary only; int8: on a
-// group's)
-template <class T>
-__device__ __forceinline__ Eight<T> get8(const T *p, int64_t left) {
-  Eight<T> r;
-  if (left >= 8) {
-    struct __attribute__((packed, aligned(sizeof(T) < 2 ? 8 : 2))) any { Eight<T> v; };
-    r = ((const any *)p)->v;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r.x[e] = e < left ? p[e] : (T)0;
-  }
-  return r;
+template <bool NARROW>
+__device__ __forceinline__ int64_t column(int64_t group, int64_t d) {
+  return NARROW ? 0 : min(group * 8, d - 8);
 }
-template <class T>
-__device__ __forceinline__ void put8(T *p, const Eight<T> &r, int64_t left) {
-  if (left >= 8) {
-    struct __attribute__((packed, aligned(sizeof(T) < 2 ? 8 : 2))) any { Eight<T> v; };
-    any a = {r};
-    *(any *)p = a;
+template <bool NARROW, class T>
+__device__ __forceinline__ Eight<T> get8(const T *p, int64_t d) {
+  if constexpr (NARROW) {
+    Eight<T> r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.x[e] = e < d ? p[e] : (T)0;
+    return r;
   } else {
+    typedef int words __attribute__((ext_vector_type(sizeof(Eight<T>) / 4)));
+    struct __attribute__((packed, aligned(sizeof(T) < 2 ? 1 : 2))) any { words v; };
+    return __builtin_bit_cast(Eight<T>, ((const any *)p)->v);
+  }
+}
+template <bool NARROW, class T>
+__device__ __forceinline__ void put8(T *p, const Eight<T> &r, int64_t d) {
+  if constexpr (NARROW) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < left) p[e] = r.x[e];
+      if (e < d) p[e] = r.x[e];
+  } else {
+    typedef int words __attribute__((ext_vector_type(sizeof(Eight<T>) / 4)));
+    struct __attribute__((packed, aligned(2))) any { words v; };
+    ((any *)p)->v = __builtin_bit_cast(words, r);
   }
 }
 
 // ---------------------------------------------------------------- forward
-template <class W, class O>
+// U groups of a thread travel together.
+template <class W, class O, bool NARROW, int U>
 __global__ __launch_bounds__(256) void k_embed(EmbedArgs a) {
   const int64_t cpr = (a.d + 7) / 8, total = a.n * cpr, st = (int64_t)gridDim.x * 256;
   int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   int64_t r = q / cpr, c = q % cpr;
   const int64_t dr = st / cpr, dc = st % cpr;
-  for (; q < total; q += st) {
-    const int64_t v = a.idx[r];
-    const bool in = v >= 0 && v < a.v;
-    if (!in && c == 0) set_status(a.status, TT_DEV_BAD_INDEX);
-    Eight<O> o;
+  for (; q < total; q += U * st) {
+    int64_t rr[U], cc[U], v[U];
+    bool in[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o.x[e] = (O)0.f;
-    if (in) {
-      const Eight<W> w = get8((const W *)a.w + v * a.wld + c * 8, a.d - c * 8);
-      if constexpr (sizeof(W) == 1) {
-        const float t = a.rs[v];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.x[e] = (O)((float)w.x[e] * t * a.scale);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.x[e] = (O)((float)w.x[e] * a.scale);
-      }
+    for (int u = 0; u < U; ++u) {
+      rr[u] = r;
+      cc[u] = column<NARROW>(c, a.d);
+      v[u] = a.idx[min(r, a.n - 1)];
+      r += dr;
+      c += dc;
+      if (c >= cpr) c -= cpr, ++r;
     }
-    put8((O *)a.out + r * a.d + c * 8, o, a.d - c * 8);
-    r += dr;
-    c += dc;
-    if (c >= cpr) c -= cpr, ++r;
+    Eight<W> w[U];
+    float t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      in[u] = v[u] >= 0 && v[u] < a.v;
+      const int64_t row = in[u] ? v[u] : 0;
+      w[u] = get8<NARROW>((const W *)a.w + row * a.wld + cc[u], a.d);
+      t[u] = sizeof(W) == 1 ? a.rs[row] : 1.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (rr[u] >= a.n) continue;
+      if (!in[u] && cc[u] == 0) set_status(a.status, TT_DEV_BAD_INDEX);
+      Eight<O> o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = sizeof(W) == 1 ? (float)w[u].x[e] * t[u] : (float)w[u].x[e];
+        o.x[e] = (O)(in[u] ? x * a.scale : 0.f);
+      }
+      put8<NARROW>((O *)a.out + rr[u] * a.d + cc[u], o, a.d);
+    }
   }
 }
 
@@ -188,24 +211,32 @@ __global__ __launch_bounds__(1024) void k_embed_sort_small(EmbedArgs a, u64 *out
     rank_rounds(key, first, u64(first) + rounds * 64 < (u64)n ? first + rounds * 64 : n, p * bits, bits,
                 count + wv * bins, rank);
     __syncthreads();
-    int all = 0;
-    if (tid < bins)
+    int all = 0, c[16];
+    if (tid < bins) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w) c[w] = count[w * bins + tid];
+#pragma unroll
+      for (int w = 0; w < 16; ++w) all += c[w];
+    }
+    int base = scan_bins<1024>(all, s_w);
+    if (tid < bins) {
+#pragma unroll
       for (int w = 0; w < 16; ++w) {
-        const int c = count[w * bins + tid];
-        count[w * bins + tid] = all;
-        all += c;
+        count[w * bins + tid] = base;
+        base += c[w];
       }
-    const int base = scan_bins<1024>(all, s_w);
-    if (tid < bins)
-      for (int w = 0; w < 16; ++w) count[w * bins + tid] += base;
+    }
     __syncthreads();
-    u64 *to = p == passes - 1 ? out : buf;
+    const bool last = p == passes - 1;
 #pragma unroll
     for (int u = 0; u < SORT_ROUNDS; ++u)
-      if (u < rounds && first + u * 64 + lane < n)
-        to[count[wv * bins + digit_of(key[u], p * bits, bits)] + rank[u]] = key[u];
+      if (u < rounds && first + u * 64 + lane < n) {
+        const int at = count[wv * bins + digit_of(key[u], p * bits, bits)] + rank[u];
+        if (last) out[at] = key[u];
+        else buf[at] = key[u];
+      }
+    if (last) break;
     __syncthreads();
-    if (p == passes - 1) break;
 #pragma unroll
     for (int u = 0; u < SORT_ROUNDS; ++u) {
       const int i = first + u * 64 + lane;
@@ -291,241 +322,353 @@ __device__ __forceinline__ void add8(float (&acc)[8], const Eight<G> &g) {
   for (int e = 0; e < 8; ++e) acc[e] += (float)g.x[e];
 }
 
-// the sums of the pieces whose tokens are all of one row
-template <class G>
+// Where each block of rows starts in the sorted order, and the sums of the pieces whose tokens
+// are all of one row.
+template <class G, bool NARROW>
 __global__ __launch_bounds__(256) void k_embed_pieces(EmbedArgs a) {
   const int64_t p = blockIdx.x, s = p * PIECE_T;
+  if (blockIdx.y == 0) {
+    const int64_t i = s + threadIdx.x;
+    const int nb = (int)((a.v + a.rows - 1) >> a.shift);
+    auto block_of = [&](int64_t k) {  // tokens without a row lie behind all blocks
+      const u64 r = a.sorted[k] >> 32;
+      return r < (u64)a.v ? (int)(r >> a.shift) : nb;
+    };
+    if (threadIdx.x < PIECE_T && i < a.n) {
+      const int b = block_of(i);
+      for (int u = i == 0 ? 0 : block_of(i - 1) + 1; u <= b; ++u) a.first[u] = (int)i;
+      if (i == a.n - 1)
+        for (int u = b + 1; u <= nb; ++u) a.first[u] = (int)a.n;
+    }
+  }
+  if (s + PIECE_T > a.n) return;
   const unsigned row = (unsigned)(a.sorted[s] >> 32);
   if (row != (unsigned)(a.sorted[s + PIECE_T - 1] >> 32) || row >= (u64)a.v) return;
   __shared__ unsigned s_pos[PIECE_T];
   if (threadIdx.x < PIECE_T) s_pos[threadIdx.x] = (unsigned)a.sorted[s + threadIdx.x];
   __syncthreads();
-  for (int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8; c < a.d;
-       c += (int64_t)gridDim.y * 2048) {
+  const int64_t cpr = (a.d + 7) / 8;
+  for (int64_t q = (int64_t)blockIdx.y * 256 + threadIdx.x; q < cpr; q += (int64_t)gridDim.y * 256) {
+    const int64_t c = column<NARROW>(q, a.d);
     float acc[8] = {};
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int k = 0; k < PIECE_T; k += U) {
       Eight<G> g[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        g[u] = get8((const G *)a.w + (int64_t)s_pos[k + u] * a.gld + c, a.d - c);
+        g[u] = get8<NARROW>((const G *)a.w + (int64_t)s_pos[k + u] * a.gld + c, a.d);
 #pragma unroll
       for (int u = 0; u < U; ++u) add8(acc, g[u]);
     }
     Eight<float> o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) o.x[e] = acc[e];
-    put8(a.part + p * a.d + c, o, a.d - c);
+    put8<NARROW>(a.part + p * a.d + c, o, a.d);
   }
 }
 
-// first sorted place whose row is at least r: 64 probes at a time, all lanes of a wave
-__device__ __forceinline__ int64_t lower_bound(const u64 *sorted, int64_t n, u64 r) {
-  const int lane = threadIdx.x & 63;
-  int64_t lo = 0, len = n;
-  while (len > 0) {
-    const int64_t step = (len + 63) / 64, at = lo + lane * step;
-    const u64 less = __ballot(at < lo + len && sorted[at] >> 32 < r);
-    const int k = __popcll(less);  // probes below r: the place is past the last of them
-    if (k == 0) return lo;
-    const int64_t from = lo + (k - 1) * step + 1, to = min(lo + k * step, lo + len);
-    lo = from;
-    len = to - from;
+// The lanes of a block on some columns of the table: groups of a.lpr lanes beside each other.
+template <class G, class W, bool NARROW>
+struct Lanes {
+  int groups, grp;
+  bool live;
+  int64_t c;
+  const G *src;
+  __device__ __forceinline__ Lanes(const EmbedArgs &a, int chunk) {
+    const int tid = threadIdx.x;
+    groups = 256 / a.lpr;
+    grp = tid / a.lpr;
+    const int64_t group = (int64_t)chunk * a.lpr + tid % a.lpr;
+    c = column<NARROW>(group, a.d);
+    live = grp < groups && group * 8 < a.d;
+    src = (const G *)a.w + c;
   }
-  return lo;
-}
-
-// DIRECT: the block looks its tokens up in the unsorted list (at most LIST of them).
-template <class G, class W, bool DIRECT>
-__global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
-  __shared__ int s_start[ROWS_MAX + 1];
-  __shared__ unsigned s_pos[LIST];
-  __shared__ short s_row[DIRECT ? LIST : 1];
-  __shared__ int s_n[4];
-  __shared__ int64_t s_seg[2];
-  __shared__ float s_sum[256 * 8];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int chunk = blockIdx.x % a.chunks;
-  const int64_t r0 = (int64_t)(blockIdx.x / a.chunks) * a.rows;
-  const int R = (int)min<int64_t>(a.rows, a.v - r0);
-  int64_t seg = 0;  // the block's first sorted place
-  if constexpr (DIRECT) {
-    // tokens of these rows in their order
-    int found = 0;
-    for (int64_t i0 = 0; i0 < a.n; i0 += 256) {
-      const int64_t i = i0 + tid;
-      const u64 key = i < a.n ? token_key(a, i, blockIdx.x == 0) : (u64)a.v << 32;
-      const int64_t r = (int64_t)(key >> 32) - r0;
-      const bool on = r >= 0 && r < R;
-      const u64 m = __ballot(on);
-      if (lane == 0) s_n[wv] = __popcll(m);
-      __syncthreads();
-      int at = found + __popcll(m & ((1ull << lane) - 1));
-      for (int w = 0; w < 4; ++w) {
-        if (w < wv) at += s_n[w];
-        found += s_n[w];
-      }
-      if (on) {
-        s_row[at] = (short)r;
-        s_pos[at] = (unsigned)i;
-      }
-      __syncthreads();
-    }
-    // sorted by row: a thread counts, and then moves, one row's
-    unsigned own[4];  // (a row's first four; more are looked for again)
-    int c = 0;
-    if (tid < ROWS_MAX) {
-      for (int k = 0; k < found; ++k)
-        if (s_row[k] == tid) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c == e) own[e] = k;
-          ++c;
-        }
-      int s = c;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int m = __shfl_up(s, o);
-        if (lane >= o) s += m;
-      }
-      s_start[tid + 1] = s;
-      if (tid == 0) s_start[0] = 0;
-    }
-    __syncthreads();
-    // s_sum is free here: the sorted list goes through it
-    unsigned *list = (unsigned *)s_sum;
-    if (tid < ROWS_MAX && c > 0) {
-      int s = s_start[tid];
-      if (c <= 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < c) list[s + e] = s_pos[own[e]];
-      } else {
-        for (int k = own[0]; k < found; ++k)
-          if (s_row[k] == tid) list[s++] = s_pos[k];
-      }
-    }
-    __syncthreads();
-    for (int k = tid; k < found; k += 256) s_pos[k] = list[k];
-    __syncthreads();
-  } else {
-    if (wv < 2) {
-      const int64_t at = lower_bound(a.sorted, a.n, (u64)(r0 + (wv ? R : 0)));
-      if (lane == 0) s_seg[wv] = at;
-    }
-    __syncthreads();
-    seg = s_seg[0];
-    const int len = (int)(s_seg[1] - seg);
-    if (tid <= R) s_start[tid] = tid == 0 ? 0 : len;
-    __syncthreads();
-    // a row starts where the sorted row changes; rows without tokens start where the next does
-    for (int k = tid; k < len; k += 256) {
-      const u64 key = a.sorted[seg + k];
-      const int r = (int)((int64_t)(key >> 32) - r0);
-      const int before = k == 0 ? -1 : (int)((int64_t)(a.sorted[seg + k - 1] >> 32) - r0);
-      for (int u = before + 1; u <= r; ++u) s_start[u] = k;
-      if (k < LIST) s_pos[k] = (unsigned)key;
-    }
-    __syncthreads();
+  __device__ __forceinline__ Eight<G> token(const EmbedArgs &a, unsigned pos) const {
+    return get8<NARROW>(src + (int64_t)pos * a.gld, a.d);
   }
-  const int groups = 256 / a.lpr, grp = tid / a.lpr, own = tid % a.lpr;
-  const int64_t c = ((int64_t)chunk * a.lpr + own) * 8;
-  const bool live = grp < groups && c < a.d;
-  const G *src = (const G *)a.w + c;
-  const int64_t left = a.d - c;
-  auto pos_of = [&](int k) -> int64_t {
-    return k < LIST ? s_pos[k] : (unsigned)a.sorted[seg + k];
-  };
-  auto store = [&](int r, const float (&acc)[8]) {
+  __device__ __forceinline__ void store(const EmbedArgs &a, int64_t row, const float (&acc)[8]) const {
     Eight<W> o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) o.x[e] = (W)(acc[e] * a.scale);
-    put8((W *)a.out + (r0 + r) * a.d + c, o, left);
-  };
-  constexpr int B = 4, SHORT = 16;
-  if (live) {
-    // short runs, B rows side by side so that their loads travel together
-    for (int rb = grp; rb < R; rb += groups * B) {
-      int k[B], e[B], most = 0;
-      bool mine[B];
-      float acc[B][8] = {};
+    put8<NARROW>((W *)a.out + row * a.d + c, o, a.d);
+  }
+};
+
+// A long run of a row, at places [g0, g1) of the order: every group a share of it, in order, the
+// shares added in order.  Its items are the tokens up to the first whole piece, the whole pieces
+// (PIECES: where there are some), and the rest.  All threads of the block; pos_of(place): token.
+template <bool PIECES, bool NARROW, class L, class Pos>
+__device__ __forceinline__ void long_run(const EmbedArgs &a, const L &l, int64_t row, int64_t g0,
+                                         int64_t g1, Pos pos_of, float *s_sum) {
+  int64_t p0 = 0, p1 = 0;
+  if (PIECES && g1 - g0 >= LONG_RUN) {
+    p0 = (g0 + PIECE_T - 1) / PIECE_T;
+    p1 = g1 / PIECE_T;
+  }
+  const int64_t np = p1 - p0, head = np ? p0 * PIECE_T - g0 : g1 - g0;
+  const int64_t items = np ? head + np + (g1 - p1 * PIECE_T) : head;
+  const int64_t per = (items + l.groups - 1) / l.groups;
+  float acc[8] = {};
+  if (l.live) {
+    const int64_t to = min(items, (l.grp + 1) * per);
+    int64_t m = min(items, l.grp * per);
+    auto tokens = [&](int64_t g, int64_t count) {
+      constexpr int U = 8;
+      int64_t t = 0;
+      for (; t + U <= count; t += U) {
+        decltype(l.token(a, 0)) x[U];
 #pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const int r = rb + j * groups;
-        k[j] = r < R ? s_start[r] : 0;
-        e[j] = r < R ? s_start[r + 1] : 0;
-        mine[j] = r < R && e[j] - k[j] <= SHORT;
-        if (!mine[j]) e[j] = k[j];
-        most = max(most, e[j] - k[j]);
+        for (int u = 0; u < U; ++u) x[u] = l.token(a, pos_of(g + t + u));
+#pragma unroll
+        for (int u = 0; u < U; ++u) add8(acc, x[u]);
       }
-      for (int m = 0; m < most; ++m) {
-        Eight<G> g[B];
+      for (; t < count; ++t) add8(acc, l.token(a, pos_of(g + t)));
+    };
+    if (m < head) {
+      const int64_t e = min(to, head);
+      tokens(g0 + m, e - m);
+      m = max(m, e);
+    }
+    if (m < head + np && m < to) {
+      const int64_t e = min(to, head + np);
+      const float *p = a.part + (p0 + m - head) * a.d + l.c;
+#pragma unroll 8
+      for (; m < e; ++m, p += a.d) add8(acc, get8<NARROW>(p, a.d));
+    }
+    if (m < to) tokens(p1 * PIECE_T + (m - head - np), to - m);
+  }
+  if (l.groups > 1) {
+    __syncthreads();
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (k[j] + m < e[j]) g[j] = get8(src + pos_of(k[j] + m) * a.gld, left);
+    for (int e = 0; e < 8; ++e) s_sum[e * 256 + threadIdx.x] = acc[e];
+    __syncthreads();
+    if (l.live && l.grp == 0)
+      for (int w = 1; w < l.groups; ++w)
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (k[j] + m < e[j]) add8(acc[j], g[j]);
+        for (int e = 0; e < 8; ++e) acc[e] += s_sum[e * 256 + w * a.lpr + threadIdx.x];
+  }
+  if (l.live && l.grp == 0) l.store(a, row, acc);
+}
+
+// The long runs that start in one piece of the sorted order (a run of a row that half the tokens
+// name would keep a block of 64 rows busy long after the others)
+template <class G, class W, bool NARROW>
+__device__ __forceinline__ void long_runs_of_piece(const EmbedArgs &a, int64_t piece, int chunk,
+                                                   float *s_sum) {
+  const int lane = threadIdx.x & 63;  // every wave for itself
+  const int64_t i = piece * PIECE_T + lane;
+  static_assert(PIECE_T == 64, "a token per lane");
+  u64 row = a.v;
+  bool starts = false;
+  if (i + SHORT < a.n) {
+    row = a.sorted[i] >> 32;
+    starts = row < (u64)a.v && a.sorted[i + SHORT] >> 32 == row &&
+             (i == 0 || a.sorted[i - 1] >> 32 != row);
+  }
+  u64 todo = __ballot(starts);
+  if (todo == 0) return;
+  const Lanes<G, W, NARROW> l(a, chunk);
+  for (; todo; todo &= todo - 1) {
+    const int at = __ffsll(todo) - 1;
+    const u64 r = __shfl((unsigned)row, at);
+    // its end: 64 places at a time, then where it lies among 64 of them
+    int64_t g0 = piece * PIECE_T + at, lo = g0 + SHORT, step = 1;
+    // lo is in the run; the first place past it that is not
+    while (true) {  // steps of 1, 64, 4096, ..
+      const int64_t p = lo + (lane + 1) * step;
+      const u64 in = __ballot(p < a.n && a.sorted[min(p, a.n - 1)] >> 32 == r);
+      const int k = __popcll(in);
+      lo += k * step;
+      if (k < 64) break;
+      step *= 64;
+    }
+    while (step > 1) {
+      step /= 64;
+      const int64_t p = lo + (lane + 1) * step;
+      const u64 in = __ballot(p < a.n && a.sorted[min(p, a.n - 1)] >> 32 == r);
+      lo += __popcll(in) * step;
+    }
+    long_run<true, NARROW>(a, l, (int64_t)r, g0, lo + 1,
+                           [&](int64_t g) { return (unsigned)a.sorted[g]; }, s_sum);
+  }
+}
+
+// A block's rows by its columns.  The tokens of its short runs go through LDS as one list in
+// the sorted order; a group of lanes takes those of some consecutive rows and adds them up as a
+// stream, U rows of grad_out ahead of the sums, whatever rows they belong to (most rows of a large
+// vocabulary have none, so a row at a time would wait for every load).  Then the empty rows.  The
+// long runs have blocks of their own, the first ones of the launch.
+// DIRECT: the block looks its tokens up in the unsorted list (at most LIST of them), and adds its
+// long runs up itself.
+template <class G, class W, bool NARROW, bool DIRECT>
+__global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
+  __shared__ int s_start[ROWS_MAX + 1];   // a row's first token, from the block's first on
+  __shared__ int s_short[ROWS_MAX + 1];   // a row's first token in the list of short runs
+  __shared__ unsigned s_pos[LIST];        // that list: tokens, and their rows
+  __shared__ unsigned char s_row[LIST];
+  __shared__ unsigned s_all[DIRECT ? LIST : 1];  // all tokens by row
+  __shared__ int s_n[16];
+  __shared__ float s_sum[256 * 8];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int chunk = blockIdx.x % a.chunks;
+  int64_t block = blockIdx.x / a.chunks;
+  if constexpr (!DIRECT) {
+    const int64_t pieces = (a.n + PIECE_T - 1) / PIECE_T;
+    if (block < pieces) return long_runs_of_piece<G, W, NARROW>(a, block, chunk, s_sum);
+    block -= pieces;
+  }
+  const int64_t r0 = block << a.shift;
+  const int R = (int)min<int64_t>(a.rows, a.v - r0);
+  int64_t seg = 0;  // the block's first sorted place
+  int len = 0;
+  if constexpr (DIRECT) {
+    // tokens of these rows in their order: token 256 u + tid
+    static_assert(LIST == 4 * 256, "tokens of a thread");
+    u64 key[4], m[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = u * 256 + tid;
+      key[u] = i < a.n ? token_key(a, i, blockIdx.x == 0) : (u64)a.v << 32;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t r = (int64_t)(key[u] >> 32) - r0;
+      m[u] = __ballot(r >= 0 && r < R);
+      if (lane == 0) s_n[u * 4 + wv] = __popcll(m[u]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      if ((w & 3) == wv && m[w >> 2] >> lane & 1) {
+        const int at = len + __popcll(m[w >> 2] & ((1ull << lane) - 1));
+        s_row[at] = (unsigned char)((key[w >> 2] >> 32) - r0);
+        s_pos[at] = (unsigned)key[w >> 2];
       }
+      len += s_n[w];
+    }
+    __syncthreads();
+    // sorted by row: a thread counts, and then moves, one row's
+    if (wv == 0) {
+      int c = 0, at = 0;
+      for (int k = 0; k < len; ++k) {
+        if (s_row[k] == lane) {
+          if (c == 0) at = k;
+          ++c;
+        }
+      }
+      int s = c;
 #pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (mine[j]) store(rb + j * groups, acc[j]);
+      for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(s, o);
+        if (lane >= o) s += x;
+      }
+      s_start[lane + 1] = s;
+      if (lane == 0) s_start[0] = 0;
+      s -= c;
+      for (int k = at; c > 0; ++k)
+        if (s_row[k] == lane) {
+          s_all[s++] = s_pos[k];
+          --c;
+        }
+    }
+  } else {
+    seg = a.first[block];
+    len = a.first[block + 1] - (int)seg;
+    if (tid <= R) s_start[tid] = tid == 0 ? 0 : len;
+    __syncthreads();
+    if (len <= 8192) {
+      // a row starts where the sorted row changes; rows without tokens start where the next does
+#pragma unroll 4
+      for (int k = tid; k < len; k += 256) {
+        const int r = (int)((a.sorted[seg + k] >> 32) - r0);
+        const int before = k == 0 ? -1 : (int)((a.sorted[seg + k - 1] >> 32) - r0);
+        for (int u = before + 1; u <= r; ++u) s_start[u] = k;
+      }
+    } else if (tid < R) {
+      int lo = 0, hi = len;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if ((int64_t)(a.sorted[seg + mid] >> 32) - r0 < tid) lo = mid + 1;
+        else hi = mid;
+      }
+      s_start[tid] = lo;
     }
   }
-  // long ones: every group a share of the run, in order, the shares added in order.  A run's
-  // items are its tokens up to the first whole piece, the whole pieces, and the rest.
-  for (int r = 0; r < R; ++r) {
-    const int k0 = s_start[r], k1 = s_start[r + 1];
-    if (k1 - k0 <= SHORT) continue;
-    const int64_t g0 = seg + k0, g1 = seg + k1;
-    int64_t p0 = 0, p1 = 0;
-    if (!DIRECT && k1 - k0 >= LONG_RUN) {
-      p0 = (g0 + PIECE_T - 1) / PIECE_T;
-      p1 = g1 / PIECE_T;
+  __syncthreads();
+  bool any_long = false;
+  if (len > 0) {
+    const int c = lane < R ? s_start[lane + 1] - s_start[lane] : 0;
+    any_long = __any(c > SHORT);
+    if (wv == 0) {
+      int s = c <= SHORT ? c : 0;
+      const int own = s;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(s, o);
+        if (lane >= o) s += x;
+      }
+      s_short[lane + 1] = s;
+      if (lane == 0) s_short[0] = 0;
+      s -= own;
+      for (int k = 0; DIRECT && k < own; ++k) {
+        s_row[s + k] = (unsigned char)lane;
+        s_pos[s + k] = s_all[s_start[lane] + k];
+      }
     }
-    const int np = (int)(p1 - p0);
-    const int head = np ? (int)(p0 * PIECE_T - g0) : k1 - k0;
-    const int items = np ? head + np + (int)(g1 - p1 * PIECE_T) : head;
-    const int per = (items + groups - 1) / groups;
+    __syncthreads();
+    if constexpr (!DIRECT) {
+      const int r = tid >> 2, at = s_short[r], count = s_short[r + 1] - at;  // four threads a row
+      for (int k = tid & 3; k < count; k += 4) {
+        s_row[at + k] = (unsigned char)r;
+        s_pos[at + k] = (unsigned)a.sorted[seg + s_start[r] + k];
+      }
+      __syncthreads();
+    }
+  }
+  const Lanes<G, W, NARROW> l(a, chunk);
+  const int share = (R + l.groups - 1) / l.groups, ra = min(R, l.grp * share), rb = min(R, ra + share);
+  if (l.live && len > 0) {
+    constexpr int U = sizeof(G) == 2 ? 8 : 4;
+    int k = s_short[ra], cur = -1;
+    const int end = s_short[rb];
+    Eight<G> g[2][U];
+    auto load = [&](int k, Eight<G> (&to)[U]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k + u < end) to[u] = l.token(a, s_pos[k + u]);
+    };
     float acc[8] = {};
-    if (live) {
-      const int to = min(items, (grp + 1) * per);
-      int m = min(items, grp * per);
-      auto tokens = [&](int first, int count) {  // list places [first, first + count)
-        constexpr int U = 8;
-        int t = 0;
-        for (; t + U <= count; t += U) {
-          Eight<G> g[U];
+    auto add = [&](int k, const Eight<G> (&from)[U]) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) g[u] = get8(src + pos_of(first + t + u) * a.gld, left);
+      for (int u = 0; u < U; ++u)
+        if (k + u < end) {
+          const int r = s_row[k + u];
+          if (r != cur) {
+            if (cur >= 0) l.store(a, r0 + cur, acc);
 #pragma unroll
-          for (int u = 0; u < U; ++u) add8(acc, g[u]);
+            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+            cur = r;
+          }
+          add8(acc, from[u]);
         }
-        for (; t < count; ++t) add8(acc, get8(src + pos_of(first + t) * a.gld, left));
-      };
-      if (m < head) {
-        const int e = min(to, head);
-        tokens(k0 + m, e - m);
-        m = max(m, e);
-      }
-      if (m < head + np && m < to) {
-        const int e = min(to, head + np);
-        const float *p = a.part + (p0 + m - head) * a.d + c;
-#pragma unroll 4
-        for (; m < e; ++m, p += a.d) add8(acc, get8(p, left));
-      }
-      if (m < to) tokens((int)(p1 * PIECE_T - seg) + (m - head - np), to - m);
+    };
+    load(k, g[0]);
+    for (; k < end; k += 2 * U) {
+      load(k + U, g[1]);
+      add(k, g[0]);
+      load(k + 2 * U, g[0]);
+      add(k + U, g[1]);
     }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s_sum[e * 256 + tid] = acc[e];
-    __syncthreads();
-    if (live && grp == 0) {
-      for (int w = 1; w < groups; ++w)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += s_sum[e * 256 + w * a.lpr + tid];
-      store(r, acc);
-    }
+    if (cur >= 0) l.store(a, r0 + cur, acc);
+  }
+  for (int r = 0; DIRECT && any_long && r < R; ++r)
+    if (s_start[r + 1] - s_start[r] > SHORT)
+      long_run<false, NARROW>(a, l, r0 + r, s_start[r], s_start[r + 1],
+                              [&](int64_t g) { return s_all[g]; }, s_sum);
+  if (l.live) {
+    const float none[8] = {};
+    for (int r = ra; r < rb; ++r)
+      if (s_start[r + 1] == s_start[r]) l.store(a, r0 + r, none);
   }
 }
 
@@ -549,12 +692,20 @@ static int embed_args(const tt_embed_desc *d, EmbedArgs &a) {
   a.n = d->n; a.v = d->v; a.d = d->d; a.wld = d->weight_stride; a.gld = d->grad_stride;
   a.pad = d->padding_idx;
   a.scale = d->scale;
+  // few blocks along a row, with as many of a block's lanes in use as can be
   const int64_t cpr = (a.d + 7) / 8;
-  a.chunks = (int)((cpr + 63) / 64);
-  a.lpr = (int)((cpr + a.chunks - 1) / a.chunks);
+  int best = 0;
+  for (int64_t chunks = (cpr + 255) / 256; chunks <= (cpr + 63) / 64; ++chunks) {
+    const int lpr = (int)((cpr + chunks - 1) / chunks), used = 256 / lpr * lpr;
+    if (used < best + 16) continue;
+    best = used;
+    a.chunks = (int)chunks;
+    a.lpr = lpr;
+  }
   // enough blocks to fill the chip, and rows enough to pay for finding their tokens
-  a.rows = ROWS_MAX;
-  while (a.rows > 8 && (a.v + a.rows - 1) / a.rows * a.chunks < 2048) a.rows /= 2;
+  a.shift = 6;
+  while (a.shift > 3 && (a.v >> a.shift) * a.chunks < 2048) --a.shift;
+  a.rows = 1 << a.shift;
   return TT_OK;
 }
 
@@ -562,6 +713,7 @@ struct EmbedWs {
   u64 *a, *b;
   int *hist;
   float *part;
+  int *first;
   int64_t bytes;
 };
 struct Digits {
@@ -590,6 +742,7 @@ static EmbedWs embed_ws(const EmbedArgs &a, void *ws) {
       w.hist = (int *)take((a.n + TILE_T - 1) / TILE_T * (4ll << digits(a).bits));
     }
     w.part = (float *)take(a.n / PIECE_T * a.d * 4);
+    w.first = (int *)take(((a.v + a.rows - 1) / a.rows + 1) * 4);
   }
   w.bytes = std::max<int64_t>(off, 256);
   return w;
@@ -598,8 +751,14 @@ static EmbedWs embed_ws(const EmbedArgs &a, void *ws) {
 template <class W, class O>
 static void go_forward(const EmbedArgs &a, hipStream_t s) {
   const int64_t groups = a.n * ((a.d + 7) / 8);
-  tt_launch(K_EMBED, k_embed<W, O>, dim3((unsigned)std::min<int64_t>((groups + 255) / 256, 1 << 16)),
-            dim3(256), 0, s, a);
+  auto go = [&](auto *kernel, int u) {
+    tt_launch(K_EMBED, kernel,
+              dim3((unsigned)std::min<int64_t>((groups + 256 * u - 1) / (256 * u), 1 << 20)),
+              dim3(256), 0, s, a);
+  };
+  if (a.d < 8) return go(k_embed<W, O, true, 1>, 1);
+  if (groups < 1 << 21) return go(k_embed<W, O, false, 1>, 1);
+  go(k_embed<W, O, false, 4>, 4);
 }
 template <class W>
 static void go_forward(const EmbedArgs &a, int out, hipStream_t s) {
@@ -635,17 +794,23 @@ static hipError_t sort_tokens(const EmbedArgs &a, const EmbedWs &w, const u64 **
   return hipGetLastError();
 }
 
-template <class G, class W>
+template <class G, class W, bool NARROW>
 static void go_rows(const EmbedArgs &a, hipStream_t s) {
-  const int64_t blocks = (a.v + a.rows - 1) / a.rows * a.chunks;
+  const unsigned blocks = (unsigned)((a.v + a.rows - 1) / a.rows * a.chunks);
   if (direct(a)) {
-    tt_launch(K_EMBED_GRAD, k_embed_rows<G, W, true>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+    tt_launch(K_EMBED_GRAD, k_embed_rows<G, W, NARROW, true>, dim3(blocks), dim3(256), 0, s, a);
     return;
   }
-  tt_launch(K_EMBED_GRAD, k_embed_pieces<G>,
-            dim3((unsigned)(a.n / PIECE_T), (unsigned)std::min<int64_t>((a.d + 2047) / 2048, 64)),
+  tt_launch(K_EMBED_GRAD, k_embed_pieces<G, NARROW>,
+            dim3((unsigned)((a.n + PIECE_T - 1) / PIECE_T), (unsigned)std::min<int64_t>((a.d + 2047) / 2048, 64)),
             dim3(256), 0, s, a);
-  tt_launch(K_EMBED_GRAD, k_embed_rows<G, W, false>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+  const unsigned pieces = (unsigned)((a.n + PIECE_T - 1) / PIECE_T) * a.chunks;
+  tt_launch(K_EMBED_GRAD, k_embed_rows<G, W, NARROW, false>, dim3(pieces + blocks), dim3(256), 0, s, a);
+}
+template <class G, class W>
+static void go_rows(const EmbedArgs &a, hipStream_t s) {
+  if (a.d < 8) go_rows<G, W, true>(a, s);
+  else go_rows<G, W, false>(a, s);
 }
 template <class G>
 static void go_rows(const EmbedArgs &a, int w, hipStream_t s) {
@@ -700,8 +865,9 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
   if ((uintptr_t)ws % 256) return TT_EWORKSPACE;
   const EmbedWs w = embed_ws(a, ws);
   if ((size_t)w.bytes > ws_bytes) return TT_EWORKSPACE;
-  if ((a.v + a.rows - 1) / a.rows * a.chunks > 0x7fffffffll) return TT_ESHAPE;
-  a.idx = indices; a.w = grad_out; a.out = grad_weight; a.status = dev_status; a.part = w.part;
+  if (((a.v + a.rows - 1) / a.rows + a.n / PIECE_T + 1) * a.chunks > 0x7fffffffll) return TT_ESHAPE;
+  a.idx = indices; a.w = grad_out; a.out = grad_weight; a.status = dev_status;
+  a.part = w.part; a.first = w.first;
   hipStream_t s = (hipStream_t)stream;
   if (!direct(a)) {
     const hipError_t e = sort_tokens(a, w, &a.sorted, s);
