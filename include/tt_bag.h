@@ -525,6 +525,36 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
                       void *grad_weight, void *ws, size_t ws_bytes, int32_t *dev_status,
                       void *stream);
 
+/* ---------------------------------------------------------------- tables in 8-bit integers
+ * tt_int8_quantize: rows x [n, d] (dtype fp32, bf16 or fp16, `stride` elements apart, any alignment
+ * of the elements) as int8 values [n][pitch] (pitch a multiple of 16 >= d, from a multiple of 16 on;
+ * bytes from d on are cleared) with a scale each:
+ *   scales[i] = max |x_i| / 127 (fp32),  values[i][k] = x_ik / scales[i] rounded to the nearest, ties
+ *   to even, within -127 .. 127.
+ * A row with a value that is not finite gets the scale NaN and zeros; one whose scale would be below
+ * 2^-126 the scale 0 and zeros.
+ * tt_int8_linear: out[i][r] = (sum_k q_ik weight[r][k]) s_i weight_scales[r], contiguous [n][v] of
+ * out_dtype, q_i and s_i as above from hidden [n, d] of desc->dtype (hidden_stride elements apart),
+ * or given: dtype TT_DTYPE_I8 with hidden_scales (NULL otherwise), laid out like the weight: rows
+ * weight_pitch (hidden_stride) bytes apart, a multiple of 16, whose memory reaches to the next
+ * multiple of 16 behind d, with any values there.  The sums are exact, scaled in fp32 and rounded
+ * once.  The calls enqueue kernels only and may be captured into a HIP graph.
+ * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, n v <= 2^40, d <= 2^17, pitches <= 2^22, strides <= 2^32
+ * (quantize: n <= 2^30, d <= 2^20). */
+typedef struct tt_int8_desc {
+    int64_t n, v, d;                      /* tokens, rows of the table, width              */
+    int64_t hidden_stride, weight_pitch;  /* elements; bytes                               */
+    int32_t dtype, out_dtype;             /* TT_DTYPE_* of hidden, of out                  */
+} tt_int8_desc;
+
+int tt_int8_quantize(int64_t n, int64_t d, int32_t dtype, const void *x, int64_t stride,
+                     int8_t *values, int64_t pitch, float *scales, void *stream);
+/* workspace of tt_int8_linear (256-byte aligned): hidden in 8 bits; 0: the descriptor is rejected */
+size_t tt_int8_workspace_size(const tt_int8_desc *desc);
+int tt_int8_linear(const tt_int8_desc *desc, const void *hidden, const float *hidden_scales,
+                   const int8_t *weight, const float *weight_scales, void *out, void *ws,
+                   size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- backward over distinct indices
  * The loss is linear in the rows, so the gradient of a batch equals that of a virtual
  * batch with one element per distinct (table, index) u, weight 1, alone in its bag, whose

@@ -87,6 +87,11 @@ class TTEmbedDesc(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class TTInt8Desc(ctypes.Structure):
+    _fields_ = [("n", _I64), ("v", _I64), ("d", _I64), ("hidden_stride", _I64),
+                ("weight_pitch", _I64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 class TTCacheView(ctypes.Structure):
     _fields_ = [("slots", ctypes.c_void_p), ("rows", ctypes.c_void_p),
                 ("cache_size", ctypes.c_int64)]
@@ -164,6 +169,9 @@ _SIG = {
     "tt_embed_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P]),
     "tt_embed_workspace_size": (ctypes.c_size_t, [_P]),
     "tt_embed_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "tt_int8_quantize": (ctypes.c_int, [_I64, _I64, ctypes.c_int32, _P, _I64, _P, _I64, _P, _P]),
+    "tt_int8_workspace_size": (ctypes.c_size_t, [_P]),
+    "tt_int8_linear": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "tt_loss_saved_size": (ctypes.c_size_t, [_P]),
     "tt_loss_workspace_size": (ctypes.c_size_t, [_P, _P, ctypes.c_int]),
     "tt_loss_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P,

@@ -15,6 +15,7 @@
 
 #include "tt_internal.h"
 #include "tt_mfma.h"
+#include "tt_rows.h"
 
 namespace ttb {
 
@@ -48,44 +49,6 @@ struct EmbedArgs {
   const u64 *sorted;           // row << 32 | token; tokens without a row last, as row v
   float *part;                 // [n / PIECE_T][d] sums of the whole pieces
 };
-
-// Eight elements of a row, on an element's boundary (int8: on a group's).  A row's last group
-// takes its last eight, whatever its width: two lanes then work the same columns out from the
-// same values in the same order and store the same bits, and no load hides behind a branch.
-// Rows narrower than eight are a variant of their own (NARROW).
-template <class T>
-struct Eight {
-  T x[8];
-};
-template <bool NARROW>
-__device__ __forceinline__ int64_t column(int64_t group, int64_t d) {
-  return NARROW ? 0 : min(group * 8, d - 8);
-}
-template <bool NARROW, class T>
-__device__ __forceinline__ Eight<T> get8(const T *p, int64_t d) {
-  if constexpr (NARROW) {
-    Eight<T> r;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r.x[e] = e < d ? p[e] : (T)0;
-    return r;
-  } else {
-    typedef int words __attribute__((ext_vector_type(sizeof(Eight<T>) / 4)));
-    struct __attribute__((packed, aligned(sizeof(T) < 2 ? 1 : 2))) any { words v; };
-    return __builtin_bit_cast(Eight<T>, ((const any *)p)->v);
-  }
-}
-template <bool NARROW, class T>
-__device__ __forceinline__ void put8(T *p, const Eight<T> &r, int64_t d) {
-  if constexpr (NARROW) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < d) p[e] = r.x[e];
-  } else {
-    typedef int words __attribute__((ext_vector_type(sizeof(Eight<T>) / 4)));
-    struct __attribute__((packed, aligned(2))) any { words v; };
-    ((any *)p)->v = __builtin_bit_cast(words, r);
-  }
-}
 
 // ---------------------------------------------------------------- forward
 // U groups of a thread travel together.

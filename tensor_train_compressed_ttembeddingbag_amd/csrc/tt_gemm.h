@@ -1,4 +1,5 @@
-// tt_gemm.h -- the 16-bit matrix-core product that the vocabulary-head losses are built of.
+// tt_gemm.h -- the 16-bit matrix-core product that the vocabulary-head losses are built of (and, on
+// bytes in pairs, the 8-bit one of int8 tables).
 //
 // out[y][x] = sum_k P(x, k) Q(y, k): P's index x runs along the contiguous axis of the
 // result, Q's index y along its rows.  v_mfma_f32_16x16x32 (fp16 or bf16 in, fp32 sums) takes
@@ -54,6 +55,7 @@ struct Bf16 {
   typedef __bf16 e;
   typedef bf8 v8;
   typedef bf4 v4;
+  typedef f4 acc4;
   static __device__ __forceinline__ f4 mfma(v8 a, v8 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -62,8 +64,20 @@ struct Fp16 {
   typedef _Float16 e;
   typedef hf8 v8;
   typedef hf4 v4;
+  typedef f4 acc4;
   static __device__ __forceinline__ f4 mfma(v8 a, v8 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// v_mfma_i32_16x16x64_i8: sixteen 8-bit integers a lane where the others have eight 16-bit values, so
+// an operand of 2 c columns of 8 bits is one of c columns here, and lies in tiles and registers the
+// same way (both operands name the same k of a lane's 16 bytes, whatever its order).
+struct Int8 {
+  typedef i32x4 v8;
+  typedef i32x4 acc4;
+  static __device__ __forceinline__ i32x4 mfma(v8 a, v8 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
   }
 };
 
@@ -364,7 +378,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
   };
   aim();
   constexpr int LPT = Feed<T::X, PC, PL, T::NT>::L + Feed<T::Y, QC, PL, T::NT>::L;
-  f4 acc[T::MI][T::NI];
+  typename E::acc4 acc[T::MI][T::NI];
   typename E::v8 p[2][T::MI], q[2][T::NI];
   auto read_p = [&](int set, int buf) {
 #pragma unroll
@@ -386,6 +400,8 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
   // product over four k.  The reads wait for their use here: both register sets beside the
   // accumulators and the joined values do not fit.
   auto mul_whole = [&](int buf) {
+    if constexpr (!WHOLE) return;
+    else {
     read_q(0, buf);
     read_q(1, buf);
 #pragma unroll
@@ -399,6 +415,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
               whole(hi, lo, e), whole(q[0][j], q[1][j], e), acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
+    }
     }
   };
   // one LDS read to every few products, so that neither unit waits for the other's burst
@@ -422,7 +439,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-      for (int j = 0; j < T::NI; ++j) acc[i][j] = zero4();
+      for (int j = 0; j < T::NI; ++j) acc[i][j] = typename E::acc4{};
     const int steps = now.nk;
     auto mend = [&](int b) {
       Feed<T::X, PC, PL, T::NT>::mend(a.P, lds + b * SB, (int64_t)now.ix * T::X,

@@ -28,7 +28,8 @@ const char *g_names[K_COUNT] = {"k_route_coop", "k_route_a", "k_route_b", "k_rou
                                 "k_dd_frag", "k_dd_gu", "k_meta",
                                 "k_pack", "k_logits", "k_logits (G)", "k_dhidden", "k_dweight",
                                 "loss rows",
-                                "k_embed", "embed sort", "k_embed_rows"};
+                                "k_embed", "embed sort", "k_embed_rows",
+                                "k_quantize", "k_int8"};
 
 hipEvent_t take() {
   if (!g_pool.empty()) {

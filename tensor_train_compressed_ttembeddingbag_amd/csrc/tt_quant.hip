@@ -1,0 +1,316 @@
+// tt_quant.hip -- tables in 8-bit integers with a scale for each row, and their product with
+// hidden states that get a scale for each token:
+//   s_i = max |x_i| / 127,  q_i = round(x_i / s_i) to even,   out_iv = s_i t_v sum_k q_ik w_vk
+// The sum is one of whole numbers, exact in 32 bits up to 131072 columns; the two scales are
+// multiplied onto it in fp32 and the result is rounded once.
+//
+// The product runs on the tiles of tt_gemm.h: v_mfma_i32_16x16x64_i8 has the operand layout of the
+// 16-bit instructions byte for byte, at twice the operations, so a row of d bytes is one of d / 2
+// 16-bit columns there.
+#include "tt_gemm.h"
+#include "tt_internal.h"
+#include "tt_loss.h"
+#include "tt_rows.h"
+
+#include <algorithm>
+
+namespace ttb {
+
+struct QuantArgs {
+  int64_t n, d, ld, pitch;  // ld in elements, pitch in bytes
+  const void *x;
+  int8_t *q;
+  float *s;
+};
+
+// NT lanes a row; U groups of eight of each stay in registers between the maximum and the rounding,
+// wider rows are read twice.  A row with a value that is not finite gets the scale NaN and zeros, one
+// whose scale would be below the normal numbers the scale 0 and zeros.
+template <class S, int NT, bool NARROW>
+__global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
+  constexpr int U = 4;
+  __shared__ float s_m[4];
+  const int tid = threadIdx.x % NT, lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * (256 / NT) + threadIdx.x / NT;
+  const bool on = r < a.n;
+  const S *x = (const S *)a.x + (on ? r : 0) * a.ld;
+  const int64_t cpr = (a.d + 7) / 8;
+  Eight<S> v[U];
+  auto load = [&](int64_t g0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = get8<NARROW>(x + column<NARROW>(min(g0 + u * NT + tid, cpr - 1), a.d), a.d);
+  };
+  float m = 0.f;
+  for (int64_t g0 = 0; g0 < cpr; g0 += U * NT) {
+    load(g0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = fabsf((float)v[u].x[e]);
+        m = f <= m ? m : f == f ? f : INFINITY;
+      }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if constexpr (NT > 64) {
+    if (lane == 0) s_m[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  }
+  if (!on) return;
+  float s = m / 127.f;
+  if (!(m < INFINITY)) s = __builtin_nanf("");
+  else if (s < 0x1p-126f) s = 0.f;
+  if (tid == 0) a.s[r] = s;
+  const bool zero = !(s > 0.f);
+  int8_t *q = a.q + r * a.pitch;
+  for (int64_t g0 = 0; g0 < cpr; g0 += U * NT) {
+    if (cpr > U * NT) load(g0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t g = g0 + u * NT + tid;
+      if (g >= cpr) break;
+      Eight<int8_t> o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o.x[e] = zero ? (int8_t)0 : (int8_t)(int)fminf(fmaxf(rintf((float)v[u].x[e] / s), -127.f), 127.f);
+      put8<NARROW>(q + column<NARROW>(g, a.d), o, a.d);
+    }
+  }
+  for (int64_t c = a.d + tid; c < a.pitch; c += NT) q[c] = 0;
+}
+
+// Rows that come in 8 bits, with the bytes behind them cleared: a product runs over whole groups of
+// 16, and the table's may hold anything there.
+__global__ __launch_bounds__(256) void k_pad_rows(QuantArgs a) {
+  const int8_t *x = (const int8_t *)a.x;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n * a.pitch; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / a.pitch, c = i - r * a.pitch;
+    a.q[i] = c < a.d ? x[r * a.ld + c] : (int8_t)0;
+  }
+}
+
+template <class O>
+struct Int8Out {
+  O *out;
+  const float *s, *t;  // a scale per token, per row of the table
+  int64_t ld;
+  int n, v;
+};
+
+template <class O, class T>
+__global__ __launch_bounds__(T::NT) void k_int8(GemmArgs a, Int8Out<O> ep) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  typedef O o4 __attribute__((ext_vector_type(4)));
+  gemm_tiles<Int8, T, 1, false, false, false, false>(
+      a, lds, [&](const TileAt &at, i32x4 (&acc)[T::MI][T::NI], char *) {
+        const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
+        const int x = at.ix * T::X + (wv % T::NWX) * T::wx;
+        const int y = at.iy * T::Y + (wv / T::NWX) * T::wy + c;
+        float s[T::NI];
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) s[j] = ep.s[min(y + 16 * j, ep.n - 1)];
+#pragma unroll
+        for (int i = 0; i < T::MI; i += 2) {
+          float t[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[u][r] = ep.t[min(x + 16 * (i + u) + 4 * g + r, ep.v - 1)];
+          const int left = ep.v - (x + 16 * i);  // columns from this pair on
+#pragma unroll
+          for (int j = 0; j < T::NI; ++j) {
+            const bool in = y + 16 * j < ep.n;
+            O *o = ep.out + (int64_t)(y + 16 * j) * ep.ld + x + 16 * i;
+            o4 v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                // (kept: fp32 by itself, not one rounding with the conversion to fp16)
+                const float z = keep((float)acc[i + u][j][r] * s[j] * t[u][r]);
+                v[u][r] = (O)z;
+              }
+            if constexpr (sizeof(O) == 2) {
+              if (left >= 32) {  // a whole pair: 16 bytes a lane (the same for every lane)
+                store_pair_if(in, (char *)o, v[0], v[1], g);
+                continue;
+              }
+            }
+            if (!in) continue;
+            struct __attribute__((packed, aligned(2))) any { o4 v; };
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int e = 16 * u + 4 * g;
+              if (left >= e + 4) {
+                const any w = {v[u]};
+                *(any *)(o + e) = w;
+              } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (e + r < left) o[e + r] = v[u][r];
+              }
+            }
+          }
+        }
+      });
+}
+
+// ---------------------------------------------------------------- host
+template <class S, bool NARROW>
+static void go_quantize(const QuantArgs &a, hipStream_t s) {
+  // a wave a row where it holds one in registers, or where rows are many
+  if (a.d <= 1024 || (a.d <= 2048 && a.n >= 1024))
+    tt_launch(K_INT8_QUANT, k_quantize<S, 64, NARROW>, dim3((unsigned)((a.n + 3) / 4)), dim3(256), 0, s, a);
+  else
+    tt_launch(K_INT8_QUANT, k_quantize<S, 256, NARROW>, dim3((unsigned)a.n), dim3(256), 0, s, a);
+}
+template <class S>
+static void go_quantize(const QuantArgs &a, hipStream_t s) {
+  if (a.d < 8) go_quantize<S, true>(a, s);
+  else go_quantize<S, false>(a, s);
+}
+static hipError_t quantize(const QuantArgs &a, int dtype, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  if (dtype == TT_DTYPE_F32) go_quantize<float>(a, s);
+  else if (dtype == TT_DTYPE_BF16) go_quantize<__bf16>(a, s);
+  else go_quantize<_Float16>(a, s);
+  return hipGetLastError();
+}
+
+template <class O, class T>
+static hipError_t go_int8(const GemmArgs &g, const Int8Out<O> &ep, int cus, hipStream_t s) {
+  const hipError_t e = lds_limit<T>(&k_int8<O, T>);
+  if (e != hipSuccess) return e;
+  const int64_t tiles = (int64_t)g.tx * g.ty, most = (int64_t)cus * (160 * 1024 / T::LDS);
+  tt_launch(K_INT8, k_int8<O, T>, dim3((unsigned)std::min(tiles, most)), dim3(T::NT), T::LDS, s, g, ep);
+  return hipGetLastError();
+}
+
+struct Int8Args {
+  int64_t n, v, d, wpitch, pitch, qpitch;  // bytes; pitch: d in whole groups of 16
+  const int8_t *w, *q;
+  const float *s, *t;
+  void *out;
+};
+
+template <class O>
+static hipError_t product(const Int8Args &a, hipStream_t s) {
+  const int cus = std::max(device_cus(), 1);
+  int64_t large = 0;
+  if (a.n > 128 && a.v > 128)
+    large = std::min(a.v, large_tiles((a.v + 255) / 256, (a.n + 255) / 256, cus) * 256);
+  hipError_t e = hipSuccess;
+  auto part = [&](int64_t r0, int64_t rows, GemmShape t) {  // rows of the table
+    if (rows <= 0 || e != hipSuccess) return;
+    GemmArgs g = {};
+    g.P.p = (const char *)a.w + r0 * a.wpitch; g.P.ld = a.wpitch; g.P.rows = rows; g.P.cols = a.pitch / 2;
+    g.Q.p = (const char *)a.q; g.Q.ld = a.qpitch; g.Q.rows = a.n; g.Q.cols = a.pitch / 2;
+    g.K = a.pitch / 2;
+    g.xn = (int)rows; g.yn = (int)a.n;
+    g.tx = (int)((rows + t.bx - 1) / t.bx); g.ty = (int)((a.n + t.by - 1) / t.by);
+    g.splits = 1;
+    Int8Out<O> ep = {(O *)a.out + r0, a.s, a.t + r0, a.v, (int)a.n, (int)rows};
+    if (t.cfg == 0) e = go_int8<O, TileL>(g, ep, cus, s);
+    else if (t.cfg == 1) e = go_int8<O, TileM>(g, ep, cus, s);
+    else if (t.cfg == 3) e = go_int8<O, TileN>(g, ep, cus, s);
+    else if (t.cfg == 4) e = go_int8<O, TileT>(g, ep, cus, s);
+    else if (t.cfg == 5) e = go_int8<O, TileM1>(g, ep, cus, s);
+    else e = go_int8<O, TileS>(g, ep, cus, s);
+  };
+  part(0, large, {0, 256, 256});
+  part(large, a.v - large, gemm_shape(a.v - large, a.n, cus));
+  return e;
+}
+
+static int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+static int64_t elem_size(int dtype) {
+  return dtype == TT_DTYPE_F32 ? 4 : dtype == TT_DTYPE_I8 ? 1 : 2;
+}
+constexpr int64_t MAX_INT8_D = 1 << 17;  // 127^2 2^17 < 2^31
+
+static int int8_args(const tt_int8_desc *d, Int8Args &a) {
+  if (!d) return TT_EINVAL;
+  if (d->n < 0 || d->v < 1 || d->d < 1) return TT_EINVAL;
+  if (d->dtype < TT_DTYPE_F32 || d->dtype > TT_DTYPE_I8) return TT_EINVAL;
+  if (d->out_dtype < TT_DTYPE_F32 || d->out_dtype > TT_DTYPE_F16) return TT_EINVAL;
+  a = {};
+  a.n = d->n; a.v = d->v; a.d = d->d; a.wpitch = d->weight_pitch;
+  a.pitch = round_up(a.d, 16);
+  if (d->hidden_stride < d->d || a.wpitch < a.pitch || a.wpitch % 16) return TT_EINVAL;
+  if (d->dtype == TT_DTYPE_I8 && (d->hidden_stride < a.pitch || d->hidden_stride % 16)) return TT_EINVAL;
+  if (a.n > (1 << 23) || a.v > (1 << 30) || a.d > MAX_INT8_D || a.n * a.v > (1ll << 40)) return TT_ESHAPE;
+  // a tile's rows inside one buffer descriptor
+  if (a.wpitch > (1 << 22) || (d->dtype == TT_DTYPE_I8 && d->hidden_stride > (1 << 22)) ||
+      d->hidden_stride > (1ll << 32))
+    return TT_ESHAPE;
+  return TT_OK;
+}
+static int64_t int8_ws(const tt_int8_desc *d, const Int8Args &a) {
+  if (d->dtype == TT_DTYPE_I8 && a.d % 16 == 0) return 256;  // read as they lie
+  return round_up(std::max<int64_t>(a.n, 1) * a.pitch, 256) + round_up(std::max<int64_t>(a.n, 1) * 4, 256);
+}
+
+}  // namespace ttb
+
+using namespace ttb;
+
+extern "C" {
+
+int tt_int8_quantize(int64_t n, int64_t d, int32_t dtype, const void *x, int64_t stride,
+                     int8_t *values, int64_t pitch, float *scales, void *stream) {
+  if (n < 0 || d < 1 || dtype < TT_DTYPE_F32 || dtype > TT_DTYPE_F16) return TT_EINVAL;
+  if (stride < d || pitch < round_up(d, 16) || pitch % 16) return TT_EINVAL;
+  if (n > (1 << 30) || d > (1 << 20) || stride > (1ll << 32) || pitch > (1ll << 32)) return TT_ESHAPE;
+  if (n && (!x || !values || !scales)) return TT_EINVAL;
+  if ((uintptr_t)x % elem_size(dtype) || (uintptr_t)values % 16 || (uintptr_t)scales % 4) return TT_EINVAL;
+  QuantArgs a = {n, d, stride, pitch, x, values, scales};
+  return quantize(a, dtype, (hipStream_t)stream) == hipSuccess ? TT_OK : TT_EHIP;
+}
+
+size_t tt_int8_workspace_size(const tt_int8_desc *desc) {
+  Int8Args a;
+  return int8_args(desc, a) == TT_OK ? (size_t)int8_ws(desc, a) : 0;
+}
+
+int tt_int8_linear(const tt_int8_desc *desc, const void *hidden, const float *hidden_scales,
+                   const int8_t *weight, const float *weight_scales, void *out, void *ws,
+                   size_t ws_bytes, void *stream) {
+  Int8Args a;
+  const int rc = int8_args(desc, a);
+  if (rc != TT_OK) return rc;
+  const bool given = desc->dtype == TT_DTYPE_I8;
+  if (!weight || !weight_scales || (a.n && (!hidden || !out))) return TT_EINVAL;
+  if (given != (hidden_scales != nullptr) || !ws) return TT_EINVAL;
+  if ((uintptr_t)weight % 16 || (uintptr_t)weight_scales % 4 || (uintptr_t)hidden_scales % 4 ||
+      (uintptr_t)hidden % (given ? 16 : elem_size(desc->dtype)) ||
+      (uintptr_t)out % elem_size(desc->out_dtype))
+    return TT_EINVAL;
+  if ((uintptr_t)ws % 256) return TT_EWORKSPACE;
+  if ((size_t)int8_ws(desc, a) > ws_bytes) return TT_EWORKSPACE;
+  if (a.n == 0) return TT_OK;
+  hipStream_t s = (hipStream_t)stream;
+  a.w = weight; a.t = weight_scales; a.out = out;
+  QuantArgs q = {a.n, a.d, desc->hidden_stride, a.pitch, hidden, (int8_t *)ws,
+                 (float *)((char *)ws + round_up(a.n * a.pitch, 256))};
+  a.q = q.q; a.qpitch = a.pitch; a.s = given ? hidden_scales : q.s;
+  if (given && a.d % 16 == 0) {
+    a.q = (const int8_t *)hidden;
+    a.qpitch = a.n > 1 ? desc->hidden_stride : a.pitch;
+  } else if (given) {
+    tt_launch(K_INT8_QUANT, k_pad_rows, dim3((unsigned)std::min<int64_t>((a.n * a.pitch + 255) / 256, 4096)),
+              dim3(256), 0, s, q);
+    if (hipGetLastError() != hipSuccess) return TT_EHIP;
+  } else if (quantize(q, desc->dtype, s) != hipSuccess) {
+    return TT_EHIP;
+  }
+  hipError_t e;
+  if (desc->out_dtype == TT_DTYPE_F32) e = product<float>(a, s);
+  else if (desc->out_dtype == TT_DTYPE_BF16) e = product<__bf16>(a, s);
+  else e = product<_Float16>(a, s);
+  return e == hipSuccess ? TT_OK : TT_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,233 @@
+"""Tables in 8-bit integers and their product on the GPU.
+
+Everything here has one right answer, bit for bit: the scale is a float32 quotient, the values are
+float32 quotients rounded to even, the sums are whole numbers below 2^31, and two float32 products and
+one rounding follow.  The references are worked out on the CPU with those operations (the sums in
+float64, where whole numbers below 2^53 are exact); beside that the product is held against float64
+without quantisation, within the bound that the rounding to 8 bits sets.
+"""
+import pytest
+import torch
+
+from tensor_train_compressed_ttembeddingbag_amd.embedding import embedding
+from tensor_train_compressed_ttembeddingbag_amd.quant import Int8Rows, int8_linear, quantize_rows
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def quantised(x):
+    """values and scales on the CPU."""
+    x = x.float().cpu()
+    top = torch.where(torch.isfinite(x), x.abs(), torch.inf).amax(1)
+    s = top / 127.0
+    s[s < 2.0 ** -126] = 0.0
+    s[~torch.isfinite(top)] = float("nan")
+    q = torch.round(x / s[:, None])
+    q[~(s > 0)] = 0.0
+    return q.clamp(-127, 127), s
+
+
+def product(q, s, w, t, dtype):
+    acc = (q.double().cuda() @ w.double().cuda().t().contiguous()).float()  # one rounding
+    return (acc * s.cuda()[:, None] * t.cuda()[None]).to(dtype)
+
+
+def same(a, b):
+    return a.shape == b.shape and a.dtype == b.dtype and bool(
+        ((a == b) | (torch.isnan(a) & torch.isnan(b))).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,d", [(1, 1), (3, 7), (5, 8), (2, 15), (9, 129), (4, 1024), (3, 2047),
+                                 (1100, 1040), (2, 8200), (2, 40000)])
+def test_rows_in_8_bits(n, d, dtype):
+    g = gen(n + d)
+    x = (torch.randn(n, d, device="cuda", generator=g) *
+         10.0 ** torch.randint(-3, 3, (n, 1), device="cuda", generator=g)).to(dtype)
+    rows = quantize_rows(x)
+    q, s = quantised(x)
+    assert torch.equal(rows.scales.cpu(), s)
+    assert torch.equal(rows.values.cpu().float(), q)
+    pad = rows.values.as_strided((n, rows.pitch - d), (rows.pitch, 1), d)
+    assert not bool(pad.any())
+    # half a step of the row's own
+    err = (rows.values.double() * rows.scales.double()[:, None] - x.double()).abs()
+    assert bool((err <= rows.scales.double()[:, None] * 0.5 * (1 + 2.0 ** -16)).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_of_any_values(dtype):
+    """Zeros, ties, tiny and huge rows, infinities and NaN."""
+    f = torch.finfo(dtype)
+    x = torch.zeros(12, 21, device="cuda")
+    x[1] = torch.arange(21, device="cuda") - 10.0
+    x[2, 0], x[2, 1:5] = 127.0, torch.tensor([0.5, 1.5, -2.5, 126.5], device="cuda")
+    x[3, 4] = float("inf")
+    x[4, 20] = float("nan")
+    x[5, 0] = -float("inf")
+    x[6] = f.max
+    x[7] = -f.max
+    x[8, 3] = f.tiny
+    x[9] = f.tiny * f.eps
+    x[10, 7] = f.tiny * 200
+    x[11, 0], x[11, 1] = float("nan"), float("inf")
+    x = x.to(dtype)
+    rows = quantize_rows(x)
+    q, s = quantised(x)
+    assert same(rows.scales.cpu(), s)
+    assert torch.equal(rows.values.cpu().float(), q)
+    w = quantize_rows(torch.randn(70, 21, device="cuda", generator=gen(1)))
+    out = int8_linear(x, w, dtype=torch.float32)
+    assert bool(torch.isnan(out[[3, 4, 5, 11]]).all())
+    assert not bool(torch.isnan(out[[0, 1, 2, 8, 9, 10]]).any())
+    table = int8_linear(torch.ones(2, 21, device="cuda"), rows, dtype=torch.float32)
+    assert bool(torch.isnan(table[:, [3, 4, 5, 11]]).all())
+    assert not bool(torch.isnan(table[:, [0, 1, 2, 8, 9, 10]]).any())
+
+
+@pytest.mark.parametrize("n", [1, 2, 17, 64, 65, 130, 300])
+@pytest.mark.parametrize("v,d", [(1, 1), (5, 7), (63, 16), (64, 100), (65, 128), (257, 130), (1000, 515),
+                                 (4099, 1024), (33000, 64)])
+def test_sizes(n, v, d):
+    g = gen(n + v + d)
+    dtype = TYPES[(n + v + d) % 3]
+    x = torch.randn(n, d, device="cuda", generator=g).to(dtype)
+    w = torch.randn(v, d, device="cuda", generator=g)
+    rows = quantize_rows(w)
+    out = int8_linear(x, rows)
+    want = product(*quantised(x), *quantised(w), dtype)
+    assert same(out, want)
+    # against the product that was quantised: both operands off by half a step of their own
+    q, s = x.double(), x.double().abs().amax(1) / 127
+    u, t = w.double(), w.double().abs().amax(1) / 127
+    exact = q @ u.t().contiguous()
+    bound = 0.5 * (s[:, None] * u.abs().sum(1)[None] + q.abs().sum(1)[:, None] * t[None]) + \
+        0.25 * d * s[:, None] * t[None]
+    assert bool(((out.double() - exact).abs() <=
+                 bound * 1.001 + torch.finfo(dtype).eps * exact.abs() + 1e-6).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("n", [3, 200])
+def test_types(dtype, out, n):
+    g = gen(7)
+    x = torch.randn(n, 70, device="cuda", generator=g).to(dtype)
+    w = torch.randn(301, 70, device="cuda", generator=g).to(dtype)
+    got = int8_linear(x, quantize_rows(w), dtype=out)
+    assert same(got, product(*quantised(x), *quantised(w), out))
+
+
+def test_largest_sums():
+    """All of one sign at the limit of the width: sums up to 127^2 2^17 fit 32 bits."""
+    d = 1 << 17
+    x = torch.full((70, d), 3.0, device="cuda")
+    x[1] = -3.0
+    w = quantize_rows(torch.full((130, d), 0.5, device="cuda"))
+    out = int8_linear(x, w)
+    s, t = torch.tensor(3.0) / 127, torch.tensor(0.5) / 127
+    want = torch.tensor(float(127 * 127 * d)) * s * t
+    assert bool((out[0] == want.cuda()).all()) and bool((out[1] == -want.cuda()).all())
+
+
+@pytest.mark.parametrize("n", [5, 150])
+@pytest.mark.parametrize("d", [45, 64])
+def test_layouts(n, d):
+    """Rows any distance apart, garbage behind them, several dimensions, values given in 8 bits."""
+    g = gen(n)
+    x = torch.randn(n, 3 * d, device="cuda", generator=g).bfloat16()[:, d + 1:2 * d + 1]
+    w = torch.randn(200, d, device="cuda", generator=g)
+    wq, wt = quantised(w)
+    padded = torch.randint(-128, 128, (200, 112), device="cuda", generator=g, dtype=torch.int8)
+    padded[:, 16:16 + d] = wq.to(torch.int8).cuda()
+    rows = Int8Rows(padded[:, 16:16 + d], wt.cuda())
+    assert rows.values.data_ptr() == padded.data_ptr() + 16
+    q, s = quantised(x)
+    want = product(q, s, wq, wt, torch.bfloat16)
+    assert same(int8_linear(x, rows), want)
+    if n % 5 == 0:
+        assert same(int8_linear(x.view(5, n // 5, d).transpose(0, 1), rows),
+                    want.view(5, n // 5, 200).transpose(0, 1))
+    assert same(int8_linear(x[0], rows), want[0])
+    # garbage behind the rows of both operands
+    hp = torch.randint(-128, 128, (n, 96), device="cuda", generator=g, dtype=torch.int8)
+    hp[:, :d] = q.to(torch.int8).cuda()
+    given = Int8Rows(hp[:, :d], s.cuda())
+    assert given.values.data_ptr() == hp.data_ptr()
+    out = int8_linear(given, rows)
+    assert same(out, product(q, s, wq, wt, torch.float32))
+    # a layout that has to be copied
+    odd = Int8Rows(padded[:, 17:16 + d], wt.cuda())
+    assert same(embedding(torch.arange(200, device="cuda"), odd),
+                (wq[:, 1:].cuda() * wt.cuda()[:, None]))
+
+
+def test_no_tokens():
+    rows = quantize_rows(torch.randn(30, 8, device="cuda"))
+    assert int8_linear(torch.zeros(0, 8, device="cuda"), rows).shape == (0, 30)
+
+
+def test_outputs_past_four_gigabytes():
+    """Places of the result are counted in 64 bits."""
+    g = gen(2)
+    n, v = 70000, 33000
+    x = torch.randn(n, 16, device="cuda", generator=g).bfloat16()
+    w = torch.randn(v, 16, device="cuda", generator=g)
+    rows = quantize_rows(w)
+    out = int8_linear(x, rows)
+    assert out.numel() * 2 > 1 << 32
+    at = torch.tensor([0, 1, n // 2, n - 2, n - 1], device="cuda")
+    assert same(out[at], product(*quantised(x[at]), *quantised(w), torch.bfloat16))
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_captured(n):
+    g = gen(n)
+    x = torch.randn(n, 200, device="cuda", generator=g).half()
+    rows = quantize_rows(torch.randn(500, 200, device="cuda", generator=g))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        int8_linear(x, rows)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = int8_linear(x, rows)
+    for _ in range(4):
+        x.copy_(torch.randn(n, 200, device="cuda", generator=g))
+        graph.replay()
+        want = int8_linear(x, rows)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_arguments_are_refused():
+    rows = quantize_rows(torch.randn(30, 8, device="cuda"))
+    x = torch.randn(4, 8, device="cuda")
+    with pytest.raises(TypeError, match="Int8Rows"):
+        int8_linear(x, x)
+    with pytest.raises(ValueError, match="rows of"):
+        int8_linear(x[:, :7], rows)
+    with pytest.raises(TypeError, match="hidden"):
+        int8_linear(x.double(), rows)
+    with pytest.raises(TypeError, match="dtype"):
+        int8_linear(x, rows, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        int8_linear(x.cpu(), rows)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        int8_linear(x.requires_grad_(), rows)
+    with torch.no_grad():
+        int8_linear(x, rows)
+    with pytest.raises(ValueError, match="two dimensions"):
+        quantize_rows(torch.zeros(0, 8, device="cuda"))
+    with pytest.raises(ValueError, match="last dimension"):
+        quantize_rows(torch.zeros(3, 0, device="cuda"))
+    with pytest.raises(ValueError, match="scales"):
+        Int8Rows(rows.values, rows.scales[:3])

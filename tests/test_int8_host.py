@@ -1,0 +1,82 @@
+"""Refusals of the 8-bit tables, on the host."""
+import ctypes
+
+import pytest
+import torch
+
+from tensor_train_compressed_ttembeddingbag_amd import abi
+from tensor_train_compressed_ttembeddingbag_amd.quant import int8_linear, quantize_rows
+
+FAKE = 0x10000  # 256-byte aligned, never dereferenced
+BIG = 1 << 40
+
+
+def desc(**kw):
+    d = dict(n=10, v=100, d=60, hidden_stride=60, weight_pitch=64, dtype=abi.TT_DTYPE_BF16,
+             out_dtype=abi.TT_DTYPE_BF16)
+    d.update(kw)
+    return abi.TTInt8Desc(*[d[f[0]] for f in abi.TTInt8Desc._fields_])
+
+
+BAD = [(-1, dict(n=-1)), (-1, dict(v=0)), (-1, dict(d=0)), (-1, dict(dtype=4)), (-1, dict(dtype=-1)),
+       (-1, dict(out_dtype=3)), (-1, dict(hidden_stride=59)), (-1, dict(weight_pitch=60)),
+       (-1, dict(weight_pitch=72)), (-1, dict(dtype=3, hidden_stride=60)),
+       (-1, dict(dtype=3, hidden_stride=72)), (-2, dict(n=(1 << 23) + 1)),
+       (-2, dict(v=(1 << 30) + 1)), (-2, dict(n=1 << 20, v=1 << 21)),
+       (-2, dict(d=(1 << 17) + 1, hidden_stride=1 << 18, weight_pitch=1 << 18)),
+       (-2, dict(weight_pitch=(1 << 22) + 16)), (-2, dict(dtype=3, hidden_stride=(1 << 22) + 16)),
+       (-2, dict(hidden_stride=(1 << 32) + 1))]
+
+
+@pytest.mark.parametrize("code,kw", BAD, ids=[str(b[1]) for b in BAD])
+def test_bad_descriptors(code, kw):
+    lib, d = abi.lib(), desc(**kw)
+    r = ctypes.byref(d)
+    s = FAKE if kw.get("dtype") == 3 else None
+    assert lib.tt_int8_workspace_size(r) == 0
+    assert lib.tt_int8_linear(r, FAKE, s, FAKE, FAKE, FAKE, FAKE, BIG, None) == code
+
+
+def test_bad_pointers_and_workspaces():
+    lib, d = abi.lib(), desc()
+    r = ctypes.byref(d)
+    size = lib.tt_int8_workspace_size(r)
+    assert size >= 10 * 64 + 40
+    assert lib.tt_int8_workspace_size(None) == 0
+    good = [FAKE, None, FAKE, FAKE, FAKE, FAKE]
+    assert lib.tt_int8_linear(None, *good, BIG, None) == -1
+    for i in (0, 2, 3, 4, 5):
+        a = list(good)
+        a[i] = None
+        assert lib.tt_int8_linear(r, *a, BIG, None) == -1, i
+    for i, off, code in ((0, 1, -1), (1, 0, -1), (2, 8, -1), (3, 2, -1), (4, 1, -1), (5, 16, -3)):
+        a = list(good)
+        a[i] = FAKE + off
+        assert lib.tt_int8_linear(r, *a, BIG, None) == code, i
+    assert lib.tt_int8_linear(r, *good, size - 1, None) == -3
+    d8 = desc(dtype=abi.TT_DTYPE_I8, hidden_stride=64)
+    assert lib.tt_int8_linear(ctypes.byref(d8), *good, BIG, None) == -1  # no scales
+    a = list(good)
+    a[0], a[1] = FAKE + 8, FAKE
+    assert lib.tt_int8_linear(ctypes.byref(d8), *a, BIG, None) == -1
+
+
+@pytest.mark.parametrize("code,args", [
+    (-1, dict(n=-1)), (-1, dict(d=0)), (-1, dict(dtype=3)), (-1, dict(stride=59)), (-1, dict(pitch=60)),
+    (-1, dict(pitch=72)), (-1, dict(x=None)), (-1, dict(values=None)), (-1, dict(scales=None)),
+    (-1, dict(x=FAKE + 1)), (-1, dict(values=FAKE + 8)), (-1, dict(scales=FAKE + 2)),
+    (-2, dict(n=(1 << 30) + 1)), (-2, dict(d=(1 << 20) + 1, stride=1 << 21, pitch=1 << 21)),
+    (-2, dict(stride=(1 << 32) + 1)), (-2, dict(pitch=(1 << 32) + 16))])
+def test_bad_quantize(code, args):
+    a = dict(n=10, d=60, dtype=abi.TT_DTYPE_F16, x=FAKE, stride=60, values=FAKE, pitch=64, scales=FAKE)
+    a.update(args)
+    assert abi.lib().tt_int8_quantize(*a.values(), None) == code
+
+
+def test_arguments():
+    with pytest.raises(ValueError, match="GPU"):
+        quantize_rows(torch.zeros(3, 8))
+    with pytest.raises(TypeError, match="float32"):
+        quantize_rows(torch.zeros(3, 8, dtype=torch.int8))
+    with pytest.raises(TypeError, match="Int8Rows"):
+        int8_linear(torch.zeros(3, 8), torch.zeros(3, 8))
