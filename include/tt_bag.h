@@ -490,6 +490,76 @@ int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *w
                      void *grad_hidden, void *grad_weight, void *ws, size_t ws_bytes,
                      void *stream);
 
+/* ---------------------------------------------------------------- preference and policy losses
+ * Losses through the same head, of the targets' log-probabilities
+ *   l_i = log softmax(<hidden_i, weight_v> / T) at v = t(i)   (T = 1 for the preference losses).
+ * What is said above of hidden, weight, their gradients, types, targets that do not count and limits
+ * holds here too.  grad_hidden and grad_weight are of sum_i dL/dl_i l_i; log-probabilities and advantages
+ * that come in are constants, fp32 and contiguous, and are not looked at where a position does not
+ * count.  Everything between l and dL/dl is fp64.
+ *
+ * tt_prefer: pairs of sequences.  offsets [2 pairs + 1] int64, CSR over the positions: sequences
+ * 0 .. pairs - 1 are preferred to pairs .. 2 pairs - 1; positions from offsets[2 pairs] on (at most n) do not
+ * count.  Offsets that do not start at 0, fall, or pass n set TT_DEV_BAD_OFFSETS (the outputs are then
+ * unspecified).  With h_j the sum (average: the mean) of l_i - reference_logps_i (NULL: l_i) over the
+ * sequence's positions that count (none: 0) and x = h_p - h_(pairs + p), S(y) = 1 / (1 + exp -y), the pair's loss is
+ *   TT_PREFER_SIGMOID  -(1 - e) log S(y) - e log S(-y),  y = beta x - margin, e = label_smoothing
+ *   TT_PREFER_HINGE    max(0, 1 - y)
+ *   TT_PREFER_SQUARE   (x - 1 / (2 beta))^2
+ * loss [pairs] (TT_REDUCE_NONE) or [1] (sum, or mean over the pairs; of none: 0).  ratios [2 pairs] (may be
+ * NULL): h.
+ *
+ * tt_policy: with r = exp(l_i - old_logps_i) (old_logps NULL: r = 1), d = reference_logps_i - l_i, A =
+ * advantages_i,
+ *   loss_i = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp d - d - 1)
+ *   dloss_i/dl_i = (r A <= clamp(..) A ? -r A : 0) - kl_coef (exp d - 1)
+ * (old_logps NULL: the same at r = 1).  loss [n], 0 where a position does not count, or [1] (sum, or mean over
+ * the positions that count).  logps [n] (may be NULL): l_i, 0 where a position does not count.  Without kl_coef
+ * reference_logps is not used and may be NULL. */
+#define TT_PREFER_SIGMOID 0
+#define TT_PREFER_HINGE   1
+#define TT_PREFER_SQUARE  2
+
+typedef struct tt_prefer_desc {
+    int64_t n, v, d;                       /* positions, vocabulary, width              */
+    int64_t hidden_stride, weight_stride;  /* elements between rows, >= d               */
+    int64_t ignore_index;
+    int64_t pairs;                         /* at most 2^23                              */
+    double beta, label_smoothing, margin;  /* > 0; in [0, 1], sigmoid; not with square   */
+    int32_t dtype, reduction, kind;        /* TT_DTYPE_*, TT_REDUCE_*, TT_PREFER_*      */
+    int32_t average;                       /* 0: h is a sum, else a mean                */
+} tt_prefer_desc;
+
+typedef struct tt_policy_desc {
+    int64_t n, v, d;
+    int64_t hidden_stride, weight_stride;
+    int64_t ignore_index;
+    double clip_low, clip_high, kl_coef;   /* >= 0, kl_coef finite                      */
+    int32_t dtype, reduction;
+    float temperature;                     /* > 0, finite                               */
+} tt_policy_desc;
+
+/* as tt_loss_saved_size and tt_loss_workspace_size, and at most 16 bytes a position and pair more */
+size_t tt_prefer_saved_size(const tt_prefer_desc *desc);
+size_t tt_prefer_workspace_size(const tt_prefer_desc *desc, int mode);
+int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void *weight,
+                      const int64_t *targets, const int64_t *offsets, const float *reference_logps,
+                      float *loss, float *ratios, void *saved, size_t saved_bytes, void *ws,
+                      size_t ws_bytes, int32_t *dev_status, void *stream);
+int tt_prefer_backward(const tt_prefer_desc *desc, const void *weight, const void *saved,
+                       size_t saved_bytes, const float *grad_loss, void *grad_hidden,
+                       void *grad_weight, void *ws, size_t ws_bytes, void *stream);
+size_t tt_policy_saved_size(const tt_policy_desc *desc);
+size_t tt_policy_workspace_size(const tt_policy_desc *desc, int mode);
+int tt_policy_forward(const tt_policy_desc *desc, const void *hidden, const void *weight,
+                      const int64_t *actions, const float *advantages, const float *old_logps,
+                      const float *reference_logps, float *loss, float *logps, void *saved,
+                      size_t saved_bytes, void *ws, size_t ws_bytes, int32_t *dev_status,
+                      void *stream);
+int tt_policy_backward(const tt_policy_desc *desc, const void *weight, const void *saved,
+                       size_t saved_bytes, const float *grad_loss, void *grad_hidden,
+                       void *grad_weight, void *ws, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- rows of a dense table
  * The rows of an ordinary table weight [v, d] times a scale, and the table's gradient:
  *   out[n] = scale weight[i_n]

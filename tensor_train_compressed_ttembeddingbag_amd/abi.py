@@ -42,6 +42,9 @@ TT_DTYPE_I8 = 3
 TT_REDUCE_NONE = 0
 TT_REDUCE_MEAN = 1
 TT_REDUCE_SUM = 2
+TT_PREFER_SIGMOID = 0
+TT_PREFER_HINGE = 1
+TT_PREFER_SQUARE = 2
 TT_LOSS_FORWARD = 0
 TT_LOSS_BACKWARD = 1
 TT_LOSS_ONLY = 2
@@ -90,6 +93,23 @@ class TTEmbedDesc(ctypes.Structure):
 class TTInt8Desc(ctypes.Structure):
     _fields_ = [("n", _I64), ("v", _I64), ("d", _I64), ("hidden_stride", _I64),
                 ("weight_pitch", _I64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class TTPreferDesc(ctypes.Structure):
+    _fields_ = [("n", _I64), ("v", _I64), ("d", _I64), ("hidden_stride", _I64),
+                ("weight_stride", _I64), ("ignore_index", _I64), ("pairs", _I64),
+                ("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double),
+                ("margin", ctypes.c_double), ("dtype", ctypes.c_int32),
+                ("reduction", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("average", ctypes.c_int32)]
+
+
+class TTPolicyDesc(ctypes.Structure):
+    _fields_ = [("n", _I64), ("v", _I64), ("d", _I64), ("hidden_stride", _I64),
+                ("weight_stride", _I64), ("ignore_index", _I64), ("clip_low", ctypes.c_double),
+                ("clip_high", ctypes.c_double), ("kl_coef", ctypes.c_double),
+                ("dtype", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("temperature", ctypes.c_float)]
 
 
 class TTCacheView(ctypes.Structure):
@@ -172,6 +192,18 @@ _SIG = {
     "tt_int8_quantize": (ctypes.c_int, [_I64, _I64, ctypes.c_int32, _P, _I64, _P, _I64, _P, _P]),
     "tt_int8_workspace_size": (ctypes.c_size_t, [_P]),
     "tt_int8_linear": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "tt_prefer_saved_size": (ctypes.c_size_t, [_P]),
+    "tt_prefer_workspace_size": (ctypes.c_size_t, [_P, ctypes.c_int]),
+    "tt_prefer_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P,
+                                         ctypes.c_size_t, _P, _P]),
+    "tt_prefer_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_size_t, _P, _P, _P, _P,
+                                          ctypes.c_size_t, _P]),
+    "tt_policy_saved_size": (ctypes.c_size_t, [_P]),
+    "tt_policy_workspace_size": (ctypes.c_size_t, [_P, ctypes.c_int]),
+    "tt_policy_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
+                                         _P, ctypes.c_size_t, _P, _P]),
+    "tt_policy_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_size_t, _P, _P, _P, _P,
+                                          ctypes.c_size_t, _P]),
     "tt_loss_saved_size": (ctypes.c_size_t, [_P]),
     "tt_loss_workspace_size": (ctypes.c_size_t, [_P, _P, ctypes.c_int]),
     "tt_loss_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P,

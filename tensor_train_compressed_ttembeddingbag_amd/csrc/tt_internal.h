@@ -211,7 +211,7 @@ enum KernelId {
   K_ROUTE_COOP, K_ROUTE_A, K_ROUTE_B, K_ROUTE_C, K_FWD, K_BWD, K_SEG,
   K_CACHE_LOOKUP, K_YINIT, K_ZERO, K_DMERGE, K_DSPLIT, K_DAPPLY, K_DD_FRAG, K_DD_GU, K_META,
   K_LOSS_PACK, K_LOSS_LOGITS, K_LOSS_G, K_LOSS_DH, K_LOSS_DW, K_LOSS_ROWS,
-  K_EMBED, K_EMBED_SORT, K_EMBED_GRAD, K_INT8_QUANT, K_INT8,
+  K_EMBED, K_EMBED_SORT, K_EMBED_GRAD, K_INT8_QUANT, K_INT8, K_ALIGN,
   K_COUNT
 };
 // Start / stop events for one launch of kernel `id`, recorded by the kernel's own

@@ -5,7 +5,8 @@
 //   cross entropy  loss_i = lse_i - (1 - e) z_i,t - (e / V) sum_v z_iv
 //   distillation   loss_i = T^2 (sum_j q_ij log q_ij - sum_j q_ij z_i,idx(ij) + lse_i)
 //   dloss_i/d<hidden_i, weight_v> = s g_iv,  g_iv = exp(z_iv - lse_i) - e / V - sum of the
-//   position's q on v (the target's q is 1 - e), s = 1 or T.
+//   position's q on v (the target's q is 1 - e), s = 1 / T or T.  (T is 1 with cross entropy by
+//   itself; the policy loss, which is built on it, has one.)
 //
 // forward:  k_entries (distillation: q, sorted, repeated rows merged) -> k_pack (positions that
 //           count, packed) -> k_logits (running maximum and sum per position and tile of the
@@ -63,6 +64,7 @@ struct LossArgs {
   float smoothing, temp;
   const void *hidden, *weight;
   const int64_t *tgt;      // targets [N] or teacher indices [N][k]
+  const int64_t *limit;    // device word: positions from it on do not count, or null
   const void *tlogits;     // teacher logits [N][k]
   float *loss;
   const float *up;         // gradient of the loss
@@ -164,7 +166,7 @@ struct GradScale {
   }
 };
 inline GradScale grad_scale(const LossArgs &a) {
-  return {a.reduction == TT_REDUCE_NONE ? a.cm : a.up, a.sv.sc, a.k ? a.temp : 1.f,
+  return {a.reduction == TT_REDUCE_NONE ? a.cm : a.up, a.sv.sc, a.k ? a.temp : 1.f / a.temp,
           a.reduction == TT_REDUCE_MEAN};
 }
 
@@ -194,6 +196,26 @@ inline LogitsCut logits_cut(const LossArgs &a, int64_t nv) {
   c.rest = gemm_shape(nv - c.large, a.N, a.cus);
   c.tiles = (int)((c.large + 255) / 256 + (nv - c.large + c.rest.bx - 1) / c.rest.bx);
   return c;
+}
+
+// The pieces of the two entry points, for losses that are functions of the target's cross entropy.
+int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a);
+int64_t saved_layout(LossArgs &a, void *saved);
+int64_t ws_layout(LossArgs &a, void *ws, int mode);
+hipError_t loss_forward(const LossArgs &a, hipStream_t s);
+hipError_t loss_backward(const LossArgs &a, hipStream_t s);
+
+__device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
+  if (a.k) return a.sv.tgt[i] != 0;
+  if (a.limit && i >= *a.limit) return false;
+  const int64_t t = a.tgt[i];
+  return t != a.ignore && t >= 0 && t < a.V;
+}
+
+__device__ __forceinline__ bool bad_target(const LossArgs &a, int64_t i) {
+  if (a.limit && i >= *a.limit) return false;
+  const int64_t t = a.tgt[i];
+  return t != a.ignore && (t < 0 || t >= a.V);
 }
 
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,

@@ -204,12 +204,6 @@ __global__ __launch_bounds__(256) void k_entries(LossArgs a, int pow2) {
 }
 
 // ---------------------------------------------------------------- packing
-__device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
-  if (a.k) return a.sv.tgt[i] != 0;
-  const int64_t t = a.tgt[i];
-  return t != a.ignore && t >= 0 && t < a.V;
-}
-
 // amax: the weight (blocks 0 ..) and the positions that count
 __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
   const bool w = blockIdx.x < AMAX_BLOCKS;
@@ -336,7 +330,7 @@ __global__ __launch_bounds__(256) void k_pack(LossArgs a) {
       if (!a.k) {
         const int64_t t = a.tgt[i];
         if (ok) a.sv.tgt[rank] = (int)t;
-        else if (t != a.ignore) set_status(a.status, TT_DEV_BAD_INDEX);
+        else if (bad_target(a, i)) set_status(a.status, TT_DEV_BAD_INDEX);
       }
       if (i == a.N - 1) a.sv.sc->count = rank + ok;
     }
@@ -581,7 +575,7 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, int ticket) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, part = wv % NW;
   const int64_t i = (int64_t)blockIdx.x * (4 / NW) + wv / NW;
   const int slot = i < a.N ? slot_of(a, i) : -1;
-  if (a.direct && !a.k && slot < 0 && i < a.N && lane == 0 && a.tgt[i] != a.ignore)
+  if (a.direct && !a.k && slot < 0 && i < a.N && lane == 0 && bad_target(a, i))
     set_status(a.status, TT_DEV_BAD_INDEX);
   const float zs = a.direct ? LOG2E / a.temp : a.sv.sc->zs;
   float out = 0.f, wm = -INFINITY, s = 0.f, z = 0.f;
@@ -880,7 +874,7 @@ struct Bump {
   }
 };
 
-static int64_t saved_layout(LossArgs &a, void *saved) {
+int64_t saved_layout(LossArgs &a, void *saved) {
   Bump b{(char *)saved};
   b.take(a.sv.sc, 1);
   if (!a.direct) b.take(a.sv.hp, a.Npad * a.Dp * 2 * a.planes);
@@ -912,7 +906,7 @@ constexpr int64_t CHUNKS_AT = 8192;
 constexpr int64_t FACTORS_AT = 16384;
 
 // mode: TT_LOSS_FORWARD, _BACKWARD or _ONLY (what is saved otherwise is in the workspace then)
-static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
+int64_t ws_layout(LossArgs &a, void *ws, int mode) {
   const bool grad = mode == TT_LOSS_BACKWARD;
   Bump b{(char *)ws};
   if (mode == TT_LOSS_ONLY) {
@@ -976,7 +970,7 @@ static int64_t ws_layout(LossArgs &a, void *ws, int mode) {
   return b.off;
 }
 
-static int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
+int loss_args(const tt_loss_desc *d, const void *weight, LossArgs &a) {
   if (!d) return TT_EINVAL;
   if (d->n < 0 || d->v < 1 || d->d < 1 || d->k < 0) return TT_EINVAL;
   if (d->dtype < TT_DTYPE_F32 || d->dtype > TT_DTYPE_F16) return TT_EINVAL;
@@ -1123,6 +1117,44 @@ static hipError_t fill0(void *x, int64_t bytes, hipStream_t s) {
   return hipGetLastError();
 }
 
+hipError_t loss_forward(const LossArgs &a, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (a.k) e = launch_entries(a, s);
+  if (e == hipSuccess && !a.direct) e = launch_pack(a, s);
+  int tile0 = 0;
+  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
+    const int64_t nv = std::min(a.piece, a.V - v0);
+    e = launch_pack_w(a, v0, nv, s);
+    const int tiles = logits_cut(a, nv).tiles;
+    if (e == hipSuccess) e = launch_logits(a, v0, nv, a.fold ? 1 : tile0, false, s);
+    if (e == hipSuccess && a.fold) e = launch_fold(a, tiles, v0 == 0, s);
+    tile0 += tiles;
+  }
+  return e == hipSuccess ? launch_loss(a, s) : e;
+}
+
+hipError_t loss_backward(const LossArgs &a, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (a.N == 0) return a.dw ? fill0(a.dw, a.V * a.D * elem_size(a.dtype), s) : e;
+  if (!a.dh && !a.dw) return e;
+  if (a.reduction == TT_REDUCE_NONE) {
+    if (a.upmax) tt_launch(K_LOSS_ROWS, k_row_max, dim3(FACTOR_BLOCKS), dim3(256), 0, s, a);
+    tt_launch(K_LOSS_ROWS, k_row_factors, dim3((unsigned)std::min<int64_t>((a.N + 255) / 256, 1024)),
+              dim3(256), 0, s, a);
+    e = hipGetLastError();
+  }
+  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
+    const int64_t nv = std::min(a.piece, a.V - v0);
+    e = launch_pack_w(a, v0, nv, s);
+    if (e == hipSuccess) e = launch_logits(a, v0, nv, 0, true, s);
+    if (e == hipSuccess) e = launch_entries_g(a, v0, nv, s);
+    if (e == hipSuccess && a.dh) e = launch_dhidden(a, v0, nv, s);
+    if (e == hipSuccess && a.dw) e = launch_light_rows(a, s);
+    if (e == hipSuccess && a.dw) e = launch_dweight(a, v0, nv, s);
+  }
+  return e == hipSuccess && a.dh ? launch_dhidden_out(a, s) : e;
+}
+
 }  // namespace ttb
 
 using namespace ttb;
@@ -1158,22 +1190,8 @@ int tt_loss_forward(const tt_loss_desc *desc, const void *hidden, const void *we
   a.status = dev_status;
   hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;
-  if (a.N == 0) {  // no position: a sum or mean of nothing is 0
-    if (a.reduction != TT_REDUCE_NONE) e = fill0(loss, 4, s);
-    return e == hipSuccess ? TT_OK : TT_EHIP;
-  }
-  if (a.k) e = launch_entries(a, s);
-  if (e == hipSuccess && !a.direct) e = launch_pack(a, s);
-  int tile0 = 0;
-  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
-    const int64_t nv = std::min(a.piece, a.V - v0);
-    e = launch_pack_w(a, v0, nv, s);
-    const int tiles = logits_cut(a, nv).tiles;
-    if (e == hipSuccess) e = launch_logits(a, v0, nv, a.fold ? 1 : tile0, false, s);
-    if (e == hipSuccess && a.fold) e = launch_fold(a, tiles, v0 == 0, s);
-    tile0 += tiles;
-  }
-  if (e == hipSuccess) e = launch_loss(a, s);
+  if (a.N > 0) e = loss_forward(a, s);
+  else if (a.reduction != TT_REDUCE_NONE) e = fill0(loss, 4, s);  // a sum or mean of nothing is 0
   return e == hipSuccess ? TT_OK : TT_EHIP;
 }
 
@@ -1192,30 +1210,7 @@ int tt_loss_backward(const tt_loss_desc *desc, const void *hidden, const void *w
   if ((size_t)saved_layout(a, (void *)saved) > saved_bytes) return TT_EWORKSPACE;
   if ((size_t)ws_layout(a, ws, TT_LOSS_BACKWARD) > ws_bytes) return TT_EWORKSPACE;
   a.hidden = hidden; a.up = grad_loss; a.dh = grad_hidden; a.dw = grad_weight;
-  hipStream_t s = (hipStream_t)stream;
-  hipError_t e = hipSuccess;
-  if (a.N == 0) {
-    if (grad_weight) e = fill0(grad_weight, a.V * a.D * elem_size(a.dtype), s);
-    return e == hipSuccess ? TT_OK : TT_EHIP;
-  }
-  if (!grad_hidden && !grad_weight) return TT_OK;
-  if (a.reduction == TT_REDUCE_NONE) {
-    if (a.upmax) tt_launch(K_LOSS_ROWS, k_row_max, dim3(FACTOR_BLOCKS), dim3(256), 0, s, a);
-    tt_launch(K_LOSS_ROWS, k_row_factors, dim3((unsigned)std::min<int64_t>((a.N + 255) / 256, 1024)),
-              dim3(256), 0, s, a);
-    e = hipGetLastError();
-  }
-  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
-    const int64_t nv = std::min(a.piece, a.V - v0);
-    e = launch_pack_w(a, v0, nv, s);
-    if (e == hipSuccess) e = launch_logits(a, v0, nv, 0, true, s);
-    if (e == hipSuccess) e = launch_entries_g(a, v0, nv, s);
-    if (e == hipSuccess && grad_hidden) e = launch_dhidden(a, v0, nv, s);
-    if (e == hipSuccess && grad_weight) e = launch_light_rows(a, s);
-    if (e == hipSuccess && grad_weight) e = launch_dweight(a, v0, nv, s);
-  }
-  if (e == hipSuccess && grad_hidden) e = launch_dhidden_out(a, s);
-  return e == hipSuccess ? TT_OK : TT_EHIP;
+  return loss_backward(a, (hipStream_t)stream) == hipSuccess ? TT_OK : TT_EHIP;
 }
 
 }  // extern "C"

@@ -29,7 +29,7 @@ const char *g_names[K_COUNT] = {"k_route_coop", "k_route_a", "k_route_b", "k_rou
                                 "k_pack", "k_logits", "k_logits (G)", "k_dhidden", "k_dweight",
                                 "loss rows",
                                 "k_embed", "embed sort", "k_embed_rows",
-                                "k_quantize", "k_int8"};
+                                "k_quantize", "k_int8", "preference and policy rows"};
 
 hipEvent_t take() {
   if (!g_pool.empty()) {

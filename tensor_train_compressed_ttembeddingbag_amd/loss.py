@@ -194,3 +194,239 @@ def linear_distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_logi
     return _loss(hidden, weight, teacher_indices.contiguous(),
                  teacher_logits.detach().contiguous(), teacher_indices.shape[:-1], k, reduction,
                  dev_status, temperature=temperature, teacher_dtype=teacher_logits.dtype)
+
+
+# ---------------------------------------------------------------- preference and policy losses
+_KIND = {"sigmoid": abi.TT_PREFER_SIGMOID, "hinge": abi.TT_PREFER_HINGE,
+         "square": abi.TT_PREFER_SQUARE}
+
+
+class _LogpPlan:
+    """The descriptor of one kind of preference or policy loss, its entry points and sizes."""
+
+    def __init__(self, name, desc, hidden, weight):
+        lib = abi.lib()
+        self.name, self.desc, self.ref = name, desc, ctypes.byref(desc)
+        self.forward = getattr(lib, "tt_%s_forward" % name)
+        self.backward = getattr(lib, "tt_%s_backward" % name)
+        size = getattr(lib, "tt_%s_workspace_size" % name)
+        self.saved = getattr(lib, "tt_%s_saved_size" % name)(self.ref)
+        if not self.saved:
+            raise abi.TTError("tt_%s_saved_size" % name, -2)
+        self.fwd = size(self.ref, abi.TT_LOSS_FORWARD)
+        self.bwd = size(self.ref, abi.TT_LOSS_BACKWARD)
+        self.only = size(self.ref, abi.TT_LOSS_ONLY)
+        self.dtype, self.n, self.d, self.v = hidden.dtype, *hidden.shape, weight.shape[0]
+
+
+def _logp_forward(plan, hidden, weight, inputs, shape, more_shape, dev_status, save):
+    """(loss, the second output or None, saved or None)"""
+    dev = hidden.device
+    loss = torch.empty(shape, dtype=torch.float32, device=dev)
+    more = None if more_shape is None else torch.empty(more_shape, dtype=torch.float32, device=dev)
+    saved = _bytes(plan.saved, dev) if save else None
+    size = plan.fwd if save else plan.only
+    ws = _bytes(size, dev)
+    with abi._device_of(hidden):
+        abi._check("tt_%s_forward" % plan.name, plan.forward(
+            plan.ref, hidden.data_ptr(), weight.data_ptr(), *[abi._ptr(t) for t in inputs],
+            loss.data_ptr(), abi._ptr(more), abi._ptr(saved), plan.saved, ws.data_ptr(), size,
+            abi._ptr(dev_status), abi._stream(None, hidden)))
+    return loss, more, saved
+
+
+def _logp_backward(ctx, grad_loss, _):
+    weight, saved = ctx.saved_tensors
+    plan, dev = ctx.plan, weight.device
+    if grad_loss is None:
+        return (None,) * 7
+    grad_loss = grad_loss.contiguous()
+    need_h, need_w = ctx.needs_input_grad[:2]
+    dh = torch.empty((plan.n, plan.d), dtype=plan.dtype, device=dev) if need_h else None
+    dw = torch.empty((plan.v, plan.d), dtype=plan.dtype, device=dev) if need_w else None
+    ws = _bytes(plan.bwd, dev)
+    with abi._device_of(weight):
+        abi._check("tt_%s_backward" % plan.name, plan.backward(
+            plan.ref, weight.data_ptr(), saved.data_ptr(), plan.saved, grad_loss.data_ptr(),
+            abi._ptr(dh), abi._ptr(dw), ws.data_ptr(), plan.bwd, abi._stream(None, weight)))
+    return dh, dw, None, None, None, None, None
+
+
+_logp_backward_once = torch.autograd.function.once_differentiable(_logp_backward)
+
+
+class _LogpFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, plan, inputs, shape, more_shape, dev_status):
+        loss, more, saved = _logp_forward(plan, hidden, weight, inputs, shape, more_shape,
+                                          dev_status, True)
+        ctx.plan = plan
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(weight, saved)
+        if more is not None:
+            ctx.mark_non_differentiable(more)
+        return loss, more
+
+    @staticmethod
+    def backward(ctx, grad_loss, _):
+        # gradients of gradients are refused; only create_graph=True runs with them enabled
+        return (_logp_backward_once if torch.is_grad_enabled() else _logp_backward)(
+            ctx, grad_loss, None)
+
+
+def _logp_loss(name, hidden, weight, inputs, shape, more_shape, reduction, dev_status, make, key):
+    """key: what make(desc of the product) depends on beside hidden and weight."""
+    abi._no_dual("linear_%s" % ("preference" if name == "prefer" else name), hidden, weight)
+    hidden, weight = _rows(hidden, True), _rows(weight, False)
+    key = (name, hidden.shape, hidden.stride(), weight.shape, weight.stride(), hidden.dtype,
+           weight.dtype, hidden.device, weight.device, reduction, *key)
+    plan = _plans.get(key)
+    if plan is None:
+        if reduction not in _REDUCTION:
+            raise ValueError("reduction must be one of %s" % sorted(_REDUCTION))
+        if len(_plans) > 1024:
+            _plans.clear()
+        head = abi.make_loss_desc(hidden, weight)  # checks the two
+        plan = _plans[key] = _LogpPlan(name, make(head, _REDUCTION[reduction]), hidden, weight)
+    for t in (*inputs, dev_status):
+        if t is not None and t.device != hidden.device:
+            raise ValueError("a buffer is on %s, hidden on %s" % (t.device, hidden.device))
+    if dev_status is not None:
+        abi._need(dev_status, torch.int32, "dev_status")
+        abi._numel(dev_status, 1, "dev_status")
+    if reduction != "none":
+        shape = ()
+    if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
+        return _LogpFunction.apply(hidden, weight, plan, inputs, shape, more_shape, dev_status)
+    return _logp_forward(plan, hidden, weight, inputs, shape, more_shape, dev_status, False)[:2]
+
+
+def _integers(t: torch.Tensor, name: str) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype == torch.int32:
+        t = t.to(torch.int64)
+    if t.dtype != torch.int64:
+        raise TypeError("%s must be int64 or int32, got %s" % (name, t.dtype))
+    return t.contiguous()
+
+
+def _constant(t, shape, name: str, broadcast: bool = False):
+    """A constant per position, float32 and contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in abi._DTYPE:
+        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+    if t.shape != shape:
+        if not broadcast:
+            raise ValueError("%s must have the shape of hidden without its last dimension" % name)
+        try:
+            t = t.broadcast_to(shape)
+        except RuntimeError:
+            raise ValueError("%s does not broadcast to the shape of hidden without its last "
+                             "dimension" % name) from None
+    return t.detach().float().contiguous()
+
+
+def linear_preference(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                      offsets: torch.Tensor, reference_logps: Optional[torch.Tensor] = None, *,
+                      beta: float = 0.1, kind: str = "sigmoid", label_smoothing: float = 0.0,
+                      margin: float = 0.0, average: bool = False, ignore_index: int = -100,
+                      reduction: str = "mean", return_ratios: bool = False,
+                      dev_status: Optional[torch.Tensor] = None):
+    """A preference loss over P pairs of sequences, from their tokens' log-probabilities under the
+    logits ``hidden @ weight.T``.
+
+    hidden [..., D], weight [V, D], targets [...] (as in ``linear_cross_entropy``: ignore_index for
+    positions that do not count, a prompt's for instance), offsets [2 P + 1]: sequence j has the
+    positions offsets[j] .. offsets[j + 1] - 1 of the flattened ones; sequences 0 .. P - 1 are
+    preferred to P .. 2 P - 1, and positions behind the last one do not count.  reference_logps
+    [...]: the tokens' log-probabilities under the reference, for instance
+    ``-linear_cross_entropy(..., reduction="none")`` of its hidden states; None: no reference.
+
+    With h_j the sum (average: the mean) of logp - reference_logp over the sequence and
+    ``x_p = h_p - h_(P + p)``, ``y = beta x - margin``, e = label_smoothing:
+
+    * "sigmoid": ``-(1 - e) log sigmoid(y) - e log sigmoid(-y)``
+    * "hinge": ``max(0, 1 - y)``
+    * "square": ``(x - 1 / (2 beta))^2`` (no margin)
+
+    reduction "none" returns [P], "sum" their sum, "mean" their mean (0 if there are none).
+    return_ratios: also h as [2, P], without gradient.  Offsets that do not start at 0, fall or
+    pass the positions set ``TT_DEV_BAD_OFFSETS`` in dev_status, and the result is unspecified."""
+    if hidden.dim() < 1 or targets.shape != hidden.shape[:-1]:
+        raise ValueError("targets must have the shape of hidden without its last dimension")
+    targets, offsets = _integers(targets, "targets"), _integers(offsets, "offsets")
+    if offsets.dim() != 1 or offsets.numel() % 2 != 1:
+        raise ValueError("offsets must have 2 P + 1 entries")
+    if kind not in _KIND:
+        raise ValueError("kind must be one of %s" % sorted(_KIND))
+    if not 0.0 < beta < float("inf"):
+        raise ValueError("beta must be positive and finite")
+    if not 0.0 <= label_smoothing <= 1.0 or label_smoothing and kind != "sigmoid":
+        raise ValueError("label_smoothing must be in [0, 1], and is for kind \"sigmoid\"")
+    if not -float("inf") < margin < float("inf") or margin and kind == "square":
+        raise ValueError("margin must be finite, and is not for kind \"square\"")
+    if reference_logps is not None:
+        reference_logps = _constant(reference_logps, targets.shape, "reference_logps")
+    pairs = offsets.numel() // 2
+
+    def make(h, r):
+        return abi.TTPreferDesc(h.n, h.v, h.d, h.hidden_stride, h.weight_stride, ignore_index,
+                                pairs, beta, label_smoothing, margin, h.dtype, r, _KIND[kind],
+                                bool(average))
+
+    loss, ratios = _logp_loss("prefer", hidden, weight, (targets, offsets, reference_logps),
+                              (pairs,), (2, pairs) if return_ratios else None, reduction,
+                              dev_status, make, (pairs, beta, label_smoothing, margin, kind,
+                                                 bool(average), ignore_index))
+    return (loss, ratios) if return_ratios else loss
+
+
+def linear_policy(hidden: torch.Tensor, weight: torch.Tensor, actions: torch.Tensor,
+                  advantages: torch.Tensor, old_logps: Optional[torch.Tensor] = None,
+                  reference_logps: Optional[torch.Tensor] = None, *, clip_low: float = 0.2,
+                  clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0,
+                  ignore_index: int = -100, reduction: str = "mean", return_logps: bool = False,
+                  dev_status: Optional[torch.Tensor] = None):
+    """The clipped policy loss with a KL term, of actions under the logits
+    ``hidden @ weight.T / temperature``.
+
+    hidden [..., D], weight [V, D], actions [...] (integers in [0, V), or ignore_index for a
+    position that does not count), advantages (broadcast to [...]), old_logps [...]: the actions'
+    log-probabilities under the policy that took them (None: this one), reference_logps [...]:
+    those under the reference (needed with kl_coef).  With logp the actions' log-probabilities,
+    ``r = exp(logp - old_logp)`` and ``d = reference_logp - logp``:
+
+    ``loss_i = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(d) - d - 1)``
+
+    reduction "none" returns [...] (0 where a position does not count), "sum" their sum, "mean"
+    the sum over the positions that count.  return_logps: also logp [...], without gradient (0
+    where a position does not count): the old_logps of the next steps.  Advantages and the given
+    log-probabilities are constants.  dev_status as in ``linear_cross_entropy``."""
+    if hidden.dim() < 1 or actions.shape != hidden.shape[:-1]:
+        raise ValueError("actions must have the shape of hidden without its last dimension")
+    actions = _integers(actions, "actions")
+    if not clip_low >= 0.0 or not clip_high >= 0.0:
+        raise ValueError("clip_low and clip_high must not be negative")
+    if not 0.0 <= kl_coef < float("inf"):
+        raise ValueError("kl_coef must be finite and not negative")
+    if not 0.0 < ctypes.c_float(temperature).value < float("inf"):  # the library's type
+        raise ValueError("temperature must be positive and finite in float32")
+    if kl_coef and reference_logps is None:
+        raise ValueError("kl_coef needs reference_logps")
+    advantages = _constant(advantages, actions.shape, "advantages", True)
+    if old_logps is not None:
+        old_logps = _constant(old_logps, actions.shape, "old_logps")
+    if reference_logps is not None:
+        reference_logps = _constant(reference_logps, actions.shape, "reference_logps")
+
+    def make(h, r):
+        return abi.TTPolicyDesc(h.n, h.v, h.d, h.hidden_stride, h.weight_stride, ignore_index,
+                                clip_low, clip_high, kl_coef, h.dtype, r, temperature)
+
+    loss, logps = _logp_loss("policy", hidden, weight,
+                             (actions, advantages, old_logps, reference_logps), actions.shape,
+                             actions.shape if return_logps else None, reduction, dev_status, make,
+                             (clip_low, clip_high, kl_coef, temperature, ignore_index))
+    return (loss, logps) if return_logps else loss
