@@ -539,7 +539,9 @@ typedef struct tt_policy_desc {
     float temperature;                     /* > 0, finite                               */
 } tt_policy_desc;
 
-/* as tt_loss_saved_size and tt_loss_workspace_size, and at most 16 bytes a position and pair more */
+/* as tt_loss_saved_size and tt_loss_workspace_size, and at most 16 bytes a position and pair more; a backward
+ * in which positions may have no gradient (tt_policy without kl_coef, TT_PREFER_HINGE) and n v d >= 2^36 also
+ * has the packed positions a second time */
 size_t tt_prefer_saved_size(const tt_prefer_desc *desc);
 size_t tt_prefer_workspace_size(const tt_prefer_desc *desc, int mode);
 int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void *weight,

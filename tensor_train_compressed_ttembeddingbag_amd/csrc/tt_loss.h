@@ -205,6 +205,17 @@ int64_t ws_layout(LossArgs &a, void *ws, int mode);
 hipError_t loss_forward(const LossArgs &a, hipStream_t s);
 hipError_t loss_backward(const LossArgs &a, hipStream_t s);
 
+// Of the positions that count, those whose loss has a gradient at all (a.up not 0): a copy of what is
+// saved with the others left out, for the three products of the backward.
+struct Kept {
+  LossSaved to;
+  int *chunk;  // [N / CHUNK] kept before each chunk, or null
+};
+// its buffers at p; returns the bytes (a multiple of 256)
+int64_t kept_layout(const LossArgs &a, void *p, Kept &k);
+// a.sv becomes the copy
+hipError_t keep_rows(LossArgs &a, const Kept &k, hipStream_t s);
+
 __device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
   if (a.k) return a.sv.tgt[i] != 0;
   if (a.limit && i >= *a.limit) return false;

@@ -241,6 +241,14 @@ static int cross_entropy(const Desc *d, const void *weight, float temperature, L
   return rc;
 }
 
+// Products of positions, rows and columns from which on the backward of a loss whose slope is exactly 0 for
+// some positions (clipped, or without an advantage; hinge: pairs that are far enough apart) leaves these
+// out: a copy of the others costs some 10 us at 2^36, of which three products are 320 us.
+constexpr double KEEP_FROM = (double)(1ll << 36);
+static bool keeps(const LossArgs &a, bool zero_slopes) {
+  return zero_slopes && !a.twin && (double)a.N * (double)a.V * (double)a.D >= KEEP_FROM;
+}
+
 static bool finite(double x) { return x > -INFINITY && x < INFINITY; }
 
 static int prefer_args(const tt_prefer_desc *d, const void *weight, LossArgs &a, PreferArgs &p) {
@@ -264,10 +272,27 @@ static int64_t prefer_saved(LossArgs &a, PreferArgs &p, void *saved) {
   b.take(p.coef, 2 * p.P);
   return b.off;
 }
-static int64_t prefer_ws(LossArgs &a, PreferArgs &p, void *ws, int mode, float *&up) {
+static bool zero_slopes(const PreferArgs &p) { return p.kind == TT_PREFER_HINGE; }
+static bool zero_slopes(const PolicyArgs &p) { return p.kl == 0.0; }
+// what a backward has beside the cross entropy's: dL/dl, and the rows that are kept
+template <class Args>
+static void backward_part(const LossArgs &a, const Args &p, Part &b, float *&up, Kept &kept) {
+  b.take(up, p.N);
+  if (keeps(a, zero_slopes(p))) b.off += kept_layout(a, b.base + b.off, kept);
+}
+template <class Args>
+static hipError_t backward_from(LossArgs &a, const Args &p, const Kept &kept, hipStream_t s) {
+  if (p.N && keeps(a, zero_slopes(p))) {
+    const hipError_t e = keep_rows(a, kept, s);
+    if (e != hipSuccess) return e;
+  }
+  return loss_backward(a, s);
+}
+
+static int64_t prefer_ws(LossArgs &a, PreferArgs &p, void *ws, int mode, float *&up, Kept &kept) {
   Part b = {(char *)ws, ws_layout(a, ws, mode)};
   if (mode == TT_LOSS_BACKWARD) {
-    b.take(up, p.N);
+    backward_part(a, p, b, up, kept);
   } else {
     b.take(a.loss, p.N);
     b.take(p.rows, p.P);
@@ -291,10 +316,10 @@ static int64_t policy_saved(LossArgs &a, PolicyArgs &p, void *saved) {
   b.take(p.coef, p.N);
   return b.off;
 }
-static int64_t policy_ws(LossArgs &a, PolicyArgs &p, void *ws, int mode, float *&up) {
+static int64_t policy_ws(LossArgs &a, PolicyArgs &p, void *ws, int mode, float *&up, Kept &kept) {
   Part b = {(char *)ws, ws_layout(a, ws, mode)};
   if (mode == TT_LOSS_BACKWARD) {
-    b.take(up, p.N);
+    backward_part(a, p, b, up, kept);
   } else {
     b.take(a.loss, p.N);
     b.take(p.part, 2 * ((p.N + SUM_BLOCK - 1) / SUM_BLOCK));
@@ -321,8 +346,9 @@ size_t tt_prefer_workspace_size(const tt_prefer_desc *desc, int mode) {
   LossArgs a;
   PreferArgs p;
   float *up;
+  Kept kept;
   if (mode < TT_LOSS_FORWARD || mode > TT_LOSS_ONLY) return 0;
-  return prefer_args(desc, nullptr, a, p) == TT_OK ? (size_t)prefer_ws(a, p, nullptr, mode, up) : 0;
+  return prefer_args(desc, nullptr, a, p) == TT_OK ? (size_t)prefer_ws(a, p, nullptr, mode, up, kept) : 0;
 }
 
 int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void *weight,
@@ -332,6 +358,7 @@ int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void
   LossArgs a;
   PreferArgs p;
   float *up;
+  Kept kept;
   const int rc = prefer_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
   if (!weight || !ws || !offsets) return TT_EINVAL;
@@ -340,7 +367,7 @@ int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void
   if (misaligned(weight, elem_size(a.dtype)) || misaligned(hidden, elem_size(a.dtype))) return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if (saved && (size_t)prefer_saved(a, p, saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)prefer_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, up) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)prefer_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, up, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   a.hidden = hidden; a.tgt = targets; a.limit = offsets + 2 * p.P; a.status = dev_status;
   p.tgt = targets; p.off = offsets; p.ref = reference_logps; p.loss = loss; p.ratios = ratios;
@@ -359,6 +386,7 @@ int tt_prefer_backward(const tt_prefer_desc *desc, const void *weight, const voi
   LossArgs a;
   PreferArgs p;
   float *up;
+  Kept kept;
   const int rc = prefer_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
   if (!weight || !saved || !ws) return TT_EINVAL;
@@ -368,14 +396,14 @@ int tt_prefer_backward(const tt_prefer_desc *desc, const void *weight, const voi
     return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if ((size_t)prefer_saved(a, p, (void *)saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)prefer_ws(a, p, ws, TT_LOSS_BACKWARD, up) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)prefer_ws(a, p, ws, TT_LOSS_BACKWARD, up, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   if (p.N)
     tt_launch(K_ALIGN, k_prefer_up, dim3((unsigned)((p.N + 255) / 256)), dim3(256), 0, s,
               (const int *)p.seq, (const float *)p.coef, p.N, p.P, p.reduction, grad_loss, up);
   if (hipGetLastError() != hipSuccess) return TT_EHIP;
   a.up = up; a.dh = grad_hidden; a.dw = grad_weight;
-  return loss_backward(a, s) == hipSuccess ? TT_OK : TT_EHIP;
+  return backward_from(a, p, kept, s) == hipSuccess ? TT_OK : TT_EHIP;
 }
 
 size_t tt_policy_saved_size(const tt_policy_desc *desc) {
@@ -388,8 +416,9 @@ size_t tt_policy_workspace_size(const tt_policy_desc *desc, int mode) {
   LossArgs a;
   PolicyArgs p;
   float *up;
+  Kept kept;
   if (mode < TT_LOSS_FORWARD || mode > TT_LOSS_ONLY) return 0;
-  return policy_args(desc, nullptr, a, p) == TT_OK ? (size_t)policy_ws(a, p, nullptr, mode, up) : 0;
+  return policy_args(desc, nullptr, a, p) == TT_OK ? (size_t)policy_ws(a, p, nullptr, mode, up, kept) : 0;
 }
 
 int tt_policy_forward(const tt_policy_desc *desc, const void *hidden, const void *weight,
@@ -399,6 +428,7 @@ int tt_policy_forward(const tt_policy_desc *desc, const void *hidden, const void
   LossArgs a;
   PolicyArgs p;
   float *up;
+  Kept kept;
   const int rc = policy_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
   if (!weight || !ws || (p.N && (!hidden || !actions || !advantages))) return TT_EINVAL;
@@ -407,7 +437,7 @@ int tt_policy_forward(const tt_policy_desc *desc, const void *hidden, const void
   if (misaligned(weight, elem_size(a.dtype)) || misaligned(hidden, elem_size(a.dtype))) return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if (saved && (size_t)policy_saved(a, p, saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)policy_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, up) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)policy_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, up, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   a.hidden = hidden; a.tgt = actions; a.status = dev_status;
   p.tgt = actions; p.adv = advantages; p.old = old_logps; p.ref = reference_logps;
@@ -430,6 +460,7 @@ int tt_policy_backward(const tt_policy_desc *desc, const void *weight, const voi
   LossArgs a;
   PolicyArgs p;
   float *up;
+  Kept kept;
   const int rc = policy_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
   if (!weight || !saved || !ws) return TT_EINVAL;
@@ -439,14 +470,14 @@ int tt_policy_backward(const tt_policy_desc *desc, const void *weight, const voi
     return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if ((size_t)policy_saved(a, p, (void *)saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)policy_ws(a, p, ws, TT_LOSS_BACKWARD, up) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)policy_ws(a, p, ws, TT_LOSS_BACKWARD, up, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   if (p.N)
     tt_launch(K_ALIGN, k_policy_up, dim3((unsigned)((p.N + 255) / 256)), dim3(256), 0, s,
               (const float *)p.coef, (const LossScalars *)a.sv.sc, p.N, p.reduction, grad_loss, up);
   if (hipGetLastError() != hipSuccess) return TT_EHIP;
   a.up = up; a.dh = grad_hidden; a.dw = grad_weight;
-  return loss_backward(a, s) == hipSuccess ? TT_OK : TT_EHIP;
+  return backward_from(a, p, kept, s) == hipSuccess ? TT_OK : TT_EHIP;
 }
 
 }  // extern "C"

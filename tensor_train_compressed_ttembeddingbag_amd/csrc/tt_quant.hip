@@ -109,16 +109,26 @@ __global__ __launch_bounds__(T::NT) void k_int8(GemmArgs a, Int8Out<O> ep) {
         const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
         const int x = at.ix * T::X + (wv % T::NWX) * T::wx;
         const int y = at.iy * T::Y + (wv / T::NWX) * T::wy + c;
-        float s[T::NI];
+        // all scales at once: one wait for memory, not one for each pair of columns
+        float s[T::NI], t[T::MI][4];
 #pragma unroll
         for (int j = 0; j < T::NI; ++j) s[j] = ep.s[min(y + 16 * j, ep.n - 1)];
+        if (at.ix * T::X + T::X <= ep.v) {
+          struct __attribute__((packed, aligned(4))) any { f4 v; };
+#pragma unroll
+          for (int i = 0; i < T::MI; ++i) {
+            const f4 v = ((const any *)(ep.t + x + 16 * i + 4 * g))->v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[i][r] = v[r];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[i][r] = ep.t[min(x + 16 * i + 4 * g + r, ep.v - 1)];
+        }
 #pragma unroll
         for (int i = 0; i < T::MI; i += 2) {
-          float t[2][4];
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) t[u][r] = ep.t[min(x + 16 * (i + u) + 4 * g + r, ep.v - 1)];
           const int left = ep.v - (x + 16 * i);  // columns from this pair on
 #pragma unroll
           for (int j = 0; j < T::NI; ++j) {
@@ -130,7 +140,7 @@ __global__ __launch_bounds__(T::NT) void k_int8(GemmArgs a, Int8Out<O> ep) {
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 // (kept: fp32 by itself, not one rounding with the conversion to fp16)
-                const float z = keep((float)acc[i + u][j][r] * s[j] * t[u][r]);
+                const float z = keep((float)acc[i + u][j][r] * s[j] * t[i + u][r]);
                 v[u][r] = (O)z;
               }
             if constexpr (sizeof(O) == 2) {

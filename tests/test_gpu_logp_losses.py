@@ -539,3 +539,37 @@ def test_arguments_are_refused():
             ("dev_status", TypeError, lambda: L.linear_preference(h, w, t, off, dev_status=t))):
         with pytest.raises(error, match=match):
             f()
+
+
+@pytest.mark.parametrize("dt,n,v,d", [("bf16", 2100, 33000, 1024), ("fp32", 8300, 8300, 1024),
+                                      ("fp16", 8300, 8300, 1024)])
+def test_positions_without_a_gradient_are_left_out(dt, n, v, d):
+    """Large enough for the backward to work on the positions with a slope alone."""
+    print("case kept", n, v, d, dt, flush=True)
+    h, w, t, g = make(n, v, d, dt, seed=12)
+    t[5::7] = IGN
+    lp = Head(h, w, t, dt, 1.0, t != IGN).l
+    noise = torch.randn(2, n, device="cuda", generator=g)
+    adv, old = noise[0], (lp + 0.4 * noise[1]).float()
+    adv[n // 3:n // 2] = 0.0
+    up = upstream(n, "mean", g)
+    want = want_policy(h, w, t, dt, "mean", up, adv, old, None, 0.1, 0.1, 0.0, 1.0)
+    compare(lambda a, b: L.linear_policy(a, b, t, adv, old, clip_low=0.1, clip_high=0.1, return_logps=True),
+            want, h, w, up, "mean")
+    del want
+    up = upstream(n, "none", g)
+    up[::3] = 0.0
+    want = want_policy(h, w, t, dt, "none", up, adv, old, None, 0.1, 0.1, 0.0, 1.0)
+    compare(lambda a, b: L.linear_policy(a, b, t, adv, old, clip_low=0.1, clip_high=0.1, reduction="none",
+                                         return_logps=True), want, h, w, up, "none")
+    del want
+    off = ragged(n, 50, g, 20)
+    ref = (lp + 0.3 * noise[0] - 0.02).float()
+    up = upstream(50, "sum", g)
+    want = want_prefer(h, w, t, dt, "sum", up, off, ref, "hinge", 0.2, 0.0, 0.0, False)
+    compare(lambda a, b: L.linear_preference(a, b, t, off, ref, beta=0.2, kind="hinge", reduction="sum",
+                                             return_ratios=True), want, h, w, up, "sum")
+    del want
+    a, b = h.clone().requires_grad_(), w.clone().requires_grad_()  # nothing has one
+    dh, dw = torch.autograd.grad(L.linear_policy(a, b, t, torch.zeros_like(adv), old), (a, b))
+    assert not bool(dh.any()) and not bool(dw.any())
