@@ -32,6 +32,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tt_mfma.h"
 
 namespace ttb {
@@ -78,6 +80,18 @@ struct Int8 {
   typedef i32x4 acc4;
   static __device__ __forceinline__ i32x4 mfma(v8 a, v8 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+  }
+};
+
+// fp32 rows as they lie, four values a lane where the others have eight of 16 bits (columns of k count
+// 16 bits here too): element e of a lane's four is one product over the four lane groups' k.
+struct Fp32 {
+  typedef f4 v8;
+  typedef f4 acc4;
+  static __device__ __forceinline__ f4 mfma(v8 a, v8 b, f4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
   }
 };
 
@@ -442,8 +456,10 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
       for (int j = 0; j < T::NI; ++j) acc[i][j] = typename E::acc4{};
     const int steps = now.nk;
     auto mend = [&](int b) {
-      Feed<T::X, PC, PL, T::NT>::mend(a.P, lds + b * SB, (int64_t)now.ix * T::X,
-                                  now.k0 + (int64_t)(now.nk - 1) * (GK / PL));
+      const int64_t k0 = now.k0 + (int64_t)(now.nk - 1) * (GK / PL);
+      Feed<T::X, PC, PL, T::NT>::mend(a.P, lds + b * SB, (int64_t)now.ix * T::X, k0);
+      if constexpr (std::is_same<E, Fp32>::value)  // Q lies as it came, too: 0 x inf is not 0
+        Feed<T::Y, QC, PL, T::NT>::mend(a.Q, lds + b * SB + PB, (int64_t)now.iy * T::Y, k0);
       lds_barrier();
     };
     // a wave whose part of a ragged tile lies outside has its loads and barriers only (1800

@@ -77,6 +77,8 @@ struct LossArgs {
   int twin;                // 16-bit, up to 32 positions: G's rows are followed, twin rows on, by
                            // what their rounding left (hp's by themselves); else 0
   int direct;              // loss alone, few positions: the hidden rows as they lie, all of them
+  int few32;               // set before the plan: fp32 may be read as it lies where direct is
+  int f32;                 // it is (planes 1, nothing packed)
   int64_t piece;           // rows of the weight per piece
   int ptiles;              // running statistics per position
   int fold;                // those of a piece are added up into slot 0
@@ -240,15 +242,17 @@ inline Operand weight_operand(const LossArgs &a, int64_t v0, int64_t nv) {
   if (a.pack_w) {
     o.p = a.wp; o.ld = a.Dp * 2 * a.planes; o.plane = a.Dp * 2; o.rows = nv; o.cols = a.Dp;
   } else {
-    o.p = (const char *)a.weight + v0 * a.wld * 2; o.ld = a.wld * 2; o.plane = 0;
-    o.rows = a.V - v0; o.cols = a.D;
+    const int e = a.f32 ? 4 : 2;
+    o.p = (const char *)a.weight + v0 * a.wld * e; o.ld = a.wld * e; o.plane = 0;
+    o.rows = a.V - v0; o.cols = a.D * (e / 2);
   }
   return o;
 }
 inline Operand hidden_operand(const LossArgs &a) {
   Operand o;
   if (a.direct) {
-    o.p = (const char *)a.hidden; o.ld = a.hld * 2; o.plane = 0; o.rows = a.N; o.cols = a.D;
+    const int e = a.f32 ? 4 : 2;
+    o.p = (const char *)a.hidden; o.ld = a.hld * e; o.plane = 0; o.rows = a.N; o.cols = a.D * (e / 2);
     return o;
   }
   o.p = a.sv.hp; o.ld = a.Dp * 2 * a.planes; o.plane = a.Dp * 2; o.rows = a.Npad; o.cols = a.Dp;

@@ -247,7 +247,7 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     g.P.p += r0 * g.P.ld;
     g.P.rows -= r0;
     g.Q = hidden_operand(a);
-    g.K = a.pack_w ? a.Dp : a.D;
+    g.K = a.pack_w ? a.Dp : a.f32 ? 2 * a.D : a.D;
     g.xn = (int)n;
     g.yn = (int)a.N;
     // twin rows of G are used whole, so all are written
@@ -258,7 +258,8 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     ep.v0 = v0 + r0;
     ep.nv = n;
     ep.G = a.G + r0 * 2;
-    if (a.dtype == TT_DTYPE_BF16) e = pick<Bf16, 1>(grad, t.cfg, a, g, ep, s);
+    if (a.f32) e = a.D % 4 ? pick<Fp32, 1, false, true>(t.cfg, a, g, ep, s) : pick<Fp32, 1, false, false>(t.cfg, a, g, ep, s);
+    else if (a.dtype == TT_DTYPE_BF16) e = pick<Bf16, 1>(grad, t.cfg, a, g, ep, s);
     else if (a.dtype == TT_DTYPE_F16) e = pick<Fp16, 1>(grad, t.cfg, a, g, ep, s);
     else e = pick<Fp16, 2>(grad, t.cfg, a, g, ep, s);
     ep.tile0 += g.tx;

@@ -15,7 +15,7 @@
 namespace ttb {
 
 // positions whose sum one workgroup takes in the launch that works them out
-constexpr int64_t ONE_BLOCK = 8192;
+constexpr int64_t ONE_BLOCK = 2048;
 constexpr int SUM_BLOCK = 1024;  // positions per partial sum past that
 
 struct PreferArgs {
@@ -238,6 +238,7 @@ static int cross_entropy(const Desc *d, const void *weight, float temperature, L
   if (!(temperature > 0.f && temperature < INFINITY)) return TT_EINVAL;
   const int rc = loss_args(&l, weight, a);
   a.temp = temperature;
+  a.few32 = 1;
   return rc;
 }
 

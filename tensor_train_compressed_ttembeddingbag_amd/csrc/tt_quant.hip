@@ -23,9 +23,22 @@ struct QuantArgs {
   float *s;
 };
 
+// A row with a value that is not finite gets the scale NaN and zeros, one whose scale would be below the
+// normal numbers the scale 0 and zeros.
+__device__ __forceinline__ float row_max(float m, float x) {
+  const float f = fabsf(x);
+  return f <= m ? m : f == f ? f : INFINITY;
+}
+__device__ __forceinline__ float row_scale(float m) {
+  const float s = m / 127.f;
+  return !(m < INFINITY) ? __builtin_nanf("") : s < 0x1p-126f ? 0.f : s;
+}
+__device__ __forceinline__ int8_t row_value(float x, float s) {
+  return s > 0.f ? (int8_t)(int)fminf(fmaxf(rintf(x / s), -127.f), 127.f) : (int8_t)0;
+}
+
 // NT lanes a row; U groups of eight of each stay in registers between the maximum and the rounding,
-// wider rows are read twice.  A row with a value that is not finite gets the scale NaN and zeros, one
-// whose scale would be below the normal numbers the scale 0 and zeros.
+// wider rows are read twice.
 template <class S, int NT, bool NARROW>
 __global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
   constexpr int U = 4;
@@ -47,10 +60,7 @@ __global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = fabsf((float)v[u].x[e]);
-        m = f <= m ? m : f == f ? f : INFINITY;
-      }
+      for (int e = 0; e < 8; ++e) m = row_max(m, (float)v[u].x[e]);
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
@@ -60,11 +70,8 @@ __global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
     m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
   }
   if (!on) return;
-  float s = m / 127.f;
-  if (!(m < INFINITY)) s = __builtin_nanf("");
-  else if (s < 0x1p-126f) s = 0.f;
+  const float s = row_scale(m);
   if (tid == 0) a.s[r] = s;
-  const bool zero = !(s > 0.f);
   int8_t *q = a.q + r * a.pitch;
   for (int64_t g0 = 0; g0 < cpr; g0 += U * NT) {
     if (cpr > U * NT) load(g0);
@@ -74,8 +81,7 @@ __global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
       if (g >= cpr) break;
       Eight<int8_t> o;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o.x[e] = zero ? (int8_t)0 : (int8_t)(int)fminf(fmaxf(rintf((float)v[u].x[e] / s), -127.f), 127.f);
+      for (int e = 0; e < 8; ++e) o.x[e] = row_value((float)v[u].x[e], s);
       put8<NARROW>(q + column<NARROW>(g, a.d), o, a.d);
     }
   }
@@ -168,6 +174,108 @@ __global__ __launch_bounds__(T::NT) void k_int8(GemmArgs a, Int8Out<O> ep) {
       });
 }
 
+// A few tokens in one launch: every workgroup quantises them for itself, into LDS, while its first rows of
+// the table travel.  A wave takes 16 rows of the table at a time, straight from memory to the registers of
+// v_mfma_i32_16x16x64_i8 (a lane has 16 bytes of a row), U loads ahead of the products.
+// Bound by the table's bytes; what one launch less saves is 4 us of 15 (1 x 32000 x 1024).
+constexpr int FEW_TOKENS = 16, FEW_VALUES = 8192;
+struct FewArgs {
+  int64_t d, hld, pitch, wpitch, v;
+  int n, lp;               // tokens; bytes between them in LDS
+  const void *x;
+  const int8_t *w;
+  const float *t;
+  void *out;
+};
+template <class S, class O, bool NARROW>
+__global__ __launch_bounds__(256) void k_int8_few(FewArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char q[];  // [n][lp], zeros behind d
+  __shared__ float s_s[FEW_TOKENS];
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int nk = (int)((a.d + 64 * U - 1) / (64 * U));  // loads of U x 64 bytes along a row
+  const int64_t tiles = (a.v + 15) / 16, stride = (int64_t)gridDim.x * 4;
+  int64_t tile = (int64_t)blockIdx.x * 4 + wv;
+  i32x4 p[2][U];
+  auto load = [&](int64_t tile, int kk, i32x4 (&to)[U]) {
+    const int8_t *row = a.w + min(tile * 16 + c, a.v - 1) * a.wpitch;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = ((int64_t)kk * U + u) * 64 + 16 * g;
+      to[u] = *(const i32x4 *)(row + (k < a.pitch ? k : 0));  // past the row: its q are zeros
+    }
+  };
+  if (tile < tiles) load(tile, 0, p[0]);
+  const int64_t cpr = (a.d + 7) / 8;
+  for (int i = wv; i < a.n; i += 4) {
+    const S *x = (const S *)a.x + i * a.hld;
+    float m = 0.f;
+#pragma unroll 4
+    for (int64_t r = lane; r < cpr; r += 64) {
+      const Eight<S> v = get8<NARROW>(x + column<NARROW>(r, a.d), a.d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = row_max(m, (float)v.x[e]);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    const float s = row_scale(m);
+    if (lane == 0) s_s[i] = s;
+    char *o = q + i * a.lp;
+    for (int64_t k = a.d + lane; k < a.lp; k += 64) o[k] = 0;
+#pragma unroll 4
+    for (int64_t r = lane; r < cpr; r += 64) {
+      const int64_t col = column<NARROW>(r, a.d);
+      const Eight<S> v = get8<NARROW>(x + col, a.d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!NARROW || e < a.d) o[col + e] = row_value((float)v.x[e], s);
+    }
+  }
+  __syncthreads();
+  const char *qc = q + min(c, a.n - 1) * a.lp + 16 * g;
+  const float sc = s_s[min(c, a.n - 1)];
+  auto multiply = [&](const i32x4 (&from)[U], int kk, i32x4 &acc) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      acc = Int8::mfma(from[u], *(const i32x4 *)(qc + (kk * U + u) * 64), acc);
+  };
+  for (; tile < tiles; tile += stride) {
+    i32x4 acc = {};
+    // pairs of loads, so that the register sets have their names at compile time
+    for (int kk = 0; kk < nk; kk += 2) {
+      if (kk + 1 < nk) load(tile, kk + 1, p[1]);
+      else if (tile + stride < tiles) load(tile + stride, 0, p[1]);
+      multiply(p[0], kk, acc);
+      if (kk + 1 < nk) {
+        if (kk + 2 < nk) load(tile, kk + 2, p[0]);
+        else if (tile + stride < tiles) load(tile + stride, 0, p[0]);
+        multiply(p[1], kk + 1, acc);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) p[0][u] = p[1][u];
+      }
+    }
+    const int64_t row = tile * 16 + 4 * g;
+    if (c < a.n) {
+      O *o = (O *)a.out + c * a.v + row;
+      O v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float z = keep((float)acc[r] * sc * a.t[min(row + r, a.v - 1)]);
+        v[r] = (O)z;
+      }
+      if (row + 4 <= a.v) {
+        struct __attribute__((packed, aligned(2))) any { O v[4]; };
+        *(any *)o = {{v[0], v[1], v[2], v[3]}};
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (row + r < a.v) o[r] = v[r];
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host
 template <class S, bool NARROW>
 static void go_quantize(const QuantArgs &a, hipStream_t s) {
@@ -233,6 +341,22 @@ static hipError_t product(const Int8Args &a, hipStream_t s) {
   part(0, large, {0, 256, 256});
   part(large, a.v - large, gemm_shape(a.v - large, a.n, cus));
   return e;
+}
+
+template <class S, class O>
+static void go_few(const FewArgs &a, int cus, hipStream_t s) {
+  const int64_t blocks = ((a.v + 15) / 16 + 3) / 4;
+  auto go = [&](auto *kernel) {
+    tt_launch(K_INT8, kernel, dim3((unsigned)std::min<int64_t>(blocks, 8 * cus)), dim3(256), a.n * a.lp, s, a);
+  };
+  if (a.d < 8) go(k_int8_few<S, O, true>);
+  else go(k_int8_few<S, O, false>);
+}
+template <class S>
+static void go_few(const FewArgs &a, int out, int cus, hipStream_t s) {
+  if (out == TT_DTYPE_F32) go_few<S, float>(a, cus, s);
+  else if (out == TT_DTYPE_BF16) go_few<S, __bf16>(a, cus, s);
+  else go_few<S, _Float16>(a, cus, s);
 }
 
 static int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -303,6 +427,16 @@ int tt_int8_linear(const tt_int8_desc *desc, const void *hidden, const float *hi
   if (a.n == 0) return TT_OK;
   hipStream_t s = (hipStream_t)stream;
   a.w = weight; a.t = weight_scales; a.out = out;
+  if (!given && a.n <= FEW_TOKENS && a.n * a.d <= FEW_VALUES) {
+    // LDS rows of whole loads, and 16 bytes off each other's banks
+    const FewArgs f = {a.d, desc->hidden_stride, a.pitch, a.wpitch, a.v, (int)a.n,
+                       (int)(round_up(a.d, 512) + 16), hidden, weight, weight_scales, out};
+    const int cus = std::max(device_cus(), 1);
+    if (desc->dtype == TT_DTYPE_F32) go_few<float>(f, desc->out_dtype, cus, s);
+    else if (desc->dtype == TT_DTYPE_BF16) go_few<__bf16>(f, desc->out_dtype, cus, s);
+    else go_few<_Float16>(f, desc->out_dtype, cus, s);
+    return hipGetLastError() == hipSuccess ? TT_OK : TT_EHIP;
+  }
   QuantArgs q = {a.n, a.d, desc->hidden_stride, a.pitch, hidden, (int8_t *)ws,
                  (float *)((char *)ws + round_up(a.n * a.pitch, 256))};
   a.q = q.q; a.qpitch = a.pitch; a.s = given ? hidden_scales : q.s;
