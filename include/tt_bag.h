@@ -589,8 +589,8 @@ typedef struct tt_embed_desc {
 
 int tt_embed_forward(const tt_embed_desc *desc, const int64_t *indices, const void *weight,
                      const float *row_scales, void *out, int32_t *dev_status, void *stream);
-/* workspace of tt_embed_backward (256-byte aligned): up to 1024 tokens 256 bytes; past that at most
- * 17 bytes a token, the fp32 sums of one row in 64 tokens and a byte for every two rows of the
+/* workspace of tt_embed_backward (256-byte aligned): up to 1024 tokens none (256, and NULL will do); past that at most
+ * 17 bytes a token, the fp32 sums of one row in 64 tokens and a byte for every row of the
  * table; 0: the descriptor is rejected */
 size_t tt_embed_workspace_size(const tt_embed_desc *desc);
 int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const void *grad_out,
@@ -621,7 +621,8 @@ typedef struct tt_int8_desc {
 
 int tt_int8_quantize(int64_t n, int64_t d, int32_t dtype, const void *x, int64_t stride,
                      int8_t *values, int64_t pitch, float *scales, void *stream);
-/* workspace of tt_int8_linear (256-byte aligned): hidden in 8 bits; 0: the descriptor is rejected */
+/* workspace of tt_int8_linear (256-byte aligned): hidden in 8 bits; where there is none, 256, and NULL will do;
+ * 0: the descriptor is rejected */
 size_t tt_int8_workspace_size(const tt_int8_desc *desc);
 int tt_int8_linear(const tt_int8_desc *desc, const void *hidden, const float *hidden_scales,
                    const int8_t *weight, const float *weight_scales, void *out, void *ws,

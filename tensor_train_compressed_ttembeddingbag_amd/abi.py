@@ -8,7 +8,6 @@ loudly (``RuntimeError``) when the library has not been built.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -306,13 +305,17 @@ def _stream(stream, like: Optional[torch.Tensor] = None):
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_same_device = contextlib.nullcontext()
 
-
-def _device_of(like: torch.Tensor):
-    """A context in which the device that holds `like` is the current one: a kernel is launched on
-    a stream of the current device."""
-    return _same_device if like.get_device() == _current_device() else torch.cuda.device(like.device)
+def _launch(name: str, like: torch.Tensor, *args):
+    """The entry point `name` with these arguments, then the current stream of the device that holds
+    `like`; a kernel is launched on a stream of the current device."""
+    if like.get_device() == _current_device():
+        rc = getattr(lib(), name)(*args, _stream(None, like))
+    else:
+        with torch.cuda.device(like.device):
+            rc = getattr(lib(), name)(*args, _stream(None, like))
+    if rc:
+        raise TTError(name, rc)
 
 
 def _no_dual(what: str, *tensors: torch.Tensor):

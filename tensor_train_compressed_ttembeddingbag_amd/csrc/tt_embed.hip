@@ -27,11 +27,15 @@ constexpr int ROWS_MAX = 64;     // rows of the table per block, at most
 constexpr int SHORT = 16;        // tokens of a run that one group of lanes adds up by itself
 constexpr int LIST = 1024;       // tokens that are looked for without a sort
 static_assert(ROWS_MAX * SHORT <= LIST, "all short runs of a block in LDS");
+// What a block writes, from measurements (us of the rows' kernel, cold, blocks of 16, 32 and 64 KiB): 4096 tokens x
+// 2048 of 32000 rows bf16 42, 50, 65; 20000 x 512 of 131072 53, 60, 74; 65536 x 4096 of 131072 396, 312, 313.
+constexpr int BLOCK_BYTES = 16384;
+constexpr int64_t MOST_BLOCKS = 32768;
 constexpr int MAX_BITS = 10;     // of a digit
 constexpr int BINS = 1 << MAX_BITS;
 constexpr int SORT_ROUNDS = 8;   // elements per thread
 constexpr int TILE_T = 512 * SORT_ROUNDS;    // tokens per workgroup of the sort of many
-constexpr int SMALL_T = 1024 * SORT_ROUNDS;  // tokens that one workgroup sorts
+constexpr int SMALL_T = 16384;   // tokens that are sorted by counting
 
 struct EmbedArgs {
   int64_t n, v, d, wld, gld;   // strides in elements
@@ -95,11 +99,15 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a) {
 }
 
 // ---------------------------------------------------------------- sort
-__device__ __forceinline__ u64 token_key(const EmbedArgs &a, int64_t i, bool tell) {
-  const int64_t v = a.idx[i];
+// the row of a token, or v for none; bad: whether its index is outside the table (to be told later: an
+// atomic between loads would make each wait for the one before)
+__device__ __forceinline__ unsigned row_of(const EmbedArgs &a, int64_t v, bool &bad) {
   const bool in = v >= 0 && v < a.v;
-  if (!in && tell) set_status(a.status, TT_DEV_BAD_INDEX);
-  return (u64)(in && v != a.pad ? v : a.v) << 32 | (unsigned)i;
+  bad |= !in;
+  return (unsigned)(in && v != a.pad ? v : a.v);
+}
+__device__ __forceinline__ void tell(const EmbedArgs &a, bool bad) {
+  if (bad) set_status(a.status, TT_DEV_BAD_INDEX);
 }
 __device__ __forceinline__ int digit_of(u64 key, int shift, int bits) {
   return (int)(key >> (32 + shift)) & ((1 << bits) - 1);
@@ -150,63 +158,74 @@ __device__ __forceinline__ int scan_bins(int x, int *s_w) {
   return before + s - x;
 }
 
-// All passes of at most SMALL_T tokens, in LDS.
-__global__ __launch_bounds__(1024) void k_embed_sort_small(EmbedArgs a, u64 *out, int passes,
-                                                           int bits) {
-  extern __shared__ __attribute__((aligned(16))) char dyn[];
-  u64 *buf = (u64 *)dyn;                                 // [SMALL_T]
-  int *count = (int *)(dyn + SMALL_T * sizeof(u64));     // [16][1 << bits]
-  __shared__ int s_w[16];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = (int)a.n, bins = 1 << bits;
-  // each wave takes as many rounds as the tokens need
-  const int rounds = (n + 1023) / 1024;
-  const int first = wv * rounds * 64;
-  u64 key[SORT_ROUNDS];
-  int rank[SORT_ROUNDS];
+// Up to SMALL_T tokens: a token's place is the number of those with a smaller row, or the same row before
+// it.  Every workgroup compares its T tokens with all of them, staged in LDS, 256 / T lanes a token: n^2
+// comparisons over the whole chip take less than the passes of a radix sort, each of them a launch or a
+// workgroup by itself (4096 tokens: 14 us in one workgroup).
+template <int T>
+__global__ __launch_bounds__(256) void k_embed_rank(EmbedArgs a, u64 *out) {
+  extern __shared__ __attribute__((aligned(16))) unsigned s_key[];  // [n rounded up to 4]
+  typedef unsigned u4 __attribute__((ext_vector_type(4)));
+  constexpr int L = 256 / T;
+  const int tid = threadIdx.x, n = (int)a.n, quads = (n + 3) / 4;
+  bool bad = false;
+  for (int i0 = tid; i0 < quads * 4; i0 += 256 * 16) {
+    int64_t v[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) v[u] = a.idx[min(i0 + 256 * u, n - 1)];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const int i = i0 + 256 * u;
+      if (i < quads * 4) s_key[i] = i < n ? row_of(a, v[u], bad) : ~0u;
+    }
+  }
+  if (blockIdx.x == 0) tell(a, bad);
+  __syncthreads();
+  const int first = blockIdx.x * T, i = first + tid / L, sub = tid % L;
+  const unsigned own = s_key[min(i, n - 1)];
+  const u4 *q = (const u4 *)s_key;
+  int place = 0;
+  const int q0 = first / 4, q1 = min(quads, (first + T + 3) / 4);
+  // before this workgroup's tokens equal rows count, behind them they do not
+#pragma unroll 4
+  for (int k = sub; k < q0; k += L) {
+    const u4 v = q[k];
+    place += (v.x <= own) + (v.y <= own) + (v.z <= own) + (v.w <= own);
+  }
+  for (int k = q0 + sub; k < q1; k += L) {
+    const u4 v = q[k];
+    place += v.x < own || (v.x == own && 4 * k < i);
+    place += v.y < own || (v.y == own && 4 * k + 1 < i);
+    place += v.z < own || (v.z == own && 4 * k + 2 < i);
+    place += v.w < own || (v.w == own && 4 * k + 3 < i);
+  }
+#pragma unroll 4
+  for (int k = q1 + sub; k < quads; k += L) {
+    const u4 v = q[k];
+    place += (v.x < own) + (v.y < own) + (v.z < own) + (v.w < own);
+  }
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) place += __shfl_xor(place, o);
+  if (sub == 0 && i < n) out[place] = (u64)own << 32 | (unsigned)i;
+}
+
+// SORT_ROUNDS keys of a thread, STEP places apart: of the first pass from the indices
+template <int STEP>
+__device__ __forceinline__ void load_keys(const EmbedArgs &a, const u64 *in, int64_t i0, bool first,
+                                          u64 (&key)[SORT_ROUNDS]) {
+  int64_t v[SORT_ROUNDS];
 #pragma unroll
   for (int u = 0; u < SORT_ROUNDS; ++u) {
-    const int i = first + u * 64 + lane;
-    key[u] = u < rounds && i < n ? token_key(a, i, true) : 0;
+    const int64_t i = min(i0 + u * STEP, a.n - 1);
+    v[u] = in ? (int64_t)in[i] : a.idx[i];
   }
-  for (int p = 0; p < passes; ++p) {
-    for (int i = tid; i < 16 * bins; i += 1024) count[i] = 0;
-    __syncthreads();
-    rank_rounds(key, first, u64(first) + rounds * 64 < (u64)n ? first + rounds * 64 : n, p * bits, bits,
-                count + wv * bins, rank);
-    __syncthreads();
-    int all = 0, c[16];
-    if (tid < bins) {
+  bool bad = false;
 #pragma unroll
-      for (int w = 0; w < 16; ++w) c[w] = count[w * bins + tid];
-#pragma unroll
-      for (int w = 0; w < 16; ++w) all += c[w];
-    }
-    int base = scan_bins<1024>(all, s_w);
-    if (tid < bins) {
-#pragma unroll
-      for (int w = 0; w < 16; ++w) {
-        count[w * bins + tid] = base;
-        base += c[w];
-      }
-    }
-    __syncthreads();
-    const bool last = p == passes - 1;
-#pragma unroll
-    for (int u = 0; u < SORT_ROUNDS; ++u)
-      if (u < rounds && first + u * 64 + lane < n) {
-        const int at = count[wv * bins + digit_of(key[u], p * bits, bits)] + rank[u];
-        if (last) out[at] = key[u];
-        else buf[at] = key[u];
-      }
-    if (last) break;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < SORT_ROUNDS; ++u) {
-      const int i = first + u * 64 + lane;
-      if (u < rounds && i < n) key[u] = buf[i];
-    }
-    __syncthreads();
+  for (int u = 0; u < SORT_ROUNDS; ++u) {
+    const int64_t i = i0 + u * STEP;
+    key[u] = in ? (u64)v[u] : i < a.n ? (u64)row_of(a, v[u], bad) << 32 | (unsigned)i : 0;
   }
+  if (first && !in) tell(a, bad);
 }
 
 // One pass of more tokens: a tile's digits counted ..
@@ -216,12 +235,12 @@ __global__ __launch_bounds__(512) void k_embed_hist(EmbedArgs a, const u64 *in, 
   const int tid = threadIdx.x, bins = 1 << bits;
   for (int i = tid; i < bins; i += 512) count[i] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * TILE_T;
+  const int64_t i0 = (int64_t)blockIdx.x * TILE_T + tid;
+  u64 v[SORT_ROUNDS];
+  load_keys<512>(a, in, i0, true, v);
 #pragma unroll
-  for (int u = 0; u < SORT_ROUNDS; ++u) {
-    const int64_t i = i0 + u * 512 + tid;
-    if (i < a.n) atomicAdd(&count[digit_of(in ? in[i] : token_key(a, i, true), shift, bits)], 1);
-  }
+  for (int u = 0; u < SORT_ROUNDS; ++u)
+    if (i0 + u * 512 < a.n) atomicAdd(&count[digit_of(v[u], shift, bits)], 1);
   __syncthreads();
   for (int i = tid; i < bins; i += 512) hist[(int64_t)blockIdx.x * bins + i] = count[i];
 }
@@ -237,11 +256,7 @@ __global__ __launch_bounds__(512) void k_embed_scatter(EmbedArgs a, const u64 *i
   const int64_t first = (int64_t)blockIdx.x * TILE_T + wv * SORT_ROUNDS * 64;
   u64 key[SORT_ROUNDS];
   int rank[SORT_ROUNDS];
-#pragma unroll
-  for (int u = 0; u < SORT_ROUNDS; ++u) {
-    const int64_t i = first + u * 64 + lane;
-    key[u] = i < a.n ? (in ? in[i] : token_key(a, i, false)) : 0;
-  }
+  load_keys<64>(a, in, first + lane, false, key);
   rank_rounds(key, first, a.n, shift, bits, count + wv * bins, rank);
   __syncthreads();
   int carry = 0;  // of the digits before this block of 512
@@ -376,7 +391,7 @@ __device__ __forceinline__ void long_run(const EmbedArgs &a, const L &l, int64_t
     const int64_t to = min(items, (l.grp + 1) * per);
     int64_t m = min(items, l.grp * per);
     auto tokens = [&](int64_t g, int64_t count) {
-      constexpr int U = 8;
+      constexpr int U = 128 / (int)sizeof(decltype(l.token(a, 0)));
       int64_t t = 0;
       for (; t + U <= count; t += U) {
         decltype(l.token(a, 0)) x[U];
@@ -459,7 +474,7 @@ __device__ __forceinline__ void long_runs_of_piece(const EmbedArgs &a, int64_t p
 // A block's rows by its columns.  The tokens of its short runs go through LDS as one list in
 // the sorted order; a group of lanes takes those of some consecutive rows and adds them up as a
 // stream, U rows of grad_out ahead of the sums, whatever rows they belong to (most rows of a large
-// vocabulary have none, so a row at a time would wait for every load).  Then the empty rows.  The
+// vocabulary have none, so a row at a time would wait for every load).  The
 // long runs have blocks of their own, the first ones of the launch.
 // DIRECT: the block looks its tokens up in the unsorted list (at most LIST of them), and adds its
 // long runs up itself.
@@ -470,7 +485,7 @@ __global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
   __shared__ unsigned s_pos[LIST];        // that list: tokens, and their rows
   __shared__ unsigned char s_row[LIST];
   __shared__ unsigned s_all[DIRECT ? LIST : 1];  // all tokens by row
-  __shared__ int s_n[16];
+  __shared__ int s_n[DIRECT ? 256 : 1];
   __shared__ float s_sum[256 * 8];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int chunk = blockIdx.x % a.chunks;
@@ -485,55 +500,63 @@ __global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
   int64_t seg = 0;  // the block's first sorted place
   int len = 0;
   if constexpr (DIRECT) {
-    // tokens of these rows in their order: token 256 u + tid
-    static_assert(LIST == 4 * 256, "tokens of a thread");
-    u64 key[4], m[4];
+    // the tokens of these rows by row, stably: token 256 wv + 64 u + lane, waves without any pass
+    static_assert(LIST == 4 * 256 && ROWS_MAX == 64, "tokens of a thread, rows of six bits");
+    int *count = s_n + wv * 64;  // the wave's tokens of each row so far
+    int64_t v[4];
+    int row[4], rank[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = a.n > 0 ? a.idx[min<int64_t>(wv * 256 + u * 64 + lane, a.n - 1)] : 0;
+    bool bad = false;
+    count[lane] = 0;
+    wave_lds_sync();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t i = u * 256 + tid;
-      key[u] = i < a.n ? token_key(a, i, blockIdx.x == 0) : (u64)a.v << 32;
-    }
+      const bool there = wv * 256 + u * 64 + lane < a.n;
+      const int64_t r = there ? (int64_t)row_of(a, v[u], bad) - r0 : -1;
+      const bool on = r >= 0 && r < R;
+      row[u] = on ? (int)r : -1;
+      u64 same = __ballot(on);
+      if (same == 0) continue;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t r = (int64_t)(key[u] >> 32) - r0;
-      m[u] = __ballot(r >= 0 && r < R);
-      if (lane == 0) s_n[u * 4 + wv] = __popcll(m[u]);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      if ((w & 3) == wv && m[w >> 2] >> lane & 1) {
-        const int at = len + __popcll(m[w >> 2] & ((1ull << lane) - 1));
-        s_row[at] = (unsigned char)((key[w >> 2] >> 32) - r0);
-        s_pos[at] = (unsigned)key[w >> 2];
+      for (int b = 0; b < 6; ++b) {
+        const u64 one = __ballot(row[u] >> b & 1);
+        same &= row[u] >> b & 1 ? one : ~one;
       }
-      len += s_n[w];
+      const u64 below = same & ((1ull << lane) - 1);
+      const int before = on ? count[row[u]] : 0;
+      wave_lds_sync();
+      if (on && below == 0) count[row[u]] = before + __popcll(same);
+      wave_lds_sync();
+      rank[u] = before + __popcll(below);
     }
     __syncthreads();
-    // sorted by row: a thread counts, and then moves, one row's
+    // (each wave for itself, so that one barrier less is needed)
+    int before = 0, c = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int x = s_n[w * 64 + lane];
+      before += w < wv ? x : 0;
+      c += x;
+    }
+    int end = c;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(end, o);
+      if (lane >= o) end += x;
+    }
+    len = __shfl(end, 63);
     if (wv == 0) {
-      int c = 0, at = 0;
-      for (int k = 0; k < len; ++k) {
-        if (s_row[k] == lane) {
-          if (c == 0) at = k;
-          ++c;
-        }
-      }
-      int s = c;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int x = __shfl_up(s, o);
-        if (lane >= o) s += x;
-      }
-      s_start[lane + 1] = s;
+      s_start[lane + 1] = end;
       if (lane == 0) s_start[0] = 0;
-      s -= c;
-      for (int k = at; c > 0; ++k)
-        if (s_row[k] == lane) {
-          s_all[s++] = s_pos[k];
-          --c;
-        }
     }
+    const int at = end - c + before;  // of this wave's first token of row `lane`
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int from = __shfl(at, max(row[u], 0));
+      if (row[u] >= 0) s_all[from + rank[u]] = (unsigned)(wv * 256 + u * 64 + lane);
+    }
+    if (blockIdx.x == 0) tell(a, bad);
   } else {
     seg = a.first[block];
     len = a.first[block + 1] - (int)seg;
@@ -590,10 +613,10 @@ __global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
   }
   const Lanes<G, W, NARROW> l(a, chunk);
   const int share = (R + l.groups - 1) / l.groups, ra = min(R, l.grp * share), rb = min(R, ra + share);
-  if (l.live && len > 0) {
-    constexpr int U = sizeof(G) == 2 ? 8 : 4;
-    int k = s_short[ra], cur = -1;
-    const int end = s_short[rb];
+  if (l.live) {
+    constexpr int U = (DIRECT ? 8 : 16) / sizeof(G);
+    int k = len > 0 ? s_short[ra] : 0, cur = -1;
+    const int end = len > 0 ? s_short[rb] : 0;
     Eight<G> g[2][U];
     auto load = [&](int k, Eight<G> (&to)[U]) {
 #pragma unroll
@@ -616,6 +639,10 @@ __global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
         }
     };
     load(k, g[0]);
+    // the empty rows under the first loads
+    const float none[8] = {};
+    for (int r = ra; r < rb; ++r)
+      if (s_start[r + 1] == s_start[r]) l.store(a, r0 + r, none);
     for (; k < end; k += 2 * U) {
       load(k + U, g[1]);
       add(k, g[0]);
@@ -628,11 +655,6 @@ __global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
     if (s_start[r + 1] - s_start[r] > SHORT)
       long_run<false, NARROW>(a, l, r0 + r, s_start[r], s_start[r + 1],
                               [&](int64_t g) { return s_all[g]; }, s_sum);
-  if (l.live) {
-    const float none[8] = {};
-    for (int r = ra; r < rb; ++r)
-      if (s_start[r + 1] == s_start[r]) l.store(a, r0 + r, none);
-  }
 }
 
 // ---------------------------------------------------------------- host
@@ -665,9 +687,12 @@ static int embed_args(const tt_embed_desc *d, EmbedArgs &a) {
     a.chunks = (int)chunks;
     a.lpr = lpr;
   }
-  // enough blocks to fill the chip, and rows enough to pay for finding their tokens
-  a.shift = 6;
-  while (a.shift > 3 && (a.v >> a.shift) * a.chunks < 2048) --a.shift;
+  // rows enough to pay for finding their tokens, and enough blocks to fill the chip
+  const int64_t bytes = a.lpr * 8ll * (d->dtype == TT_DTYPE_F32 ? 4 : 2);
+  a.shift = 2;
+  while (a.shift < 6 && (bytes << a.shift) < BLOCK_BYTES) ++a.shift;
+  while (a.shift < 6 && (a.v >> a.shift) * a.chunks > MOST_BLOCKS) ++a.shift;
+  while (a.shift > 2 && (a.v >> a.shift) * a.chunks < 1024) --a.shift;
   a.rows = 1 << a.shift;
   return TT_OK;
 }
@@ -734,12 +759,12 @@ static hipError_t sort_tokens(const EmbedArgs &a, const EmbedWs &w, const u64 **
                               hipStream_t s) {
   const Digits g = digits(a);
   if (a.n <= SMALL_T) {
-    const int lds = SMALL_T * 8 + (64 << g.bits);
-    static const hipError_t e = hipFuncSetAttribute(
-        (const void *)k_embed_sort_small, hipFuncAttributeMaxDynamicSharedMemorySize,
-        SMALL_T * 8 + (64 << MAX_BITS));
-    if (e != hipSuccess) return e;
-    tt_launch(K_EMBED_SORT, k_embed_sort_small, dim3(1), dim3(1024), lds, s, a, w.a, g.passes, g.bits);
+    const int lds = (int)round_up(a.n, 4) * 4;
+    auto go = [&](auto *kernel, int t) {  // a workgroup for every CU, if there are so many
+      tt_launch(K_EMBED_SORT, kernel, dim3((unsigned)((a.n + t - 1) / t)), dim3(256), lds, s, a, w.a);
+    };
+    if (a.n <= 8192) go(k_embed_rank<16>, 16);
+    else go(k_embed_rank<32>, 32);
     *sorted = w.a;
     return hipGetLastError();
   }
@@ -821,7 +846,7 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
   const int rc = embed_args(desc, a);
   if (rc != TT_OK) return rc;
   if (desc->dtype == TT_DTYPE_I8) return TT_EINVAL;
-  if (!grad_weight || !ws || (a.n && (!indices || !grad_out))) return TT_EINVAL;
+  if (!grad_weight || (!ws && !direct(a)) || (a.n && (!indices || !grad_out))) return TT_EINVAL;
   if ((uintptr_t)grad_out % elem_size(desc->out_dtype) ||
       (uintptr_t)grad_weight % elem_size(desc->dtype))
     return TT_EINVAL;

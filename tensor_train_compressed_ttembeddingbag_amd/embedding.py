@@ -73,11 +73,8 @@ def _forward(indices, weight, scale, padding_idx, dtype, dev_status):
                          abi.TT_DTYPE_I8 if int8 else abi._DTYPE[values.dtype],
                          abi._DTYPE[dtype], scale)
     out = torch.empty(indices.shape + (d,), dtype=dtype, device=values.device)
-    with abi._device_of(values):
-        abi._check("tt_embed_forward", abi.lib().tt_embed_forward(
-            ref, indices.data_ptr(), values.data_ptr(),
-            weight.scales.data_ptr() if int8 else None, out.data_ptr(), abi._ptr(dev_status),
-            abi._stream(None, values)))
+    abi._launch("tt_embed_forward", values, ref, indices.data_ptr(), values.data_ptr(),
+                weight.scales.data_ptr() if int8 else None, out.data_ptr(), abi._ptr(dev_status))
     return out
 
 
@@ -91,11 +88,10 @@ def _gradient(grad_out, indices, v, d, scale, padding_idx, dtype, dev_status):
     if not size:
         raise abi.TTError("tt_embed_workspace_size", -2)
     dw = torch.empty((v, d), dtype=dtype, device=g.device)
-    ws = torch.empty(size, dtype=torch.uint8, device=g.device)
-    with abi._device_of(g):
-        abi._check("tt_embed_backward", abi.lib().tt_embed_backward(
-            ref, indices.data_ptr(), g.data_ptr(), dw.data_ptr(), ws.data_ptr(), size,
-            abi._ptr(dev_status), abi._stream(None, g)))
+    # (256 bytes stand for none)
+    ws = torch.empty(size, dtype=torch.uint8, device=g.device) if size > 256 else None
+    abi._launch("tt_embed_backward", g, ref, indices.data_ptr(), g.data_ptr(), dw.data_ptr(),
+                abi._ptr(ws), size, abi._ptr(dev_status))
     return dw
 
 

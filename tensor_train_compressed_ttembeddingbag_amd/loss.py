@@ -206,9 +206,8 @@ class _LogpPlan:
 
     def __init__(self, name, desc, hidden, weight):
         lib = abi.lib()
-        self.name, self.desc, self.ref = name, desc, ctypes.byref(desc)
-        self.forward = getattr(lib, "tt_%s_forward" % name)
-        self.backward = getattr(lib, "tt_%s_backward" % name)
+        self.desc, self.ref = desc, ctypes.byref(desc)
+        self.forward, self.backward = "tt_%s_forward" % name, "tt_%s_backward" % name
         size = getattr(lib, "tt_%s_workspace_size" % name)
         self.saved = getattr(lib, "tt_%s_saved_size" % name)(self.ref)
         if not self.saved:
@@ -227,11 +226,9 @@ def _logp_forward(plan, hidden, weight, inputs, shape, more_shape, dev_status, s
     saved = _bytes(plan.saved, dev) if save else None
     size = plan.fwd if save else plan.only
     ws = _bytes(size, dev)
-    with abi._device_of(hidden):
-        abi._check("tt_%s_forward" % plan.name, plan.forward(
-            plan.ref, hidden.data_ptr(), weight.data_ptr(), *[abi._ptr(t) for t in inputs],
-            loss.data_ptr(), abi._ptr(more), abi._ptr(saved), plan.saved, ws.data_ptr(), size,
-            abi._ptr(dev_status), abi._stream(None, hidden)))
+    abi._launch(plan.forward, hidden, plan.ref, hidden.data_ptr(), weight.data_ptr(),
+                *[abi._ptr(t) for t in inputs], loss.data_ptr(), abi._ptr(more), abi._ptr(saved),
+                plan.saved, ws.data_ptr(), size, abi._ptr(dev_status))
     return loss, more, saved
 
 
@@ -245,10 +242,8 @@ def _logp_backward(ctx, grad_loss, _):
     dh = torch.empty((plan.n, plan.d), dtype=plan.dtype, device=dev) if need_h else None
     dw = torch.empty((plan.v, plan.d), dtype=plan.dtype, device=dev) if need_w else None
     ws = _bytes(plan.bwd, dev)
-    with abi._device_of(weight):
-        abi._check("tt_%s_backward" % plan.name, plan.backward(
-            plan.ref, weight.data_ptr(), saved.data_ptr(), plan.saved, grad_loss.data_ptr(),
-            abi._ptr(dh), abi._ptr(dw), ws.data_ptr(), plan.bwd, abi._stream(None, weight)))
+    abi._launch(plan.backward, weight, plan.ref, weight.data_ptr(), saved.data_ptr(), plan.saved,
+                grad_loss.data_ptr(), abi._ptr(dh), abi._ptr(dw), ws.data_ptr(), plan.bwd)
     return dh, dw, None, None, None, None, None
 
 

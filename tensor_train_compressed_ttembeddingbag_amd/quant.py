@@ -99,10 +99,8 @@ def quantize_rows(x: torch.Tensor) -> Int8Rows:
     pitch = (d + 15) // 16 * 16
     values = torch.empty((n, pitch), dtype=torch.int8, device=x.device)
     scales = torch.empty(n, dtype=torch.float32, device=x.device)
-    with abi._device_of(x):
-        abi._check("tt_int8_quantize", abi.lib().tt_int8_quantize(
-            n, d, abi._DTYPE[x.dtype], x.data_ptr(), x.stride(0) if n > 1 else d,
-            values.data_ptr(), pitch, scales.data_ptr(), abi._stream(None, x)))
+    abi._launch("tt_int8_quantize", x, n, d, abi._DTYPE[x.dtype], x.data_ptr(),
+                x.stride(0) if n > 1 else d, values.data_ptr(), pitch, scales.data_ptr())
     return Int8Rows(values[:, :d], scales)
 
 
@@ -150,10 +148,9 @@ def int8_linear(hidden, weight: Int8Rows, *, dtype: Optional[torch.dtype] = None
         plan = _plans[key] = (desc, ref, size)
     _, ref, size = plan
     out = torch.empty(shape + (v,), dtype=dtype, device=rows.device)
-    ws = torch.empty(size, dtype=torch.uint8, device=rows.device)
-    with abi._device_of(rows):
-        abi._check("tt_int8_linear", abi.lib().tt_int8_linear(
-            ref, rows.data_ptr(), hidden.scales.data_ptr() if given else None,
-            weight.values.data_ptr(), weight.scales.data_ptr(), out.data_ptr(), ws.data_ptr(), size,
-            abi._stream(None, rows)))
+    # (256 bytes stand for none)
+    ws = torch.empty(size, dtype=torch.uint8, device=rows.device) if size > 256 else None
+    abi._launch("tt_int8_linear", rows, ref, rows.data_ptr(),
+                hidden.scales.data_ptr() if given else None, weight.values.data_ptr(),
+                weight.scales.data_ptr(), out.data_ptr(), abi._ptr(ws), size)
     return out

@@ -56,10 +56,11 @@ def test_bad_pointers_and_workspaces():
     assert lib.tt_embed_forward(r8, FAKE, FAKE + 8, FAKE, FAKE, None, None) == -1
     odd = desc(dtype=abi.TT_DTYPE_I8, weight_stride=72)
     assert lib.tt_embed_forward(ctypes.byref(odd), FAKE, FAKE, FAKE, FAKE, None, None) == -1
+    more = ctypes.byref(desc(n=1025))  # up to 1024 tokens there is no workspace
     for i in range(4):
         a = [FAKE] * 4
         a[i] = None
-        assert lib.tt_embed_backward(r, *a, BIG, None, None) == -1
+        assert lib.tt_embed_backward(more, *a, BIG, None, None) == -1
     assert lib.tt_embed_backward(r8, FAKE, FAKE, FAKE, FAKE, BIG, None, None) == -1
     assert lib.tt_embed_backward(r, FAKE, FAKE + 1, FAKE, FAKE, BIG, None, None) == -1
     assert lib.tt_embed_backward(r, FAKE, FAKE, FAKE + 1, FAKE, BIG, None, None) == -1
@@ -67,7 +68,7 @@ def test_bad_pointers_and_workspaces():
     for n in (10, 5000, 50000):
         d = desc(n=n)
         size = lib.tt_embed_workspace_size(ctypes.byref(d))
-        assert 0 < size <= 17 * n + n // 64 * 64 * 4 + 50 + 8192
+        assert 0 < size <= 17 * n + n // 64 * 64 * 4 + 100 + 8192
         assert lib.tt_embed_backward(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, size - 1, None,
                                      None) == -3
 
