@@ -106,19 +106,39 @@ struct Int8Out {
   int n, v;
 };
 
+// A tile with room for a wave's results on their way out: 16 tokens by ROW bytes, as much as leaves the tile
+// its place beside another one on the CU.
+template <class O, class T>
+struct WithRows : T {
+  static constexpr int MOST = T::X == 256 ? 256 : 128;
+  static constexpr int ROW = T::wx * (int)sizeof(O) < MOST ? T::wx * (int)sizeof(O) : MOST;
+  static constexpr int EXTRA = T::NT / 64 * 16 * ROW;
+  static constexpr int LDS = T::LDS - T::EXTRA + EXTRA;
+  // 16-byte group k of row r, permuted so that neither writes nor reads meet in a bank
+  static __device__ __forceinline__ int at(int r, int k) {
+    return r * ROW + (k ^ (r * ROW / 256 & (ROW / 16 - 1))) * 16;
+  }
+};
+
+// A lane's results are four columns of one token.  Stored from there they are 64 bytes of each of 16 rows
+// at a time; they go through LDS instead, for each wave by itself, and leave as whole rows of up to 256
+// bytes: 4096 x 50021 x 2048 to bf16 500 -> 403 us, to fp32 645 -> 514, with 50048 rows 428 -> 390.
 template <class O, class T>
 __global__ __launch_bounds__(T::NT) void k_int8(GemmArgs a, Int8Out<O> ep) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
+  constexpr int C = 16 / sizeof(O);                 // columns of 16 bytes
+  constexpr int W = T::ROW / (int)sizeof(O);          // columns that go together
   typedef O o4 __attribute__((ext_vector_type(4)));
   gemm_tiles<Int8, T, 1, false, false, false, false>(
-      a, lds, [&](const TileAt &at, i32x4 (&acc)[T::MI][T::NI], char *) {
+      a, lds, [&](const TileAt &at, i32x4 (&acc)[T::MI][T::NI], char *tmp) {
         const int tid = own_thread(), lane = tid & 63, wv = tid >> 6, g = lane >> 4, c = lane & 15;
         const int x = at.ix * T::X + (wv % T::NWX) * T::wx;
-        const int y = at.iy * T::Y + (wv / T::NWX) * T::wy + c;
+        const int y = at.iy * T::Y + (wv / T::NWX) * T::wy;
+        char *rows = tmp + wv * 16 * T::ROW;
         // all scales at once: one wait for memory, not one for each pair of columns
         float s[T::NI], t[T::MI][4];
 #pragma unroll
-        for (int j = 0; j < T::NI; ++j) s[j] = ep.s[min(y + 16 * j, ep.n - 1)];
+        for (int j = 0; j < T::NI; ++j) s[j] = ep.s[min(y + 16 * j + c, ep.n - 1)];
         if (at.ix * T::X + T::X <= ep.v) {
           struct __attribute__((packed, aligned(4))) any { f4 v; };
 #pragma unroll
@@ -134,43 +154,45 @@ __global__ __launch_bounds__(T::NT) void k_int8(GemmArgs a, Int8Out<O> ep) {
             for (int r = 0; r < 4; ++r) t[i][r] = ep.t[min(x + 16 * i + 4 * g + r, ep.v - 1)];
         }
 #pragma unroll
-        for (int i = 0; i < T::MI; i += 2) {
-          const int left = ep.v - (x + 16 * i);  // columns from this pair on
+        for (int j = 0; j < T::NI; ++j)
 #pragma unroll
-          for (int j = 0; j < T::NI; ++j) {
-            const bool in = y + 16 * j < ep.n;
-            O *o = ep.out + (int64_t)(y + 16 * j) * ep.ld + x + 16 * i;
-            o4 v[2];
+          for (int i0 = 0; i0 < T::MI; i0 += W / 16) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < W / 16; ++i) {
+              o4 v;
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 // (kept: fp32 by itself, not one rounding with the conversion to fp16)
-                const float z = keep((float)acc[i + u][j][r] * s[j] * t[i + u][r]);
-                v[u][r] = (O)z;
+                const float z = keep((float)acc[i0 + i][j][r] * s[j] * t[i0 + i][r]);
+                v[r] = (O)z;
               }
-            if constexpr (sizeof(O) == 2) {
-              if (left >= 32) {  // a whole pair: 16 bytes a lane (the same for every lane)
-                store_pair_if(in, (char *)o, v[0], v[1], g);
-                continue;
-              }
+              const int col = 16 * i + 4 * g;
+              *(o4 *)(rows + T::at(c, col / C) + col % C * sizeof(O)) = v;
             }
-            if (!in) continue;
-            struct __attribute__((packed, aligned(2))) any { o4 v; };
+            wave_lds_sync();
+            constexpr int LPR = W / C;  // lanes of a row
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int e = 16 * u + 4 * g;
-              if (left >= e + 4) {
-                const any w = {v[u]};
-                *(any *)(o + e) = w;
+            for (int p = 0; p < LPR / 4; ++p) {
+              const int r = p * (64 / LPR) + lane / LPR, k = lane % LPR;
+              const i32x4 v = *(const i32x4 *)(rows + T::at(r, k));
+              const int col = x + 16 * i0 + k * C, left = ep.v - col;
+              if (y + 16 * j + r >= ep.n || left <= 0) continue;
+              O *o = ep.out + (int64_t)(y + 16 * j + r) * ep.ld + col;
+              if (left >= C) {
+                struct __attribute__((packed, aligned(2))) any { i32x4 v; };
+                ((any *)o)->v = v;
               } else {
+                union {
+                  i32x4 v;
+                  O e[C];
+                } u = {v};
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (e + r < left) o[e + r] = v[u][r];
+                for (int e = 0; e < C; ++e)
+                  if (e < left) o[e] = u.e[e];
               }
             }
+            wave_lds_sync();
           }
-        }
       });
 }
 
@@ -178,7 +200,7 @@ __global__ __launch_bounds__(T::NT) void k_int8(GemmArgs a, Int8Out<O> ep) {
 // the table travel.  A wave takes 16 rows of the table at a time, straight from memory to the registers of
 // v_mfma_i32_16x16x64_i8 (a lane has 16 bytes of a row), U loads ahead of the products.
 // Bound by the table's bytes; what one launch less saves is 4 us of 15 (1 x 32000 x 1024).
-constexpr int FEW_TOKENS = 16, FEW_VALUES = 8192;
+constexpr int FEW_TOKENS = 16, FEW_VALUES = 4096;
 constexpr int64_t FEW_BYTES = 48 << 20;
 struct FewArgs {
   int64_t d, hld, pitch, wpitch, v;
@@ -299,8 +321,9 @@ static hipError_t quantize(const QuantArgs &a, int dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class O, class T>
+template <class O, class Plain>
 static hipError_t go_int8(const GemmArgs &g, const Int8Out<O> &ep, int cus, hipStream_t s) {
+  typedef WithRows<O, Plain> T;
   const hipError_t e = lds_limit<T>(&k_int8<O, T>);
   if (e != hipSuccess) return e;
   const int64_t tiles = (int64_t)g.tx * g.ty, most = (int64_t)cus * (160 * 1024 / T::LDS);
