@@ -35,7 +35,7 @@ constexpr int MAX_BITS = 10;     // of a digit
 constexpr int BINS = 1 << MAX_BITS;
 constexpr int SORT_ROUNDS = 8;   // elements per thread
 constexpr int TILE_T = 512 * SORT_ROUNDS;    // tokens per workgroup of the sort of many
-constexpr int SMALL_T = 16384;   // tokens that are sorted by counting
+constexpr int SMALL_T = 8192;    // tokens that are sorted by counting
 
 struct EmbedArgs {
   int64_t n, v, d, wld, gld;   // strides in elements
@@ -48,6 +48,7 @@ struct EmbedArgs {
   int32_t *status;
   // backward
   int lpr, chunks;             // groups of eight columns per block, blocks along a row
+  int long_lpr, long_chunks;   // the same of the blocks for long runs
   int rows, shift;             // rows per block: 2^shift
   int *first;                  // [blocks of rows + 1] sorted place of a block's first token
   const u64 *sorted;           // row << 32 | token; tokens without a row last, as row v
@@ -345,18 +346,35 @@ __global__ __launch_bounds__(256) void k_embed_pieces(EmbedArgs a) {
   }
 }
 
-// The lanes of a block on some columns of the table: groups of a.lpr lanes beside each other.
+// first sorted place whose row is at least r: 64 probes at a time, all lanes of a wave
+__device__ __forceinline__ int64_t lower_bound(const u64 *sorted, int64_t n, u64 r) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, len = n;
+  while (len > 0) {
+    const int64_t step = (len + 63) / 64, at = lo + lane * step;
+    // probes below r: the place is past the last of them
+    const int k = __popcll(__ballot(at < lo + len && sorted[min(at, n - 1)] >> 32 < r));
+    if (k == 0) return lo;
+    const int64_t from = lo + (k - 1) * step + 1, to = min(lo + k * step, lo + len);
+    lo = from;
+    len = to - from;
+  }
+  return lo;
+}
+
+// The lanes of a block on some columns of the table: groups of lpr lanes beside each other.
 template <class G, class W, bool NARROW>
 struct Lanes {
-  int groups, grp;
+  int lpr, groups, grp;
   bool live;
   int64_t c;
   const G *src;
-  __device__ __forceinline__ Lanes(const EmbedArgs &a, int chunk) {
+  __device__ __forceinline__ Lanes(const EmbedArgs &a, int chunk, int n) {
     const int tid = threadIdx.x;
-    groups = 256 / a.lpr;
-    grp = tid / a.lpr;
-    const int64_t group = (int64_t)chunk * a.lpr + tid % a.lpr;
+    lpr = n;
+    groups = 256 / lpr;
+    grp = tid / lpr;
+    const int64_t group = (int64_t)chunk * lpr + tid % lpr;
     c = column<NARROW>(group, a.d);
     live = grp < groups && group * 8 < a.d;
     src = (const G *)a.w + c;
@@ -410,7 +428,7 @@ __device__ __forceinline__ void long_run(const EmbedArgs &a, const L &l, int64_t
     if (m < head + np && m < to) {
       const int64_t e = min(to, head + np);
       const float *p = a.part + (p0 + m - head) * a.d + l.c;
-#pragma unroll 8
+#pragma unroll 4
       for (; m < e; ++m, p += a.d) add8(acc, get8<NARROW>(p, a.d));
     }
     if (m < to) tokens(p1 * PIECE_T + (m - head - np), to - m);
@@ -423,15 +441,15 @@ __device__ __forceinline__ void long_run(const EmbedArgs &a, const L &l, int64_t
     if (l.live && l.grp == 0)
       for (int w = 1; w < l.groups; ++w)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += s_sum[e * 256 + w * a.lpr + threadIdx.x];
+        for (int e = 0; e < 8; ++e) acc[e] += s_sum[e * 256 + w * l.lpr + threadIdx.x];
   }
   if (l.live && l.grp == 0) l.store(a, row, acc);
 }
 
 // The long runs that start in one piece of the sorted order (a run of a row that half the tokens
 // name would keep a block of 64 rows busy long after the others)
-template <class G, class W, bool NARROW>
-__device__ __forceinline__ void long_runs_of_piece(const EmbedArgs &a, int64_t piece, int chunk,
+template <class G, class W, bool NARROW, bool PIECES>
+__device__ __forceinline__ void long_runs_of_piece(const EmbedArgs &a, int64_t piece, int chunk, int lpr,
                                                    float *s_sum) {
   const int lane = threadIdx.x & 63;  // every wave for itself
   const int64_t i = piece * PIECE_T + lane;
@@ -445,7 +463,7 @@ __device__ __forceinline__ void long_runs_of_piece(const EmbedArgs &a, int64_t p
   }
   u64 todo = __ballot(starts);
   if (todo == 0) return;
-  const Lanes<G, W, NARROW> l(a, chunk);
+  const Lanes<G, W, NARROW> l(a, chunk, lpr);
   for (; todo; todo &= todo - 1) {
     const int at = __ffsll(todo) - 1;
     const u64 r = __shfl((unsigned)row, at);
@@ -466,7 +484,7 @@ __device__ __forceinline__ void long_runs_of_piece(const EmbedArgs &a, int64_t p
       const u64 in = __ballot(p < a.n && a.sorted[min(p, a.n - 1)] >> 32 == r);
       lo += __popcll(in) * step;
     }
-    long_run<true, NARROW>(a, l, (int64_t)r, g0, lo + 1,
+    long_run<PIECES, NARROW>(a, l, (int64_t)r, g0, lo + 1,
                            [&](int64_t g) { return (unsigned)a.sorted[g]; }, s_sum);
   }
 }
@@ -477,24 +495,30 @@ __device__ __forceinline__ void long_runs_of_piece(const EmbedArgs &a, int64_t p
 // vocabulary have none, so a row at a time would wait for every load).  The
 // long runs have blocks of their own, the first ones of the launch.
 // DIRECT: the block looks its tokens up in the unsorted list (at most LIST of them), and adds its
-// long runs up itself.
-template <class G, class W, bool NARROW, bool DIRECT>
-__global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
+// long runs up itself.  SEARCH: there is no launch before that says where a block's tokens start and adds
+// whole pieces up: it looks for them in the sorted order, and long runs are cut over more, narrower groups.
+enum { DIRECT_T, SEARCH_T, SORTED_T };
+template <class G, class W, bool NARROW, int HOW>
+__global__ __launch_bounds__(256, NARROW ? 1 : 6) void k_embed_rows(EmbedArgs a) {
+  constexpr bool DIRECT = HOW == DIRECT_T, SEARCH = HOW == SEARCH_T;
   __shared__ int s_start[ROWS_MAX + 1];   // a row's first token, from the block's first on
   __shared__ int s_short[ROWS_MAX + 1];   // a row's first token in the list of short runs
   __shared__ unsigned s_pos[LIST];        // that list: tokens, and their rows
   __shared__ unsigned char s_row[LIST];
   __shared__ unsigned s_all[DIRECT ? LIST : 1];  // all tokens by row
-  __shared__ int s_n[DIRECT ? 256 : 1];
+  __shared__ int s_n[DIRECT ? 256 : 2];
   __shared__ float s_sum[256 * 8];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int chunk = blockIdx.x % a.chunks;
-  int64_t block = blockIdx.x / a.chunks;
+  int id = blockIdx.x;
   if constexpr (!DIRECT) {
-    const int64_t pieces = (a.n + PIECE_T - 1) / PIECE_T;
-    if (block < pieces) return long_runs_of_piece<G, W, NARROW>(a, block, chunk, s_sum);
-    block -= pieces;
+    const int pieces = (int)((a.n + PIECE_T - 1) / PIECE_T) * a.long_chunks;
+    if (id < pieces)
+      return long_runs_of_piece<G, W, NARROW, !SEARCH>(a, id / a.long_chunks, id % a.long_chunks, a.long_lpr,
+                                                       s_sum);
+    id -= pieces;
   }
+  const int chunk = id % a.chunks;
+  const int64_t block = id / a.chunks;
   const int64_t r0 = block << a.shift;
   const int R = (int)min<int64_t>(a.rows, a.v - r0);
   int64_t seg = 0;  // the block's first sorted place
@@ -558,8 +582,18 @@ __global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
     }
     if (blockIdx.x == 0) tell(a, bad);
   } else {
-    seg = a.first[block];
-    len = a.first[block + 1] - (int)seg;
+    if constexpr (SEARCH) {
+      if (wv < 2) {
+        const int64_t at = lower_bound(a.sorted, a.n, (u64)(r0 + (wv ? R : 0)));
+        if (lane == 0) s_n[wv] = (int)at;
+      }
+      __syncthreads();
+      seg = s_n[0];
+      len = s_n[1] - (int)seg;
+    } else {
+      seg = a.first[block];
+      len = a.first[block + 1] - (int)seg;
+    }
     if (tid <= R) s_start[tid] = tid == 0 ? 0 : len;
     __syncthreads();
     if (len <= 8192) {
@@ -611,10 +645,10 @@ __global__ __launch_bounds__(256) void k_embed_rows(EmbedArgs a) {
       __syncthreads();
     }
   }
-  const Lanes<G, W, NARROW> l(a, chunk);
+  const Lanes<G, W, NARROW> l(a, chunk, a.lpr);
   const int share = (R + l.groups - 1) / l.groups, ra = min(R, l.grp * share), rb = min(R, ra + share);
   if (l.live) {
-    constexpr int U = (DIRECT ? 8 : 16) / sizeof(G);
+    constexpr int U = 8 / sizeof(G);  // (more of them cost workgroups on a CU)
     int k = len > 0 ? s_short[ra] : 0, cur = -1;
     const int end = len > 0 ? s_short[rb] : 0;
     Eight<G> g[2][U];
@@ -663,6 +697,9 @@ static int64_t elem_size(int dtype) {
   return dtype == TT_DTYPE_F32 ? 4 : dtype == TT_DTYPE_I8 ? 1 : 2;
 }
 
+static bool direct(const EmbedArgs &a) { return a.n <= LIST; }
+static bool searches(const EmbedArgs &a) { return !direct(a) && a.n <= SMALL_T; }
+
 static int embed_args(const tt_embed_desc *d, EmbedArgs &a) {
   if (!d) return TT_EINVAL;
   if (d->n < 0 || d->v < 1 || d->d < 1) return TT_EINVAL;
@@ -680,7 +717,9 @@ static int embed_args(const tt_embed_desc *d, EmbedArgs &a) {
   // few blocks along a row, with as many of a block's lanes in use as can be
   const int64_t cpr = (a.d + 7) / 8;
   int best = 0;
-  for (int64_t chunks = (cpr + 255) / 256; chunks <= (cpr + 63) / 64; ++chunks) {
+  // (a block that adds its long runs up itself: at least four groups)
+  const int64_t most = a.n <= LIST ? 64 : 256;
+  for (int64_t chunks = (cpr + most - 1) / most; chunks <= (cpr + 63) / 64; ++chunks) {
     const int lpr = (int)((cpr + chunks - 1) / chunks), used = 256 / lpr * lpr;
     if (used < best + 16) continue;
     best = used;
@@ -694,6 +733,10 @@ static int embed_args(const tt_embed_desc *d, EmbedArgs &a) {
   while (a.shift < 6 && (a.v >> a.shift) * a.chunks > MOST_BLOCKS) ++a.shift;
   while (a.shift > 2 && (a.v >> a.shift) * a.chunks < 1024) --a.shift;
   a.rows = 1 << a.shift;
+  // a long run over several CUs, and over several groups of lanes of each
+  const int64_t narrow = searches(a) ? std::max<int64_t>(16, (cpr + 15) / 16) : 64;
+  a.long_lpr = (int)std::min<int64_t>({cpr, narrow, 64});
+  a.long_chunks = (int)((cpr + a.long_lpr - 1) / a.long_lpr);
   return TT_OK;
 }
 
@@ -713,8 +756,6 @@ static Digits digits(const EmbedArgs &a) {
   const int passes = (all + MAX_BITS - 1) / MAX_BITS;
   return {passes, (all + passes - 1) / passes};
 }
-static bool direct(const EmbedArgs &a) { return a.n <= LIST; }
-
 static EmbedWs embed_ws(const EmbedArgs &a, void *ws) {
   EmbedWs w = {};
   int64_t off = 0;
@@ -729,8 +770,10 @@ static EmbedWs embed_ws(const EmbedArgs &a, void *ws) {
       w.b = (u64 *)take(a.n * 8);
       w.hist = (int *)take((a.n + TILE_T - 1) / TILE_T * (4ll << digits(a).bits));
     }
-    w.part = (float *)take(a.n / PIECE_T * a.d * 4);
-    w.first = (int *)take(((a.v + a.rows - 1) / a.rows + 1) * 4);
+    if (!searches(a)) {
+      w.part = (float *)take(a.n / PIECE_T * a.d * 4);
+      w.first = (int *)take(((a.v + a.rows - 1) / a.rows + 1) * 4);
+    }
   }
   w.bytes = std::max<int64_t>(off, 256);
   return w;
@@ -763,8 +806,7 @@ static hipError_t sort_tokens(const EmbedArgs &a, const EmbedWs &w, const u64 **
     auto go = [&](auto *kernel, int t) {  // a workgroup for every CU, if there are so many
       tt_launch(K_EMBED_SORT, kernel, dim3((unsigned)((a.n + t - 1) / t)), dim3(256), lds, s, a, w.a);
     };
-    if (a.n <= 8192) go(k_embed_rank<16>, 16);
-    else go(k_embed_rank<32>, 32);
+    go(k_embed_rank<16>, 16);
     *sorted = w.a;
     return hipGetLastError();
   }
@@ -785,15 +827,13 @@ static hipError_t sort_tokens(const EmbedArgs &a, const EmbedWs &w, const u64 **
 template <class G, class W, bool NARROW>
 static void go_rows(const EmbedArgs &a, hipStream_t s) {
   const unsigned blocks = (unsigned)((a.v + a.rows - 1) / a.rows * a.chunks);
-  if (direct(a)) {
-    tt_launch(K_EMBED_GRAD, k_embed_rows<G, W, NARROW, true>, dim3(blocks), dim3(256), 0, s, a);
-    return;
-  }
+  const unsigned pieces = (unsigned)((a.n + PIECE_T - 1) / PIECE_T), longs = pieces * a.long_chunks;
+  auto go = [&](auto *kernel, unsigned grid) { tt_launch(K_EMBED_GRAD, kernel, dim3(grid), dim3(256), 0, s, a); };
+  if (direct(a)) return go(k_embed_rows<G, W, NARROW, DIRECT_T>, blocks);
+  if (searches(a)) return go(k_embed_rows<G, W, NARROW, SEARCH_T>, longs + blocks);
   tt_launch(K_EMBED_GRAD, k_embed_pieces<G, NARROW>,
-            dim3((unsigned)((a.n + PIECE_T - 1) / PIECE_T), (unsigned)std::min<int64_t>((a.d + 2047) / 2048, 64)),
-            dim3(256), 0, s, a);
-  const unsigned pieces = (unsigned)((a.n + PIECE_T - 1) / PIECE_T) * a.chunks;
-  tt_launch(K_EMBED_GRAD, k_embed_rows<G, W, NARROW, false>, dim3(pieces + blocks), dim3(256), 0, s, a);
+            dim3(pieces, (unsigned)std::min<int64_t>((a.d + 2047) / 2048, 64)), dim3(256), 0, s, a);
+  go(k_embed_rows<G, W, NARROW, SORTED_T>, longs + blocks);
 }
 template <class G, class W>
 static void go_rows(const EmbedArgs &a, hipStream_t s) {
@@ -853,7 +893,7 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
   if ((uintptr_t)ws % 256) return TT_EWORKSPACE;
   const EmbedWs w = embed_ws(a, ws);
   if ((size_t)w.bytes > ws_bytes) return TT_EWORKSPACE;
-  if (((a.v + a.rows - 1) / a.rows + a.n / PIECE_T + 1) * a.chunks > 0x7fffffffll) return TT_ESHAPE;
+  if ((a.v + a.rows - 1) / a.rows * a.chunks + (a.n / PIECE_T + 1) * a.long_chunks > 0x7fffffffll) return TT_ESHAPE;
   a.idx = indices; a.w = grad_out; a.out = grad_weight; a.status = dev_status;
   a.part = w.part; a.first = w.first;
   hipStream_t s = (hipStream_t)stream;
