@@ -33,8 +33,7 @@ constexpr int BLOCK_BYTES = 16384;
 constexpr int64_t MOST_BLOCKS = 32768;
 constexpr int MAX_BITS = 10;     // of a digit
 constexpr int BINS = 1 << MAX_BITS;
-constexpr int SORT_ROUNDS = 8;   // elements per thread
-constexpr int TILE_T = 512 * SORT_ROUNDS;    // tokens per workgroup of the sort of many
+constexpr int SEARCH_T_MAX = 32768;  // tokens that go without the launch for pieces
 constexpr int SMALL_T = 8192;    // tokens that are sorted by counting
 
 struct EmbedArgs {
@@ -210,19 +209,19 @@ __global__ __launch_bounds__(256) void k_embed_rank(EmbedArgs a, u64 *out) {
   if (sub == 0 && i < n) out[place] = (u64)own << 32 | (unsigned)i;
 }
 
-// SORT_ROUNDS keys of a thread, STEP places apart: of the first pass from the indices
-template <int STEP>
+// ROUNDS keys of a thread, STEP places apart: of the first pass from the indices
+template <int STEP, int ROUNDS>
 __device__ __forceinline__ void load_keys(const EmbedArgs &a, const u64 *in, int64_t i0, bool first,
-                                          u64 (&key)[SORT_ROUNDS]) {
-  int64_t v[SORT_ROUNDS];
+                                          u64 (&key)[ROUNDS]) {
+  int64_t v[ROUNDS];
 #pragma unroll
-  for (int u = 0; u < SORT_ROUNDS; ++u) {
+  for (int u = 0; u < ROUNDS; ++u) {
     const int64_t i = min(i0 + u * STEP, a.n - 1);
     v[u] = in ? (int64_t)in[i] : a.idx[i];
   }
   bool bad = false;
 #pragma unroll
-  for (int u = 0; u < SORT_ROUNDS; ++u) {
+  for (int u = 0; u < ROUNDS; ++u) {
     const int64_t i = i0 + u * STEP;
     key[u] = in ? (u64)v[u] : i < a.n ? (u64)row_of(a, v[u], bad) << 32 | (unsigned)i : 0;
   }
@@ -230,22 +229,24 @@ __device__ __forceinline__ void load_keys(const EmbedArgs &a, const u64 *in, int
 }
 
 // One pass of more tokens: a tile's digits counted ..
+template <int ROUNDS>
 __global__ __launch_bounds__(512) void k_embed_hist(EmbedArgs a, const u64 *in, int *hist, int shift,
                                                     int bits) {
   __shared__ int count[BINS];
   const int tid = threadIdx.x, bins = 1 << bits;
   for (int i = tid; i < bins; i += 512) count[i] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * TILE_T + tid;
-  u64 v[SORT_ROUNDS];
+  const int64_t i0 = (int64_t)blockIdx.x * (512 * ROUNDS) + tid;
+  u64 v[ROUNDS];
   load_keys<512>(a, in, i0, true, v);
 #pragma unroll
-  for (int u = 0; u < SORT_ROUNDS; ++u)
+  for (int u = 0; u < ROUNDS; ++u)
     if (i0 + u * 512 < a.n) atomicAdd(&count[digit_of(v[u], shift, bits)], 1);
   __syncthreads();
   for (int i = tid; i < bins; i += 512) hist[(int64_t)blockIdx.x * bins + i] = count[i];
 }
 // .. and put behind those of smaller digits and of the same digit in the tiles before
+template <int ROUNDS>
 __global__ __launch_bounds__(512) void k_embed_scatter(EmbedArgs a, const u64 *in, u64 *out,
                                                        const int *hist, int tiles, int shift,
                                                        int bits) {
@@ -254,9 +255,9 @@ __global__ __launch_bounds__(512) void k_embed_scatter(EmbedArgs a, const u64 *i
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, bins = 1 << bits;
   for (int i = tid; i < 8 * bins; i += 512) count[i] = 0;
   __syncthreads();
-  const int64_t first = (int64_t)blockIdx.x * TILE_T + wv * SORT_ROUNDS * 64;
-  u64 key[SORT_ROUNDS];
-  int rank[SORT_ROUNDS];
+  const int64_t first = (int64_t)blockIdx.x * (512 * ROUNDS) + wv * ROUNDS * 64;
+  u64 key[ROUNDS];
+  int rank[ROUNDS];
   load_keys<64>(a, in, first + lane, false, key);
   rank_rounds(key, first, a.n, shift, bits, count + wv * bins, rank);
   __syncthreads();
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(512) void k_embed_scatter(EmbedArgs a, const u64 *i
     __syncthreads();
   }
 #pragma unroll
-  for (int u = 0; u < SORT_ROUNDS; ++u)
+  for (int u = 0; u < ROUNDS; ++u)
     if (first + u * 64 + lane < a.n)
       out[count[wv * bins + digit_of(key[u], shift, bits)] + rank[u]] = key[u];
 }
@@ -698,7 +699,7 @@ static int64_t elem_size(int dtype) {
 }
 
 static bool direct(const EmbedArgs &a) { return a.n <= LIST; }
-static bool searches(const EmbedArgs &a) { return !direct(a) && a.n <= SMALL_T; }
+static bool searches(const EmbedArgs &a) { return !direct(a) && a.n <= SEARCH_T_MAX; }
 
 static int embed_args(const tt_embed_desc *d, EmbedArgs &a) {
   if (!d) return TT_EINVAL;
@@ -756,6 +757,9 @@ static Digits digits(const EmbedArgs &a) {
   const int passes = (all + MAX_BITS - 1) / MAX_BITS;
   return {passes, (all + passes - 1) / passes};
 }
+// tokens of a workgroup of the sort: few, so that the passes are short, while their counts are few too
+static int sort_tile(const EmbedArgs &a) { return a.n <= 1 << 17 ? 1024 : 4096; }
+
 static EmbedWs embed_ws(const EmbedArgs &a, void *ws) {
   EmbedWs w = {};
   int64_t off = 0;
@@ -768,7 +772,7 @@ static EmbedWs embed_ws(const EmbedArgs &a, void *ws) {
     w.a = (u64 *)take(a.n * 8);
     if (a.n > SMALL_T) {
       w.b = (u64 *)take(a.n * 8);
-      w.hist = (int *)take((a.n + TILE_T - 1) / TILE_T * (4ll << digits(a).bits));
+      w.hist = (int *)take((a.n + sort_tile(a) - 1) / sort_tile(a) * (4ll << digits(a).bits));
     }
     if (!searches(a)) {
       w.part = (float *)take(a.n / PIECE_T * a.d * 4);
@@ -810,16 +814,20 @@ static hipError_t sort_tokens(const EmbedArgs &a, const EmbedWs &w, const u64 **
     *sorted = w.a;
     return hipGetLastError();
   }
-  const int tiles = (int)((a.n + TILE_T - 1) / TILE_T);
+  const int tile = sort_tile(a), tiles = (int)((a.n + tile - 1) / tile);
   const u64 *in = nullptr;
   u64 *to = w.a;
-  for (int p = 0; p < g.passes; ++p) {
-    tt_launch(K_EMBED_SORT, k_embed_hist, dim3(tiles), dim3(512), 0, s, a, in, w.hist, p * g.bits, g.bits);
-    tt_launch(K_EMBED_SORT, k_embed_scatter, dim3(tiles), dim3(512), 0, s, a, in, to,
-              (const int *)w.hist, tiles, p * g.bits, g.bits);
-    in = to;
-    to = to == w.a ? w.b : w.a;
-  }
+  auto passes = [&](auto *hist, auto *scatter) {
+    for (int p = 0; p < g.passes; ++p) {
+      tt_launch(K_EMBED_SORT, hist, dim3(tiles), dim3(512), 0, s, a, in, w.hist, p * g.bits, g.bits);
+      tt_launch(K_EMBED_SORT, scatter, dim3(tiles), dim3(512), 0, s, a, in, to, (const int *)w.hist,
+                tiles, p * g.bits, g.bits);
+      in = to;
+      to = to == w.a ? w.b : w.a;
+    }
+  };
+  if (tile == 1024) passes(k_embed_hist<2>, k_embed_scatter<2>);
+  else passes(k_embed_hist<8>, k_embed_scatter<8>);
   *sorted = in;
   return hipGetLastError();
 }
