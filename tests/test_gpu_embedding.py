@@ -337,3 +337,26 @@ def test_arguments_are_refused():
         embedding_gradient(torch.zeros(5, 8, device="cuda"), i, 20)
     with pytest.raises(ValueError, match="num_rows"):
         embedding_gradient(torch.zeros(4, 8, device="cuda"), i, 0)
+
+
+@pytest.mark.parametrize("n,v", [(131072, 5), (140001, 3000), (600001, 70000), (530000, (1 << 20) + 1)])
+def test_many_tokens(n, v):
+    """Sorted in larger tiles, with their counts summed in a launch of its own, in one to three passes."""
+    g = gen(n)
+    i = tokens(n, v, g)
+    i[::1000] = -3
+    up = torch.randn(n, 3, device="cuda", generator=g)
+    check_gradient(embedding_gradient(up, i, v), i, up, v, 1.0)
+    up = torch.randn(n, 9, device="cuda", generator=g).half()
+    check_gradient(embedding_gradient(up, i, v, padding_idx=v // 3), i, up, v, 1.0, v // 3)
+
+
+def test_repeated_backward():
+    g = gen(3)
+    w = torch.randn(50, 12, device="cuda", generator=g, requires_grad=True)
+    i = tokens(2000, 50, g)
+    up = torch.randn(2000, 12, device="cuda", generator=g)
+    out = embedding(i, w)
+    a, = torch.autograd.grad(out, w, up, retain_graph=True)
+    b, = torch.autograd.grad(out, w, 2 * up)
+    assert torch.equal(2 * a, b)

@@ -573,3 +573,26 @@ def test_positions_without_a_gradient_are_left_out(dt, n, v, d):
     a, b = h.clone().requires_grad_(), w.clone().requires_grad_()  # nothing has one
     dh, dw = torch.autograd.grad(L.linear_policy(a, b, t, torch.zeros_like(adv), old), (a, b))
     assert not bool(dh.any()) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_repeated_backward(dt):
+    """What is saved is left as it was."""
+    h, w, t, g = make(40, 300, 64, dt, seed=14)
+    h.requires_grad_(), w.requires_grad_()
+    off = torch.tensor([0, 11, 20, 29, 38], device="cuda")
+    for loss in (L.linear_policy(h, w, t, torch.randn(40, device="cuda", generator=g)),
+                 L.linear_preference(h, w, t, off)):
+        first = torch.autograd.grad(loss, (h, w), retain_graph=True)
+        for a, b in zip(first, torch.autograd.grad(loss, (h, w))):
+            assert torch.equal(a, b)
+
+
+def test_changed_inputs_are_noticed():
+    h, w, t, g = make(8, 30, 16, "fp32", seed=4)
+    h.requires_grad_(), w.requires_grad_()
+    loss = L.linear_policy(h, w, t, torch.ones(8, device="cuda"))
+    with torch.no_grad():
+        w.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified"):
+        loss.backward()
