@@ -68,6 +68,12 @@ struct LossArgs {
   const void *tlogits;     // teacher logits [N][k]
   float *loss;
   const float *up;         // gradient of the loss
+  // a loss that is a function of the positions' cross entropies: its slopes, see gradient_of
+  const float *coef;       // by position, or by sequence, or null
+  const int *seq;          // [N] a position's sequence, or null
+  int64_t pairs;
+  int of;                  // TT_REDUCE_*: what up is of
+  const LossScalars *all;  // with the count that a mean's gradient is divided by
   void *dh, *dw;
   int32_t *status;
   // plan
@@ -223,6 +229,22 @@ __device__ __forceinline__ bool counts(const LossArgs &a, int64_t i) {
   if (a.limit && i >= *a.limit) return false;
   const int64_t t = a.tgt[i];
   return t != a.ignore && t >= 0 && t < a.V;
+}
+
+// The gradient that reaches position i's cross entropy: the caller's, or minus the slope by the position's
+// log-probability times the gradient of what it is a slope of.  (A position of no sequence does not
+// count, so what is made up for it is not used.)
+__device__ __forceinline__ float gradient_of(const LossArgs &a, int64_t i) {
+  if (!a.coef) return a.up[i];
+  int64_t at = i, of = i;
+  if (a.seq) {
+    at = a.seq[i];
+    if (at < 0 || at >= 2 * a.pairs) return 0.f;
+    of = at % a.pairs;
+  }
+  double u = -(double)a.coef[at] * (double)a.up[a.of == TT_REDUCE_NONE ? of : 0];
+  if (a.of == TT_REDUCE_MEAN) u /= a.seq ? (double)a.pairs : (double)max(a.all->count, 1);
+  return (float)u;
 }
 
 __device__ __forceinline__ bool bad_target(const LossArgs &a, int64_t i) {

@@ -249,7 +249,7 @@ __global__ __launch_bounds__(256) void k_amax(LossArgs a) {
 
 // counts and its loss has a gradient (one that is not a number is one)
 __device__ __forceinline__ bool kept(const LossArgs &a, int64_t i) {
-  return a.sv.slot[i] >= 0 && !(a.up[i] == 0.f);
+  return a.sv.slot[i] >= 0 && !(gradient_of(a, i) == 0.f);
 }
 
 // Positions that count (KEPT: and have a gradient) in each chunk, and (one block) in all chunks
@@ -744,7 +744,7 @@ __device__ __forceinline__ float block_max_factor(const LossArgs &a, int64_t i0,
   float m = 0.f;
 #pragma unroll 4
   for (int64_t i = i0 + tid; i < a.N; i += step) {
-    const float u = fabsf(a.up[i]);
+    const float u = fabsf(gradient_of(a, i));
     if (u < INFINITY && a.sv.slot[i] >= 0) m = fmaxf(m, u);
   }
 #pragma unroll
@@ -781,7 +781,7 @@ __global__ __launch_bounds__(256) void k_row_factors(LossArgs a) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < a.N; i += (int64_t)gridDim.x * 256) {
     const int slot = a.sv.slot[i];
     if (slot < 0) continue;
-    const float f = a.up[i] / cm;
+    const float f = gradient_of(a, i) / cm;
     int e = 0;
     if (scaled && fabsf(f) < INFINITY) {
       frexpf(f, &e);

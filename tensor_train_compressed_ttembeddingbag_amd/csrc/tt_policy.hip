@@ -18,6 +18,9 @@ namespace ttb {
 constexpr int64_t ONE_BLOCK = 2048;
 constexpr int SUM_BLOCK = 1024;  // positions per partial sum past that
 
+// pairs whose rows the last workgroup adds up (tickets go through one address at some 13 ns each)
+constexpr int64_t TICKETS = 256;
+
 struct PreferArgs {
   int64_t N, V, P, ignore;
   int kind, average, reduction;
@@ -27,6 +30,7 @@ struct PreferArgs {
   float *loss, *ratios;     // [P] or [1]; [2 P] or null
   double *rows;             // [P] (workspace)
   int32_t *status;
+  int *ticket;              // the last workgroup adds the rows up, or null
   // saved, or null
   int *seq;                 // [N] a position's sequence
   float *coef;              // [2 P] dL/dl of its positions, for a gradient of 1 of its pair's loss
@@ -62,34 +66,8 @@ __device__ __forceinline__ void block_sums(double &x, double &y, double (*s)[2])
   for (int w = 0; w < NT / 64; ++w) x += s[w][0], y += s[w][1];
 }
 
-// A pair per workgroup: half of it adds the preferred sequence up, half the other one.
-__global__ __launch_bounds__(512) void k_prefer(PreferArgs a) {
-  __shared__ double s_sum[8][2];
-  const int tid = threadIdx.x, half = tid >> 8, t = tid & 255;
-  const int64_t p = blockIdx.x, q = p + half * a.P;
-  int64_t i0 = a.off[q], i1 = a.off[q + 1];
-  if (i0 < 0 || i1 < i0 || i1 > a.N || (q == 0 && i0 != 0)) {
-    if (t == 0) set_status(a.status, TT_DEV_BAD_OFFSETS);
-    i0 = i1 = 0;
-  }
-  double sum = 0.0, n = 0.0;
-#pragma unroll 4
-  for (int64_t i = i0 + t; i < i1; i += 256) {
-    const float l = -a.nll[i], r = a.ref ? a.ref[i] : 0.f;
-    if (in_vocabulary(a.tgt[i], a.ignore, a.V)) {
-      sum += (double)l - (double)r;
-      n += 1.0;
-    }
-    if (a.seq) a.seq[i] = (int)q;
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    sum += __shfl_xor(sum, o);
-    n += __shfl_xor(n, o);
-  }
-  if ((tid & 63) == 0) s_sum[tid >> 6][0] = sum, s_sum[tid >> 6][1] = n;
-  __syncthreads();
-  if (tid != 0) return;
+// the loss and the slopes of pair p from its sequences' sums and counts, four of each
+__device__ __forceinline__ void prefer_pair(const PreferArgs &a, int64_t p, const double (*s_sum)[2]) {
   double h[2], share[2];
   for (int k = 0; k < 2; ++k) {
     double s = 0.0, c = 0.0;
@@ -121,7 +99,7 @@ __global__ __launch_bounds__(512) void k_prefer(PreferArgs a) {
       slope = a.beta * (y >= 0.0 ? e - small : small - (1.0 - e));
     }
   }
-  a.rows[p] = row;
+  __hip_atomic_store(&a.rows[p], row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (a.reduction == TT_REDUCE_NONE) a.loss[p] = (float)row;
   if (a.coef) {
     a.coef[p] = (float)(slope * share[0]);
@@ -129,28 +107,58 @@ __global__ __launch_bounds__(512) void k_prefer(PreferArgs a) {
   }
 }
 
-// loss: the sum of n rows, or of the partial sums of two columns, over the divisor
-__global__ __launch_bounds__(256) void k_prefer_sum(const double *rows, int64_t n, int mean, float *loss) {
-  __shared__ double s_sum[4][2];
+// the rows' sum in a fixed order
+template <int NT>
+__device__ __forceinline__ void add_rows(const PreferArgs &a) {
+  __shared__ double s_add[NT / 64][2];
   double x = 0.0, none = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 256) x += rows[i];
-  block_sums<256>(x, none, s_sum);
-  if (threadIdx.x == 0) loss[0] = (float)(mean ? x / (double)max(n, (int64_t)1) : x);
+  for (int64_t i = threadIdx.x; i < a.P; i += NT)
+    x += __hip_atomic_load(&a.rows[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  block_sums<NT>(x, none, s_add);
+  if (threadIdx.x == 0)
+    a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? x / (double)max(a.P, (int64_t)1) : x);
 }
 
-__global__ __launch_bounds__(256) void k_prefer_up(const int *seq, const float *coef, int64_t N, int64_t P,
-                                                   int reduction, const float *grad, float *up) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= N) return;
-  const int q = seq[i];
-  double u = 0.0;
-  if (q >= 0 && q < 2 * P) {  // (a position of no sequence does not count: any value will do)
-    const float g = reduction == TT_REDUCE_NONE ? grad[q % P] : grad[0];
-    u = -(double)coef[q] * (double)g;
-    if (reduction == TT_REDUCE_MEAN) u /= (double)P;
+// A pair per workgroup: half of it adds the preferred sequence up, half the other one.
+__global__ __launch_bounds__(512) void k_prefer(PreferArgs a) {
+  __shared__ double s_sum[8][2];
+  const int tid = threadIdx.x, half = tid >> 8, t = tid & 255;
+  const int64_t p = blockIdx.x, q = p + half * a.P;
+  int64_t i0 = a.off[q], i1 = a.off[q + 1];
+  if (i0 < 0 || i1 < i0 || i1 > a.N || (q == 0 && i0 != 0)) {
+    if (t == 0) set_status(a.status, TT_DEV_BAD_OFFSETS);
+    i0 = i1 = 0;
   }
-  up[i] = (float)u;
+  double sum = 0.0, n = 0.0;
+#pragma unroll 4
+  for (int64_t i = i0 + t; i < i1; i += 256) {
+    const float l = -a.nll[i], r = a.ref ? a.ref[i] : 0.f;
+    if (in_vocabulary(a.tgt[i], a.ignore, a.V)) {
+      sum += (double)l - (double)r;
+      n += 1.0;
+    }
+    if (a.seq) a.seq[i] = (int)q;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    sum += __shfl_xor(sum, o);
+    n += __shfl_xor(n, o);
+  }
+  if ((tid & 63) == 0) s_sum[tid >> 6][0] = sum, s_sum[tid >> 6][1] = n;
+  __syncthreads();
+  __shared__ int s_last;
+  if (tid == 0) prefer_pair(a, p, s_sum);
+  if (!a.ticket) return;
+  // A row is written through to memory by its own scope, and the ticket waits for it alone.
+  if (tid == 0) {
+    vmem_drain();
+    s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (s_last) add_rows<512>(a);
 }
+
+__global__ __launch_bounds__(256) void k_prefer_sum(PreferArgs a) { add_rows<256>(a); }
 
 struct PolicyRow {
   double loss, coef;
@@ -204,15 +212,6 @@ __global__ __launch_bounds__(256) void k_policy_sum(PolicyArgs a, int64_t blocks
   for (int64_t b = threadIdx.x; b < blocks; b += 256) sum += a.part[2 * b], n += a.part[2 * b + 1];
   block_sums<256>(sum, n, s_sum);
   if (threadIdx.x == 0) a.loss[0] = (float)(a.reduction == TT_REDUCE_MEAN ? sum / fmax(n, 1.0) : sum);
-}
-
-__global__ __launch_bounds__(256) void k_policy_up(const float *coef, const LossScalars *sc, int64_t N,
-                                                   int reduction, const float *grad, float *up) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= N) return;
-  double u = -(double)coef[i] * (double)(reduction == TT_REDUCE_NONE ? grad[i] : grad[0]);
-  if (reduction == TT_REDUCE_MEAN) u /= (double)max(sc->count, 1);
-  up[i] = (float)u;
 }
 
 // ---------------------------------------------------------------- host
@@ -275,10 +274,9 @@ static int64_t prefer_saved(LossArgs &a, PreferArgs &p, void *saved) {
 }
 static bool zero_slopes(const PreferArgs &p) { return p.kind == TT_PREFER_HINGE; }
 static bool zero_slopes(const PolicyArgs &p) { return p.kl == 0.0; }
-// what a backward has beside the cross entropy's: dL/dl, and the rows that are kept
+// what a backward has beside the cross entropy's: the rows that are kept
 template <class Args>
-static void backward_part(const LossArgs &a, const Args &p, Part &b, float *&up, Kept &kept) {
-  b.take(up, p.N);
+static void backward_part(const LossArgs &a, const Args &p, Part &b, Kept &kept) {
   if (keeps(a, zero_slopes(p))) b.off += kept_layout(a, b.base + b.off, kept);
 }
 template <class Args>
@@ -290,10 +288,10 @@ static hipError_t backward_from(LossArgs &a, const Args &p, const Kept &kept, hi
   return loss_backward(a, s);
 }
 
-static int64_t prefer_ws(LossArgs &a, PreferArgs &p, void *ws, int mode, float *&up, Kept &kept) {
+static int64_t prefer_ws(LossArgs &a, PreferArgs &p, void *ws, int mode, Kept &kept) {
   Part b = {(char *)ws, ws_layout(a, ws, mode)};
   if (mode == TT_LOSS_BACKWARD) {
-    backward_part(a, p, b, up, kept);
+    backward_part(a, p, b, kept);
   } else {
     b.take(a.loss, p.N);
     b.take(p.rows, p.P);
@@ -317,10 +315,10 @@ static int64_t policy_saved(LossArgs &a, PolicyArgs &p, void *saved) {
   b.take(p.coef, p.N);
   return b.off;
 }
-static int64_t policy_ws(LossArgs &a, PolicyArgs &p, void *ws, int mode, float *&up, Kept &kept) {
+static int64_t policy_ws(LossArgs &a, PolicyArgs &p, void *ws, int mode, Kept &kept) {
   Part b = {(char *)ws, ws_layout(a, ws, mode)};
   if (mode == TT_LOSS_BACKWARD) {
-    backward_part(a, p, b, up, kept);
+    backward_part(a, p, b, kept);
   } else {
     b.take(a.loss, p.N);
     b.take(p.part, 2 * ((p.N + SUM_BLOCK - 1) / SUM_BLOCK));
@@ -346,10 +344,9 @@ size_t tt_prefer_saved_size(const tt_prefer_desc *desc) {
 size_t tt_prefer_workspace_size(const tt_prefer_desc *desc, int mode) {
   LossArgs a;
   PreferArgs p;
-  float *up;
   Kept kept;
   if (mode < TT_LOSS_FORWARD || mode > TT_LOSS_ONLY) return 0;
-  return prefer_args(desc, nullptr, a, p) == TT_OK ? (size_t)prefer_ws(a, p, nullptr, mode, up, kept) : 0;
+  return prefer_args(desc, nullptr, a, p) == TT_OK ? (size_t)prefer_ws(a, p, nullptr, mode, kept) : 0;
 }
 
 int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void *weight,
@@ -358,7 +355,6 @@ int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void
                       size_t ws_bytes, int32_t *dev_status, void *stream) {
   LossArgs a;
   PreferArgs p;
-  float *up;
   Kept kept;
   const int rc = prefer_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
@@ -368,16 +364,17 @@ int tt_prefer_forward(const tt_prefer_desc *desc, const void *hidden, const void
   if (misaligned(weight, elem_size(a.dtype)) || misaligned(hidden, elem_size(a.dtype))) return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if (saved && (size_t)prefer_saved(a, p, saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)prefer_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, up, kept) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)prefer_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   a.hidden = hidden; a.tgt = targets; a.limit = offsets + 2 * p.P; a.status = dev_status;
   p.tgt = targets; p.off = offsets; p.ref = reference_logps; p.loss = loss; p.ratios = ratios;
   p.status = dev_status;
   if (p.N && loss_forward(a, s) != hipSuccess) return TT_EHIP;
+  // (k_pack has cleared the ticket, which a loss without a reduction does not use)
+  if (p.reduction != TT_REDUCE_NONE && p.N && !a.direct && p.P && p.P <= TICKETS) p.ticket = &a.sv.sc->ticket;
   if (p.P) tt_launch(K_ALIGN, k_prefer, dim3((unsigned)p.P), dim3(512), 0, s, p);
-  if (p.reduction != TT_REDUCE_NONE)
-    tt_launch(K_ALIGN, k_prefer_sum, dim3(1), dim3(256), 0, s, (const double *)p.rows, p.P,
-              p.reduction == TT_REDUCE_MEAN ? 1 : 0, loss);
+  if (p.reduction != TT_REDUCE_NONE && !p.ticket)
+    tt_launch(K_ALIGN, k_prefer_sum, dim3(1), dim3(256), 0, s, p);
   return hipGetLastError() == hipSuccess ? TT_OK : TT_EHIP;
 }
 
@@ -386,7 +383,6 @@ int tt_prefer_backward(const tt_prefer_desc *desc, const void *weight, const voi
                        void *ws, size_t ws_bytes, void *stream) {
   LossArgs a;
   PreferArgs p;
-  float *up;
   Kept kept;
   const int rc = prefer_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
@@ -397,13 +393,10 @@ int tt_prefer_backward(const tt_prefer_desc *desc, const void *weight, const voi
     return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if ((size_t)prefer_saved(a, p, (void *)saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)prefer_ws(a, p, ws, TT_LOSS_BACKWARD, up, kept) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)prefer_ws(a, p, ws, TT_LOSS_BACKWARD, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
-  if (p.N)
-    tt_launch(K_ALIGN, k_prefer_up, dim3((unsigned)((p.N + 255) / 256)), dim3(256), 0, s,
-              (const int *)p.seq, (const float *)p.coef, p.N, p.P, p.reduction, grad_loss, up);
-  if (hipGetLastError() != hipSuccess) return TT_EHIP;
-  a.up = up; a.dh = grad_hidden; a.dw = grad_weight;
+  a.coef = p.coef; a.seq = p.seq; a.pairs = p.P; a.of = p.reduction;
+  a.up = grad_loss; a.dh = grad_hidden; a.dw = grad_weight;
   return backward_from(a, p, kept, s) == hipSuccess ? TT_OK : TT_EHIP;
 }
 
@@ -416,10 +409,9 @@ size_t tt_policy_saved_size(const tt_policy_desc *desc) {
 size_t tt_policy_workspace_size(const tt_policy_desc *desc, int mode) {
   LossArgs a;
   PolicyArgs p;
-  float *up;
   Kept kept;
   if (mode < TT_LOSS_FORWARD || mode > TT_LOSS_ONLY) return 0;
-  return policy_args(desc, nullptr, a, p) == TT_OK ? (size_t)policy_ws(a, p, nullptr, mode, up, kept) : 0;
+  return policy_args(desc, nullptr, a, p) == TT_OK ? (size_t)policy_ws(a, p, nullptr, mode, kept) : 0;
 }
 
 int tt_policy_forward(const tt_policy_desc *desc, const void *hidden, const void *weight,
@@ -428,7 +420,6 @@ int tt_policy_forward(const tt_policy_desc *desc, const void *hidden, const void
                       size_t saved_bytes, void *ws, size_t ws_bytes, int32_t *dev_status, void *stream) {
   LossArgs a;
   PolicyArgs p;
-  float *up;
   Kept kept;
   const int rc = policy_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
@@ -438,7 +429,7 @@ int tt_policy_forward(const tt_policy_desc *desc, const void *hidden, const void
   if (misaligned(weight, elem_size(a.dtype)) || misaligned(hidden, elem_size(a.dtype))) return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if (saved && (size_t)policy_saved(a, p, saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)policy_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, up, kept) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)policy_ws(a, p, ws, saved ? TT_LOSS_FORWARD : TT_LOSS_ONLY, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   a.hidden = hidden; a.tgt = actions; a.status = dev_status;
   p.tgt = actions; p.adv = advantages; p.old = old_logps; p.ref = reference_logps;
@@ -460,7 +451,6 @@ int tt_policy_backward(const tt_policy_desc *desc, const void *weight, const voi
                        void *ws, size_t ws_bytes, void *stream) {
   LossArgs a;
   PolicyArgs p;
-  float *up;
   Kept kept;
   const int rc = policy_args(desc, weight, a, p);
   if (rc != TT_OK) return rc;
@@ -471,13 +461,10 @@ int tt_policy_backward(const tt_policy_desc *desc, const void *weight, const voi
     return TT_EINVAL;
   if (misaligned(saved, 256) || misaligned(ws, 256)) return TT_EWORKSPACE;
   if ((size_t)policy_saved(a, p, (void *)saved) > saved_bytes) return TT_EWORKSPACE;
-  if ((size_t)policy_ws(a, p, ws, TT_LOSS_BACKWARD, up, kept) > ws_bytes) return TT_EWORKSPACE;
+  if ((size_t)policy_ws(a, p, ws, TT_LOSS_BACKWARD, kept) > ws_bytes) return TT_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
-  if (p.N)
-    tt_launch(K_ALIGN, k_policy_up, dim3((unsigned)((p.N + 255) / 256)), dim3(256), 0, s,
-              (const float *)p.coef, (const LossScalars *)a.sv.sc, p.N, p.reduction, grad_loss, up);
-  if (hipGetLastError() != hipSuccess) return TT_EHIP;
-  a.up = up; a.dh = grad_hidden; a.dw = grad_weight;
+  a.coef = p.coef; a.of = p.reduction; a.all = a.sv.sc;
+  a.up = grad_loss; a.dh = grad_hidden; a.dw = grad_weight;
   return backward_from(a, p, kept, s) == hipSuccess ? TT_OK : TT_EHIP;
 }
 

@@ -72,7 +72,7 @@ def _forward(indices, weight, scale, padding_idx, dtype, dev_status):
     desc, ref, _ = _desc(n, v, d, stride, d, padding_idx,
                          abi.TT_DTYPE_I8 if int8 else abi._DTYPE[values.dtype],
                          abi._DTYPE[dtype], scale)
-    out = torch.empty(indices.shape + (d,), dtype=dtype, device=values.device)
+    out = values.new_empty(indices.shape + (d,), dtype=dtype)
     abi._launch("tt_embed_forward", values, ref, indices.data_ptr(), values.data_ptr(),
                 weight.scales.data_ptr() if int8 else None, out.data_ptr(), abi._ptr(dev_status))
     return out
@@ -87,9 +87,9 @@ def _gradient(grad_out, indices, v, d, scale, padding_idx, dtype, dev_status):
                          abi._DTYPE[g.dtype], scale)
     if not size:
         raise abi.TTError("tt_embed_workspace_size", -2)
-    dw = torch.empty((v, d), dtype=dtype, device=g.device)
+    dw = g.new_empty((v, d), dtype=dtype)
     # (256 bytes stand for none)
-    ws = torch.empty(size, dtype=torch.uint8, device=g.device) if size > 256 else None
+    ws = g.new_empty(size, dtype=torch.uint8) if size > 256 else None
     abi._launch("tt_embed_backward", g, ref, indices.data_ptr(), g.data_ptr(), dw.data_ptr(),
                 abi._ptr(ws), size, abi._ptr(dev_status))
     return dw

@@ -147,9 +147,9 @@ def int8_linear(hidden, weight: Int8Rows, *, dtype: Optional[torch.dtype] = None
             _plans.clear()
         plan = _plans[key] = (desc, ref, size)
     _, ref, size = plan
-    out = torch.empty(shape + (v,), dtype=dtype, device=rows.device)
+    out = rows.new_empty(shape + (v,), dtype=dtype)
     # (256 bytes stand for none)
-    ws = torch.empty(size, dtype=torch.uint8, device=rows.device) if size > 256 else None
+    ws = rows.new_empty(size, dtype=torch.uint8) if size > 256 else None
     abi._launch("tt_int8_linear", rows, ref, rows.data_ptr(),
                 hidden.scales.data_ptr() if given else None, weight.values.data_ptr(),
                 weight.scales.data_ptr(), out.data_ptr(), abi._ptr(ws), size)
