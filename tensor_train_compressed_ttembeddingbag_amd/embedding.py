@@ -20,6 +20,7 @@ from . import abi
 from .quant import Int8Rows
 
 _descs = {}
+_MAX_STRIDE = 1 << 32  # elements between rows: the library's limit
 
 
 def _desc(n, v, d, weight_stride, grad_stride, padding_idx, dtype, out_dtype, scale):
@@ -81,7 +82,7 @@ def _forward(indices, weight, scale, padding_idx, dtype, dev_status):
 def _gradient(grad_out, indices, v, d, scale, padding_idx, dtype, dev_status):
     n = indices.numel()
     g = grad_out if grad_out.dim() == 2 else grad_out.reshape(n, d)
-    if d > 1 and g.stride(1) != 1 or n > 1 and g.stride(0) < d:
+    if d > 1 and g.stride(1) != 1 or n > 1 and not d <= g.stride(0) <= _MAX_STRIDE:
         g = g.contiguous()
     _, ref, size = _desc(n, v, d, d, g.stride(0) if n > 1 else d, padding_idx, abi._DTYPE[dtype],
                          abi._DTYPE[g.dtype], scale)
@@ -147,7 +148,8 @@ def embedding(indices: torch.Tensor, weight, *, scale: float = 1.0,
     indices = _indices(indices, weight.device, dev_status)
     padding_idx = _padding(padding_idx, weight.shape[0])
     if not int8 and (weight.shape[1] > 1 and weight.stride(1) != 1
-                     or weight.shape[0] > 1 and weight.stride(0) < weight.shape[1]):
+                     or weight.shape[0] > 1
+                     and not weight.shape[1] <= weight.stride(0) <= _MAX_STRIDE):
         weight = weight.contiguous()
     if not int8 and weight.requires_grad and torch.is_grad_enabled():
         return _EmbeddingFunction.apply(indices, weight, scale, padding_idx, dtype, dev_status)

@@ -360,3 +360,11 @@ def test_repeated_backward():
     a, = torch.autograd.grad(out, w, up, retain_graph=True)
     b, = torch.autograd.grad(out, w, 2 * up)
     assert torch.equal(2 * a, b)
+
+
+def test_one_token_without_dimensions():
+    w = torch.randn(9, 20, device="cuda", generator=gen(1), requires_grad=True)
+    out = embedding(torch.tensor(4, device="cuda"), w, scale=2.0)
+    assert out.shape == (20,) and torch.equal(out, 2 * w[4])
+    out.sum().backward()
+    assert bool((w.grad[4] == 2).all()) and int((w.grad != 0).sum()) == 20

@@ -231,3 +231,17 @@ def test_arguments_are_refused():
         quantize_rows(torch.zeros(3, 0, device="cuda"))
     with pytest.raises(ValueError, match="scales"):
         Int8Rows(rows.values, rows.scales[:3])
+
+
+@pytest.mark.parametrize("n", [3, 4, 9, 16])
+@pytest.mark.parametrize("d", [5, 8, 100, 256, 1024])
+@pytest.mark.parametrize("v", [7, 1000, 33001])
+def test_few_tokens(n, d, v):
+    """Quantised and multiplied in one launch where they are few enough: the same bits as from values given."""
+    g = gen(n * d + v)
+    dtype, out = TYPES[(n + d) % 3], TYPES[(n + v) % 3]
+    x = torch.randn(n, 2 * d, device="cuda", generator=g).to(dtype)[:, d // 2:d // 2 + d]
+    rows = quantize_rows(torch.randn(v, d, device="cuda", generator=g))
+    got = int8_linear(x, rows, dtype=out)
+    assert torch.equal(got, int8_linear(quantize_rows(x), rows, dtype=out))
+    assert same(got, product(*quantised(x), rows.values.cpu().float(), rows.scales.cpu(), out))
