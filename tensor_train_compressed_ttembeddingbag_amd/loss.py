@@ -215,17 +215,17 @@ class _LogpPlan:
         self.fwd = size(self.ref, abi.TT_LOSS_FORWARD)
         self.bwd = size(self.ref, abi.TT_LOSS_BACKWARD)
         self.only = size(self.ref, abi.TT_LOSS_ONLY)
-        self.dtype, self.n, self.d, self.v = hidden.dtype, *hidden.shape, weight.shape[0]
+        (self.n, self.d), self.v = hidden.shape, weight.shape[0]
 
 
 def _logp_forward(plan, hidden, weight, inputs, shape, more_shape, dev_status, save):
     """(loss, the second output or None, saved or None)"""
-    dev = hidden.device
-    loss = torch.empty(shape, dtype=torch.float32, device=dev)
-    more = None if more_shape is None else torch.empty(more_shape, dtype=torch.float32, device=dev)
-    saved = _bytes(plan.saved, dev) if save else None
+    new = hidden.new_empty
+    loss = new(shape, dtype=torch.float32)
+    more = None if more_shape is None else new(more_shape, dtype=torch.float32)
+    saved = new(plan.saved, dtype=torch.uint8) if save else None
     size = plan.fwd if save else plan.only
-    ws = _bytes(size, dev)
+    ws = new(size, dtype=torch.uint8)
     abi._launch(plan.forward, hidden, plan.ref, hidden.data_ptr(), weight.data_ptr(),
                 *[abi._ptr(t) for t in inputs], loss.data_ptr(), abi._ptr(more), abi._ptr(saved),
                 plan.saved, ws.data_ptr(), size, abi._ptr(dev_status))
@@ -234,14 +234,14 @@ def _logp_forward(plan, hidden, weight, inputs, shape, more_shape, dev_status, s
 
 def _logp_backward(ctx, grad_loss, _):
     weight, saved = ctx.saved_tensors
-    plan, dev = ctx.plan, weight.device
+    plan, new = ctx.plan, weight.new_empty
     if grad_loss is None:
         return (None,) * 7
     grad_loss = grad_loss.contiguous()
     need_h, need_w = ctx.needs_input_grad[:2]
-    dh = torch.empty((plan.n, plan.d), dtype=plan.dtype, device=dev) if need_h else None
-    dw = torch.empty((plan.v, plan.d), dtype=plan.dtype, device=dev) if need_w else None
-    ws = _bytes(plan.bwd, dev)
+    dh = new((plan.n, plan.d)) if need_h else None
+    dw = new((plan.v, plan.d)) if need_w else None
+    ws = new(plan.bwd, dtype=torch.uint8)
     abi._launch(plan.backward, weight, plan.ref, weight.data_ptr(), saved.data_ptr(), plan.saved,
                 grad_loss.data_ptr(), abi._ptr(dh), abi._ptr(dw), ws.data_ptr(), plan.bwd)
     return dh, dw, None, None, None, None, None
@@ -320,6 +320,8 @@ def _constant(t, shape, name: str, broadcast: bool = False):
         except RuntimeError:
             raise ValueError("%s does not broadcast to the shape of hidden without its last "
                              "dimension" % name) from None
+    if t.dtype == torch.float32 and not t.requires_grad and t.is_contiguous():
+        return t
     return t.detach().float().contiguous()
 
 
