@@ -393,6 +393,11 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
   aim();
   constexpr int LPT = Feed<T::X, PC, PL, T::NT>::L + Feed<T::Y, QC, PL, T::NT>::L;
   typename E::acc4 acc[T::MI][T::NI];
+  // fp32 as it lies: 128 k are summed by themselves and then added, because every 4 k of one chain are
+  // rounded at the size of the whole sum (6 positions x 5392 x 1216, logits up to 14: log-probabilities of
+  // relative error 3.7e-7 in one chain, 0.9e-7 by 32 k, 0.8e-7 by 128; 64 x 32000 x 1024: 52.0, 56.7, 53.7 us)
+  constexpr bool APART = std::is_same<E, Fp32>::value;
+  typename E::acc4 some[APART ? T::MI : 1][APART ? T::NI : 1];
   typename E::v8 p[2][T::MI], q[2][T::NI];
   auto read_p = [&](int set, int buf) {
 #pragma unroll
@@ -408,7 +413,19 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-      for (int j = 0; j < T::NI; ++j) acc[i][j] = E::mfma(p[sp][i], q[sq][j], acc[i][j]);
+      for (int j = 0; j < T::NI; ++j) {
+        typename E::acc4 &c = *(APART ? &some[APART ? i : 0][APART ? j : 0] : &acc[i][j]);
+        c = E::mfma(p[sp][i], q[sq][j], c);
+      }
+  };
+  auto gather = [&]() {
+#pragma unroll
+    for (int i = 0; APART && i < T::MI; ++i)
+#pragma unroll
+      for (int j = 0; APART && j < T::NI; ++j) {
+        acc[i][j] += some[i][j];
+        some[i][j] = typename E::acc4{};
+      }
   };
   // fp32: lane group g holds k = 8 g + e of both operands, so element e of all four is one
   // product over four k.  The reads wait for their use here: both register sets beside the
@@ -453,7 +470,10 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-      for (int j = 0; j < T::NI; ++j) acc[i][j] = typename E::acc4{};
+      for (int j = 0; j < T::NI; ++j) {
+        acc[i][j] = typename E::acc4{};
+        if (APART) some[i][j] = typename E::acc4{};
+      }
     const int steps = now.nk;
     auto mend = [&](int b) {
       const int64_t k0 = now.k0 + (int64_t)(now.nk - 1) * (GK / PL);
@@ -492,6 +512,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
         } else {
           read_q(1, buf);
           read_p(1, buf);
+          if (APART && st > 0 && st % 4 == 0) gather();
           mul(0, 0);
           pace();
         }
@@ -512,6 +533,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmArgs &a, char *lds, Done do
         buf = next;
       }
     }
+    gather();
     done(now, acc, lds + T::STAGES * SB);
     id += gridDim.x;
     if (!walk.at(id, now)) break;

@@ -983,7 +983,7 @@ int64_t ws_layout(LossArgs &a, void *ws, int mode) {
     // 16-byte groups make up their rows (and a tile of them fits a descriptor)
     a.direct = a.N <= 64 && a.D % 8 == 0 && a.planes == 1 && a.hld <= MAX_STRIDE;
     // fp32 rows of the weight are read once that way, and four times where they are packed (64 x 32000 x
-    // 1024: 50 us of products in fp32, and 102 us of the tensors' range, packing and products)
+    // 1024: 52 us of products in fp32, and 102 us of the tensors' range, packing and products)
     if (a.few32 && a.planes == 2 && !a.k && a.N <= 64 && a.hld <= MAX_STRIDE / 2 && a.wld <= MAX_STRIDE / 2) {
       a.direct = a.f32 = 1;
       a.planes = 1;

@@ -221,6 +221,15 @@ static hipError_t pick(bool grad, int cfg, const LossArgs &a, const GemmArgs &g,
   return pick<E, PL, false>(grad, cfg, a, g, ep, s);
 }
 
+// fp32 as it lies: up to 64 positions, which gemm_shape gives these two
+template <bool MEND>
+static hipError_t few(GemmShape t, const LossArgs &a, const GemmArgs &g, const LogitsEpi &ep,
+                      hipStream_t s) {
+  if (t.by != 64) return hipErrorInvalidValue;
+  return t.bx == 128 ? go<Fp32, TileS, 1, false, MEND>(a, g, ep, s)
+                   : go<Fp32, TileT, 1, false, MEND>(a, g, ep, s);
+}
+
 hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, bool grad,
                          hipStream_t s) {
   LogitsEpi ep = {};
@@ -258,7 +267,7 @@ hipError_t launch_logits(const LossArgs &a, int64_t v0, int64_t nv, int tile0, b
     ep.v0 = v0 + r0;
     ep.nv = n;
     ep.G = a.G + r0 * 2;
-    if (a.f32) e = a.D % 4 ? pick<Fp32, 1, false, true>(t.cfg, a, g, ep, s) : pick<Fp32, 1, false, false>(t.cfg, a, g, ep, s);
+    if (a.f32) e = a.D % 4 ? few<true>(t, a, g, ep, s) : few<false>(t, a, g, ep, s);
     else if (a.dtype == TT_DTYPE_BF16) e = pick<Bf16, 1>(grad, t.cfg, a, g, ep, s);
     else if (a.dtype == TT_DTYPE_F16) e = pick<Fp16, 1>(grad, t.cfg, a, g, ep, s);
     else e = pick<Fp16, 2>(grad, t.cfg, a, g, ep, s);
