@@ -596,3 +596,20 @@ def test_changed_inputs_are_noticed():
         w.add_(1.0)
     with pytest.raises(RuntimeError, match="modified"):
         loss.backward()
+
+
+@pytest.mark.parametrize("d", [1, 4, 31, 127, 128, 129, 132, 256, 385, 1024, 4097])
+@pytest.mark.parametrize("n,v", [(3, 300), (64, 16500)])
+def test_few_positions_of_fp32(n, v, d):
+    """Without a gradient: 128 products are summed by themselves and the sums added, so a sum of d is
+    rounded at most 128 + d / 128 + 1 times at the size of what it holds, not d times."""
+    h, w, t, _ = make(n, v, d, "fp32", seed=d)
+    head = Head(h, w, t, "fp32", 1.0, torch.ones(n, dtype=torch.bool, device="cuda"))
+    A = (head.H.abs() @ head.W.abs().t().contiguous()).amax(1)
+    dz = (min(d, 128) + d // 128 + 1) * 2.0 ** -24 * A
+    z = head.H @ head.W.t().contiguous()
+    lse, zt = torch.logsumexp(z, 1), z.gather(1, t[:, None])[:, 0]
+    with torch.no_grad():
+        _, logps = L.linear_policy(h, w, t, torch.ones(1, device="cuda").expand(n), return_logps=True)
+    err = (logps.double() - head.l).abs()
+    assert bool((err <= 2 * dz + 2.0 ** -21 * (1 + lse.abs() + zt.abs())).all())
