@@ -325,6 +325,20 @@ def _no_dual(what: str, *tensors: torch.Tensor):
                 raise NotImplementedError("%s has no forward-mode derivative" % what)
 
 
+def _number(x, name: str) -> float:
+    """x as a float of Python's.  What is kept per kind of call is found by its value: a tensor would be
+    found by its identity, and stay what it was when it is changed in place."""
+    if type(x) is float:
+        return x
+    if isinstance(x, torch.Tensor):
+        _no_dual(name, x)
+        if x.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("%s gets no gradient: detach it or call under torch.no_grad()" % name)
+    if not hasattr(x, "__float__") and not hasattr(x, "__index__"):
+        raise TypeError("%s must be a number, got %s" % (name, type(x).__name__))
+    return float(x)
+
+
 def _check(fn: str, rc: int):
     if rc != TT_OK:
         raise TTError(fn, rc)

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 from typing import Optional
 
 import torch
@@ -43,6 +44,7 @@ def _desc(n, v, d, weight_stride, grad_stride, padding_idx, dtype, out_dtype, sc
 def _padding(padding_idx: Optional[int], v: int) -> int:
     if padding_idx is None:
         return -1
+    padding_idx = operator.index(padding_idx)
     if not -v <= padding_idx < v:
         raise ValueError("padding_idx must be within the table's %d rows" % v)
     return padding_idx % v
@@ -128,7 +130,8 @@ def embedding(indices: torch.Tensor, weight, *, scale: float = 1.0,
     dtype (the weight's own; float32 from ``Int8Rows``).  The row padding_idx is looked up like the
     others but gets no gradient.  An index outside [0, V) gives a row of zeros, has no gradient and
     sets ``TT_DEV_BAD_INDEX`` in dev_status (an int32 GPU tensor of one element) if that is
-    given.  The gradient is dense, of the weight's dtype, summed in float32 in a fixed order."""
+    given.  The gradient is dense, of the weight's dtype, summed in float32 in a fixed order.
+    scale is a constant (a tensor of one element is read at the call)."""
     int8 = isinstance(weight, Int8Rows)
     if not int8:
         if not isinstance(weight, torch.Tensor):
@@ -145,6 +148,7 @@ def embedding(indices: torch.Tensor, weight, *, scale: float = 1.0,
         dtype = torch.float32 if int8 else weight.dtype
     elif dtype not in abi._DTYPE:
         raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
+    scale = abi._number(scale, "scale")
     indices = _indices(indices, weight.device, dev_status)
     padding_idx = _padding(padding_idx, weight.shape[0])
     if not int8 and (weight.shape[1] > 1 and weight.stride(1) != 1
@@ -175,6 +179,7 @@ def embedding_gradient(grad_out: torch.Tensor, indices: torch.Tensor, num_rows: 
     indices = _indices(indices, grad_out.device, dev_status)
     if grad_out.dim() < 1 or grad_out.shape[:-1] != indices.shape or grad_out.shape[-1] < 1:
         raise ValueError("grad_out must have the shape of indices and a last dimension")
+    num_rows, scale = operator.index(num_rows), abi._number(scale, "scale")
     if num_rows < 1:
         raise ValueError("num_rows must be positive")
     return _gradient(grad_out, indices, num_rows, grad_out.shape[-1], scale,

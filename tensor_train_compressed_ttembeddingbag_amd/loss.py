@@ -13,6 +13,7 @@ Argument marshalling only; the computation runs in libttbag (``tt_loss_forward``
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional
 
 import torch
@@ -158,6 +159,8 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: to
         raise ValueError("targets must have the shape of hidden without its last dimension")
     if targets.dtype == torch.int32:
         targets = targets.to(torch.int64)
+    ignore_index = int(ignore_index)
+    label_smoothing = abi._number(label_smoothing, "label_smoothing")
     if not 0.0 <= label_smoothing <= 1.0:
         raise ValueError("label_smoothing must be in [0, 1]")
     return _loss(hidden, weight, targets.contiguous(), None, targets.shape, 0, reduction,
@@ -187,6 +190,7 @@ def linear_distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_logi
     k = teacher_indices.shape[-1]
     if k < 1:
         raise ValueError("at least one teacher entry per position is needed")
+    temperature = abi._number(temperature, "temperature")
     if not 0.0 < ctypes.c_float(temperature).value < float("inf"):  # the library's type
         raise ValueError("temperature must be positive and finite in float32")
     if teacher_indices.dtype == torch.int32:
@@ -358,6 +362,9 @@ def linear_preference(hidden: torch.Tensor, weight: torch.Tensor, targets: torch
         raise ValueError("offsets must have 2 P + 1 entries")
     if kind not in _KIND:
         raise ValueError("kind must be one of %s" % sorted(_KIND))
+    ignore_index, beta = operator.index(ignore_index), abi._number(beta, "beta")
+    label_smoothing = abi._number(label_smoothing, "label_smoothing")
+    margin = abi._number(margin, "margin")
     if not 0.0 < beta < float("inf"):
         raise ValueError("beta must be positive and finite")
     if not 0.0 <= label_smoothing <= 1.0 or label_smoothing and kind != "sigmoid":
@@ -404,6 +411,10 @@ def linear_policy(hidden: torch.Tensor, weight: torch.Tensor, actions: torch.Ten
     if hidden.dim() < 1 or actions.shape != hidden.shape[:-1]:
         raise ValueError("actions must have the shape of hidden without its last dimension")
     actions = _integers(actions, "actions")
+    ignore_index = operator.index(ignore_index)
+    clip_low, clip_high = abi._number(clip_low, "clip_low"), abi._number(clip_high, "clip_high")
+    kl_coef = abi._number(kl_coef, "kl_coef")
+    temperature = abi._number(temperature, "temperature")
     if not clip_low >= 0.0 or not clip_high >= 0.0:
         raise ValueError("clip_low and clip_high must not be negative")
     if not 0.0 <= kl_coef < float("inf"):
