@@ -165,9 +165,14 @@ def embedding_gradient(grad_out: torch.Tensor, indices: torch.Tensor, num_rows: 
                        dtype: Optional[torch.dtype] = None,
                        dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient [num_rows, D] of the weight of ``embedding(indices, weight, ...)`` from
-    grad_out [..., D], in dtype (grad_out's own if not given)."""
+    grad_out [..., D], in dtype (grad_out's own if not given).  It has no gradient of its own: a
+    grad_out that requires one is refused while gradients are enabled."""
     if not isinstance(grad_out, torch.Tensor):
         raise TypeError("grad_out must be a torch.Tensor")
+    abi._no_dual("embedding_gradient", grad_out)
+    if grad_out.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("embedding_gradient has no gradient: detach grad_out or call it under "
+                           "torch.no_grad()")
     if grad_out.dtype not in abi._DTYPE:
         raise TypeError("grad_out must be float32, bfloat16 or float16, got %s" % grad_out.dtype)
     if dtype is None:
