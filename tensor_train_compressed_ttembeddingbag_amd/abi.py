@@ -309,6 +309,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 def _launch(name: str, like: torch.Tensor, *args):
     """The entry point `name` with these arguments, then the current stream of the device that holds
     `like`; a kernel is launched on a stream of the current device."""
+    _no_proxies(name)
     if like.get_device() == _current_device():
         rc = getattr(lib(), name)(*args, _stream(None, like))
     else:
@@ -323,6 +324,22 @@ def _no_dual(what: str, *tensors: torch.Tensor):
         for t in tensors:
             if forward_ad.unpack_dual(t).tangent is not None:
                 raise NotImplementedError("%s has no forward-mode derivative" % what)
+
+
+_proxy_mode = torch._C._TorchDispatchModeKey.PROXY
+
+
+def _no_proxies(what: str):
+    """Refuses to run under torch.fx's make_fx, which records the allocations of a call and not its kernels."""
+    if torch._C._len_torch_dispatch_stack() and torch._C._get_dispatch_mode(_proxy_mode) is not None:
+        raise RuntimeError("%s cannot be traced: its kernels are no torch operations" % what)
+
+
+def _no_trace(what: str):
+    """The same under torch.jit.trace."""
+    _no_proxies(what)
+    if torch._C._is_tracing():
+        raise RuntimeError("%s cannot be traced: its kernels are no torch operations" % what)
 
 
 def _number(x, name: str) -> float:

@@ -133,9 +133,12 @@ def embedding(indices: torch.Tensor, weight, *, scale: float = 1.0,
     given.  The gradient is dense, of the weight's dtype, summed in float32 in a fixed order.
     scale is a constant (a tensor of one element is read at the call)."""
     int8 = isinstance(weight, Int8Rows)
+    if not int8 and not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor or an Int8Rows")
+    traced = torch._C._is_tracing()
+    if int8 or not traced:
+        abi._no_trace("embedding")
     if not int8:
-        if not isinstance(weight, torch.Tensor):
-            raise TypeError("weight must be a torch.Tensor or an Int8Rows")
         abi._no_dual("embedding", weight)
         if weight.dtype not in abi._DTYPE:
             raise TypeError("weight must be float32, bfloat16, float16 or an Int8Rows, got %s"
@@ -155,7 +158,8 @@ def embedding(indices: torch.Tensor, weight, *, scale: float = 1.0,
                      or weight.shape[0] > 1
                      and not weight.shape[1] <= weight.stride(0) <= _MAX_STRIDE):
         weight = weight.contiguous()
-    if not int8 and weight.requires_grad and torch.is_grad_enabled():
+    # (torch.jit.trace records an autograd function as what it is)
+    if traced or not int8 and weight.requires_grad and torch.is_grad_enabled():
         return _EmbeddingFunction.apply(indices, weight, scale, padding_idx, dtype, dev_status)
     return _forward(indices, weight, scale, padding_idx, dtype, dev_status)
 
@@ -169,6 +173,7 @@ def embedding_gradient(grad_out: torch.Tensor, indices: torch.Tensor, num_rows: 
     grad_out that requires one is refused while gradients are enabled."""
     if not isinstance(grad_out, torch.Tensor):
         raise TypeError("grad_out must be a torch.Tensor")
+    abi._no_trace("embedding_gradient")
     abi._no_dual("embedding_gradient", grad_out)
     if grad_out.requires_grad and torch.is_grad_enabled():
         raise RuntimeError("embedding_gradient has no gradient: detach grad_out or call it under "

@@ -70,6 +70,7 @@ def _backward(ctx, grad_loss):
     dh = torch.empty((plan.n, plan.d), dtype=plan.dtype, device=dev) if need_h else None
     dw = torch.empty((plan.v, plan.d), dtype=plan.dtype, device=dev) if need_w else None
     ws = _bytes(plan.bwd, dev)
+    abi._no_proxies("tt_loss_backward")
     rc = abi.lib().tt_loss_backward(
         plan.ref, saved.data_ptr(), weight.data_ptr(), saved.data_ptr(), plan.saved,
         grad_loss.data_ptr(), dh.data_ptr() if need_h else None,
@@ -112,6 +113,7 @@ def _rows(t: torch.Tensor, far: bool) -> torch.Tensor:
 
 
 def _loss(hidden, weight, targets, teacher_logits, shape, k, reduction, dev_status, **kw):
+    abi._no_trace("a vocabulary-head loss")  # (its autograd function too: it is given a plan for these sizes)
     if forward_ad._current_level >= 0:  # (unpack_dual by itself is 3 % of a small loss)
         for t in (hidden, weight):
             if forward_ad.unpack_dual(t).tangent is not None:
@@ -275,7 +277,9 @@ class _LogpFunction(torch.autograd.Function):
 
 def _logp_loss(name, hidden, weight, inputs, shape, more_shape, reduction, dev_status, make, key):
     """key: what make(desc of the product) depends on beside hidden and weight."""
-    abi._no_dual("linear_%s" % ("preference" if name == "prefer" else name), hidden, weight)
+    what = "linear_%s" % ("preference" if name == "prefer" else name)
+    abi._no_trace(what)  # (as the losses above)
+    abi._no_dual(what, hidden, weight)
     hidden, weight = _rows(hidden, True), _rows(weight, False)
     key = (name, hidden.shape, hidden.stride(), weight.shape, weight.stride(), hidden.dtype,
            weight.dtype, hidden.device, weight.device, reduction, *key)

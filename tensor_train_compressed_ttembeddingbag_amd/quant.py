@@ -92,6 +92,7 @@ def quantize_rows(x: torch.Tensor) -> Int8Rows:
 
     A row with a value that is not finite gets the scale NaN; one whose scale would be below the
     normal numbers becomes zeros.  x gets no gradient."""
+    abi._no_trace("quantize_rows")
     if isinstance(x, torch.Tensor) and (x.dim() != 2 or x.shape[0] < 1):
         raise ValueError("x must have two dimensions and a row")
     x = _float_rows(x, "x")
@@ -113,6 +114,7 @@ def int8_linear(hidden, weight: Int8Rows, *, dtype: Optional[torch.dtype] = None
     exactly and scaled.  In dtype: hidden's own, float32 from an ``Int8Rows``.
 
     There is no gradient: a hidden that requires one is refused while gradients are enabled."""
+    abi._no_trace("int8_linear")
     if not isinstance(weight, Int8Rows):
         raise TypeError("weight must be an Int8Rows")
     given = isinstance(hidden, Int8Rows)
