@@ -300,13 +300,25 @@ __global__ __launch_bounds__(256) void k_int8_few(FewArgs a) {
 }
 
 // ---------------------------------------------------------------- host
+// A launch has less than 2^32 threads: rows past what these workgroups take have launches of their own.  (A loop
+// over rows in the kernel: 131072 x 4096 bf16 479 -> 494 us.)
+constexpr int64_t MOST_BLOCKS = 1 << 20;
 template <class S, bool NARROW>
-static void go_quantize(const QuantArgs &a, hipStream_t s) {
+static void go_quantize(const QuantArgs &all, hipStream_t s) {
   // a wave a row where it holds one in registers, or where rows are many
-  if (a.d <= 1024 || (a.d <= 2048 && a.n >= 1024))
-    tt_launch(K_INT8_QUANT, k_quantize<S, 64, NARROW>, dim3((unsigned)((a.n + 3) / 4)), dim3(256), 0, s, a);
-  else
-    tt_launch(K_INT8_QUANT, k_quantize<S, 256, NARROW>, dim3((unsigned)a.n), dim3(256), 0, s, a);
+  const bool wave = all.d <= 1024 || (all.d <= 2048 && all.n >= 1024);
+  const int64_t most = wave ? 4 * MOST_BLOCKS : MOST_BLOCKS;
+  for (int64_t r = 0; r < all.n; r += most) {
+    QuantArgs a = all;
+    a.n = std::min(all.n - r, most);
+    a.x = (const S *)all.x + r * all.ld;
+    a.q += r * all.pitch;
+    a.s += r;
+    if (wave)
+      tt_launch(K_INT8_QUANT, k_quantize<S, 64, NARROW>, dim3((unsigned)((a.n + 3) / 4)), dim3(256), 0, s, a);
+    else
+      tt_launch(K_INT8_QUANT, k_quantize<S, 256, NARROW>, dim3((unsigned)a.n), dim3(256), 0, s, a);
+  }
 }
 template <class S>
 static void go_quantize(const QuantArgs &a, hipStream_t s) {
