@@ -524,7 +524,7 @@ typedef struct tt_prefer_desc {
     int64_t n, v, d;                       /* positions, vocabulary, width              */
     int64_t hidden_stride, weight_stride;  /* elements between rows, >= d               */
     int64_t ignore_index;
-    int64_t pairs;                         /* at most 2^23                              */
+    int64_t pairs;                         /* less than 2^23                            */
     double beta, label_smoothing, margin;  /* > 0; in [0, 1], sigmoid; not with square   */
     int32_t dtype, reduction, kind;        /* TT_DTYPE_*, TT_REDUCE_*, TT_PREFER_*      */
     int32_t average;                       /* 0: h is a sum, else a mean                */

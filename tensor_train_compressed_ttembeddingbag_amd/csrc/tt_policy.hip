@@ -259,7 +259,7 @@ static int prefer_args(const tt_prefer_desc *d, const void *weight, LossArgs &a,
   if (!(d->label_smoothing >= 0.0 && d->label_smoothing <= 1.0)) return TT_EINVAL;
   if (d->label_smoothing != 0.0 && d->kind != TT_PREFER_SIGMOID) return TT_EINVAL;
   if (d->margin != 0.0 && d->kind == TT_PREFER_SQUARE) return TT_EINVAL;
-  if (d->pairs > (1 << 23)) return TT_ESHAPE;
+  if (d->pairs >= (1 << 23)) return TT_ESHAPE;  // a launch has less than 2^32 threads, 512 of them a pair
   p = {};
   p.N = d->n; p.V = d->v; p.P = d->pairs; p.ignore = d->ignore_index;
   p.kind = d->kind; p.average = d->average != 0; p.reduction = d->reduction;

@@ -1,0 +1,21 @@
+"""Calls that would need 2^32 threads or more in a launch, which goes out with what is left of their number modulo
+2^32, are refused; the largest that fit are not.  (A workspace that is one byte short stops those that pass
+before any device work.)"""
+import ctypes
+
+from tensor_train_compressed_ttembeddingbag_amd import abi
+
+FAKE = 0x10000  # 256-byte aligned, never dereferenced
+BIG = 1 << 62
+
+
+def test_pairs():
+    lib = abi.lib()
+    for pairs, fits in ((1 << 23, False), ((1 << 23) - 1, True)):
+        d = abi.TTPreferDesc(16, 100, 64, 64, 64, -100, pairs, 0.1, 0.0, 0.0, abi.TT_DTYPE_BF16,
+                             abi.TT_REDUCE_MEAN, abi.TT_PREFER_SIGMOID, 0)
+        r = ctypes.byref(d)
+        saved, size = lib.tt_prefer_saved_size(r), lib.tt_prefer_workspace_size(r, abi.TT_LOSS_FORWARD)
+        assert (saved > 0) == fits and (size > 0) == fits
+        assert lib.tt_prefer_forward(r, *[FAKE] * 8, BIG, FAKE, size - 1 if fits else BIG, None,
+                                     None) == (-3 if fits else -2)
