@@ -578,7 +578,9 @@ int tt_policy_backward(const tt_policy_desc *desc, const void *weight, const voi
  * values[r] row_scales[r], rows a multiple of 16 bytes apart from a multiple of 16 on; no gradient.
  * The calls enqueue kernels only and may be captured into a HIP graph.  The result does not
  * depend on the order of atomics.
- * Limits (TT_ESHAPE): n <= 2^28, v <= 2^30, d <= 2^20, strides <= 2^32. */
+ * Limits (TT_ESHAPE): n <= 2^28, v <= 2^30, d <= 2^20, strides <= 2^32.  The
+ * gradient is also refused where it needs 2^24 workgroups, which it never does as long as
+ * (ceil(v / 64) + ceil(n / 64)) ceil(d / 512) < 2^24 - 2^16. */
 typedef struct tt_embed_desc {
     int64_t n, v, d;                       /* tokens, rows of the table, width              */
     int64_t weight_stride, grad_stride;    /* elements between rows, >= d                   */

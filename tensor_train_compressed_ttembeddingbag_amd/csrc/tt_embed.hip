@@ -739,6 +739,13 @@ static int64_t elem_size(int dtype) {
 static bool direct(const EmbedArgs &a) { return a.n <= LIST; }
 static bool searches(const EmbedArgs &a) { return !direct(a) && a.n <= SEARCH_T_MAX; }
 
+// A launch has less than 2^32 threads.
+static bool launches(const EmbedArgs &a) {
+  const int64_t blocks = (a.v + a.rows - 1) / a.rows * a.chunks;
+  const int64_t longs = direct(a) ? 0 : (a.n + PIECE_T - 1) / PIECE_T * a.long_chunks;
+  return blocks + longs < 1 << 24;
+}
+
 static int embed_args(const tt_embed_desc *d, EmbedArgs &a) {
   if (!d) return TT_EINVAL;
   if (d->n < 0 || d->v < 1 || d->d < 1) return TT_EINVAL;
@@ -920,7 +927,7 @@ int tt_embed_forward(const tt_embed_desc *desc, const int64_t *indices, const vo
 
 size_t tt_embed_workspace_size(const tt_embed_desc *desc) {
   EmbedArgs a;
-  if (embed_args(desc, a) != TT_OK || desc->dtype == TT_DTYPE_I8) return 0;
+  if (embed_args(desc, a) != TT_OK || desc->dtype == TT_DTYPE_I8 || !launches(a)) return 0;
   return (size_t)embed_ws(a, nullptr).bytes;
 }
 
@@ -931,6 +938,7 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
   const int rc = embed_args(desc, a);
   if (rc != TT_OK) return rc;
   if (desc->dtype == TT_DTYPE_I8) return TT_EINVAL;
+  if (!launches(a)) return TT_ESHAPE;
   if (!grad_weight || (!ws && !direct(a)) || (a.n && (!indices || !grad_out))) return TT_EINVAL;
   if ((uintptr_t)grad_out % elem_size(desc->out_dtype) ||
       (uintptr_t)grad_weight % elem_size(desc->dtype))
@@ -938,7 +946,6 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
   if ((uintptr_t)ws % 256) return TT_EWORKSPACE;
   const EmbedWs w = embed_ws(a, ws);
   if ((size_t)w.bytes > ws_bytes) return TT_EWORKSPACE;
-  if ((a.v + a.rows - 1) / a.rows * a.chunks + (a.n / PIECE_T + 1) * a.long_chunks > 0x7fffffffll) return TT_ESHAPE;
   a.idx = indices; a.w = grad_out; a.out = grad_weight; a.status = dev_status;
   a.part = w.part; a.first = w.first;
   hipStream_t s = (hipStream_t)stream;

@@ -19,3 +19,16 @@ def test_pairs():
         assert (saved > 0) == fits and (size > 0) == fits
         assert lib.tt_prefer_forward(r, *[FAKE] * 8, BIG, FAKE, size - 1 if fits else BIG, None,
                                      None) == (-3 if fits else -2)
+
+
+def test_rows_of_a_table():
+    lib = abi.lib()
+    for n, v, d, fits in ((10, 1 << 30, 1, False), (10, (1 << 30) - 64, 1, True), (10, (1 << 30) - 64, 513, False),
+                          (1 << 28, 3 << 28, 8, False), (1 << 28, (3 << 28) - 64, 8, True),
+                          (1 << 16, (1 << 30) - (1 << 22) - (1 << 16), 512, True)):
+        desc = abi.TTEmbedDesc(n, v, d, d, d, -1, abi.TT_DTYPE_BF16, abi.TT_DTYPE_BF16, 1.0)
+        r = ctypes.byref(desc)
+        size = lib.tt_embed_workspace_size(r)
+        assert (size > 0) == fits, (n, v, d)
+        assert lib.tt_embed_backward(r, FAKE, FAKE, FAKE, FAKE, size - 1 if fits else BIG, None,
+                                     None) == (-3 if fits else -2)
