@@ -613,8 +613,8 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
  * weight_pitch (hidden_stride) bytes apart, a multiple of 16, whose memory reaches to the next
  * multiple of 16 behind d, with any values there.  The sums are exact, scaled in fp32 and rounded
  * once.  The calls enqueue kernels only and may be captured into a HIP graph.
- * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, n v <= 2^40, d <= 2^17, pitches <= 2^22, strides <= 2^32
- * (quantize: n <= 2^30, d <= 2^20). */
+ * Limits (TT_ESHAPE): n <= 2^23, v <= 2^30, n v <= 2^40, d <= 2^17 (less than that where hidden is given in
+ * 8 bits), pitches <= 2^22, strides <= 2^32 (quantize: n <= 2^30, d <= 2^20). */
 typedef struct tt_int8_desc {
     int64_t n, v, d;                      /* tokens, rows of the table, width              */
     int64_t hidden_stride, weight_pitch;  /* elements; bytes                               */

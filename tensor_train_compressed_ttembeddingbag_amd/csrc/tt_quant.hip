@@ -399,7 +399,7 @@ static int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 static int64_t elem_size(int dtype) {
   return dtype == TT_DTYPE_F32 ? 4 : dtype == TT_DTYPE_I8 ? 1 : 2;
 }
-constexpr int64_t MAX_INT8_D = 1 << 17;  // 127^2 2^17 < 2^31
+constexpr int64_t MAX_INT8_D = 1 << 17;  // 127 128 2^17 < 2^31: a token that is quantised has no -128
 
 static int int8_args(const tt_int8_desc *d, Int8Args &a) {
   if (!d) return TT_EINVAL;
@@ -412,6 +412,8 @@ static int int8_args(const tt_int8_desc *d, Int8Args &a) {
   if (d->hidden_stride < d->d || a.wpitch < a.pitch || a.wpitch % 16) return TT_EINVAL;
   if (d->dtype == TT_DTYPE_I8 && (d->hidden_stride < a.pitch || d->hidden_stride % 16)) return TT_EINVAL;
   if (a.n > (1 << 23) || a.v > (1 << 30) || a.d > MAX_INT8_D || a.n * a.v > (1ll << 40)) return TT_ESHAPE;
+  // one that is given may have, as its row: 128^2 2^17 = 2^31
+  if (d->dtype == TT_DTYPE_I8 && a.d == MAX_INT8_D) return TT_ESHAPE;
   // a tile's rows inside one buffer descriptor
   if (a.wpitch > (1 << 22) || (d->dtype == TT_DTYPE_I8 && d->hidden_stride > (1 << 22)) ||
       d->hidden_stride > (1ll << 32))

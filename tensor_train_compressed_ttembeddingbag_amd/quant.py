@@ -111,7 +111,7 @@ _plans = {}
 def int8_linear(hidden, weight: Int8Rows, *, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """``hidden @ weight.T`` as [..., V], both in 8-bit integers: hidden [..., D] is quantised with a
     scale for each token as by ``quantize_rows`` (or is an ``Int8Rows``), the products are summed
-    exactly and scaled.  In dtype: hidden's own, float32 from an ``Int8Rows``.
+    exactly and scaled; D is at most 2^17, and less than that where hidden is an ``Int8Rows``.  In dtype: hidden's own, float32 from an ``Int8Rows``.
 
     There is no gradient: a hidden that requires one is refused while gradients are enabled."""
     abi._no_trace("int8_linear")
