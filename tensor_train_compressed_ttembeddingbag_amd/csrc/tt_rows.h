@@ -5,9 +5,10 @@
 
 namespace ttb {
 
-// Eight elements of a row, on an element's boundary (int8: on a group's).  A row's last group
-// takes its last eight, whatever its width: two lanes then work the same columns out from the
-// same values in the same order and store the same bits, and no load hides behind a branch.
+// Eight elements of a row, on an element's boundary (int8 too: a row's last group may start on any
+// byte).  A row's last group takes its last eight, whatever its width: two lanes then work the same
+// columns out from the same values in the same order and store the same bits, and no load hides
+// behind a branch.
 // Rows narrower than eight are a variant of their own (NARROW).
 template <class T>
 struct Eight {
@@ -38,7 +39,7 @@ __device__ __forceinline__ void put8(T *p, const Eight<T> &r, int64_t d) {
       if (e < d) p[e] = r.x[e];
   } else {
     typedef int words __attribute__((ext_vector_type(sizeof(Eight<T>) / 4)));
-    struct __attribute__((packed, aligned(2))) any { words v; };
+    struct __attribute__((packed, aligned(sizeof(T) < 2 ? 1 : 2))) any { words v; };
     ((any *)p)->v = __builtin_bit_cast(words, r);
   }
 }
