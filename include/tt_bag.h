@@ -592,8 +592,8 @@ typedef struct tt_embed_desc {
 int tt_embed_forward(const tt_embed_desc *desc, const int64_t *indices, const void *weight,
                      const float *row_scales, void *out, int32_t *dev_status, void *stream);
 /* workspace of tt_embed_backward (256-byte aligned): up to 1024 tokens none (256, and NULL will do); past that at most
- * 17 bytes a token, the fp32 sums of one row in 64 tokens and a byte for every row of the
- * table; 0: the descriptor is rejected */
+ * 20 bytes a token (17 past 131072), the fp32 sums of one row in 64 tokens, a byte for every row of the table and
+ * 10 KiB; 0: the descriptor is rejected */
 size_t tt_embed_workspace_size(const tt_embed_desc *desc);
 int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const void *grad_out,
                       void *grad_weight, void *ws, size_t ws_bytes, int32_t *dev_status,
