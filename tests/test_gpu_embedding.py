@@ -63,8 +63,9 @@ def tokens(n, v, g, hot=0.1):
     return i
 
 
-# lengths around the kernels' own borders (1024 tokens found without a sort, 8192 sorted by one
-# workgroup, tiles of 4096), tables of one, two and three digits, odd widths
+# lengths around the kernels' own borders (1024 tokens found without a sort, 8192 sorted by counting, tiles
+# of 1024 behind that; whole pieces of long runs past 32768 tokens: test_gpu_embedding_many.py), tables of one,
+# two and three digits, odd widths
 SIZES = [(0, 7, 5), (1, 1, 1), (1, 5, 3), (2, 1000, 8), (333, 1007, 515), (1023, 50, 64),
          (1024, 3, 7), (1025, 50, 64), (1500, 200003, 9), (4096, 1000, 130), (8192, 1023, 33),
          (8193, 1024, 16), (30000, 70001, 24), (9000, (1 << 20) + 5, 2), (12289, 31, 520),
