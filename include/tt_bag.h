@@ -604,7 +604,8 @@ int tt_embed_backward(const tt_embed_desc *desc, const int64_t *indices, const v
  * of the elements) as int8 values [n][pitch] (pitch a multiple of 16 >= d, from a multiple of 16 on;
  * bytes from d on are cleared) with a scale each:
  *   scales[i] = max |x_i| / 127 (fp32),  values[i][k] = x_ik / scales[i] rounded to the nearest, ties
- *   to even, within -127 .. 127.
+ *   to even, within -127 .. 127.  (Half of a row's largest is a tie, 63.5, of which the rounded scale may
+ *   leave a quotient on either side.)
  * A row with a value that is not finite gets the scale NaN and zeros; one whose scale would be below
  * 2^-126 the scale 0 and zeros.
  * tt_int8_linear: out[i][r] = (sum_k q_ik weight[r][k]) s_i weight_scales[r], contiguous [n][v] of

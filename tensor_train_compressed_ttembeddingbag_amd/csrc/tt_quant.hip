@@ -420,8 +420,12 @@ static int int8_args(const tt_int8_desc *d, Int8Args &a) {
     return TT_ESHAPE;
   return TT_OK;
 }
-// Tokens that are quantised in the product's own launch.  A larger table is read faster by the tiles (1 x 131072 x
-// 4096: 131 us and 111; 4 x 50000 x 2048: 29 and 23).
+// Tokens that are quantised in the product's own launch.  us of this launch and of the two with the tiles, tables
+// that are not in a cache, without the host: 1 x 8000 x 1024 7.7 and 10.9, 1 or 4 x 32000 x 1024 11.2 and 14.4, 4 x 48000 x
+// 1024 13.7 and 18.9, 1 x 16000 x 2048 12.3 and 14.0.  More tokens are quantised too often: 8 x 32000 x 1024 14.6 and 14.6, 16
+// of them 19.2 and 15.0, 8 x 16000 x 2048 16.5 and 14.9 (in between, 4 x 16000 x 2048, 12.8 and 14.7).  Larger tables go either
+// way up to some 100 MB (4 x 64000 x 1024 22.0 and 21.5, 1 x 32000 x 2048 17.4 and 19.1, 1 x 50000 x 2048 32.4 and 30.5) and
+// are read faster by the tiles beyond (1 x 131072 x 4096 131 and 111).
 static bool few(const tt_int8_desc *d, const Int8Args &a) {
   return d->dtype != TT_DTYPE_I8 && a.n <= FEW_TOKENS && a.n * a.d <= FEW_VALUES && a.v * a.wpitch <= FEW_BYTES;
 }

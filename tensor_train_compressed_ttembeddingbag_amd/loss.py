@@ -1,14 +1,15 @@
 """Losses over the rows of an embedding table used as an output head.
 
-``linear_cross_entropy`` and ``linear_distillation`` take hidden states [..., D] and a weight
-[V, D] -- an ordinary table, or the rows of a TT table from ``full_weight()`` -- and return the
-loss of the logits ``hidden @ weight.T`` without ever holding the [N, V] logits: the forward
-keeps a running maximum and sum per position, the backward works through the vocabulary in
-pieces.  Both are differentiable in hidden and weight (once, in reverse mode), for float32,
+``linear_cross_entropy``, ``linear_distillation``, ``linear_preference`` and ``linear_policy`` take
+hidden states [..., D] and a weight [V, D] -- an ordinary table, or the rows of a TT table from
+``full_weight()`` -- and return the loss of the logits ``hidden @ weight.T`` without ever holding
+the [N, V] logits: the forward keeps a running maximum and sum per position, the backward works
+through the vocabulary in pieces, with the gradient of a piece's logits in 16 bits (float32: two
+fp16 parts).  All are differentiable in hidden and weight (once, in reverse mode), for float32,
 bfloat16 and float16, and return the loss in float32.
 
-Argument marshalling only; the computation runs in libttbag (``tt_loss_forward`` and
-``tt_loss_backward`` of ``include/tt_bag.h``).
+Argument marshalling only; the computation runs in libttbag (``tt_loss_*``, ``tt_prefer_*`` and
+``tt_policy_*`` of ``include/tt_bag.h``).
 """
 from __future__ import annotations
 
